@@ -26,7 +26,9 @@
  * (per-row E4M3 weights, W8A8 product) of `quantized_lm_head_copy` on the
  * first page; the grouped W4A16 product of
  * all experts of an NVFP4 MoE layer; the W4A4 NVFP4 product of
- * `CompressedTensorsW4A4Fp4`; an allocation-free variant of the W4A16
+ * `CompressedTensorsW4A4Fp4`; the router and the whole expert layer of an
+ * NVFP4 MoE model for a few tokens; log probabilities of given tokens from
+ * the logits, with their gradient; an allocation-free variant of the W4A16
  * product; and two self-tests.
  *
  * Conventions for every call:
@@ -521,6 +523,150 @@ nvfp4_status w4a4_lm_head_topk(const void *x, int64_t M, int64_t K, const uint8_
                                const float *input_global_scale, int64_t N, int64_t k,
                                int64_t *token_ids, float *values, void *workspace,
                                size_t workspace_bytes, void *stream);
+
+/* ----------------------------------------- MoE router and expert layer */
+
+#define NVFP4_MOE_MAX_EXPERTS 512 /* largest E of moe_route and w4a16_moe */
+#define NVFP4_ROUTE_MAX_K 32      /* largest k of moe_route */
+#define NVFP4_MOE_MAX_PAIRS 4096  /* largest M * k of w4a16_moe */
+#define NVFP4_MOE_MAX_DIM 32768   /* largest H and I of w4a16_moe */
+
+/* Scoring codes of moe_route. */
+#define NVFP4_ROUTE_SOFTMAX 0
+#define NVFP4_ROUTE_SIGMOID 1
+
+/*
+ * The router's choice: for each token m, with scores s = softmax(logits[m])
+ * or sigmoid(logits[m]),
+ *   expert_ids[m, j] (j = 0 .. k-1) = the experts with the k largest
+ *     selection keys, in descending order, of equal keys the lower expert
+ *     first; the key is s[e] + bias[e], or, without a bias, the logit itself
+ *     (both scores rise with it, so this is the same choice, unrounded);
+ *   weights[m, j] = s[expert_ids[m, j]], divided by their sum over j when
+ *     renormalize is not zero, times `scale`.
+ * Sums are fp32.  A NaN key ranks above every number and -0 equals +0.  A
+ * masked expert (logit -inf) has score 0; a token whose logits are all -inf
+ * gets the first k experts with weight 0, and so does a renormalized token
+ * whose chosen scores are all 0.
+ *
+ *   router_logits  [M, E] fp32 (dtype NVFP4_OUT_F32) or bf16 (NVFP4_OUT_BF16),
+ *                  device, aligned to an element.
+ *   M              tokens, M >= 0 (M == 0 is a no-op).
+ *   E              experts, 1 <= E <= NVFP4_MOE_MAX_EXPERTS.
+ *   k              1 <= k <= min(E, NVFP4_ROUTE_MAX_K).
+ *   bias           fp32 [E], device, or NULL: added to the scores for the
+ *                  choice only.
+ *   expert_ids     int32 [M, k], device.  Written.
+ *   weights        fp32 [M, k], device.  Written.
+ * One kernel, no workspace; an unknown dtype or scoring code is
+ * NVFP4_ERR_DTYPE.
+ */
+nvfp4_status moe_route(const void *router_logits, int dtype, int64_t M, int64_t E, int64_t k,
+                       int scoring, int renormalize, const float *bias, float scale,
+                       int32_t *expert_ids, float *weights, void *stream);
+
+/* Workspace bytes of w4a16_moe; 0 for rejected shapes. */
+size_t w4a16_moe_workspace_bytes(int64_t M, int64_t k, int64_t H, int64_t I);
+
+/*
+ * The whole expert layer of a mixture-of-experts model for a few tokens, on
+ * the layouts of w4a16_grouped_gemm: with e = expert_ids[m, j],
+ *   g = W13[e][0:I] x[m],  u = W13[e][I:2I] x[m],  h = g / (1 + exp(-g)) * u,
+ *   out[m] = sum_j weights[m, j] * W2[e] h,
+ * W13 and W2 dequantized as e2m1(code) * f32(scale) * global[e].
+ *   x            bf16 [M, H], device, 16-byte aligned.
+ *   M, k         M >= 0 (M == 0 is a no-op), k >= 1, M * k <=
+ *                NVFP4_MOE_MAX_PAIRS (more tokens: w4a16_grouped_gemm).
+ *   H, I         multiples of 16, at most NVFP4_MOE_MAX_DIM.
+ *   E            experts, 1 <= E <= NVFP4_MOE_MAX_EXPERTS.
+ *   expert_ids   int32 [M, k], device.  An id outside [0, E) adds nothing
+ *                (an expert of another rank, a padding token); a token with
+ *                no expert gets zeros.  Read by the kernels, never by the
+ *                host: the call can be captured in a CUDA graph.
+ *   weights      fp32 [M, k], device.
+ *   w13_packed, w13_scales, w13_global
+ *                u8 [E, 2I, H/2], u8 (e4m3) [E, 2I, H/16], f32 [E]: gate rows
+ *                0 .. I-1, up rows I .. 2I-1 of each expert, each expert as
+ *                nvfp4_quantize_rows writes it; 16-byte aligned.
+ *   w2_packed, w2_scales, w2_global
+ *                u8 [E, H, I/2], u8 [E, H, I/16], f32 [E].
+ *   out          [M, H] bf16 (NVFP4_OUT_BF16) or fp32 (NVFP4_OUT_F32), device,
+ *                16-byte aligned.
+ *   workspace    >= w4a16_moe_workspace_bytes(M, k, H, I), 256-byte aligned.
+ * Each weight of the experts in use is read once per 8 to 32 pairs; rows of
+ * a K that is a multiple of 64 (and bases on 32 bytes) are read in 32-byte
+ * pieces, others in 8-byte pieces.  Sums are fp32 in a fixed order (the
+ * result does not depend on the schedule); each product x * w is exact, h is
+ * rounded to 11 bits for a bf16 result and to 22 for an fp32 one (values far
+ * below the largest of 256 of them keep an absolute 2^-40 of it).  A NaN
+ * block scale in a weight that was read raises NVFP4_ERR_NONFINITE in the
+ * workspace status word.
+ */
+nvfp4_status w4a16_moe(const void *x, int64_t M, int64_t k, int64_t H, int64_t I, int64_t E,
+                       const int32_t *expert_ids, const float *weights, const uint8_t *w13_packed,
+                       const uint8_t *w13_scales, const float *w13_global,
+                       const uint8_t *w2_packed, const uint8_t *w2_scales, const float *w2_global,
+                       void *out, int out_dtype, void *workspace, size_t workspace_bytes,
+                       void *stream);
+
+/* ------------------------------------------- log probabilities of tokens */
+
+/*
+ * Log probabilities of given tokens under softmax(z), z = inv_temperature *
+ * logits, for each row m of logits[M, N]:
+ *   lse[m]      = log sum_n exp(z[m, n])
+ *   logprobs[m] = z[m, t] - lse[m], t = token_ids[m]
+ *   entropy[m]  = -sum_n p log p
+ *   ranks[m]    = 1 + the number of logits above the token's (1: most likely)
+ *   top_ids[m, j], top_logprobs[m, j] (j = 0 .. k-1) = the k largest logits'
+ *                 columns, in descending order, of equal logits the lower
+ *                 column first, and their log probabilities.
+ * A column of -inf (a masked token) has probability 0 and adds nothing to
+ * the entropy.  A row that is all -inf has lse -inf, entropy 0 and log
+ * probabilities -inf.  A token id outside [0, N) (no token: a padding
+ * position) gives log probability 0 and rank 0; the row's other outputs do
+ * not depend on it.  A row with a NaN or +inf gives NaN; NaN logits rank
+ * above every number in top_ids.  -0 equals +0.
+ *
+ *   logits        [M, N] fp32 (NVFP4_OUT_F32) or bf16 (NVFP4_OUT_BF16), rows
+ *                 `ld` elements apart (ld >= N: a padded vocabulary), device,
+ *                 aligned to an element.
+ *   M, N          M >= 0 (M == 0 is a no-op), 1 <= N < 2^31.
+ *   token_ids     int64 [M], device.
+ *   inv_temperature  positive and finite, else NVFP4_ERR_SHAPE.
+ *   k             0 <= k <= min(N, NVFP4_TOPK_MAX).
+ *   logprobs, entropy, lse  fp32 [M]; ranks int64 [M]; device.  Written.
+ *   top_ids       int64 [M, k], top_logprobs fp32 [M, k]; may be NULL if k == 0.
+ * One kernel, one read of the logits (a second look at about k / 512 of a
+ * row for the alternatives), no workspace, sums in fp32.
+ */
+nvfp4_status token_logprobs(const void *logits, int dtype, int64_t M, int64_t N, int64_t ld,
+                            const int64_t *token_ids, float inv_temperature, int64_t k,
+                            float *logprobs, float *entropy, float *lse, int64_t *ranks,
+                            int64_t *top_ids, float *top_logprobs, void *stream);
+
+/*
+ * The gradient of token_logprobs with respect to the logits, from the
+ * gradients a of logprobs and b of entropy (the alternatives and ranks have
+ * none), with p = exp(z - lse):
+ *   grad[m, n] = inv_temperature *
+ *       (a[m] (1[n == t] - p[n]) - b[m] p[n] (z[n] - lse[m] + entropy[m])).
+ * Where the token id lies outside [0, N), a[m] counts as 0; a row that was
+ * all -inf (lse -inf) gets zeros; a masked column gets 0.
+ *   logits, token_ids, inv_temperature  as given to token_logprobs.
+ *   lse, entropy        fp32 [M] as it wrote them (entropy may be NULL when
+ *                       grad_entropy is).
+ *   grad_logprobs       fp32 [M].
+ *   grad_entropy        fp32 [M], or NULL (zero).
+ *   grad                [M, N] in the logits' dtype, rows ld_grad elements
+ *                       apart; may be the logits themselves (ld_grad == ld).
+ * One kernel, one read of the logits and one write of the gradient.
+ */
+nvfp4_status token_logprobs_backward(const void *logits, int dtype, int64_t M, int64_t N,
+                                     int64_t ld, const int64_t *token_ids, float inv_temperature,
+                                     const float *lse, const float *entropy,
+                                     const float *grad_logprobs, const float *grad_entropy,
+                                     void *grad, int64_t ld_grad, void *stream);
 
 /* ------------------------------------------- allocation-free variant */
 

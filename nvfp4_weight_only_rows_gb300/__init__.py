@@ -35,6 +35,12 @@ Entry points (same names as the C ABI):
 * ``w4a16_grouped_gemm(x, group_offsets, packed, scales, global_scales)`` -- the
   NVFP4 W4A16 product of all experts of a MoE layer in one call, tokens grouped
   by expert (``ModelOptNvFp4FusedMoE`` weight layouts).
+* ``moe_route(router_logits, k)`` -> ``(expert_ids i32[M, k], weights f32[M, k])`` and
+  ``w4a16_moe(x, expert_ids, weights, w13..., w2...)`` -> ``out bf16[M, H]`` -- the
+  router's choice and the whole NVFP4 expert layer for a few tokens.
+* ``token_logprobs(logits, token_ids, k)`` -> ``(logprobs, entropy, lse, ranks,
+  top_ids, top_logprobs)`` -- log probabilities of given tokens with the top
+  alternatives; ``token_logprobs_backward`` -- their gradient.
 """
 from __future__ import annotations
 
@@ -59,6 +65,8 @@ __all__ = [
     "w4a16_grouped_gemm", "w4a16_grouped_workspace_bytes", "w4a16_lm_head_topk",
     "w4a16_lm_head_topk_workspace_bytes", "TOPK_MAX", "w8a8_lm_head_topk",
     "w8a8_lm_head_topk_workspace_bytes", "w4a4_lm_head_topk", "w4a4_lm_head_topk_workspace_bytes",
+    "moe_route", "w4a16_moe", "w4a16_moe_workspace_bytes", "token_logprobs",
+    "token_logprobs_backward",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -169,6 +177,20 @@ def load_library() -> ctypes.CDLL:
     lib.w4a16_grouped_gemm.argtypes = [vp, i64, i64, vp, i64, vp, vp, vp, i64, vp, ctypes.c_int,
                                        vp, sz, vp]
     lib.w4a16_grouped_gemm.restype = st
+    lib.moe_route.argtypes = [vp, ctypes.c_int, i64, i64, i64, ctypes.c_int, ctypes.c_int, vp,
+                              ctypes.c_float, vp, vp, vp]
+    lib.moe_route.restype = st
+    lib.w4a16_moe_workspace_bytes.argtypes = [i64, i64, i64, i64]
+    lib.w4a16_moe_workspace_bytes.restype = sz
+    lib.w4a16_moe.argtypes = [vp, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                              ctypes.c_int, vp, sz, vp]
+    lib.w4a16_moe.restype = st
+    lib.token_logprobs.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, ctypes.c_float, i64, vp,
+                                   vp, vp, vp, vp, vp, vp]
+    lib.token_logprobs.restype = st
+    lib.token_logprobs_backward.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, ctypes.c_float,
+                                            vp, vp, vp, vp, vp, i64, vp]
+    lib.token_logprobs_backward.restype = st
     lib.w4a16_lm_head_noalloc.argtypes = [vp, i64, i64, vp, vp, vp, i64, vp, ctypes.c_int, vp]
     lib.w4a16_lm_head_noalloc.restype = st
     lib.w4a16_lm_head_noalloc_status.argtypes = [ctypes.POINTER(ctypes.c_int32), vp]
@@ -643,6 +665,155 @@ def w4a16_grouped_gemm(x: torch.Tensor, group_offsets: torch.Tensor, packed: tor
                                 _ptr(global_scales), N, _ptr(out), code, _ptr(workspace),
                                 workspace.numel() * workspace.element_size(), _stream(stream))
     _check(rc, "w4a16_grouped_gemm")
+    return out
+
+
+_SCORING = {"softmax": 0, "sigmoid": 1}  # NVFP4_ROUTE_*
+_DTYPE_CODE = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
+
+
+def moe_route(router_logits: torch.Tensor, k: int, renormalize: bool = True,
+              scoring: str = "softmax", bias: torch.Tensor | None = None, scale: float = 1.0,
+              expert_ids: torch.Tensor | None = None, weights: torch.Tensor | None = None,
+              stream=None):
+    """The k experts of each token with the largest softmax or sigmoid scores
+    (plus bias f32[E] for the choice; lower expert first on ties) of
+    router_logits f32 or bf16 [M, E]: (expert_ids i32[M, k], weights f32[M, k])."""
+    lib = load_library()
+    code = _DTYPE_CODE.get(router_logits.dtype)
+    if code is None or router_logits.dim() != 2:
+        raise ValueError("router_logits must be float32 or bfloat16 [M, E]")
+    _need(router_logits, router_logits.dtype, "router_logits")
+    M, E = router_logits.shape
+    if scoring not in _SCORING:
+        raise ValueError(f"scoring must be one of {sorted(_SCORING)}, got {scoring!r}")
+    if bias is not None:
+        _need(bias, torch.float32, "bias", (E,))
+    kk = max(int(k), 0)
+    if expert_ids is None:
+        expert_ids = torch.empty((M, kk), dtype=torch.int32, device=router_logits.device)
+    else:
+        _need(expert_ids, torch.int32, "expert_ids", (M, kk))
+    if weights is None:
+        weights = torch.empty((M, kk), dtype=torch.float32, device=router_logits.device)
+    else:
+        _need(weights, torch.float32, "weights", (M, kk))
+    rc = lib.moe_route(router_logits.data_ptr(), code, M, E, k, _SCORING[scoring],
+                       int(renormalize), _ptr(bias), scale, expert_ids.data_ptr(),
+                       weights.data_ptr(), _stream(stream))
+    _check(rc, "moe_route")
+    return expert_ids, weights
+
+
+def w4a16_moe_workspace_bytes(M: int, k: int, H: int, I: int) -> int:
+    return int(load_library().w4a16_moe_workspace_bytes(M, k, H, I))
+
+
+def w4a16_moe(x: torch.Tensor, expert_ids: torch.Tensor, weights: torch.Tensor,
+              w13_packed: torch.Tensor, w13_scales: torch.Tensor, w13_global: torch.Tensor,
+              w2_packed: torch.Tensor, w2_scales: torch.Tensor, w2_global: torch.Tensor,
+              out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
+              workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The whole NVFP4 expert layer for a few tokens: out[m] = sum over j of
+    weights[m, j] * W2[e] (silu(gate) * up), gate | up = W13[e] x[m], e =
+    expert_ids[m, j].  x bf16[M, H], expert_ids i32[M, k] (an id outside
+    [0, E) adds nothing), weights f32[M, k], w13 u8[E, 2I, H/2] + e4m3 scales
+    [E, 2I, H/16] + f32[E], w2 u8[E, H, I/2] + [E, H, I/16] + f32[E]."""
+    lib = load_library()
+    _need(x, torch.bfloat16, "x")
+    M, H = x.shape
+    k = expert_ids.shape[1]
+    E, I = w2_packed.shape[0], w2_packed.shape[2] * 2
+    _need(expert_ids, torch.int32, "expert_ids", (M, k))
+    _need(weights, torch.float32, "weights", (M, k))
+    _need(w13_packed, torch.uint8, "w13_packed", (E, 2 * I, H // 2))
+    _need(w13_scales, w13_scales.dtype, "w13_scales", (E, 2 * I, H // 16))
+    _need(w13_global, torch.float32, "w13_global", (E,))
+    _need(w2_packed, torch.uint8, "w2_packed", (E, H, I // 2))
+    _need(w2_scales, w2_scales.dtype, "w2_scales", (E, H, I // 16))
+    _need(w2_global, torch.float32, "w2_global", (E,))
+    if w13_scales.element_size() != 1 or w2_scales.element_size() != 1:
+        raise ValueError("scales must be float8_e4m3fn (or uint8 bit patterns)")
+    if out is None:
+        out = torch.empty(M, H, dtype=out_dtype, device=x.device)
+    _need(out, out.dtype, "out", (M, H))
+    code = _DTYPE_CODE.get(out.dtype)
+    if code is None:
+        raise ValueError("out must be float32 or bfloat16")
+    if workspace is None:
+        workspace = _workspace(lib.w4a16_moe_workspace_bytes(M, k, H, I), x.device)
+    rc = lib.w4a16_moe(x.data_ptr(), M, k, H, I, E, expert_ids.data_ptr(), weights.data_ptr(),
+                       w13_packed.data_ptr(), w13_scales.data_ptr(), w13_global.data_ptr(),
+                       w2_packed.data_ptr(), w2_scales.data_ptr(), w2_global.data_ptr(),
+                       out.data_ptr(), code, workspace.data_ptr(),
+                       workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(rc, "w4a16_moe")
+    return out
+
+
+def _logits_args(logits, token_ids):
+    code = _DTYPE_CODE.get(logits.dtype)
+    if code is None or logits.dim() != 2 or not logits.is_cuda:
+        raise ValueError("logits must be a float32 or bfloat16 CUDA tensor [M, N]")
+    M, N = logits.shape
+    if N > 1 and logits.stride(1) != 1:
+        raise ValueError("the logits of a row must be contiguous")
+    ld = logits.stride(0) if M > 1 else N
+    if ld < N:
+        raise ValueError("the rows of logits overlap")
+    _need(token_ids, torch.int64, "token_ids", (M,))
+    return code, M, N, ld
+
+
+def token_logprobs(logits: torch.Tensor, token_ids: torch.Tensor, k: int = 0,
+                   inv_temperature: float = 1.0, stream=None):
+    """Log probabilities of token_ids i64[M] under softmax(inv_temperature *
+    logits) for logits f32 or bf16 [M, N] (rows may be strided), and the k
+    most likely tokens of each row: (logprobs f32[M], entropy f32[M], lse
+    f32[M], ranks i64[M], top_ids i64[M, k], top_logprobs f32[M, k])."""
+    lib = load_library()
+    code, M, N, ld = _logits_args(logits, token_ids)
+    dev = logits.device
+    kk = max(int(k), 0)
+    logprobs, entropy, lse = torch.empty((3, M), dtype=torch.float32, device=dev).unbind(0)
+    ranks = torch.empty(M, dtype=torch.int64, device=dev)
+    top_ids = torch.empty((M, kk), dtype=torch.int64, device=dev)
+    top_logprobs = torch.empty((M, kk), dtype=torch.float32, device=dev)
+    rc = lib.token_logprobs(logits.data_ptr(), code, M, N, ld, token_ids.data_ptr(),
+                            inv_temperature, k, logprobs.data_ptr(), entropy.data_ptr(),
+                            lse.data_ptr(), ranks.data_ptr(), top_ids.data_ptr(),
+                            top_logprobs.data_ptr(), _stream(stream))
+    _check(rc, "token_logprobs")
+    return logprobs, entropy, lse, ranks, top_ids, top_logprobs
+
+
+def token_logprobs_backward(logits: torch.Tensor, token_ids: torch.Tensor, lse: torch.Tensor,
+                            entropy: torch.Tensor | None, grad_logprobs: torch.Tensor,
+                            grad_entropy: torch.Tensor | None = None,
+                            inv_temperature: float = 1.0, out: torch.Tensor | None = None,
+                            stream=None) -> torch.Tensor:
+    """The gradient of token_logprobs' logprobs and entropy with respect to
+    the logits, in their dtype; `out` may be the logits themselves."""
+    lib = load_library()
+    code, M, N, ld = _logits_args(logits, token_ids)
+    _need(lse, torch.float32, "lse", (M,))
+    _need(grad_logprobs, torch.float32, "grad_logprobs", (M,))
+    if grad_entropy is not None:
+        _need(grad_entropy, torch.float32, "grad_entropy", (M,))
+        if entropy is None:
+            raise ValueError("grad_entropy needs the forward's entropy")
+    if entropy is not None:
+        _need(entropy, torch.float32, "entropy", (M,))
+    if out is None:
+        out = torch.empty((M, N), dtype=logits.dtype, device=logits.device)
+    elif not out.is_cuda or out.dtype != logits.dtype or tuple(out.shape) != (M, N) or (
+            N > 1 and out.stride(1) != 1):
+        raise ValueError("out must be a CUDA tensor of the logits' shape and dtype, rows contiguous")
+    rc = lib.token_logprobs_backward(logits.data_ptr(), code, M, N, ld, token_ids.data_ptr(),
+                                     inv_temperature, lse.data_ptr(), _ptr(entropy),
+                                     grad_logprobs.data_ptr(), _ptr(grad_entropy), out.data_ptr(),
+                                     out.stride(0) if M > 1 else N, _stream(stream))
+    _check(rc, "token_logprobs_backward")
     return out
 
 

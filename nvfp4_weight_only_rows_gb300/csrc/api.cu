@@ -55,6 +55,24 @@ nvfp4_status w4a4_topk_launch(const void* x, int64_t M, int64_t K, const uint8_t
                               int k, int64_t* token_ids, float* values, void* workspace,
                               cudaStream_t stream);
 
+nvfp4_status moe_route_launch(const void* logits, int dtype, int64_t M, int E, int k, int scoring,
+                              int renorm, const float* bias, float scale, int32_t* ids,
+                              float* weights, cudaStream_t stream);
+size_t moe_workspace_bytes(int64_t M, int64_t k, int64_t H, int64_t I);
+nvfp4_status moe_launch(const void* x, int64_t M, int64_t k, int64_t H, int64_t I, int64_t E,
+                        const int32_t* ids, const float* weights, const uint8_t* p13,
+                        const uint8_t* s13, const float* g13, const uint8_t* p2,
+                        const uint8_t* s2, const float* g2, void* out, int out_dtype,
+                        void* workspace, cudaStream_t stream);
+nvfp4_status logprobs_launch(const void* logits, int dtype, int64_t M, int64_t N, int64_t ld,
+                             const int64_t* tokens, float s, int k, float* logprob, float* entropy,
+                             float* lse, int64_t* rank, int64_t* top_ids, float* top_lp,
+                             cudaStream_t stream);
+nvfp4_status logprobs_grad_launch(const void* logits, int dtype, int64_t M, int64_t N, int64_t ld,
+                                  const int64_t* tokens, float s, const float* lse,
+                                  const float* entropy, const float* g_lp, const float* g_ent,
+                                  void* out, int64_t ld_out, cudaStream_t stream);
+
 static bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // The kernels are built for sm_103a only; refuse other devices up front.
@@ -483,6 +501,113 @@ nvfp4_status w4a4_lm_head_topk(const void* x, int64_t M, int64_t K, const uint8_
   return w4a4_topk_launch(x, M, K, packed, scales_swizzled, global_scale, input_global_scale, N,
                           (int)k, token_ids, values, workspace,
                           static_cast<cudaStream_t>(stream));
+}
+
+nvfp4_status moe_route(const void* router_logits, int dtype, int64_t M, int64_t E, int64_t k,
+                       int scoring, int renormalize, const float* bias, float scale,
+                       int32_t* expert_ids, float* weights, void* stream) {
+  if (M < 0 || M >= kMaxDim || E < 1 || E > NVFP4_MOE_MAX_EXPERTS || k < 1 || k > E ||
+      k > NVFP4_ROUTE_MAX_K)
+    return NVFP4_ERR_SHAPE;
+  if ((dtype != NVFP4_OUT_F32 && dtype != NVFP4_OUT_BF16) ||
+      (scoring != NVFP4_ROUTE_SOFTMAX && scoring != NVFP4_ROUTE_SIGMOID))
+    return NVFP4_ERR_DTYPE;
+  if (M == 0) return NVFP4_OK;
+  if (!router_logits || !expert_ids || !weights) return NVFP4_ERR_NULL;
+  if (!aligned(router_logits, dtype == NVFP4_OUT_F32 ? 4 : 2) || !aligned(bias, 4) ||
+      !aligned(expert_ids, 4) || !aligned(weights, 4))
+    return NVFP4_ERR_ALIGN;
+  nvfp4_status st = check_device();
+  if (st != NVFP4_OK) return st;
+  return moe_route_launch(router_logits, dtype, M, (int)E, (int)k, scoring, renormalize, bias,
+                          scale, expert_ids, weights, static_cast<cudaStream_t>(stream));
+}
+
+static bool moe_shape_ok(int64_t M, int64_t k, int64_t H, int64_t I) {
+  return M >= 0 && k >= 1 && k <= NVFP4_MOE_MAX_PAIRS && M <= NVFP4_MOE_MAX_PAIRS / k && H >= 16 &&
+         H % 16 == 0 && H <= NVFP4_MOE_MAX_DIM && I >= 16 && I % 16 == 0 && I <= NVFP4_MOE_MAX_DIM;
+}
+
+size_t w4a16_moe_workspace_bytes(int64_t M, int64_t k, int64_t H, int64_t I) {
+  return moe_shape_ok(M, k, H, I) ? moe_workspace_bytes(M, k, H, I) : 0;
+}
+
+nvfp4_status w4a16_moe(const void* x, int64_t M, int64_t k, int64_t H, int64_t I, int64_t E,
+                       const int32_t* expert_ids, const float* weights, const uint8_t* w13_packed,
+                       const uint8_t* w13_scales, const float* w13_global,
+                       const uint8_t* w2_packed, const uint8_t* w2_scales, const float* w2_global,
+                       void* out, int out_dtype, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  if (!moe_shape_ok(M, k, H, I) || E < 1 || E > NVFP4_MOE_MAX_EXPERTS) return NVFP4_ERR_SHAPE;
+  if (out_dtype != NVFP4_OUT_F32 && out_dtype != NVFP4_OUT_BF16) return NVFP4_ERR_DTYPE;
+  if (M == 0) return NVFP4_OK;
+  if (!x || !expert_ids || !weights || !w13_packed || !w13_scales || !w13_global || !w2_packed ||
+      !w2_scales || !w2_global || !out)
+    return NVFP4_ERR_NULL;
+  if (!workspace || workspace_bytes < moe_workspace_bytes(M, k, H, I)) return NVFP4_ERR_WORKSPACE;
+  if (!aligned(x, 16) || !aligned(expert_ids, 4) || !aligned(weights, 4) ||
+      !aligned(w13_packed, 16) || !aligned(w13_scales, 16) || !aligned(w13_global, 4) ||
+      !aligned(w2_packed, 16) || !aligned(w2_scales, 16) || !aligned(w2_global, 4) ||
+      !aligned(out, 16) || !aligned(workspace, 256))
+    return NVFP4_ERR_ALIGN;
+  nvfp4_status st = check_device();
+  if (st != NVFP4_OK) return st;
+  return moe_launch(x, M, k, H, I, E, expert_ids, weights, w13_packed, w13_scales, w13_global,
+                    w2_packed, w2_scales, w2_global, out, out_dtype, workspace,
+                    static_cast<cudaStream_t>(stream));
+}
+
+// What both calls on logits check of them: sizes, dtype, and a temperature
+// that is a positive number.
+static nvfp4_status check_logits(int dtype, int64_t M, int64_t N, int64_t ld, float s) {
+  if (M < 0 || M >= kMaxDim || N < 1 || N >= kMaxDim || ld < N || !(s > 0.0f) || s > 3.4e38f)
+    return NVFP4_ERR_SHAPE;
+  if (dtype != NVFP4_OUT_F32 && dtype != NVFP4_OUT_BF16) return NVFP4_ERR_DTYPE;
+  return NVFP4_OK;
+}
+
+nvfp4_status token_logprobs(const void* logits, int dtype, int64_t M, int64_t N, int64_t ld,
+                            const int64_t* token_ids, float inv_temperature, int64_t k,
+                            float* logprobs, float* entropy, float* lse, int64_t* ranks,
+                            int64_t* top_ids, float* top_logprobs, void* stream) {
+  nvfp4_status st = check_logits(dtype, M, N, ld, inv_temperature);
+  if (st != NVFP4_OK) return st;
+  if (k < 0 || k > N || k > NVFP4_TOPK_MAX) return NVFP4_ERR_SHAPE;
+  if (M == 0) return NVFP4_OK;
+  if (!logits || !token_ids || !logprobs || !entropy || !lse || !ranks ||
+      (k > 0 && (!top_ids || !top_logprobs)))
+    return NVFP4_ERR_NULL;
+  if (!aligned(logits, dtype == NVFP4_OUT_F32 ? 4 : 2) || !aligned(token_ids, 8) ||
+      !aligned(logprobs, 4) || !aligned(entropy, 4) || !aligned(lse, 4) || !aligned(ranks, 8) ||
+      !aligned(top_ids, 8) || !aligned(top_logprobs, 4))
+    return NVFP4_ERR_ALIGN;
+  st = check_device();
+  if (st != NVFP4_OK) return st;
+  return logprobs_launch(logits, dtype, M, N, ld, token_ids, inv_temperature, (int)k, logprobs,
+                         entropy, lse, ranks, top_ids, top_logprobs,
+                         static_cast<cudaStream_t>(stream));
+}
+
+nvfp4_status token_logprobs_backward(const void* logits, int dtype, int64_t M, int64_t N,
+                                     int64_t ld, const int64_t* token_ids, float inv_temperature,
+                                     const float* lse, const float* entropy,
+                                     const float* grad_logprobs, const float* grad_entropy,
+                                     void* grad, int64_t ld_grad, void* stream) {
+  nvfp4_status st = check_logits(dtype, M, N, ld, inv_temperature);
+  if (st != NVFP4_OK) return st;
+  if (ld_grad < N) return NVFP4_ERR_SHAPE;
+  if (M == 0) return NVFP4_OK;
+  if (!logits || !token_ids || !lse || !grad_logprobs || !grad || (grad_entropy && !entropy))
+    return NVFP4_ERR_NULL;
+  const uintptr_t es = dtype == NVFP4_OUT_F32 ? 4 : 2;
+  if (!aligned(logits, es) || !aligned(grad, es) || !aligned(token_ids, 8) || !aligned(lse, 4) ||
+      !aligned(entropy, 4) || !aligned(grad_logprobs, 4) || !aligned(grad_entropy, 4))
+    return NVFP4_ERR_ALIGN;
+  st = check_device();
+  if (st != NVFP4_OK) return st;
+  return logprobs_grad_launch(logits, dtype, M, N, ld, token_ids, inv_temperature, lse, entropy,
+                              grad_logprobs, grad_entropy, grad, ld_grad,
+                              static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -143,6 +143,43 @@ __device__ __forceinline__ uint32_t cvt_e2m1x8(const float (&q)[8]) {
   return mag | (w & nonzero);
 }
 
+// 8 e2m1 codes (one word; byte j = codes 2j | 2j+1 << 4) -> 4 fp16 pairs,
+// element 2j in the low half, each multiplied by the block scale pair sf2.
+__device__ __forceinline__ void dequant8(uint32_t w, uint32_t sf2, uint32_t* out) {
+  uint32_t h0, h1, h2, h3;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h0), "=r"(h1), "=r"(h2), "=r"(h3)
+      : "r"(w));
+  asm("mul.rn.f16x2 %0, %0, %4;\n\t"
+      "mul.rn.f16x2 %1, %1, %4;\n\t"
+      "mul.rn.f16x2 %2, %2, %4;\n\t"
+      "mul.rn.f16x2 %3, %3, %4;"
+      : "+r"(h0), "+r"(h1), "+r"(h2), "+r"(h3)
+      : "r"(sf2));
+  out[0] = h0;
+  out[1] = h1;
+  out[2] = h2;
+  out[3] = h3;
+}
+
+// 4 E4M3 scale bytes -> two fp16 pairs (s0, s1) and (s2, s3)
+__device__ __forceinline__ void scales4_to_f16(uint32_t s, uint32_t& s01, uint32_t& s23) {
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "mov.b32 {lo, hi}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+      : "=r"(s01), "=r"(s23)
+      : "r"(s));
+}
+
+__device__ __forceinline__ uint32_t dup_lo(uint32_t v) { return __byte_perm(v, 0, 0x1010); }
+__device__ __forceinline__ uint32_t dup_hi(uint32_t v) { return __byte_perm(v, 0, 0x3232); }
+
 // One-dimensional bulk copy global -> shared, completing on `bar` (both
 // addresses 16-byte aligned, bytes a multiple of 16).
 __device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint32_t bytes,
