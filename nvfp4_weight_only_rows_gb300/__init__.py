@@ -211,7 +211,8 @@ def _ptr(t: torch.Tensor | None) -> ctypes.c_void_p:
 
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the current device's current stream, without building a Stream object
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -775,10 +776,13 @@ def token_logprobs(logits: torch.Tensor, token_ids: torch.Tensor, k: int = 0,
     code, M, N, ld = _logits_args(logits, token_ids)
     dev = logits.device
     kk = max(int(k), 0)
-    logprobs, entropy, lse = torch.empty((3, M), dtype=torch.float32, device=dev).unbind(0)
-    ranks = torch.empty(M, dtype=torch.int64, device=dev)
-    top_ids = torch.empty((M, kk), dtype=torch.int64, device=dev)
-    top_logprobs = torch.empty((M, kk), dtype=torch.float32, device=dev)
+    empty = torch.empty  # one allocation per result: views of a shared one cost more
+    logprobs = empty(M, dtype=torch.float32, device=dev)
+    entropy = empty(M, dtype=torch.float32, device=dev)
+    lse = empty(M, dtype=torch.float32, device=dev)
+    ranks = empty(M, dtype=torch.int64, device=dev)
+    top_ids = empty((M, kk), dtype=torch.int64, device=dev)
+    top_logprobs = empty((M, kk), dtype=torch.float32, device=dev)
     rc = lib.token_logprobs(logits.data_ptr(), code, M, N, ld, token_ids.data_ptr(),
                             inv_temperature, k, logprobs.data_ptr(), entropy.data_ptr(),
                             lse.data_ptr(), ranks.data_ptr(), top_ids.data_ptr(),

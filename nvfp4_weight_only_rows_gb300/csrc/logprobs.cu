@@ -14,15 +14,10 @@
 // can hold a logit that does, so a second look (from L2) covers about k
 // threads' shares of the row and yields a few more than k keys
 // (order key << 32 | ~index: distinct, lower index first on ties).
-#include <cooperative_groups.h>
-
 #include "gemm_common.cuh"
-
-namespace cg = cooperative_groups;
 
 namespace nvfp4 {
 
-constexpr int kLpThreads = 512;
 constexpr int kLpCand = 1024;      // keys a CTA ranks in shared memory
 constexpr int kLpMaxCluster = 8;   // CTAs that share a row
 constexpr float kLowest = -3.402823466e38f;
@@ -107,18 +102,42 @@ __device__ __forceinline__ RowSplit split_row(const T* row, int64_t N) {
   return {head, (N - head) / Vec<T>::kN};
 }
 
-// The softmax state of a part of a row (of the scaled logits).
+// fma, mul and add on two fp32 at once.
+__device__ __forceinline__ uint64_t pack2f(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2f(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Softmax state of a part of a row relative to the maximum m (scaled).
 struct LpStats {
   float m, S, T;
 };
-__device__ __forceinline__ LpStats lp_merge(const LpStats& a, const LpStats& b) {
-  const float m = max_nan(a.m, b.m);
-  const float da = a.m - m, db = b.m - m;  // both finite or NaN: m starts at the lowest finite
-  const float ea = exp_neg(da), eb = exp_neg(db);
-  // a part that vanished adds nothing (da S may have overflowed)
-  const float ta = ea == 0.0f ? 0.0f : ea * (a.T + da * a.S);
-  const float tb = eb == 0.0f ? 0.0f : eb * (b.T + db * b.S);
-  return {m, a.S * ea + b.S * eb, ta + tb};
+// ... seen from a maximum m >= a.m.  A part that vanishes adds nothing (the
+// product d S may have overflowed).
+__device__ __forceinline__ LpStats lp_shift(const LpStats& a, float m) {
+  const float d = a.m - m, e = exp_neg(d);
+  return {m, a.S * e, e == 0.0f ? 0.0f : e * __fmaf_rn(d, a.S, a.T)};
 }
 
 struct LpArgs {
@@ -131,136 +150,213 @@ struct LpArgs {
   int64_t *rank, *top_ids;
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LpArgs p) {
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of this CTA's shared variable p in the cluster's first CTA.
+__device__ __forceinline__ uint32_t first_cta_addr(const void* p) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+  return r;
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, unsigned long long v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+
+// Logits are held at or above this in the main pass, so that a masked one
+// (-inf) has a finite d and 0 d = 0.  What is held there has to vanish against
+// the largest logit; where it does not (a share with nothing else left, an
+// extreme temperature) the share is looked at again without the floor.
+constexpr float kFloor = -1e25f;
+constexpr float kMaxScale = 1e12f;  // times the floor: finite
+
+// T: float, or uint16_t for bf16 bits; kT threads.
+template <typename T, int kT>
+__global__ void __launch_bounds__(kT, 1024 / kT) logprobs_kernel(const LpArgs p) {
   grid_dependency_wait();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int kV = Vec<T>::kN;
-  constexpr int kU = 32 / kV;  // vectors of a batch: their loads are in flight together
+  constexpr int kU = 4;  // vectors of a batch: their loads are in flight together
+  constexpr int kW = kT / 32;
   __shared__ unsigned long long s_cand[kLpCand];
   __shared__ unsigned long long s_top[NVFP4_TOPK_MAX];
+  __shared__ unsigned long long s_merge[kLpMaxCluster * NVFP4_TOPK_MAX];
+  __shared__ float4 s_part[kLpMaxCluster];  // per CTA: m, S, T, count
   __shared__ uint32_t s_hist[256];
-  __shared__ uint16_t s_hot[kLpThreads];
-  __shared__ LpStats s_stats[kLpThreads / 32];
-  __shared__ uint32_t s_cnt[kLpThreads / 32], s_hi[kLpThreads / 32], s_lo[kLpThreads / 32];
-  __shared__ LpStats s_row;
-  __shared__ uint32_t s_row_cnt, s_n, s_nhot;
-  __shared__ unsigned long long s_prefix;
-  __shared__ uint32_t s_need;
+  __shared__ uint16_t s_hot[kT];
+  __shared__ float s_S[kW], s_T[kW];
+  __shared__ uint32_t s_cnt[kW], s_hi[kW], s_lo[kW];
+  __shared__ uint32_t s_n, s_nhot, s_prefix, s_need, s_eq[kW];
 
-  cg::cluster_group cl = cg::this_cluster();
-  const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  const int C = (int)cluster_size(), rank = (int)cluster_rank();
+  if (C > 1) cluster_arrive();  // every CTA of the cluster runs before one writes to another
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t m_row = blockIdx.x / C;
   const T* row = static_cast<const T*>(p.logits) + m_row * p.ld;
-  const int64_t tok = p.tokens[m_row];
-  const bool has = tok >= 0 && tok < p.N;
-  const float x_tok = has ? Vec<T>::load(row + tok) : __int_as_float(0x7F800000);
   const RowSplit rs = split_row(row, p.N);
   const int64_t v0 = rs.nv * rank / C, v1 = rs.nv * (rank + 1) / C;
   const uint4* vec = reinterpret_cast<const uint4*>(row + rs.head);
   // the single elements go to the first CTA, one per thread
-  const int64_t singles = rank == 0 ? p.N - rs.nv * kV : 0;
+  const int singles = rank == 0 ? (int)(p.N - rs.nv * kV) : 0;
   auto single_at = [&](int64_t i) { return i < rs.head ? i : i + rs.nv * kV; };
 
-  // ---- one pass: softmax state, the largest logit, logits above the token's
-  float xmax = __int_as_float(0xFF800000);
-  LpStats st{kLowest, 0.0f, 0.0f};
-  uint32_t above = 0;
-  auto take = [&](const auto& x) {
-    constexpr int n = sizeof(x) / sizeof(float);
-    float bm = x[0];
+  uint4 raw[kU];
+  int64_t v = v0 + tid;
+  // past the end: -inf, which adds nothing
+  const uint32_t pad = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
+  auto fetch = [&](int64_t at) {
 #pragma unroll
-    for (int i = 1; i < n; ++i) bm = max_nan(bm, x[i]);
-    if (!(bm <= x_tok)) {
-#pragma unroll
-      for (int i = 0; i < n; ++i) above += x[i] > x_tok ? 1u : 0u;
-    }
-    if (!(bm <= xmax)) {
-      xmax = max_nan(xmax, bm);
-      const float m = max_nan(p.s * xmax, kLowest);
-      const float d = st.m - m, e = exp_neg(d);
-      st.T = e == 0.0f ? 0.0f : e * (st.T + d * st.S);
-      st.S *= e;
-      st.m = m;
-    }
-#pragma unroll
-    for (int i = 0; i < n; ++i) {
-      // a logit of -inf adds nothing: its d is held finite so that 0 d = 0
-      const float d = max_nan(__fmaf_rn(x[i], p.s, -st.m), -1e30f);
-      const float e = exp_neg(d);
-      st.S += e;
-      st.T = __fmaf_rn(d, e, st.T);
+    for (int u = 0; u < kU; ++u) {
+      const int64_t i = at + u * kT;
+      raw[u] = i < v1 ? __ldg(vec + i) : make_uint4(pad, pad, pad, pad);
     }
   };
-  int64_t v = v0 + tid;
-  for (; v + (kU - 1) * kLpThreads < v1; v += kU * kLpThreads) {
-    uint4 raw[kU];
-#pragma unroll
-    for (int u = 0; u < kU; ++u) raw[u] = __ldg(vec + v + u * kLpThreads);
+  fetch(v);
+  const int64_t tok = p.tokens[m_row];
+  const bool has = tok >= 0 && tok < p.N;
+  const float x_tok = has ? Vec<T>::load(row + tok) : __int_as_float(0x7F800000);
+
+  // ---- one pass: softmax state, the largest logit, logits above the token's
+  float xmax = kFloor;
+  LpStats st{kFloor * p.s, 0.0f, 0.0f};
+  uint64_t S2 = 0ull, T2 = 0ull;
+  const uint64_t s2 = pack2f(p.s, p.s), l2 = pack2f(kLog2e, kLog2e);
+  uint32_t above = 0;
+  auto raise = [&](float bm) {  // a new largest logit
+    xmax = max_nan(xmax, bm);
+    const float m = p.s * xmax;
+    const float d = st.m - m, e = exp_neg(d);
+    const float2 S = unpack2f(S2), t = unpack2f(T2);
+    T2 = e == 0.0f ? 0ull : pack2f(e * __fmaf_rn(d, S.x, t.x), e * __fmaf_rn(d, S.y, t.y));
+    S2 = pack2f(S.x * e, S.y * e);
+    st.m = m;
+  };
+  while (v < v1) {
     float x[kU * kV];
 #pragma unroll
     for (int u = 0; u < kU; ++u) Vec<T>::unpack(raw[u], x + u * kV);
-    take(x);
+    v += kU * kT;
+    if (v < v1) fetch(v);
+    float bm = x[0];
+#pragma unroll
+    for (int i = 1; i < kU * kV; ++i) bm = max_nan(bm, x[i]);
+    if (!(bm <= x_tok)) {
+#pragma unroll
+      for (int i = 0; i < kU * kV; ++i) above += x[i] > x_tok ? 1u : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < kU * kV; ++i) x[i] = max_nan(x[i], kFloor);
+    if (!(bm <= xmax)) raise(bm);
+    const uint64_t m2 = pack2f(-st.m, -st.m);
+#pragma unroll
+    for (int i = 0; i < kU * kV; i += 2) {
+      const uint64_t d = fma2(pack2f(x[i], x[i + 1]), s2, m2);
+      const float2 a = unpack2f(mul2(d, l2));
+      const uint64_t e = pack2f(ex2(a.x), ex2(a.y));
+      S2 = add2(S2, e);
+      T2 = fma2(d, e, T2);
+    }
   }
-  for (; v < v1; v += kLpThreads) {
-    float x[kV];
-    Vec<T>::unpack(__ldg(vec + v), x);
-    take(x);
-  }
+  float single = __int_as_float(0xFF800000);
   if (tid < singles) {
-    const float x[1] = {Vec<T>::load(row + single_at(tid))};
-    take(x);
+    single = Vec<T>::load(row + single_at(tid));
+    above += single > x_tok ? 1u : 0u;
+    const float x = max_nan(single, kFloor);
+    if (!(x <= xmax)) raise(x);
+    const float d = __fmaf_rn(x, p.s, -st.m), e = exp_neg(d);
+    S2 = add2(S2, pack2f(e, 0.0f));
+    T2 = fma2(pack2f(d, 0.0f), pack2f(e, 0.0f), T2);
+  }
+  {
+    const float2 S = unpack2f(S2), t = unpack2f(T2);
+    st.S = S.x + S.y;
+    st.T = t.x + t.y;
   }
 
-  // ---- over the block
+  // ---- over the block: the largest logit first, then plain sums
   const bool any = v0 + tid < v1 || tid < singles;
   const uint32_t key = any ? lp_key(xmax) : 0u;
-  LpStats w = st;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const LpStats other{__shfl_xor_sync(0xFFFFFFFFu, w.m, o), __shfl_xor_sync(0xFFFFFFFFu, w.S, o),
-                        __shfl_xor_sync(0xFFFFFFFFu, w.T, o)};
-    // the same order of operands on both sides, so that all lanes agree
-    w = (lane & o) ? lp_merge(other, w) : lp_merge(w, other);
-  }
-  const uint32_t wc = __reduce_add_sync(0xFFFFFFFFu, above);
-  const uint32_t whi = __reduce_max_sync(0xFFFFFFFFu, key);
-  const uint32_t wlo = __reduce_min_sync(0xFFFFFFFFu, any ? key : 0xFFFFFFFFu);
-  if (lane == 0) {
-    s_stats[warp] = w;
-    s_cnt[warp] = wc;
-    s_hi[warp] = whi;
-    s_lo[warp] = wlo;
+  {
+    const uint32_t c = __reduce_add_sync(0xFFFFFFFFu, above);
+    const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, key);
+    const uint32_t lo = __reduce_min_sync(0xFFFFFFFFu, any ? key : 0xFFFFFFFFu);
+    if (lane == 0) {
+      s_cnt[warp] = c;
+      s_hi[warp] = hi;
+      s_lo[warp] = lo;
+    }
   }
   if (tid == 0) {
     s_n = 0;
     s_nhot = 0;
   }
-  __syncthreads();
-  if (tid == 0) {
-    LpStats a = s_stats[0];
-    uint32_t c = s_cnt[0];
-    for (int i = 1; i < kLpThreads / 32; ++i) {
-      a = lp_merge(a, s_stats[i]);
-      c += s_cnt[i];
+  const int n_any = __syncthreads_count(any);
+  const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, lane < kW ? s_hi[lane] : 0u);
+  const uint32_t lo = __reduce_min_sync(0xFFFFFFFFu, lane < kW ? s_lo[lane] : 0xFFFFFFFFu);
+  float m_blk = p.s * key_value(hi);
+  // (block-uniform)
+  const bool plain = !(m_blk - p.s * kFloor >= 1000.0f) || p.s > kMaxScale;
+  if (!plain) {
+    st = lp_shift(st, m_blk);
+  } else {
+    const int64_t n_el = (v1 - v0) * kV;
+    auto at = [&](int64_t i) {
+      return Vec<T>::load(row + (i < n_el ? rs.head + v0 * kV + i : single_at(i - n_el)));
+    };
+    float bm = __int_as_float(0xFF800000);
+    for (int64_t i = tid; i < n_el + singles; i += kT) bm = max_nan(bm, at(i));
+    const uint32_t wk = __reduce_max_sync(0xFFFFFFFFu, lp_key(bm));
+    __syncthreads();
+    if (lane == 0) s_hi[warp] = wk;
+    __syncthreads();
+    m_blk = max_nan(p.s * key_value(__reduce_max_sync(0xFFFFFFFFu, lane < kW ? s_hi[lane] : 0u)),
+                    kLowest);
+    st = {m_blk, 0.0f, 0.0f};
+    for (int64_t i = tid; i < n_el + singles; i += kT) {
+      const float d = max_nan(__fmaf_rn(at(i), p.s, -m_blk), -1e30f), e = exp_neg(d);
+      st.S += e;
+      st.T = __fmaf_rn(d, e, st.T);
     }
-    s_row = a;
-    s_row_cnt = c;
+  }
+  {
+    const float S = warp_sum(st.S), t = warp_sum(st.T);
+    if (lane == 0) {
+      s_S[warp] = S;
+      s_T[warp] = t;
+    }
   }
 
   // ---- the CTA's k largest keys, sorted, zeros where its share has fewer
   if (p.k > 0) {
-    uint32_t hi = 0u, lo = 0xFFFFFFFFu;
-    for (int i = 0; i < kLpThreads / 32; ++i) {
-      hi = max(hi, s_hi[i]);
-      lo = min(lo, s_lo[i]);
-    }
     // a bound that at least k threads' maxima reach, and few more than k:
     // bisection between the smallest and the largest of them
-    uint32_t bound = 1u;
-    if (__syncthreads_count(any) >= p.k) {
-      bound = lo;
+    // The maxima say nothing at or below the floor: the bound stays above it.
+    const uint32_t floor_key = lp_key(kFloor);
+    uint32_t bound = floor_key + 1u;
+    if (n_any >= p.k && lo >= bound) bound = lo;
+    if (hi >= bound && n_any >= p.k) {
       uint64_t up = (uint64_t)hi + 1;  // no maximum reaches `up`
       while (up - bound > 1) {
         const uint32_t mid = (uint32_t)((bound + up) >> 1);
@@ -281,74 +377,141 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LpArgs p) {
       at = __shfl_sync(0xFFFFFFFFu, at, 0) + __popc(bal & ((1u << lane) - 1u));
       if (hot) s_hot[at] = (uint16_t)tid;
     }
-    __syncthreads();
-    // the hot threads' shares again, spread over the block
-    auto see = [&](float x, int64_t n) {
+    auto see = [&](float x, int64_t at_n) {
       const uint32_t kx = lp_key(x);
       if (kx >= bound) {
         const uint32_t at = atomicAdd(&s_n, 1u);
         if (at < (uint32_t)kLpCand)
-          s_cand[at] = ((unsigned long long)kx << 32) | (uint32_t)~(uint32_t)n;
+          s_cand[at] = ((unsigned long long)kx << 32) | (uint32_t)~(uint32_t)at_n;
       }
     };
-    const uint32_t per = (uint32_t)((v1 - v0 + kLpThreads - 1) / kLpThreads) + 1;  // vectors, a single
+    if (hot && tid < singles) see(single, single_at(tid));
+    __syncthreads();
+    // the hot threads' vectors again, spread over the block
+    const uint32_t per = (uint32_t)((v1 - v0 + kT - 1) / kT);
     const uint32_t todo = per * s_nhot;  // about N / kV at most
-    for (uint32_t i = tid; i < todo; i += kLpThreads) {
-      const int h = s_hot[i / per];
-      const uint32_t j = i % per;
-      if (j == per - 1) {
-        if (h < singles) see(Vec<T>::load(row + single_at(h)), single_at(h));
-        continue;
-      }
-      const int64_t vv = v0 + h + (int64_t)j * kLpThreads;
+    for (uint32_t i = tid; i < todo; i += kT) {
+      const int64_t vv = v0 + s_hot[i / per] + (int64_t)(i % per) * kT;
       if (vv >= v1) continue;
       float x[kV];
       Vec<T>::unpack(__ldg(vec + vv), x);
 #pragma unroll
       for (int q = 0; q < kV; ++q) see(x[q], rs.head + vv * kV + q);
     }
-    for (int i = tid; i < p.k; i += kLpThreads) s_top[i] = 0ull;
+    for (int i = tid; i < p.k; i += kT) s_top[i] = 0ull;
     __syncthreads();
     int n = (int)s_n;
-    if (n > kLpCand) {
-      // heavily tied logits: the k-th largest key by 8-bit digits from the
-      // top, over the whole share, then exactly the keys that reach it
-      const int64_t mine = (v1 - v0) * kV + singles;
-      auto key_at = [&](int64_t i) {
-        const int64_t at = i < (v1 - v0) * kV ? rs.head + v0 * kV + i : single_at(i - (v1 - v0) * kV);
-        return ((unsigned long long)lp_key(Vec<T>::load(row + at)) << 32) | (uint32_t)~(uint32_t)at;
-      };
-      unsigned long long prefix = 0ull, mask = 0ull;
-      uint32_t need = (uint32_t)p.k;
-      for (int shift = 56; shift >= 0; shift -= 8) {
-        for (int i = tid; i < 256; i += kLpThreads) s_hist[i] = 0;
+
+    // the share's elements in increasing order of the column: the head, the
+    // vectors, the tail
+    const int64_t n_el = (v1 - v0) * kV, mine = n_el + singles;
+    const int64_t h0 = singles ? rs.head : 0;
+    auto index_at = [&](int64_t i) {
+      return i < h0 ? i : i - h0 < n_el ? rs.head + v0 * kV + i - h0 : rs.nv * kV + i - n_el;
+    };
+    auto key_at = [&](int64_t i) { return lp_key(Vec<T>::load(row + index_at(i))); };
+    auto full_key = [&](uint32_t kx, int64_t i) {
+      return ((unsigned long long)kx << 32) | (uint32_t)~(uint32_t)index_at(i);
+    };
+    // the first `left` elements of key `kx`, in order, appended to s_cand;
+    // returns how many are missing
+    auto take_first = [&](uint32_t kx, int64_t left) {
+      constexpr int kE = 4;  // consecutive elements of a thread
+      for (int64_t i0 = 0; i0 < mine && left > 0; i0 += kT * kE) {
+        uint32_t eq = 0;
+        const int64_t i = i0 + tid * kE;
+#pragma unroll
+        for (int q = 0; q < kE; ++q)
+          if (i + q < mine && key_at(i + q) == kx) eq |= 1u << q;
+        int incl = __popc(eq);
+        const int own = incl;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+          if (lane >= o) incl += y;
+        }
+        if (lane == 31) s_eq[warp] = incl;
         __syncthreads();
-        for (int64_t i = tid; i < mine; i += kLpThreads) {
-          const unsigned long long kk = key_at(i);
-          if ((kk & mask) == prefix) atomicAdd(&s_hist[(uint32_t)(kk >> shift) & 255u], 1u);
+        int at = incl - own, total = 0;
+        for (int w = 0; w < kW; ++w) {
+          const int c = s_eq[w];
+          if (w < warp) at += c;
+          total += c;
+        }
+#pragma unroll
+        for (int q = 0; q < kE; ++q)
+          if ((eq >> q) & 1u) {
+            if (at < left) s_cand[atomicAdd(&s_n, 1u)] = full_key(kx, i + q);
+            ++at;
+          }
+        left -= total;
+        __syncthreads();
+      }
+      return left;
+    };
+    if (n > kLpCand) {
+      // heavily tied logits: the value of the k-th largest by 8-bit digits
+      // from the top, then the keys above it and the first of those equal
+      uint32_t prefix = 0u, mask = 0u, need = (uint32_t)p.k;
+      for (int shift = 24; shift >= 0; shift -= 8) {
+        __syncthreads();
+        for (int i = tid; i < 256; i += kT) s_hist[i] = 0;
+        __syncthreads();
+        for (int64_t i0 = 0; i0 < mine; i0 += kT) {
+          const int64_t i = i0 + tid;
+          const uint32_t kk = i < mine ? key_at(i) : 0u;
+          const bool in = i < mine && (kk & mask) == prefix;
+          const uint32_t bin = (kk >> shift) & 255u;
+          // lanes of one bin count at once
+          const uint32_t same = __match_any_sync(0xFFFFFFFFu, in ? bin : 256u);
+          if (in && (same & ((1u << lane) - 1u)) == 0u)
+            atomicAdd(&s_hist[bin], (uint32_t)__popc(same));
         }
         __syncthreads();
         if (tid == 0) {
           int b = 255;
           while (s_hist[b] < need) need -= s_hist[b--];
-          s_prefix = prefix | ((unsigned long long)b << shift);
+          s_prefix = prefix | ((uint32_t)b << shift);
           s_need = need;
         }
         __syncthreads();
         prefix = s_prefix;
         need = s_need;
-        mask |= 0xFFull << shift;
+        mask |= 0xFFu << shift;
       }
+      __syncthreads();
       if (tid == 0) s_n = 0;
       __syncthreads();
-      for (int64_t i = tid; i < mine; i += kLpThreads) {
-        const unsigned long long kk = key_at(i);
-        if (kk >= prefix) s_cand[atomicAdd(&s_n, 1u)] = kk;  // exactly k of them
+      for (int64_t i = tid; i < mine; i += kT) {
+        const uint32_t kk = key_at(i);
+        if (kk > prefix) s_cand[atomicAdd(&s_n, 1u)] = full_key(kk, i);  // fewer than k
+      }
+      take_first(prefix, need);
+      __syncthreads();
+      n = (int)s_n;
+    } else if (n < p.k && n < mine) {
+      // fewer than k logits above the floor: from the values below it, the
+      // largest first (a mask has one: one round)
+      int64_t left = min((int64_t)p.k, mine) - n;
+      uint32_t below = bound;
+      while (left > 0) {
+        uint32_t mx = 0u;
+        for (int64_t i = tid; i < mine; i += kT) {
+          const uint32_t kk = key_at(i);
+          if (kk < below) mx = max(mx, kk);
+        }
+        mx = __reduce_max_sync(0xFFFFFFFFu, mx);
+        __syncthreads();
+        if (lane == 0) s_eq[warp] = mx;
+        __syncthreads();
+        below = __reduce_max_sync(0xFFFFFFFFu, lane < kW ? s_eq[lane] : 0u);
+        __syncthreads();
+        left = take_first(below, left);
       }
       __syncthreads();
       n = (int)s_n;
     }
-    for (int i = tid; i < n; i += kLpThreads) {
+    for (int i = tid; i < n; i += kT) {
       const unsigned long long kk = s_cand[i];
       int r = 0;
       for (int j = 0; j < n; ++j) r += s_cand[j] > kk ? 1 : 0;
@@ -357,52 +520,69 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LpArgs p) {
   }
   __syncthreads();
 
-  // ---- over the cluster, in the first CTA
-  if (C > 1) cl.sync();
-  if (rank == 0) {
-    const unsigned long long* keys = s_top;
-    if (C > 1) {
-      if (tid == 0) {
-        LpStats a = s_row;
-        uint32_t c = s_row_cnt;
-        for (int i = 1; i < C; ++i) {
-          a = lp_merge(a, *cl.map_shared_rank(&s_row, i));
-          c += *cl.map_shared_rank(&s_row_cnt, i);
-        }
-        s_row = a;
-        s_row_cnt = c;
-      }
-      if (p.k > 0) {
-        for (int i = tid; i < C * p.k; i += kLpThreads)
-          s_cand[i] = cl.map_shared_rank(s_top, i / p.k)[i % p.k];
-        __syncthreads();
-        const int n = C * p.k;
-        for (int i = tid; i < n; i += kLpThreads) {
-          const unsigned long long kk = s_cand[i];
-          int r = 0;
-          for (int j = 0; j < n; ++j) r += s_cand[j] > kk ? 1 : 0;
-          if (kk != 0ull && r < p.k) s_top[r] = kk;  // k <= N keys are not zero
-        }
-      }
-      __syncthreads();
-    }
-    const LpStats a = s_row;
-    const bool empty = a.S == 0.0f;  // every logit is -inf
-    const float logS = empty ? __int_as_float(0xFF800000) : logf(a.S);
-    auto logp = [&](float x) { return empty ? logS : __fmaf_rn(x, p.s, -a.m) - logS; };
-    if (tid == 0) {
-      p.logprob[m_row] = has ? logp(x_tok) : 0.0f;
-      p.entropy[m_row] = empty ? 0.0f : logS - a.T / a.S;
-      p.lse[m_row] = empty ? logS : a.m + logS;
-      p.rank[m_row] = has ? (int64_t)s_row_cnt + 1 : 0;
-    }
-    for (int j = tid; j < p.k; j += kLpThreads) {
-      const unsigned long long kk = keys[j];
-      p.top_ids[m_row * p.k + j] = (int64_t)(uint32_t)~(uint32_t)kk;
-      p.top_lp[m_row * p.k + j] = logp(key_value((uint32_t)(kk >> 32)));
+  // ---- over the cluster, in its first CTA
+  if (C > 1) cluster_wait();
+  if (warp == 0) {
+    const float S = warp_sum(lane < kW ? s_S[lane] : 0.0f);
+    const float t = warp_sum(lane < kW ? s_T[lane] : 0.0f);
+    const uint32_t c = __reduce_add_sync(0xFFFFFFFFu, lane < kW ? s_cnt[lane] : 0u);
+    if (lane == 0) {
+      const uint32_t to = first_cta_addr(&s_part[rank]);
+      st_cluster(to, __float_as_uint(m_blk));
+      st_cluster(to + 4, __float_as_uint(S));
+      st_cluster(to + 8, __float_as_uint(t));
+      st_cluster(to + 12, c);
     }
   }
-  if (C > 1) cl.sync();  // no CTA leaves while the first one reads its shared memory
+  if (C > 1) {
+    for (int i = tid; i < p.k; i += kT)
+      st_cluster(first_cta_addr(&s_merge[rank * p.k + i]), s_top[i]);
+    cluster_arrive();
+    if (rank != 0) return;
+    cluster_wait();
+    // k <= N keys of the row are not zero, so every place gets one
+    for (int i = tid; i < C * p.k; i += kT) {
+      const unsigned long long kk = s_merge[i];
+      if (kk == 0ull) continue;
+      int r = i % p.k;  // its place in its own list, and the larger keys of the others
+      for (int c = 0; c < C; ++c) {
+        if (c == i / p.k) continue;
+        int a = 0, b = p.k;
+        while (a < b) {
+          const int mid = (a + b) >> 1;
+          if (s_merge[c * p.k + mid] > kk) a = mid + 1;
+          else b = mid;
+        }
+        r += a;
+      }
+      if (r < p.k) s_top[r] = kk;
+    }
+  }
+  __syncthreads();
+  float4 part = lane < C ? s_part[lane] : make_float4(kLowest, 0.0f, 0.0f, 0.0f);
+  float m = part.x;
+#pragma unroll
+  for (int o = kLpMaxCluster / 2; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  m = __shfl_sync(0xFFFFFFFFu, m, 0);
+  const LpStats a = lp_shift({part.x, part.y, part.z}, m);
+  const float S = warp_sum(a.S), t = warp_sum(a.T);
+  const bool empty = S == 0.0f;  // every logit is -inf
+  const float logS = empty ? __int_as_float(0xFF800000) : logf(S);
+  auto logp = [&](float x) { return empty ? logS : __fmaf_rn(x, p.s, -m) - logS; };
+  if (warp == 0) {
+    const uint32_t c = __reduce_add_sync(0xFFFFFFFFu, lane < C ? __float_as_uint(part.w) : 0u);
+    if (lane == 0) {
+      p.logprob[m_row] = has ? logp(x_tok) : 0.0f;
+      p.entropy[m_row] = empty ? 0.0f : logS - t / S;
+      p.lse[m_row] = empty ? logS : m + logS;
+      p.rank[m_row] = has ? (int64_t)c + 1 : 0;
+    }
+  }
+  for (int j = tid; j < p.k; j += kT) {
+    const unsigned long long kk = s_top[j];
+    p.top_ids[m_row * p.k + j] = (int64_t)(uint32_t)~(uint32_t)kk;
+    p.top_lp[m_row * p.k + j] = logp(key_value((uint32_t)(kk >> 32)));
+  }
 }
 
 // dl_n = s (a (1[n = t] - p_n) - b p_n (log p_n + H)): one read and one write
@@ -480,15 +660,21 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const LpGra
 }
 
 // ------------------------------------------------------------ host side
-// CTAs per row: enough that few rows still fill the GPU, while a CTA keeps
-// at least 4096 logits.
+// CTAs per row: as many as keep the grid within one and a half CTAs per SM
+// and a share at 8192 logits.  Measured (k = 0 / 5): 1 row of 128256 fp32
+// 9.5 / 11.4 us with one CTA, 4.3 / 8.0 with eight; 64 rows of 151936 fp32
+// 11.1 / 13.4, 8.0 / 10.6, 8.4 / 12.0 and 11.9 / 20.0 with 1, 2, 4 and 8.
 static int lp_cluster(int64_t M, int64_t N, int sms) {
   int c = 1;
-  while (c < kLpMaxCluster && M * c < 2 * sms && N / (2 * c) >= 4096) c *= 2;
+  while (c < kLpMaxCluster && M * 2 * c <= sms + sms / 2 && N / (2 * c) >= 8192) c *= 2;
   return c;
 }
 
-template <typename T>
+// Shares above this take 512 threads, others 256: 256 rows of 128256 fp32
+// 23.5 against 29.1 us, 512 rows of 32000 bf16 11.2 against 9.2 us.
+constexpr int64_t kLpWideShare = 32768;
+
+template <typename T, int kT>
 static cudaError_t lp_launch(const LpArgs& a, int64_t M, int c, cudaStream_t stream) {
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -499,11 +685,11 @@ static cudaError_t lp_launch(const LpArgs& a, int64_t M, int c, cudaStream_t str
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(M * c));
-  cfg.blockDim = dim3(kLpThreads);
+  cfg.blockDim = dim3(kT);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T>, a);
+  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, kT>, a);
 }
 
 nvfp4_status logprobs_launch(const void* logits, int dtype, int64_t M, int64_t N, int64_t ld,
@@ -514,8 +700,11 @@ nvfp4_status logprobs_launch(const void* logits, int dtype, int64_t M, int64_t N
   if (sms <= 0) return NVFP4_ERR_CUDA;
   const LpArgs a{logits, N, ld, tokens, s, k, logprob, entropy, lse, top_lp, rank, top_ids};
   const int c = lp_cluster(M, N, sms);
-  const cudaError_t err = dtype == NVFP4_OUT_BF16 ? lp_launch<uint16_t>(a, M, c, stream)
-                                                  : lp_launch<float>(a, M, c, stream);
+  const bool wide = N / c > kLpWideShare;
+  const cudaError_t err =
+      dtype == NVFP4_OUT_BF16
+          ? (wide ? lp_launch<uint16_t, 512>(a, M, c, stream) : lp_launch<uint16_t, 256>(a, M, c, stream))
+          : (wide ? lp_launch<float, 512>(a, M, c, stream) : lp_launch<float, 256>(a, M, c, stream));
   return err == cudaSuccess && cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 
