@@ -126,8 +126,9 @@ __device__ __forceinline__ uint64_t policy_evict_last() {
 
 // ------------------------------------------------------------ NVFP4 codes
 // 8 fp32 values -> 8 E2M1 codes in one word (byte j: value 2j low nibble,
-// value 2j+1 high nibble), round to nearest even, saturating at +-6.
-__device__ __forceinline__ uint32_t cvt_e2m1x8(const float (&q)[8]) {
+// value 2j+1 high nibble), round to nearest even, saturating at +-6; a zero
+// keeps its sign.
+__device__ __forceinline__ uint32_t cvt_e2m1x8_signed(const float (&q)[8]) {
   uint32_t w;
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
@@ -137,34 +138,44 @@ __device__ __forceinline__ uint32_t cvt_e2m1x8(const float (&q)[8]) {
       "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
       : "=r"(w)
       : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
-  // a code whose magnitude is zero carries no sign: 0x8 -> 0x0 per nibble
+  return w;
+}
+
+// The same without the sign of a zero: 0x8 -> 0x0 per nibble.
+__device__ __forceinline__ uint32_t cvt_e2m1x8(const float (&q)[8]) {
+  const uint32_t w = cvt_e2m1x8_signed(q);
   const uint32_t mag = w & 0x77777777u;
   const uint32_t nonzero = (mag + 0x77777777u) & 0x88888888u;
   return mag | (w & nonzero);
 }
 
 // 8 e2m1 codes (one word; byte j = codes 2j | 2j+1 << 4) -> 4 fp16 pairs,
-// element 2j in the low half, each multiplied by the block scale pair sf2.
-__device__ __forceinline__ void dequant8(uint32_t w, uint32_t sf2, uint32_t* out) {
-  uint32_t h0, h1, h2, h3;
+// element 2j in the low half.
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
       "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
       "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
       "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
       "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
       "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-      : "=r"(h0), "=r"(h1), "=r"(h2), "=r"(h3)
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
       : "r"(w));
+}
+
+// The same, each multiplied by the block scale pair sf2.
+__device__ __forceinline__ void dequant8(uint32_t w, uint32_t sf2, uint32_t* out) {
+  uint32_t h[4];
+  e2m1x8_to_f16(w, h);
   asm("mul.rn.f16x2 %0, %0, %4;\n\t"
       "mul.rn.f16x2 %1, %1, %4;\n\t"
       "mul.rn.f16x2 %2, %2, %4;\n\t"
       "mul.rn.f16x2 %3, %3, %4;"
-      : "+r"(h0), "+r"(h1), "+r"(h2), "+r"(h3)
+      : "+r"(h[0]), "+r"(h[1]), "+r"(h[2]), "+r"(h[3])
       : "r"(sf2));
-  out[0] = h0;
-  out[1] = h1;
-  out[2] = h2;
-  out[3] = h3;
+  out[0] = h[0];
+  out[1] = h[1];
+  out[2] = h[2];
+  out[3] = h[3];
 }
 
 // 4 E4M3 scale bytes -> two fp16 pairs (s0, s1) and (s2, s3)

@@ -1,0 +1,1041 @@
+// moe_tc.cu -- the expert layer of w4a16_moe on the FP4 tensor cores, with no
+// dequantization: the block-scaled MMA (kind::mxf4nvf4) reads the NVFP4
+// weights as they are stored, and the 16-bit activations are given to it as
+// sums of NVFP4 values.
+//
+// A row v (a token's x, a pair's h) times a power of two that takes its
+// largest magnitude to 2^10 .. 2^11 is split per 16 values into NVFP4 blocks,
+// r_0 = v: s_i = e4m3(max|r_i| / 6), q_i = e2m1(r_i / s_i), r_{i+1} = r_i - s_i q_i.
+// The largest error of a code is its scale, so a piece leaves at most 0.177
+// of the block's maximum: six of them 3e-5 (for a bf16 result, whose own
+// rounding is 2e-3), eight 1e-6 (for an fp32 result), or 2e-6 of the row's
+// maximum where the scales reach the E4M3 subnormals.  The pieces of a pair
+// are columns of the MMA's N side; their products, each exact, sum in fp32.
+//
+// The layer is bound by HBM (9/16 byte a weight), and this way the SMs only
+// move bytes: a 256-k stage of 128 weight rows is 18 KB, 800 cycles at the
+// copy rate, and 4 MMAs of 16 to 64 cycles.
+//
+//   moe_prep_kernel     one CTA a token: pairs sorted by expert, tiles of up
+//                       to `cap` pairs, pieces of x
+//   moe_tc_kernel       gu = W13 x: persistent, the (tile, 128-row, stage)
+//                       steps cut evenly over the SMs; a unit cut between
+//                       CTAs leaves fp32 parts that its reader adds in order
+//   moe_act_kernel      one CTA a pair: h and its pieces
+//   moe_tc_kernel       y = W2 h
+//   moe_tc_combine      out = sum over a token's slots, in slot order
+// The products derive the tiles from the expert ids themselves, so that
+// their weight loads start while the kernel before them still runs.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "gemm_common.cuh"
+
+namespace nvfp4 {
+
+constexpr int kPieces = 8;                  // columns of a pair
+constexpr int kPiecesBf16 = 6;              // of them used for a bf16 result
+constexpr int kTcMaxExperts = NVFP4_MOE_MAX_EXPERTS;
+constexpr int kTcMaxK = 64;                 // slots of a token
+constexpr uint32_t kTcAStage = 128 * 128;   // 128 rows x 256 codes
+constexpr uint32_t kTcSfStage = 4 * 512;    // 4 atoms of 128 rows x 4 blocks
+constexpr uint32_t kTcPairStage = kPieces * 128;
+constexpr int kTcMaxRing = 8;
+constexpr size_t kTcSmem = 220 << 10;       // dynamic shared memory of a product's CTA
+constexpr int64_t kTcMaxUnitK = 4096;       // largest K whose 128 rows of scales are loaded at once
+constexpr int kTcSfCols = 32;               // TMEM columns of a stage's scales: A 16 + B 16
+
+// What the kernels between the products know of a pair: where it lies.
+struct __align__(16) TcPlace {
+  int expert, tile, col, place;  // place in the order sorted by expert; -1: absent
+};
+
+// The routing as every CTA of a product derives it: pairs and tiles before
+// each expert.
+struct TcTables {
+  int cnt[kTcMaxExperts], off[kTcMaxExperts], tile[kTcMaxExperts + 1];
+};
+
+struct TcTile {
+  int expert, first, n;  // pairs first .. first + n - 1 in sorted order
+};
+
+__device__ __forceinline__ void tc_tables(const int32_t* ids, int P, int E, int cap, TcTables& s) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int mine = tid < P ? __ldg(ids + tid) : -1;  // under way while the counts are cleared
+  for (int e = tid; e < E; e += blockDim.x) s.cnt[e] = 0;
+  __syncthreads();
+  if (mine >= 0 && mine < E) atomicAdd(&s.cnt[mine], 1);
+  for (int i = tid + blockDim.x; i < P; i += blockDim.x) {
+    const int e = __ldg(ids + i);
+    if (e >= 0 && e < E) atomicAdd(&s.cnt[e], 1);
+  }
+  __syncthreads();
+  if (tid < 32) {
+    // lane l takes `per` consecutive experts
+    const int per = (E + 31) / 32, e0 = min(lane * per, E), e1 = min(e0 + per, E);
+    int both = 0;  // pairs | tiles << 16: at most 4096 of either
+    for (int e = e0; e < e1; ++e) {
+      const int n = s.cnt[e];
+      both += n | ((n + cap - 1) / cap) << 16;
+    }
+    int incl = both;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    int off = (incl - both) & 0xFFFF, tiles = (incl - both) >> 16;
+    for (int e = e0; e < e1; ++e) {
+      const int n = s.cnt[e];
+      s.off[e] = off;
+      s.tile[e] = tiles;
+      off += n;
+      tiles += (n + cap - 1) / cap;
+    }
+    if (lane == 31) s.tile[E] = tiles;
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ TcTile tc_tile(const TcTables& s, int E, int cap, int t) {
+  int lo = 0, hi = E - 1;  // the last expert whose tiles begin at or before t
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (s.tile[mid] <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  const int skip = (t - s.tile[lo]) * cap;
+  return {lo, s.off[lo] + skip, min(cap, s.cnt[lo] - skip)};
+}
+
+struct TcArgs {
+  const uint16_t* x;
+  const int32_t* ids;
+  const float* weights;
+  const float *g13, *g2;
+  void* out;
+  int M, k, H, I, E, P, cap, tiles_max, grid, pieces;
+  int2* counts;                  // pairs, tiles
+  TcPlace *by_pair, *by_place;
+  uint8_t *act1, *sf1, *act2, *sf2;
+  float *mul1, *mul2, *gu, *y, *part1, *part2;
+  int32_t* status;
+};
+
+// ------------------------------------------------------------ the schedule
+// S = units x stages steps over the first G = min(S, grid) CTAs (each has at
+// least one), step x to the CTA b with S b / G <= x < S (b + 1) / G; unit u =
+// tile x row tiles + row tile.
+__host__ __device__ __forceinline__ int64_t tc_ctas(int64_t S, int64_t grid) {
+  return S < grid ? S : grid;
+}
+__host__ __device__ __forceinline__ int64_t tc_bound(int64_t S, int64_t b, int64_t G) {
+  return S * b / G;
+}
+__host__ __device__ __forceinline__ int tc_owner(int64_t S, int64_t x, int64_t G) {
+  const int64_t a = (x + 1) * G - 1;  // at most S G
+  if (S * G < (int64_t)1 << 32) return (int)((uint32_t)a / (uint32_t)S);
+  return (int)(a / S);
+}
+
+// The part slot of CTA b for a unit it did not do alone: 1 if it began it.
+__device__ __forceinline__ int tc_slot(int b, bool opened) { return 2 * b + (opened ? 1 : 0); }
+
+// ------------------------------------------------------------ pieces
+// One warp: the pieces of 8 x 32 consecutive values v (this lane: 8 lane ..,
+// already times the row's power of two) of one stage, to the pairs dst[0, n).
+// They are gathered in the warp's kSplitBytes of shared memory and written
+// from there in 16-byte pieces; the loop is kept rolled, because this runs
+// once and cold (unrolled, instruction fetch took longer than the work).
+constexpr int kSplitBytes = kTcPairStage + kPieces * 16;
+
+__device__ __forceinline__ void tc_split(float (&v)[8], int stage, const TcPlace* dst, int n,
+                                         int pieces, int P, int tiles_max, uint8_t* act,
+                                         uint8_t* sf, uint8_t* buf) {
+  const int lane = threadIdx.x & 31;
+  uint8_t* scales = buf + kTcPairStage;  // [piece][16 blocks]
+  __syncwarp();
+#pragma unroll 1
+  for (int p = 0; p < kPieces; ++p) {
+    uint32_t w = 0u, s8 = 0u;
+    if (p < pieces) {
+      float a = fmaxf(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))),
+                      fmaxf(fmaxf(fabsf(v[4]), fabsf(v[5])), fmaxf(fabsf(v[6]), fabsf(v[7]))));
+      a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1));  // the block's other half
+      s8 = __nv_cvt_float_to_fp8(a * (1.0f / 6.0f), __NV_SATFINITE, __NV_E4M3);
+      const float s =
+          __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)s8, __NV_E4M3)));
+      // a quotient one ulp off may take the neighbouring code: its error is
+      // in the residual like any other
+      const float inv = s == 0.0f ? 0.0f : __fdividef(1.0f, s);
+      float q[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[i] = v[i] * inv;
+      w = cvt_e2m1x8_signed(q);
+      uint32_t h[4];
+      e2m1x8_to_f16(w, h);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+        v[2 * i] = __fmaf_rn(-f.x, s, v[2 * i]);
+        v[2 * i + 1] = __fmaf_rn(-f.y, s, v[2 * i + 1]);
+      }
+    }
+    // rows of 128 bytes, 16-byte pieces swizzled by the row
+    *reinterpret_cast<uint32_t*>(buf + p * 128 + (((lane >> 2) ^ p) << 4) + ((lane & 3) << 2)) = w;
+    if ((lane & 1) == 0) scales[p * 16 + (lane >> 1)] = (uint8_t)s8;
+  }
+  __syncwarp();
+  const uint4 lo = reinterpret_cast<const uint4*>(buf)[lane];
+  const uint4 hi = reinterpret_cast<const uint4*>(buf)[lane + 32];
+  const uint32_t sw = reinterpret_cast<const uint32_t*>(scales)[(lane & 7) * 4 + (lane >> 3)];
+  for (int j = 0; j < n; ++j) {
+    const TcPlace d = dst[j];
+    uint4* to = reinterpret_cast<uint4*>(act + ((int64_t)stage * P + d.place) * kTcPairStage) + lane;
+    to[0] = lo;
+    to[32] = hi;
+    // atom lane / 8, the tile's rows 8 d.col ..: row 32 a + b at b 16 + a 4
+    *reinterpret_cast<uint32_t*>(sf + ((int64_t)stage * tiles_max + d.tile) * kTcSfStage +
+                                 (lane >> 3) * 512 + ((d.col & 3) * 8 + (lane & 7)) * 16 +
+                                 (d.col >> 2) * 4) = sw;
+  }
+}
+
+// The power of two that takes a row's largest magnitude (bits mx) to 2^10 ..,
+// and the multiplier that undoes it (NaN where the row is not finite).
+__device__ __forceinline__ float tc_scale(uint32_t mx, float& undo) {
+  const int e = max((int)(mx >> 23), 12);
+  undo = e == 255 ? __int_as_float(0x7FFFFFFF) : __uint_as_float((uint32_t)(e - 10) << 23);
+  return __uint_as_float((uint32_t)(264 - e) << 23);
+}
+
+// ------------------------------------------------------------ prep
+constexpr int kPrepThreads = 256;
+
+__global__ void __launch_bounds__(kPrepThreads) moe_prep_kernel(const TcArgs p) {
+  __shared__ TcTables s_tab;
+  __shared__ TcPlace s_dst[kTcMaxK];
+  __shared__ __align__(16) uint8_t s_buf[kPrepThreads / 32][kSplitBytes];
+  __shared__ int s_n;
+  __shared__ uint32_t s_max;
+  grid_dependency_wait();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int m = blockIdx.x, n_stages = (p.H + 255) / 256;
+  if (tid == 0) {
+    s_n = 0;
+    s_max = 0u;
+  }
+  // the row's largest magnitude: this warp's stages warp, warp + 8, ..
+  constexpr int kWarps = kPrepThreads / 32;
+  const uint4* row = reinterpret_cast<const uint4*>(p.x + (int64_t)m * p.H);
+  auto load = [&](int s) {
+    const int i = 32 * s + lane;
+    return i < p.H / 8 ? __ldg(row + i) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  uint32_t mx = 0;
+  for (int s = warp; s < n_stages; s += kWarps) {
+    const uint4 r = load(s);
+    const uint32_t c = __vmaxu2(__vmaxu2(r.x & 0x7FFF7FFFu, r.y & 0x7FFF7FFFu),
+                                __vmaxu2(r.z & 0x7FFF7FFFu, r.w & 0x7FFF7FFFu));
+    mx = max(mx, max(c & 0xFFFFu, c >> 16));
+  }
+  // the place of pair i is its rank among its expert's; this warp's slots are
+  // j = warp, warp + 8, .., lane j / 8 keeping slot j's
+  int my_e = -1, my_rank = 0;
+  for (int j = warp; j < p.k; j += kWarps) {
+    const int i = m * p.k + j, e = __ldg(p.ids + i);
+    int rank = 0;
+    for (int b = lane; b < i; b += 32) rank += __ldg(p.ids + b) == e ? 1 : 0;
+    rank = __reduce_add_sync(0xFFFFFFFFu, rank);
+    if (lane == j / kWarps) {
+      my_e = e;
+      my_rank = rank;
+    }
+  }
+  tc_tables(p.ids, p.P, p.E, p.cap, s_tab);
+  mx = __reduce_max_sync(0xFFFFFFFFu, mx);
+  if (lane == 0) atomicMax(&s_max, mx << 16);
+  if (m == 0 && tid == 0) {
+    *p.status = NVFP4_OK;
+    *p.counts = make_int2(s_tab.off[p.E - 1] + s_tab.cnt[p.E - 1], s_tab.tile[p.E]);
+  }
+  if (warp + kWarps * lane < p.k) {
+    TcPlace d{0, 0, 0, -1};
+    if (my_e >= 0 && my_e < p.E) {
+      d = {my_e, s_tab.tile[my_e] + my_rank / p.cap, my_rank % p.cap, s_tab.off[my_e] + my_rank};
+      p.by_place[d.place] = d;
+      s_dst[atomicAdd(&s_n, 1)] = d;
+    }
+    p.by_pair[m * p.k + warp + kWarps * lane] = d;
+  }
+  __syncthreads();
+  float undo;
+  const float up = tc_scale(s_max, undo);
+  if (tid < s_n) p.mul1[s_dst[tid].place] = undo;
+  for (int s = warp; s < n_stages; s += kWarps) {
+    const uint4 r = load(s);
+    const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+    float v[8];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      v[2 * q] = __uint_as_float(u[q] << 16) * up;
+      v[2 * q + 1] = __uint_as_float(u[q] & 0xFFFF0000u) * up;
+    }
+    tc_split(v, s, s_dst, s_n, p.pieces, p.P, p.tiles_max, p.act1, p.sf1, s_buf[warp]);
+  }
+}
+
+// ------------------------------------------------------------ the product
+struct TcGemm {
+  const int32_t* ids;
+  const uint8_t *codes, *scales;
+  int64_t rows;  // E N: rows of the whole tensor
+  int N, K, E, cap, ring, P, tiles_max;
+  int unit_scales;  // buffers for the scales of a unit's 128 rows; 0: a stage's at a time
+  const uint8_t *act, *sf;
+  const float* mul;
+  float *dst, *part;
+  int32_t* status;
+};
+
+// Warps: 0 weight codes (and, per stage, scales), 1 MMA, 2 scales per unit,
+// 3 activations, 4-7 epilogue, 8-11 scale layout, then the code loaders.
+constexpr int kTcScaleWarps = 4;
+constexpr int kTcThreads = 32 * (8 + kTcScaleWarps);
+constexpr int kTcLoaderWarps = 8;     // where TMA cannot read the code rows
+constexpr int kTcLoaderDepth = 3;     // stages a loader keeps in flight (the ring has 4 or more)
+constexpr int kTcMaxUnits = 8;        // unit buffers of scales
+
+struct TcPiece {
+  int tile, rt, kb0, kb1;
+};
+template <typename F>
+__device__ __forceinline__ void tc_pieces(int64_t x0, int64_t x1, int n_st, int RT, F f) {
+  for (int64_t x = x0; x < x1;) {
+    const int64_t u = x / n_st;
+    const int kb0 = (int)(x - u * n_st);
+    const int kb1 = (int)min((int64_t)n_st, kb0 + (x1 - x));
+    const TcPiece pc{(int)(u / RT), (int)(u % RT), kb0, kb1};
+    if (!f(pc)) return;
+    x += kb1 - kb0;
+  }
+}
+
+// 16 bytes of shared memory at any address, those past the first `valid` as
+// zero (whole words around them are read).
+__device__ __forceinline__ uint4 tc_lds16(uint32_t addr, int valid, bool aligned) {
+  uint32_t w[5];
+  if (aligned) {
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(addr));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  const uint32_t base = addr & ~3u, sh = (addr & 3u) * 8;
+#pragma unroll
+  for (int i = 0; i < 5; ++i)
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[i]) : "r"(base + 4 * i));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[i] = __funnelshift_r(w[i], w[i + 1], sh);
+    const int left = valid - 4 * i;
+    if (left < 4) w[i] = left <= 0 ? 0u : w[i] & ((1u << (8 * left)) - 1u);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__host__ __device__ __forceinline__ uint32_t tc_unit_bytes(int K) {
+  return (uint32_t)align_up((size_t)128 * (K / 16) + 16, 128);
+}
+
+template <bool kTma>
+__global__ void __launch_bounds__(kTcThreads + (kTma ? 0 : 32 * kTcLoaderWarps), 1)
+    moe_tc_kernel(const __grid_constant__ CUtensorMap tm_w,
+                  const __grid_constant__ CUtensorMap tm_s, const TcGemm p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const int ring = p.ring;
+  const uint32_t b_stage = (uint32_t)p.cap * kTcPairStage;
+  uint8_t* s_a = smem;
+  uint8_t* s_b = s_a + ring * kTcAStage;
+  uint8_t* s_sfa = s_b + ring * b_stage;
+  uint8_t* s_sfb = s_sfa + ring * kTcSfStage;
+  uint8_t* s_raw = s_sfb + ring * kTcSfStage;  // scales as stored: a slot a stage, or whole units
+  __shared__ TcTables s_tab;
+  __shared__ uint64_t full[kTcMaxRing], empty[kTcMaxRing], raw_full[kTcMaxRing], raw_empty[kTcMaxUnits];
+  __shared__ uint64_t d_full[2], d_empty[2], done_bar;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int32_t s_abort;
+  volatile int32_t* abort_flag = &s_abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ring; ++i) {
+      mbar_init(&full[i], 1 + kTcScaleWarps + (kTma ? 1 : kTcLoaderWarps));
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < kTcMaxUnits; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], kTcScaleWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&d_full[i], 1);
+      mbar_init(&d_empty[i], 4);
+    }
+    mbar_init(&done_bar, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    if (kTma) tma_prefetch_desc(&tm_w);
+    if (!p.unit_scales) tma_prefetch_desc(&tm_s);
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_slot, 512);
+    tc_fence_before();
+  }
+  // The expert ids were complete before the kernel ahead of this one let it
+  // start; its own results are waited for where they are read.
+  tc_tables(p.ids, p.P, p.E, p.cap, s_tab);
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, tmem_slot, 0);
+  const WaitCtl wc{p.status, abort_flag, kWaitLimitNs};
+
+  const int n_st = (p.K + 255) / 256, RT = (p.N + 127) / 128, nb = p.K / 16;
+  const int64_t S = (int64_t)s_tab.tile[p.E] * RT * n_st;
+  const int64_t G = tc_ctas(S, gridDim.x);
+  const bool works = blockIdx.x < G;
+  const int64_t x0 = works ? tc_bound(S, blockIdx.x, G) : 0;
+  const int64_t x1 = works ? tc_bound(S, blockIdx.x + 1, G) : 0;
+  // a tile is looked up once: its units follow one another
+  int known = -1;
+  TcTile tile{};
+  auto tile_at = [&](int t) {
+    if (t != known) {
+      tile = tc_tile(s_tab, p.E, p.cap, t);
+      known = t;
+    }
+    return tile;
+  };
+
+  if (warp == 0) {
+    // ---------------- weight codes, and scales where they come per stage
+    const uint64_t once = policy_evict_first();
+    uint32_t issued = 0;
+    if (kTma || !p.unit_scales)
+      tc_pieces(x0, x1, n_st, RT, [&](const TcPiece& pc) {
+        const int r0 = tile_at(pc.tile).expert * p.N + pc.rt * 128;
+        for (int kb = pc.kb0; kb < pc.kb1; ++kb, ++issued) {
+          const uint32_t st = issued % ring, ph = (issued / ring) & 1;
+          if (!warp_wait(&empty[st], ph ^ 1, wc)) return false;
+          if (elect_one()) {
+            if (!p.unit_scales) {
+              mbar_arrive_expect_tx(&raw_full[st], kTcSfStage);
+              tma_load_2d_hint(s_raw + st * kTcSfStage, &tm_s, kb * 16, r0, &raw_full[st], once);
+            }
+            if (kTma) {
+              mbar_arrive_expect_tx(&full[st], kTcAStage);
+              tma_load_2d_hint(s_a + st * kTcAStage, &tm_w, kb * 128, r0, &full[st], once);
+            }
+          }
+          __syncwarp();
+        }
+        return true;
+      });
+    if (!p.unit_scales) drain_loads(raw_full, ring, issued, 0, p.status);
+    // codes and activations of a stage land on one barrier, which the MMA
+    // warp waits for; what an aborted call left in flight lands here
+    if (*abort_flag && kTma) drain_loads(full, ring, issued, 0, p.status);
+  } else if (warp == 3) {
+    // ---------------- the pairs' pieces and their scales
+    grid_dependency_wait();
+    const uint64_t keep = policy_evict_last();
+    uint32_t issued = 0;
+    tc_pieces(x0, x1, n_st, RT, [&](const TcPiece& pc) {
+      const TcTile t = tile_at(pc.tile);
+      for (int kb = pc.kb0; kb < pc.kb1; ++kb, ++issued) {
+        const uint32_t st = issued % ring, ph = (issued / ring) & 1;
+        if (!warp_wait(&empty[st], ph ^ 1, wc)) return false;
+        if (elect_one()) {
+          const uint32_t bytes = (uint32_t)t.n * kTcPairStage;
+          mbar_arrive_expect_tx(&full[st], bytes + kTcSfStage);
+          bulk_load(s_b + st * b_stage, p.act + ((int64_t)kb * p.P + t.first) * kTcPairStage, bytes,
+                    &full[st], keep);
+          bulk_load(s_sfb + st * kTcSfStage, p.sf + ((int64_t)kb * p.tiles_max + pc.tile) * kTcSfStage,
+                    kTcSfStage, &full[st], keep);
+        }
+        __syncwarp();
+      }
+      return true;
+    });
+    drain_loads(full, ring, issued, 0, p.status);
+  } else if (warp == 2) {
+    // ---------------- the scales of a unit's rows, one contiguous copy
+    if (p.unit_scales) {
+      const uint64_t once = policy_evict_first();
+      uint32_t issued = 0;
+      tc_pieces(x0, x1, n_st, RT, [&](const TcPiece& pc) {
+        const uint32_t buf = issued % p.unit_scales, ph = (issued / p.unit_scales) & 1;
+        if (!warp_wait(&raw_empty[buf], ph ^ 1, wc)) return false;
+        const int64_t r0 = (int64_t)tile_at(pc.tile).expert * p.N + pc.rt * 128;
+        if (elect_one()) {
+          const uint32_t bytes = (uint32_t)min(128, p.N - pc.rt * 128) * nb;
+          mbar_arrive_expect_tx(&raw_full[buf], bytes);
+          bulk_load(s_raw + buf * tc_unit_bytes(p.K), p.scales + r0 * nb, bytes, &raw_full[buf], once);
+        }
+        __syncwarp();
+        ++issued;
+        return true;
+      });
+      drain_loads(raw_full, p.unit_scales, issued, 0, p.status);
+    }
+  } else if (warp == 1) {
+    // ---------------- scales into TMEM, then one MMA per 64 k
+    const uint64_t ad0 = smem_desc_sw128(smem_u32(s_a)), bd0 = smem_desc_sw128(smem_u32(s_b));
+    const uint32_t n_cols = (uint32_t)p.cap * kPieces;
+    const uint32_t sf_base = tmem + 2 * n_cols;
+    uint32_t g = 0;
+    int i = 0;
+    tc_pieces(x0, x1, n_st, RT, [&](const TcPiece& pc) {
+      const TcTile t = tile_at(pc.tile);
+      // 16 columns are the MMA's step: an odd pair count computes 8 that
+      // nobody reads
+      const uint32_t idesc = idesc_e2m1_bs((uint32_t)((t.n * kPieces + 15) / 16 * 16));
+      const uint32_t buf = i & 1, dph = (i >> 1) & 1;
+      ++i;
+      if (!warp_wait(&d_empty[buf], dph ^ 1, wc)) return false;
+      tc_fence_after();
+      const uint32_t d = tmem + buf * n_cols;
+      for (int kb = pc.kb0; kb < pc.kb1; ++kb, ++g) {
+        const uint32_t st = g % ring, ph = (g / ring) & 1;
+        if (!warp_wait(&full[st], ph, wc)) return false;
+        tc_fence_after();
+        const uint64_t ad = ad0 + ((st * kTcAStage) >> 4), bd = bd0 + ((st * b_stage) >> 4);
+        const uint32_t sfa = sf_base + st * kTcSfCols, sfb = sfa + 16;
+        const int n_at = min(4, (p.K - 256 * kb + 63) / 64);
+        if (elect_one()) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (j < n_at) {
+              tc_cp_32x128b_x4(sfa + 4 * j, smem_u32(s_sfa + st * kTcSfStage + 512 * j));
+              tc_cp_32x128b_x4(sfb + 4 * j, smem_u32(s_sfb + st * kTcSfStage + 512 * j));
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (j < n_at)
+              tc_mma_fp4_bs(d, ad + 2 * j, bd + 2 * j, idesc, sfa + 4 * j, sfb + 4 * j,
+                            (kb != pc.kb0) || (j != 0));
+          tc_commit(&empty[st]);
+        }
+        __syncwarp();
+      }
+      if (elect_one()) tc_commit(&d_full[buf]);
+      __syncwarp();
+      return true;
+    });
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (elect_one()) tc_commit(&done_bar);
+    __syncwarp();
+    volatile int32_t zero = 0;
+    WaitCtl drain{p.status, &zero, 100000000ull};
+    mbar_wait(&done_bar, 0, drain);
+  } else if (warp < 8) {
+    // ---------------- epilogue: a row a thread; a pair's pieces are summed
+    grid_dependency_wait();  // the multipliers
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    int i = 0, mul_of = -1;
+    float mul = 0.0f;
+    tc_pieces(x0, x1, n_st, RT, [&](const TcPiece& pc) {
+      const TcTile t = tile_at(pc.tile);
+      const uint32_t buf = i & 1, dph = (i >> 1) & 1;
+      ++i;
+      if (pc.tile != mul_of) {
+        mul = lane < t.n ? __ldcg(p.mul + t.first + lane) : 0.0f;
+        mul_of = pc.tile;
+      }
+      if (!warp_wait(&d_full[buf], dph, wc)) return false;
+      tc_fence_after();
+      const bool whole = pc.kb0 == 0 && pc.kb1 == n_st;
+      const int n = pc.rt * 128 + row;
+      float* out;
+      int64_t stride;
+      if (whole) {
+        out = p.dst + (int64_t)t.first * p.N + n;
+        stride = p.N;
+      } else {
+        out = p.part + (int64_t)tc_slot(blockIdx.x, pc.kb0 == 0) * p.cap * 128 + row;
+        stride = 128;
+      }
+      const uint32_t d = tmem + buf * (uint32_t)p.cap * kPieces + lane_off;
+      for (int c = 0; c < t.n; c += 4) {
+        uint32_t v[2][16];
+        tmem_ld16(d + c * kPieces, v[0]);
+        if (c + 2 < t.n) tmem_ld16(d + (c + 2) * kPieces, v[1]);
+        tc_wait_ld();
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const float m = __shfl_sync(0xFFFFFFFFu, mul, (c + h) & 31);
+          if (c + h < t.n && n < p.N) {
+            // the pieces from the smallest up
+            float sum = __uint_as_float(v[h >> 1][8 * (h & 1) + 7]);
+#pragma unroll
+            for (int q = 6; q >= 0; --q) sum += __uint_as_float(v[h >> 1][8 * (h & 1) + q]);
+            out[(c + h) * stride] = sum * m;
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&d_empty[buf]);
+      return true;
+    });
+  } else if (warp < 8 + kTcScaleWarps) {
+    // ---------------- weight scales from the order they are stored in to the
+    // one tcgen05.cp reads (atom j, row 32 a + b: byte b 16 + a 4 of atom j);
+    // warp a takes rows 32 a ..: one warp for all four took 1480 cycles a
+    // stage where rows are not 16-byte multiples
+    const int a = warp - 8, r = 32 * a + lane;
+    const bool aligned = !p.unit_scales || nb % 16 == 0;
+    uint32_t nan_bits = 0, it = 0, units = 0;
+    tc_pieces(x0, x1, n_st, RT, [&](const TcPiece& pc) {
+      const bool live = r < p.N - pc.rt * 128;  // a row of the unit
+      const uint32_t buf = p.unit_scales ? units % p.unit_scales : 0;
+      if (p.unit_scales && !warp_wait(&raw_full[buf], (units / p.unit_scales) & 1, wc)) return false;
+      for (int kb = pc.kb0; kb < pc.kb1; ++kb, ++it) {
+        const uint32_t st = it % ring, ph = (it / ring) & 1;
+        if (!p.unit_scales && !warp_wait(&raw_full[st], ph, wc)) return false;
+        const uint32_t from = p.unit_scales
+                                  ? smem_u32(s_raw) + buf * tc_unit_bytes(p.K) + r * nb + 16 * kb
+                                  : smem_u32(s_raw) + st * kTcSfStage + r * 16;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (live) v = tc_lds16(from, nb - 16 * kb, aligned);
+        if (!warp_wait(&empty[st], ph ^ 1, wc)) return false;
+        uint32_t* to = reinterpret_cast<uint32_t*>(s_sfa + st * kTcSfStage) + lane * 4 + a;
+        to[0] = v.x;
+        to[128] = v.y;
+        to[256] = v.z;
+        to[384] = v.w;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[st]);
+        nan_bits |= ((v.x & 0x7F7F7F7Fu) + 0x01010101u) | ((v.y & 0x7F7F7F7Fu) + 0x01010101u) |
+                    ((v.z & 0x7F7F7F7Fu) + 0x01010101u) | ((v.w & 0x7F7F7F7Fu) + 0x01010101u);
+      }
+      ++units;
+      __syncwarp();
+      if (p.unit_scales && lane == 0) mbar_arrive(&raw_empty[buf]);
+      return true;
+    });
+    // a block scale that is NaN (0x7F or 0xFF: never loaded)
+    if (__any_sync(0xFFFFFFFFu, (nan_bits & 0x80808080u) != 0u) && lane == 0)
+      raise_status(p.status, NVFP4_ERR_NONFINITE);
+  } else if constexpr (!kTma) {
+    // ---------------- weight codes in 8-byte pieces (rows that are not a
+    // 16-byte multiple), kTcLoaderDepth stages in flight
+    constexpr int kRowsAt = kTcLoaderWarps * 2;  // rows of one round: 16 lanes a row
+    const int tid = threadIdx.x - kTcThreads;
+    const int64_t rb = p.K / 2;
+    const int r_in = tid >> 4, o = (tid & 15) * 8;
+    const uint32_t to = r_in * 128 + (((o >> 4) ^ (r_in & 7)) << 4) + (o & 8);
+    uint32_t it = 0, landed = 0;
+    bool ok = true;
+    auto land = [&]() {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[landed % ring]);
+      ++landed;
+    };
+    tc_pieces(x0, x1, n_st, RT, [&](const TcPiece& pc) {
+      const int64_t r0 = (int64_t)tile_at(pc.tile).expert * p.N + pc.rt * 128 + r_in;
+      const int rows = (int)min((int64_t)128, p.rows - r0);  // from r0 on
+      const uint8_t* src = p.codes + r0 * rb + o;
+      for (int kb = pc.kb0; kb < pc.kb1; ++kb, ++it) {
+        const uint32_t st = it % ring, ph = (it / ring) & 1;
+        ok = warp_wait(&empty[st], ph ^ 1, wc);
+        if (!ok) return false;
+        const uint32_t dst = smem_u32(s_a + st * kTcAStage) + to;
+        const int64_t c = (int64_t)kb * 128;
+        const bool in_row = c + o < rb;
+#pragma unroll
+        for (int q = 0; q < 128 / kRowsAt; ++q) {
+          const bool in = in_row && q * kRowsAt < rows;
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst + q * kRowsAt * 128),
+                       "l"(in ? src + c + q * kRowsAt * rb : p.codes), "r"(in ? 8 : 0)
+                       : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (it + 1 >= (uint32_t)kTcLoaderDepth) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(kTcLoaderDepth - 1) : "memory");
+          land();
+        }
+      }
+      return true;
+    });
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    while (ok && landed < it) land();
+  }
+
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------ between the products
+// The CTAs that share the unit of (tile, row tile), and where its sum lies.
+struct TcSpan {
+  int b0, b1;
+};
+__device__ __forceinline__ TcSpan tc_span(int64_t S, int grid, int n_st, int RT, int tile, int rt) {
+  const int64_t x = ((int64_t)tile * RT + rt) * n_st;
+  const int64_t G = tc_ctas(S, grid);
+  return {tc_owner(S, x, G), tc_owner(S, x + n_st - 1, G)};
+}
+
+// Threads by the pair's length: a quarter of its values, so that its loads are
+// one round trip.
+constexpr int kActMaxThreads = 768;
+static int act_threads(int64_t I) { return I <= 1024 ? 256 : I <= 2048 ? 512 : kActMaxThreads; }
+
+__global__ void __launch_bounds__(kActMaxThreads) moe_act_kernel(const TcArgs p) {
+  // a split buffer a warp, I values, the spans of the 2I / 128 row tiles
+  extern __shared__ __align__(16) uint8_t s_act_mem[];
+  __shared__ uint32_t s_max;
+  __shared__ TcPlace s_dst;
+  const int n_threads = blockDim.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int N = 2 * p.I, RT = (N + 127) / 128, n_st = (p.H + 255) / 256;
+  float* s_h = reinterpret_cast<float*>(s_act_mem + (n_threads / 32) * kSplitBytes);
+  TcSpan* s_span = reinterpret_cast<TcSpan*>(s_h + p.I);
+  // where the pair and its sums lie: written by the prep kernel, which was
+  // complete before the product this kernel waits for began
+  const int q = blockIdx.x;
+  const int2 counts = __ldcg(p.counts);
+  const int4 at = __ldcg(reinterpret_cast<const int4*>(p.by_place) + q);  // not set past counts.x
+  const bool present = q < counts.x;
+  const int tile = at.y, col = at.z;
+  const int64_t S = (int64_t)counts.y * RT * n_st;
+  if (present)
+    for (int r = tid; r < RT; r += n_threads) s_span[r] = tc_span(S, p.grid, n_st, RT, tile, r);
+  if (tid == 0) {
+    s_max = 0u;
+    s_dst = {at.x, tile, col, q};
+  }
+  __syncthreads();
+  grid_dependency_wait();
+  if (!present) return;
+  const float g13 = __ldg(p.g13 + at.x);
+  // four values in flight per thread; a unit that was cut has its other parts
+  // added in order
+  const int64_t slot = (int64_t)p.cap * 128;
+  auto first = [&](int n) {
+    const TcSpan sp = s_span[n >> 7];
+    return __ldcg(sp.b0 == sp.b1 ? p.gu + (int64_t)q * N + n
+                                 : p.part1 + tc_slot(sp.b0, true) * slot + (int64_t)col * 128 + (n & 127));
+  };
+  auto rest = [&](int n, float sum) {
+    const TcSpan sp = s_span[n >> 7];
+    for (int b = sp.b0 + 1; b <= sp.b1; ++b)
+      sum += __ldcg(p.part1 + tc_slot(b, false) * slot + (int64_t)col * 128 + (n & 127));
+    return sum;
+  };
+  constexpr int kAhead = 4;
+  uint32_t mx = 0;
+  for (int i0 = tid; i0 < p.I; i0 += kAhead * n_threads) {
+    float g[kAhead], u[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      const int i = i0 + a * n_threads;
+      g[a] = i < p.I ? first(i) : 0.0f;
+      u[a] = i < p.I ? first(p.I + i) : 0.0f;
+    }
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      const int i = i0 + a * n_threads;
+      if (i >= p.I) break;
+      const float gv = rest(i, g[a]) * g13, uv = rest(p.I + i, u[a]) * g13;
+      const float h = gv / (1.0f + __expf(-gv)) * uv;
+      s_h[i] = h;
+      mx = max(mx, __float_as_uint(h) & 0x7FFFFFFFu);
+    }
+  }
+  mx = __reduce_max_sync(0xFFFFFFFFu, mx);
+  if (lane == 0) atomicMax(&s_max, mx);
+  __syncthreads();
+  // the next product's CTAs take a whole SM each: not before the loads
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  float undo;
+  const float up = tc_scale(s_max, undo);
+  if (tid == 0) p.mul2[q] = undo;
+  const int stages = (p.I + 255) / 256;
+  for (int s = warp; s < stages; s += n_threads / 32) {
+    const int k0 = 256 * s + 8 * lane;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = k0 < p.I ? s_h[k0 + i] * up : 0.0f;
+    tc_split(v, s, &s_dst, 1, p.pieces, p.P, p.tiles_max, p.act2, p.sf2,
+             s_act_mem + warp * kSplitBytes);
+  }
+}
+
+// out[m, :] = sum over the slots j of w[m, j] G2[e] y[pair], a 128-row tile of
+// y a warp, four rows a lane.
+template <bool kBf16>
+__global__ void __launch_bounds__(256) moe_tc_combine_kernel(const TcArgs p) {
+  const int lane = threadIdx.x & 31;
+  const int RT = (p.H + 127) / 128, n_st = (p.I + 255) / 256;
+  const int rt = blockIdx.x * 8 + (threadIdx.x >> 5), m = blockIdx.y;
+  const int64_t S = (int64_t)__ldcg(p.counts).y * RT * n_st;
+  const int n = rt * 128 + 4 * lane;
+  const bool live = n < p.H;
+  const int64_t slot = (int64_t)p.cap * 128;
+  constexpr int kAt = 8;  // slots whose loads are in flight together
+  float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int j0 = 0; j0 < p.k; j0 += kAt) {
+    // lane j looks up slot j0 + j (what the prep kernel wrote: the first
+    // round's ahead of the wait for the product)
+    int4 at = make_int4(0, 0, 0, -1);
+    TcSpan sp{0, 0};
+    float w = 0.0f;
+    if (lane < kAt && j0 + lane < p.k) {
+      const int64_t i = (int64_t)m * p.k + j0 + lane;
+      w = __ldg(p.weights + i);
+      at = __ldcg(reinterpret_cast<const int4*>(p.by_pair) + i);
+      if (at.w >= 0) {
+        sp = tc_span(S, p.grid, n_st, RT, at.y, rt < RT ? rt : 0);
+        w *= __ldg(p.g2 + at.x);
+      }
+    }
+    if (j0 == 0) {
+      grid_dependency_wait();
+      asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    }
+    float4 v[kAt];
+#pragma unroll
+    for (int j = 0; j < kAt; ++j) {
+      const int place = __shfl_sync(0xFFFFFFFFu, at.w, j), col = __shfl_sync(0xFFFFFFFFu, at.z, j);
+      const int b0 = __shfl_sync(0xFFFFFFFFu, sp.b0, j), b1 = __shfl_sync(0xFFFFFFFFu, sp.b1, j);
+      v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (place >= 0 && live)
+        v[j] = __ldcg(reinterpret_cast<const float4*>(
+            b0 == b1 ? p.y + (int64_t)place * p.H + n
+                     : p.part2 + tc_slot(b0, true) * slot + (int64_t)col * 128 + 4 * lane));
+    }
+#pragma unroll
+    for (int j = 0; j < kAt; ++j) {
+      const int place = __shfl_sync(0xFFFFFFFFu, at.w, j), col = __shfl_sync(0xFFFFFFFFu, at.z, j);
+      const int b0 = __shfl_sync(0xFFFFFFFFu, sp.b0, j), b1 = __shfl_sync(0xFFFFFFFFu, sp.b1, j);
+      const float wj = __shfl_sync(0xFFFFFFFFu, w, j);
+      if (place < 0 || !live) continue;
+      for (int b = b0 + 1; b <= b1; ++b) {
+        const float4 o = __ldcg(reinterpret_cast<const float4*>(
+            p.part2 + tc_slot(b, false) * slot + (int64_t)col * 128 + 4 * lane));
+        v[j].x += o.x;
+        v[j].y += o.y;
+        v[j].z += o.z;
+        v[j].w += o.w;
+      }
+      sum.x = __fmaf_rn(wj, v[j].x, sum.x);
+      sum.y = __fmaf_rn(wj, v[j].y, sum.y);
+      sum.z = __fmaf_rn(wj, v[j].z, sum.z);
+      sum.w = __fmaf_rn(wj, v[j].w, sum.w);
+    }
+  }
+  if (!live) return;
+  const int64_t at = ((int64_t)m * p.H + n) >> 2;
+  if constexpr (kBf16) {
+    uint2 o;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o.x) : "f"(sum.y), "f"(sum.x));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o.y) : "f"(sum.w), "f"(sum.z));
+    reinterpret_cast<uint2*>(p.out)[at] = o;
+  } else {
+    reinterpret_cast<float4*>(p.out)[at] = sum;
+  }
+}
+
+// ------------------------------------------------------------ host side
+struct TcLayout {
+  size_t counts, by_pair, by_place, mul1, mul2, sf1, sf2, act1, act2, gu, y, part1, part2, total;
+  int tiles_max;
+};
+
+// Pairs of a tile: 8 (the MMA's columns: 64) where no expert can have more
+// without repeating a token, else 16.
+static int tc_cap(int64_t M) { return M <= 8 ? 8 : 16; }
+
+static TcLayout tc_layout(int64_t M, int64_t k, int64_t H, int64_t I, int sms) {
+  const int64_t P = M * k, cap = tc_cap(M);
+  const int64_t st1 = (H + 255) / 256, st2 = (I + 255) / 256;
+  TcLayout L;
+  // every tile but one per expert is full
+  L.tiles_max = (int)(std::min<int64_t>(P, kTcMaxExperts) + P / cap);
+  size_t at = kWsHeader;
+  auto put = [&](size_t bytes) {
+    const size_t here = at;
+    at = align_up(at + bytes, 256);
+    return here;
+  };
+  L.counts = put(sizeof(int2));
+  L.by_pair = put((size_t)P * sizeof(TcPlace));
+  L.by_place = put((size_t)P * sizeof(TcPlace));
+  L.mul1 = put((size_t)P * 4);
+  L.mul2 = put((size_t)P * 4);
+  L.sf1 = put((size_t)st1 * L.tiles_max * kTcSfStage);
+  L.sf2 = put((size_t)st2 * L.tiles_max * kTcSfStage);
+  L.act1 = put((size_t)st1 * P * kTcPairStage);
+  L.act2 = put((size_t)st2 * P * kTcPairStage);
+  L.gu = put((size_t)P * 2 * I * 4);
+  L.y = put((size_t)P * H * 4);
+  L.part1 = put((size_t)2 * sms * cap * 128 * 4);
+  L.part2 = put((size_t)2 * sms * cap * 128 * 4);
+  L.total = at;
+  return L;
+}
+
+size_t moe_tc_workspace_bytes(int64_t M, int64_t k, int64_t H, int64_t I) {
+  return tc_layout(M, k, H, I, std::max(sm_count(), 1)).total;
+}
+
+// Scales of a unit's rows are loaded at once, or per stage by TMA, whose row
+// stride is a 16-byte multiple.
+static bool tc_k_ok(int64_t K) { return K <= kTcMaxUnitK || K % 256 == 0; }
+bool moe_tc_takes(int64_t k, int64_t H, int64_t I) {
+  return k <= kTcMaxK && tc_k_ok(H) && tc_k_ok(I);
+}
+
+static cudaError_t tc_gemm_launch(TcGemm g, int grid, cudaStream_t stream) {
+  CUtensorMap tm = {}, tm_s = {};
+  const bool tma = g.K % 32 == 0;  // the code rows' stride for TMA
+  // two units' scales, or as many as 32 KB hold: the next unit's are asked for
+  // one buffer round ahead (K = 768, 64 tokens: 23 us with two)
+  g.unit_scales = g.K > kTcMaxUnitK
+                      ? 0
+                      : std::max(2, std::min(kTcMaxUnits, (int)((32 << 10) / tc_unit_bytes(g.K))));
+  if (tma && !encode_2d(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.codes, (uint64_t)g.K / 2,
+                        (uint64_t)g.rows, (uint64_t)g.K / 2, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorUnknown;
+  if (!g.unit_scales &&
+      !encode_2d(&tm_s, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.scales, (uint64_t)g.K / 16,
+                 (uint64_t)g.rows, (uint64_t)g.K / 16, 16, 128, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return cudaErrorUnknown;
+  // 28 to 38 KB a stage beside two units' scales: 4 to 7 stages
+  const size_t stage = kTcAStage + (size_t)g.cap * kTcPairStage +
+                       (g.unit_scales ? 2 : 3) * (size_t)kTcSfStage;
+  const size_t units = g.unit_scales * (size_t)tc_unit_bytes(g.K);
+  g.ring = (int)std::min<size_t>((kTcSmem - 1024 - units) / stage, kTcMaxRing);
+  const size_t smem = 1024 + units + (size_t)g.ring * stage;
+  static std::atomic<uint64_t> limit_set[2];
+  auto kern = tma ? moe_tc_kernel<true> : moe_tc_kernel<false>;
+  const cudaError_t err =
+      smem_limit_once(limit_set[tma], reinterpret_cast<const void*>(kern), kTcSmem);
+  if (err != cudaSuccess) return err;
+  PdlLaunch l(dim3((unsigned)grid), dim3(kTcThreads + (tma ? 0 : 32 * kTcLoaderWarps)), smem, stream);
+  return cudaLaunchKernelEx(&l.cfg, kern, tm, tm_s, g);
+}
+
+nvfp4_status moe_tc_launch(const void* x, int64_t M, int64_t k, int64_t H, int64_t I, int64_t E,
+                           const int32_t* ids, const float* weights, const uint8_t* p13,
+                           const uint8_t* s13, const float* g13, const uint8_t* p2,
+                           const uint8_t* s2, const float* g2, void* out, int out_dtype,
+                           void* workspace, cudaStream_t stream) {
+  const int sms = sm_count();
+  if (sms <= 0) return NVFP4_ERR_CUDA;
+  const TcLayout L = tc_layout(M, k, H, I, sms);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  TcArgs a = {};
+  a.x = static_cast<const uint16_t*>(x);
+  a.ids = ids;
+  a.weights = weights;
+  a.g13 = g13;
+  a.g2 = g2;
+  a.out = out;
+  a.M = (int)M;
+  a.k = (int)k;
+  a.H = (int)H;
+  a.I = (int)I;
+  a.E = (int)E;
+  a.P = (int)(M * k);
+  a.cap = tc_cap(M);
+  a.tiles_max = L.tiles_max;
+  a.grid = sms;
+  a.pieces = out_dtype == NVFP4_OUT_BF16 ? kPiecesBf16 : kPieces;
+  a.counts = reinterpret_cast<int2*>(ws + L.counts);
+  a.by_pair = reinterpret_cast<TcPlace*>(ws + L.by_pair);
+  a.by_place = reinterpret_cast<TcPlace*>(ws + L.by_place);
+  a.act1 = ws + L.act1;
+  a.sf1 = ws + L.sf1;
+  a.act2 = ws + L.act2;
+  a.sf2 = ws + L.sf2;
+  a.mul1 = reinterpret_cast<float*>(ws + L.mul1);
+  a.mul2 = reinterpret_cast<float*>(ws + L.mul2);
+  a.gu = reinterpret_cast<float*>(ws + L.gu);
+  a.y = reinterpret_cast<float*>(ws + L.y);
+  a.part1 = reinterpret_cast<float*>(ws + L.part1);
+  a.part2 = reinterpret_cast<float*>(ws + L.part2);
+  a.status = reinterpret_cast<int32_t*>(ws);
+
+  TcGemm g = {};
+  g.cap = a.cap;
+  g.ids = ids;
+  g.E = a.E;
+  g.P = a.P;
+  g.tiles_max = a.tiles_max;
+  g.status = a.status;
+  TcGemm g1 = g, g2a = g;
+  g1.codes = p13;
+  g1.scales = s13;
+  g1.rows = E * 2 * I;
+  g1.N = (int)(2 * I);
+  g1.K = (int)H;
+  g1.act = a.act1;
+  g1.sf = a.sf1;
+  g1.mul = a.mul1;
+  g1.dst = a.gu;
+  g1.part = a.part1;
+  g2a.codes = p2;
+  g2a.scales = s2;
+  g2a.rows = E * H;
+  g2a.N = (int)H;
+  g2a.K = (int)I;
+  g2a.act = a.act2;
+  g2a.sf = a.sf2;
+  g2a.mul = a.mul2;
+  g2a.dst = a.y;
+  g2a.part = a.part2;
+
+  cudaError_t err;
+  {
+    PdlLaunch l(dim3((unsigned)M), dim3(kPrepThreads), 0, stream);
+    err = cudaLaunchKernelEx(&l.cfg, moe_prep_kernel, a);
+  }
+  if (err == cudaSuccess) err = tc_gemm_launch(g1, sms, stream);
+  if (err == cudaSuccess) {
+    auto bytes = [](int64_t I) {
+      return (size_t)(act_threads(I) / 32) * kSplitBytes + (size_t)I * 4 +
+             (size_t)((2 * I + 127) / 128) * sizeof(TcSpan);
+    };
+    const size_t smem = bytes(I);
+    static std::atomic<uint64_t> limit_set{0};
+    err = smem_limit_once(limit_set, reinterpret_cast<const void*>(moe_act_kernel),
+                          bytes(NVFP4_MOE_MAX_DIM));
+    if (err == cudaSuccess) {
+      PdlLaunch l(dim3((unsigned)a.P), dim3(act_threads(I)), smem, stream);
+      err = cudaLaunchKernelEx(&l.cfg, moe_act_kernel, a);
+    }
+  }
+  if (err == cudaSuccess) err = tc_gemm_launch(g2a, sms, stream);
+  if (err == cudaSuccess) {
+    const int RT = (int)((H + 127) / 128);
+    PdlLaunch l(dim3((unsigned)((RT + 7) / 8), (unsigned)M), dim3(256), 0, stream);
+    err = out_dtype == NVFP4_OUT_BF16 ? cudaLaunchKernelEx(&l.cfg, moe_tc_combine_kernel<true>, a)
+                                      : cudaLaunchKernelEx(&l.cfg, moe_tc_combine_kernel<false>, a);
+  }
+  return err == cudaSuccess && cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+}
+
+}  // namespace nvfp4

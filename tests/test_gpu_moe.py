@@ -126,6 +126,70 @@ def test_moe(M, E, k, H, I, out_dtype):
     check(out, args)
 
 
+# more work: the FP4 tensor-core route, with inner sizes that are and are not
+# multiples of 256, 64 and 32, units and tiles that are cut, row counts that
+# are not multiples of 128, and more pairs of an expert than a tile takes
+WIDE = [
+    (16, 8, 4, 1024, 512), (24, 6, 2, 4352, 272), (33, 16, 4, 2048, 144), (300, 3, 3, 256, 144),
+    (17, 512, 8, 1024, 336), (8, 8, 2, 4096, 528), (1, 64, 64, 720, 720), (9, 4, 1, 8192, 464),
+    (512, 12, 8, 128, 64), (512, 12, 8, 80, 112), (40, 10, 3, 16, 16384), (70, 5, 2, 16128, 16),
+]
+
+
+@pytest.mark.parametrize("M,E,k,H,I", WIDE)
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+def test_moe_wide(M, E, k, H, I, out_dtype):
+    args = make(M, E, k, H, I, seed=M + H + 1)
+    args[1][M // 2, 0] = -1
+    check(nv.w4a16_moe(*on_gpu(*args), out_dtype=out_dtype), args)
+
+
+def test_moe_wide_absent_repeated_special_and_dirty():
+    x, ids, w, w13, w2 = make(64, 16, 8, 512, 256, seed=15, absent=0.4)
+    ids[0] = -1
+    ids[1, :] = 3
+    ids[2, 0], ids[2, 1], ids[3, 0] = 16, 2 ** 31 - 1, -2 ** 31
+    dev = on_gpu(x, ids, w, w13, w2)
+    ws = torch.empty(nv.w4a16_moe_workspace_bytes(64, 8, 512, 256), dtype=torch.uint8, device="cuda")
+    ws.fill_(255)
+    clean = nv.w4a16_moe(*dev, out_dtype=torch.float32, workspace=ws)
+    check(clean, (x, ids, w, w13, w2))
+    assert bool((clean[0] == 0).all())
+    assert nv.nvfp4_read_device_status(ws) == nv.Status.OK
+    for fill in (0, 127, 255):  # NaN and every other byte left in the workspace
+        ws.fill_(fill)
+        assert torch.equal(nv.w4a16_moe(*dev, out_dtype=torch.float32, workspace=ws), clean)
+    ids[4:7, 0] = 5  # each of these tokens has an expert
+    clean = nv.w4a16_moe(*on_gpu(x, ids, w, w13, w2), workspace=ws)
+    x[4, 9], x[5, 511] = float("inf"), float("nan")
+    x[6] = 0.0
+    x[7] = (x[7].float() * 2.0 ** -120).to(torch.bfloat16)
+    out = nv.w4a16_moe(*on_gpu(x, ids, w, w13, w2), workspace=ws)
+    same = torch.ones(64, dtype=torch.bool)
+    same[4:8] = False
+    assert torch.equal(out[same], clean[same])
+    assert not bool(torch.isfinite(out[4:6]).any())
+    assert bool((out[6] == 0).all()) and bool(torch.isfinite(out[7]).all())
+    none = nv.w4a16_moe(*on_gpu(x, torch.full_like(ids, -1), w, w13, w2), workspace=ws)
+    assert bool((none == 0).all())
+
+
+def test_moe_wide_nan_block_scale_raises_the_status():
+    """... in an expert that is read, and not in the rows behind it."""
+    x, ids, w, w13, w2 = make(48, 6, 4, 720, 336, seed=4)
+    ids[:] = torch.tensor([0, 1, 3, 4], dtype=torch.int32)
+    ws = torch.empty(nv.w4a16_moe_workspace_bytes(48, 4, 720, 336), dtype=torch.uint8, device="cuda")
+    for at, e, status in ((1, 3, nv.Status.ERR_NONFINITE), (2, 1, nv.Status.ERR_NONFINITE),
+                          (1, 2, nv.Status.OK), (2, 5, nv.Status.OK), (0, 0, nv.Status.OK)):
+        bad = [x, list(w13), list(w2)]
+        if at:
+            s = bad[at][1].clone().view(torch.uint8)
+            s[e, 3, 5] = 0x7F
+            bad[at][1] = s.view(torch.float8_e4m3fn)
+        nv.w4a16_moe(*on_gpu(x, ids, w, *bad[1:]), workspace=ws)
+        assert nv.nvfp4_read_device_status(ws) == status, (at, e)
+
+
 @pytest.mark.parametrize("M,E,k,H,I", [(5, 8, 4, 512, 256), (64, 16, 8, 256, 80), (9, 512, 8, 64, 32)])
 def test_moe_absent_and_repeated_experts(M, E, k, H, I):
     """Ids outside [0, E) add nothing, a token without experts gets zeros, and
@@ -187,7 +251,8 @@ def test_moe_nan_block_scale_raises_the_status():
         assert nv.nvfp4_read_device_status(ws) == status, (e, status)
 
 
-@pytest.mark.parametrize("M,E,k,H,I", [(1, 128, 8, 2048, 768), (48, 16, 4, 320, 720)])
+@pytest.mark.parametrize("M,E,k,H,I", [(1, 128, 8, 2048, 768), (48, 16, 4, 320, 720),
+                                        (64, 32, 8, 1024, 528)])
 def test_moe_deterministic_on_a_dirty_workspace_and_another_stream(M, E, k, H, I):
     args = on_gpu(*make(M, E, k, H, I, seed=6))
     ws = torch.empty(nv.w4a16_moe_workspace_bytes(M, k, H, I), dtype=torch.uint8, device="cuda")
