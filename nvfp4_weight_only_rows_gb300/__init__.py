@@ -670,7 +670,21 @@ def w4a16_grouped_gemm(x: torch.Tensor, group_offsets: torch.Tensor, packed: tor
 
 
 _SCORING = {"softmax": 0, "sigmoid": 1}  # NVFP4_ROUTE_*
-_DTYPE_CODE = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
+_native = None
+
+
+def _load_native():
+    """The compiled side of the calls below (checks, allocation, C ABI call in
+    C++: at decode sizes they are shorter than the same in Python)."""
+    global _native
+    load_library()
+    try:
+        from . import _calls
+    except ImportError as e:
+        raise RuntimeError("_calls.so is missing or does not match the installed torch: build it "
+                           "first (python -c 'import __graft_entry__ as g; g.build()')") from e
+    _native = _calls
+    return _calls
 
 
 def moe_route(router_logits: torch.Tensor, k: int, renormalize: bool = True,
@@ -680,30 +694,11 @@ def moe_route(router_logits: torch.Tensor, k: int, renormalize: bool = True,
     """The k experts of each token with the largest softmax or sigmoid scores
     (plus bias f32[E] for the choice; lower expert first on ties) of
     router_logits f32 or bf16 [M, E]: (expert_ids i32[M, k], weights f32[M, k])."""
-    lib = load_library()
-    code = _DTYPE_CODE.get(router_logits.dtype)
-    if code is None or router_logits.dim() != 2:
-        raise ValueError("router_logits must be float32 or bfloat16 [M, E]")
-    _need(router_logits, router_logits.dtype, "router_logits")
-    M, E = router_logits.shape
-    if scoring not in _SCORING:
+    code = _SCORING.get(scoring)
+    if code is None:
         raise ValueError(f"scoring must be one of {sorted(_SCORING)}, got {scoring!r}")
-    if bias is not None:
-        _need(bias, torch.float32, "bias", (E,))
-    kk = max(int(k), 0)
-    if expert_ids is None:
-        expert_ids = torch.empty((M, kk), dtype=torch.int32, device=router_logits.device)
-    else:
-        _need(expert_ids, torch.int32, "expert_ids", (M, kk))
-    if weights is None:
-        weights = torch.empty((M, kk), dtype=torch.float32, device=router_logits.device)
-    else:
-        _need(weights, torch.float32, "weights", (M, kk))
-    rc = lib.moe_route(router_logits.data_ptr(), code, M, E, k, _SCORING[scoring],
-                       int(renormalize), _ptr(bias), scale, expert_ids.data_ptr(),
-                       weights.data_ptr(), _stream(stream))
-    _check(rc, "moe_route")
-    return expert_ids, weights
+    return (_native or _load_native()).moe_route(router_logits, k, renormalize, code, bias, scale,
+                                               expert_ids, weights, stream)
 
 
 def w4a16_moe_workspace_bytes(M: int, k: int, H: int, I: int) -> int:
@@ -720,50 +715,11 @@ def w4a16_moe(x: torch.Tensor, expert_ids: torch.Tensor, weights: torch.Tensor,
     expert_ids[m, j].  x bf16[M, H], expert_ids i32[M, k] (an id outside
     [0, E) adds nothing), weights f32[M, k], w13 u8[E, 2I, H/2] + e4m3 scales
     [E, 2I, H/16] + f32[E], w2 u8[E, H, I/2] + [E, H, I/16] + f32[E]."""
-    lib = load_library()
-    _need(x, torch.bfloat16, "x")
-    M, H = x.shape
-    k = expert_ids.shape[1]
-    E, I = w2_packed.shape[0], w2_packed.shape[2] * 2
-    _need(expert_ids, torch.int32, "expert_ids", (M, k))
-    _need(weights, torch.float32, "weights", (M, k))
-    _need(w13_packed, torch.uint8, "w13_packed", (E, 2 * I, H // 2))
-    _need(w13_scales, w13_scales.dtype, "w13_scales", (E, 2 * I, H // 16))
-    _need(w13_global, torch.float32, "w13_global", (E,))
-    _need(w2_packed, torch.uint8, "w2_packed", (E, H, I // 2))
-    _need(w2_scales, w2_scales.dtype, "w2_scales", (E, H, I // 16))
-    _need(w2_global, torch.float32, "w2_global", (E,))
-    if w13_scales.element_size() != 1 or w2_scales.element_size() != 1:
-        raise ValueError("scales must be float8_e4m3fn (or uint8 bit patterns)")
-    if out is None:
-        out = torch.empty(M, H, dtype=out_dtype, device=x.device)
-    _need(out, out.dtype, "out", (M, H))
-    code = _DTYPE_CODE.get(out.dtype)
-    if code is None:
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise ValueError("out must be float32 or bfloat16")
-    if workspace is None:
-        workspace = _workspace(lib.w4a16_moe_workspace_bytes(M, k, H, I), x.device)
-    rc = lib.w4a16_moe(x.data_ptr(), M, k, H, I, E, expert_ids.data_ptr(), weights.data_ptr(),
-                       w13_packed.data_ptr(), w13_scales.data_ptr(), w13_global.data_ptr(),
-                       w2_packed.data_ptr(), w2_scales.data_ptr(), w2_global.data_ptr(),
-                       out.data_ptr(), code, workspace.data_ptr(),
-                       workspace.numel() * workspace.element_size(), _stream(stream))
-    _check(rc, "w4a16_moe")
-    return out
-
-
-def _logits_args(logits, token_ids):
-    code = _DTYPE_CODE.get(logits.dtype)
-    if code is None or logits.dim() != 2 or not logits.is_cuda:
-        raise ValueError("logits must be a float32 or bfloat16 CUDA tensor [M, N]")
-    M, N = logits.shape
-    if N > 1 and logits.stride(1) != 1:
-        raise ValueError("the logits of a row must be contiguous")
-    ld = logits.stride(0) if M > 1 else N
-    if ld < N:
-        raise ValueError("the rows of logits overlap")
-    _need(token_ids, torch.int64, "token_ids", (M,))
-    return code, M, N, ld
+    return (_native or _load_native()).w4a16_moe(
+        x, expert_ids, weights, w13_packed, w13_scales, w13_global, w2_packed, w2_scales,
+        w2_global, out, out_dtype is torch.bfloat16, workspace, stream)
 
 
 def token_logprobs(logits: torch.Tensor, token_ids: torch.Tensor, k: int = 0,
@@ -772,23 +728,7 @@ def token_logprobs(logits: torch.Tensor, token_ids: torch.Tensor, k: int = 0,
     logits) for logits f32 or bf16 [M, N] (rows may be strided), and the k
     most likely tokens of each row: (logprobs f32[M], entropy f32[M], lse
     f32[M], ranks i64[M], top_ids i64[M, k], top_logprobs f32[M, k])."""
-    lib = load_library()
-    code, M, N, ld = _logits_args(logits, token_ids)
-    dev = logits.device
-    kk = max(int(k), 0)
-    empty = torch.empty  # one allocation per result: views of a shared one cost more
-    logprobs = empty(M, dtype=torch.float32, device=dev)
-    entropy = empty(M, dtype=torch.float32, device=dev)
-    lse = empty(M, dtype=torch.float32, device=dev)
-    ranks = empty(M, dtype=torch.int64, device=dev)
-    top_ids = empty((M, kk), dtype=torch.int64, device=dev)
-    top_logprobs = empty((M, kk), dtype=torch.float32, device=dev)
-    rc = lib.token_logprobs(logits.data_ptr(), code, M, N, ld, token_ids.data_ptr(),
-                            inv_temperature, k, logprobs.data_ptr(), entropy.data_ptr(),
-                            lse.data_ptr(), ranks.data_ptr(), top_ids.data_ptr(),
-                            top_logprobs.data_ptr(), _stream(stream))
-    _check(rc, "token_logprobs")
-    return logprobs, entropy, lse, ranks, top_ids, top_logprobs
+    return (_native or _load_native()).token_logprobs(logits, token_ids, k, inv_temperature, stream)
 
 
 def token_logprobs_backward(logits: torch.Tensor, token_ids: torch.Tensor, lse: torch.Tensor,
@@ -798,27 +738,8 @@ def token_logprobs_backward(logits: torch.Tensor, token_ids: torch.Tensor, lse: 
                             stream=None) -> torch.Tensor:
     """The gradient of token_logprobs' logprobs and entropy with respect to
     the logits, in their dtype; `out` may be the logits themselves."""
-    lib = load_library()
-    code, M, N, ld = _logits_args(logits, token_ids)
-    _need(lse, torch.float32, "lse", (M,))
-    _need(grad_logprobs, torch.float32, "grad_logprobs", (M,))
-    if grad_entropy is not None:
-        _need(grad_entropy, torch.float32, "grad_entropy", (M,))
-        if entropy is None:
-            raise ValueError("grad_entropy needs the forward's entropy")
-    if entropy is not None:
-        _need(entropy, torch.float32, "entropy", (M,))
-    if out is None:
-        out = torch.empty((M, N), dtype=logits.dtype, device=logits.device)
-    elif not out.is_cuda or out.dtype != logits.dtype or tuple(out.shape) != (M, N) or (
-            N > 1 and out.stride(1) != 1):
-        raise ValueError("out must be a CUDA tensor of the logits' shape and dtype, rows contiguous")
-    rc = lib.token_logprobs_backward(logits.data_ptr(), code, M, N, ld, token_ids.data_ptr(),
-                                     inv_temperature, lse.data_ptr(), _ptr(entropy),
-                                     grad_logprobs.data_ptr(), _ptr(grad_entropy), out.data_ptr(),
-                                     out.stride(0) if M > 1 else N, _stream(stream))
-    _check(rc, "token_logprobs_backward")
-    return out
+    return (_native or _load_native()).token_logprobs_backward(
+        logits, token_ids, lse, entropy, grad_logprobs, grad_entropy, inv_temperature, out, stream)
 
 
 def w4a16_lm_head_noalloc(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,

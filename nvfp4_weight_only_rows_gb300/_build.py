@@ -3,6 +3,8 @@
 Each translation unit is compiled by nvcc in parallel, then linked into one
 shared library next to this file.  The library links the CUDA runtime
 dynamically, so inside a PyTorch process it shares torch's runtime instance.
+calls.cpp, the Python side of some calls, is compiled beside them against the
+installed torch's headers into _calls.so, which links that library.
 """
 from __future__ import annotations
 
@@ -10,10 +12,12 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libnvfp4_lm_head.so")
+CALLS = os.path.join(HERE, "_calls.so")
 SOURCES = ("quantize.cu", "lm_head.cu", "fp8.cu", "w4a4.cu", "topk.cu", "api.cu", "noalloc.cu",
            "selftest.cu", "moe_route.cu", "moe.cu", "moe_tc.cu",
            "logprobs.cu")
@@ -38,8 +42,26 @@ def _stale(sources, target) -> bool:
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
 
 
+def _compile_calls(obj_dir: str):
+    """calls.cpp against the installed torch: (object, link arguments)."""
+    import torch
+
+    home = os.path.dirname(torch.__file__)
+    obj = os.path.join(obj_dir, "calls.o")
+    inc = [os.path.join(home, "include"),
+           os.path.join(home, "include", "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"],
+           os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    cmd = ["g++", "-O2", "-fPIC", "-std=c++17", "-Wall", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f"-isystem{p}" for p in inc], "-c", os.path.join(CSRC, "calls.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on calls.cpp:\n{r.stderr}")
+    return obj, ["-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    if not force and not _stale(SOURCES, LIB):
+    if not force and not _stale(SOURCES, LIB) and not _stale(SOURCES, CALLS):
         return LIB
     obj_dir = os.path.join(HERE, "_build")
     os.makedirs(obj_dir, exist_ok=True)
@@ -55,8 +77,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        calls = ex.submit(_compile_calls, obj_dir)
         results = list(ex.map(compile_one, SOURCES))
+        calls_obj, calls_libs = calls.result()
     if verbose:
         for _, log in results:
             print(log)
@@ -67,6 +91,13 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = CALLS + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, calls_obj, "-L" + HERE, "-l:" + os.path.basename(LIB),
+           "-Wl,-rpath,$ORIGIN", *calls_libs]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of _calls.so failed:\n{r.stderr}")
+    os.replace(tmp, CALLS)
     return LIB
 
 
