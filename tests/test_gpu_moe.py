@@ -85,6 +85,35 @@ def test_route_special_rows():
     assert empty_ids.shape == (0, 4) and empty_w.shape == (0, 4)
 
 
+@pytest.mark.parametrize("E", [7, 64, 100, 256, 400])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_route_near_ties(E, scoring):
+    """fp32 logits that differ in their last bits only, equal ones among
+    them, and NaNs of either sign: the exact order, the lower expert first."""
+    g = torch.Generator().manual_seed(E)
+    x = torch.ones(64, E) + torch.randint(0, 9, (64, E), generator=g) * 2.0 ** -23
+    x[32:] *= -1
+    x[5, 3], x[5, 6] = float("nan"), -float("nan")
+    k = min(E, 8)
+    ids, w = nv.moe_route(x.cuda(), k, scoring=scoring)
+    want, want_w = route_reference(torch.nan_to_num(x, nan=1e4), k, scoring, True, None, 1.0)
+    assert torch.equal(ids.cpu().long(), want)
+    live = torch.arange(64) != 5
+    assert bool(((w.cpu().double() - want_w).abs()[live] <= (E + 16) * 2.0 ** -23).all())
+    assert bool(torch.isnan(w[5]).all())
+
+
+def test_route_unaligned_rows():
+    """A base and rows off a 16-byte boundary."""
+    for E, at in ((128, 1), (130, 0), (250, 3)):
+        buf = torch.randn(at + 9 * E, generator=torch.Generator().manual_seed(E))
+        for t in (buf, buf.to(torch.bfloat16)):
+            x = t.cuda()[at:].view(9, E)
+            ids, _ = nv.moe_route(x, 6)
+            want, _ = route_reference(x.cpu(), 6, "softmax", True, None, 1.0)
+            assert torch.equal(ids.cpu().long(), want)
+
+
 # ------------------------------------------------------------ expert layer
 def make(M, E, k, H, I, seed, absent=0.0):
     g = torch.Generator().manual_seed(seed)
