@@ -145,19 +145,24 @@ __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_kernel(
       word[r] = key[r] == kTaken ? kTaken : (key[r] & ~kIdMask) | (~(uint32_t)(e0 + r) & kIdMask);
     sort_desc(word);
     const bool whole = sizeof(T) == 2 && bias == nullptr;  // the words hold the keys
-    uint32_t last = kTaken;
-    for (int j = 0; j < k + (whole ? 0 : 1); ++j) {
+    uint32_t mine = kTaken;  // lane j: the word of round j
+    const int rounds = k + (whole ? 0 : 1);
+#pragma unroll 2
+    for (int j = 0; j < rounds; ++j) {
       const uint32_t mx = __reduce_max_sync(0xFFFFFFFFu, word[0]);
-      near = near || (j > 0 && ((mx ^ last) & ~kIdMask) == 0u);
-      last = mx;
-      if (word[0] == mx) {
+      const bool pop = word[0] == mx;
 #pragma unroll
-        for (int r = 0; r + 1 < kR; ++r) word[r] = word[r + 1];
-        word[kR - 1] = kTaken;
-      }
-      if (lane == j) my_id = (int)(~mx & kIdMask);
+      for (int r = 0; r + 1 < kR; ++r) word[r] = pop ? word[r + 1] : word[r];
+      word[kR - 1] = pop ? kTaken : word[kR - 1];
+      mine = lane == j ? mx : mine;
     }
-    near = near && !whole;
+    my_id = (int)(~mine & kIdMask);
+    if (!whole) {
+      // round 32 (k of 32) is in no lane: such tokens go by whole keys
+      const uint32_t before = __shfl_up_sync(0xFFFFFFFFu, mine, 1);
+      near = rounds > 32 || __any_sync(0xFFFFFFFFu, lane > 0 && lane < rounds &&
+                                                        ((mine ^ before) & ~kIdMask) == 0u);
+    }
   }
   if (near) {  // warp-uniform
     uint32_t best = kTaken;
@@ -179,7 +184,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_kernel(
       if (lane == j) my_id = (int)e;
     }
   }
-  float w = lane < k ? score(route_logit(row + my_id)) : 0.0f;
+  float w = lane < k ? score(route_logit(row + min(my_id, E - 1))) : 0.0f;
   if (renorm) {
     float sum = w;
 #pragma unroll
