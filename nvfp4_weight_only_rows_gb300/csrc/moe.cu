@@ -186,39 +186,53 @@ __device__ __forceinline__ void moe_build(const MoeArgs& p, const int* list, int
   }
 }
 
-// One warp's steps [f0, f1) of a segment: step f is stage f % n_stages of
-// tile q0 + f / n_stages.  Tiles the warp has from first to last stage go to
-// dst; a first or last tile it shares goes to part[0] (begun by an earlier
-// warp) or part[1] (begun here).
-template <int kNT, bool kWide, bool kSplit>
-__device__ __forceinline__ void moe_steps(const uint8_t* codes, const uint8_t* scales, int N, int K,
-                                          int n_stages, int q0, int f0, int f1, int T,
-                                          const int* list, const uint8_t* s_act, size_t lo_off,
-                                          const float* s_mul, float* dst, float4* part,
-                                          uint32_t& nan_bits) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int64_t cs = K / 2, ss = K / 16;
-  // fetch: the (tile, stage) of the next load
-  int fq = q0 + f0 / n_stages, fs = f0 % n_stages, ff = f0;
-  auto fetch = [&](MoeFrag& a) {
-    if (ff < f1) {
-      const int k0 = 256 * fs + 64 * t;
-      const int64_t r = (int64_t)fq * 16 + g;
+// A warp's loads of its steps [f0, f1) of a segment: step f is stage f %
+// n_stages of the 16-row tile q0 + f / n_stages.  kMoeDepth of them are in
+// flight, the first ones before the activations are built.
+template <bool kWide>
+struct MoeStream {
+  const uint8_t *codes, *scales;
+  int K, n_stages, tile, stage, left;
+  MoeFrag ring[kMoeDepth];
+
+  __device__ __forceinline__ void fetch(MoeFrag& a) {
+    if (left > 0) {
+      const int lane = threadIdx.x & 31, k0 = 256 * stage + 64 * (lane & 3);
+      const int64_t r = (int64_t)tile * 16 + (lane >> 2);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        moe_load_row<kWide>(codes + (r + 8 * h) * cs + k0 / 2, scales + (r + 8 * h) * ss + k0 / 16,
-                            K - k0, a.w[h], a.s[h]);
-      ++ff;
-      if (++fs == n_stages) {
-        fs = 0;
-        ++fq;
+        moe_load_row<kWide>(codes + (r + 8 * h) * (K / 2) + k0 / 2,
+                            scales + (r + 8 * h) * (K / 16) + k0 / 16, K - k0, a.w[h], a.s[h]);
+      --left;
+      if (++stage == n_stages) {
+        stage = 0;
+        ++tile;
       }
     }
-  };
-  MoeFrag ring[kMoeDepth];
+  }
+  __device__ __forceinline__ void begin(const uint8_t* c, const uint8_t* s, int k, int ns, int q0,
+                                        int f0, int f1) {
+    codes = c;
+    scales = s;
+    K = k;
+    n_stages = ns;
+    tile = q0 + f0 / ns;
+    stage = f0 % ns;
+    left = f1 - f0;
 #pragma unroll
-  for (int d = 0; d < kMoeDepth; ++d) fetch(ring[d]);
+    for (int d = 0; d < kMoeDepth; ++d) fetch(ring[d]);
+  }
+};
 
+// The products of those steps.  Tiles the warp has from first to last stage
+// go to dst; a first or last tile it shares goes to part[0] (begun by an
+// earlier warp) or part[1] (begun here).
+template <int kNT, bool kWide, bool kSplit>
+__device__ __forceinline__ void moe_steps(MoeStream<kWide>& in, int N, int n_stages, int q0, int f0,
+                                          int f1, int T, const int* list, const uint8_t* s_act,
+                                          size_t lo_off, const float* s_mul, float* dst,
+                                          float4* part, uint32_t& nan_bits) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   float acc[kNT][4];
 #pragma unroll
   for (int n = 0; n < kNT; ++n)
@@ -307,8 +321,8 @@ __device__ __forceinline__ void moe_steps(const uint8_t* codes, const uint8_t* s
 #pragma unroll
     for (int d = 0; d < kMoeDepth; ++d) {
       if (f + d < f1) {
-        step(ring[d]);
-        fetch(ring[d]);
+        step(in.ring[d]);
+        in.fetch(in.ring[d]);
       }
     }
   }
@@ -342,48 +356,73 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_gemm_kernel(const MoeArgs 
   }
 
   // ---- the experts that have pairs, and their segments
-  for (int e = tid; e < p.E; e += kMoeThreads) s_cnt[e] = 0;
-  __syncthreads();
-  for (int i = tid; i < P; i += kMoeThreads) {
-    const int e = __ldg(p.ids + i);
-    if (e >= 0 && e < p.E) atomicAdd(&s_cnt[e], 1);
-  }
-  __syncthreads();
-  if (warp == 0) {
-    int a = 0, before = 0;
-    for (int e0 = 0; e0 < p.E; e0 += 32) {
-      const int e = e0 + lane;
-      const int n = e < p.E ? (s_cnt[e] + seg - 1) / seg : 0;
-      const uint32_t bal = __ballot_sync(0xFFFFFFFFu, n > 0);
+  if (P <= 32) {
+    // a pair a lane, the experts in order of their first pair
+    if (warp == 0) {
+      const int e = lane < P ? __ldg(p.ids + lane) : -1;
+      const bool valid = e >= 0 && e < p.E;
+      const uint32_t same = __match_any_sync(0xFFFFFFFFu, valid ? e : -1);
+      const bool leads = valid && (same & ((1u << lane) - 1u)) == 0u;
+      const uint32_t leaders = __ballot_sync(0xFFFFFFFFu, leads);
+      const int n = leads ? (__popc(same) + seg - 1) / seg : 0;
       int incl = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
         if (lane >= o) incl += y;
       }
-      if (n > 0) {
-        const int at = a + __popc(bal & ((1u << lane) - 1u));
+      if (leads) {
+        const int at = __popc(leaders & ((1u << lane) - 1u));
         s_exp[at] = e;
-        s_seg[at] = before + incl - n;
+        s_cnt[e] = __popc(same);
+        s_seg[at] = incl - n;
       }
-      a += __popc(bal);
-      before += __shfl_sync(0xFFFFFFFFu, incl, 31);
+      if (lane == 31) {
+        s_active = __popc(leaders);
+        s_seg[__popc(leaders)] = incl;
+      }
     }
-    if (lane == 0) {
-      s_seg[a] = before;
-      s_active = a;
+    __syncthreads();
+  } else {
+    for (int e = tid; e < p.E; e += kMoeThreads) s_cnt[e] = 0;
+    __syncthreads();
+    for (int i = tid; i < P; i += kMoeThreads) {
+      const int e = __ldg(p.ids + i);
+      if (e >= 0 && e < p.E) atomicAdd(&s_cnt[e], 1);
     }
+    __syncthreads();
+    if (warp == 0) {
+      int a = 0, before = 0;
+      for (int e0 = 0; e0 < p.E; e0 += 32) {
+        const int e = e0 + lane;
+        const int n = e < p.E ? (s_cnt[e] + seg - 1) / seg : 0;
+        const uint32_t bal = __ballot_sync(0xFFFFFFFFu, n > 0);
+        int incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+          if (lane >= o) incl += y;
+        }
+        if (n > 0) {
+          const int at = a + __popc(bal & ((1u << lane) - 1u));
+          s_exp[at] = e;
+          s_seg[at] = before + incl - n;
+        }
+        a += __popc(bal);
+        before += __shfl_sync(0xFFFFFFFFu, incl, 31);
+      }
+      if (lane == 0) {
+        s_seg[a] = before;
+        s_active = a;
+      }
+    }
+    __syncthreads();
   }
-  __syncthreads();
   const int n_act = s_active;
   const int64_t total = (int64_t)s_seg[n_act] * RT;
   int64_t it = total * blockIdx.x / gridDim.x;
   const int64_t end = total * (blockIdx.x + 1) / gridDim.x;
-  if constexpr (kStep == 2) {
-    grid_dependency_wait();  // gu
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  }
-
+  bool waited = kStep == 1;  // step 2 waits for gu with its first weights under way
   uint32_t nan_bits = 0;
   while (it < end) {
     const int sg = (int)(it / RT), q0 = (int)(it % RT);
@@ -410,20 +449,24 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_gemm_kernel(const MoeArgs 
         seen += __popc(bal);
       }
     }
-    __syncthreads();
-    moe_build<kStep, kSplit>(p, s_list, T, n_stages, __ldg(p.g13 + e), s_act, lo_off, s_mul);
-    __syncthreads();
-
     const int steps = nq * n_stages;
     auto first = [&](int w) { return (int)((int64_t)steps * w / kMoeWarps); };
     const int f0 = first(warp), f1 = first(warp + 1);
-    const uint8_t* codes = (kStep == 1 ? p.p13 : p.p2) + (int64_t)e * N * (K / 2);
-    const uint8_t* scales = (kStep == 1 ? p.s13 : p.s2) + (int64_t)e * N * (K / 16);
+    MoeStream<kWide> in;
+    in.begin((kStep == 1 ? p.p13 : p.p2) + (int64_t)e * N * (K / 2),
+             (kStep == 1 ? p.s13 : p.s2) + (int64_t)e * N * (K / 16), K, n_stages, q0, f0, f1);
+    if (!waited) {
+      grid_dependency_wait();
+      asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+      waited = true;
+    }
+    __syncthreads();
+    moe_build<kStep, kSplit>(p, s_list, T, n_stages, __ldg(p.g13 + e), s_act, lo_off, s_mul);
+    __syncthreads();
     if (f0 < f1) {
       auto go = [&](auto nt) {
-        moe_steps<decltype(nt)::value, kWide, kSplit>(codes, scales, N, K, n_stages, q0, f0, f1, T,
-                                              s_list, s_act, lo_off, s_mul, dst, s_part[warp],
-                                              nan_bits);
+        moe_steps<decltype(nt)::value, kWide, kSplit>(in, N, n_stages, q0, f0, f1, T, s_list, s_act,
+                                                      lo_off, s_mul, dst, s_part[warp], nan_bits);
       };
       if (T <= 8) go(std::integral_constant<int, 1>{});
       else if (T <= 16) go(std::integral_constant<int, 2>{});
@@ -457,7 +500,11 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_gemm_kernel(const MoeArgs 
         }
       }
     }
-    __syncthreads();
+    if (it < end) __syncthreads();
+  }
+  if (!waited) {  // no work here: the flags below are read after this kernel all the same
+    grid_dependency_wait();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   }
   // a block scale that is NaN (0x7F or 0xFF: never loaded)
   const int bad = __syncthreads_or((nan_bits & 0x80808080u) != 0u);
@@ -468,36 +515,56 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_gemm_kernel(const MoeArgs 
 // columns a thread.
 template <bool kBf16>
 __global__ void __launch_bounds__(256) moe_combine_kernel(const MoeArgs p, int n_flags) {
-  grid_dependency_wait();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int m = blockIdx.y, c = blockIdx.x * blockDim.x + threadIdx.x;
+  constexpr int kAt = 8;  // slots whose loads are in flight together
+  float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  bool waited = false;
+  for (int j0 = 0; j0 < p.k; j0 += kAt) {
+    float w[kAt];
+    bool live[kAt];
+#pragma unroll
+    for (int j = 0; j < kAt; ++j) {
+      const int64_t pair = (int64_t)m * p.k + j0 + j;
+      const int e = j0 + j < p.k ? __ldg(p.ids + pair) : -1;
+      live[j] = e >= 0 && e < p.E;
+      w[j] = live[j] ? __ldg(p.weights + pair) * __ldg(p.g2 + e) : 0.0f;
+    }
+    if (!waited) {
+      grid_dependency_wait();
+      asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+      waited = true;
+    }
+    float4 v[kAt];
+#pragma unroll
+    for (int j = 0; j < kAt; ++j)
+      if (live[j] && 4 * c < p.H)
+        v[j] = __ldcg(reinterpret_cast<const float4*>(p.y + ((int64_t)m * p.k + j0 + j) * p.H) + c);
+#pragma unroll
+    for (int j = 0; j < kAt; ++j) {
+      if (live[j]) {
+        sum.x = __fmaf_rn(w[j], v[j].x, sum.x);
+        sum.y = __fmaf_rn(w[j], v[j].y, sum.y);
+        sum.z = __fmaf_rn(w[j], v[j].z, sum.z);
+        sum.w = __fmaf_rn(w[j], v[j].w, sum.w);
+      }
+    }
+  }
+  if (4 * c < p.H) {
+    const int64_t at = ((int64_t)m * p.H >> 2) + c;
+    if constexpr (kBf16) {
+      uint2 o;
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o.x) : "f"(sum.y), "f"(sum.x));
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o.y) : "f"(sum.w), "f"(sum.z));
+      reinterpret_cast<uint2*>(p.out)[at] = o;
+    } else {
+      reinterpret_cast<float4*>(p.out)[at] = sum;
+    }
+  }
   if (blockIdx.x == 0 && blockIdx.y == 0) {
     int bad = 0;
     for (int i = threadIdx.x; i < n_flags; i += blockDim.x) bad |= __ldcg(p.nan_flags + i);
     bad = __syncthreads_or(bad);
     if (threadIdx.x == 0) *p.status = bad ? NVFP4_ERR_NONFINITE : NVFP4_OK;
-  }
-  const int m = blockIdx.y, c = blockIdx.x * blockDim.x + threadIdx.x;
-  if (4 * c >= p.H) return;
-  float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int j = 0; j < p.k; ++j) {
-    const int64_t pair = (int64_t)m * p.k + j;
-    const int e = __ldg(p.ids + pair);
-    if (e < 0 || e >= p.E) continue;
-    const float w = __ldg(p.weights + pair) * __ldg(p.g2 + e);
-    const float4 v = __ldcg(reinterpret_cast<const float4*>(p.y + pair * p.H) + c);
-    sum.x = __fmaf_rn(w, v.x, sum.x);
-    sum.y = __fmaf_rn(w, v.y, sum.y);
-    sum.z = __fmaf_rn(w, v.z, sum.z);
-    sum.w = __fmaf_rn(w, v.w, sum.w);
-  }
-  const int64_t at = ((int64_t)m * p.H >> 2) + c;
-  if constexpr (kBf16) {
-    uint2 o;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o.x) : "f"(sum.y), "f"(sum.x));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o.y) : "f"(sum.w), "f"(sum.z));
-    reinterpret_cast<uint2*>(p.out)[at] = o;
-  } else {
-    reinterpret_cast<float4*>(p.out)[at] = sum;
   }
 }
 
@@ -523,20 +590,25 @@ nvfp4_status moe_tc_launch(const void* x, int64_t M, int64_t k, int64_t H, int64
                            const uint8_t* s2, const float* g2, void* out, int out_dtype,
                            void* workspace, cudaStream_t stream);
 
-// Where the weights of as many experts as there are pairs exceed about 48 MB
-// (27/16 byte per element of an H x I matrix), the layer goes to the FP4
-// tensor cores (moe_tc.cu): five kernels instead of three, but 6 TB/s instead
-// of 2.6.  Measured, pairs x H x I (here / there): 42 MB 31.1 / 32.0 us, 64 MB
-// 39.6 / 35.0, 340 MB 82 / 55 (H 2048, I 768); 40 MB 27.6 / 29.7, 80 MB 33.3 /
-// 32.7 (H 2048, I 720).
-constexpr int64_t kMoeFewWork = 28 << 20;
-static bool moe_use_tc(int64_t M, int64_t k, int64_t H, int64_t I) {
-  return M * k * H * I > kMoeFewWork && moe_tc_takes(k, H, I);
+// The FP4 tensor-core route (moe_tc.cu: five kernels instead of three, but 6
+// TB/s between them) is taken for more weight than about 113 MB counted once
+// per pair (27/16 byte per element of an H x I matrix), or for 6 pairs an
+// expert, where the products here turn from bandwidth to issue bound.
+// Measured (here / there): 1 token of H 2048, I 768, top 8 of 128 14.8 / 28.9
+// us, 4 tokens 33.5 / 37.8, 8 tokens 46.9 / 45.8, 16 tokens 64.0 / 54.9; H 1024,
+// I 512, top 2 of 64: 32 tokens 23.3 / 27.0, 64 tokens 32.5 / 30.2; H 512, I
+// 256, top 2 of 16: 32 tokens 16.6 / 17.5, 128 tokens 31.6 / 22.4.
+constexpr int64_t kMoeFewWork = 64 << 20;
+constexpr int64_t kMoeFewPairs = 6;
+static bool moe_use_tc(int64_t M, int64_t k, int64_t H, int64_t I, int64_t E) {
+  const int64_t P = M * k;
+  return (P * H * I >= kMoeFewWork || P >= kMoeFewPairs * E) && moe_tc_takes(k, H, I);
 }
 
+// Enough for either route: which one is taken depends on E too.
 size_t moe_workspace_bytes(int64_t M, int64_t k, int64_t H, int64_t I) {
-  if (moe_use_tc(M, k, H, I)) return moe_tc_workspace_bytes(M, k, H, I);
-  return moe_layout(M * k, H, I, std::max(sm_count(), 1)).total;
+  const size_t few = moe_layout(M * k, H, I, std::max(sm_count(), 1)).total;
+  return moe_tc_takes(k, H, I) ? std::max(few, moe_tc_workspace_bytes(M, k, H, I)) : few;
 }
 
 // Pairs of a segment: what fits the activation budget, in whole tiles of 8
@@ -570,7 +642,7 @@ nvfp4_status moe_launch(const void* x, int64_t M, int64_t k, int64_t H, int64_t 
                         const uint8_t* s13, const float* g13, const uint8_t* p2,
                         const uint8_t* s2, const float* g2, void* out, int out_dtype,
                         void* workspace, cudaStream_t stream) {
-  if (moe_use_tc(M, k, H, I))
+  if (moe_use_tc(M, k, H, I, E))
     return moe_tc_launch(x, M, k, H, I, E, ids, weights, p13, s13, g13, p2, s2, g2, out, out_dtype,
                          workspace, stream);
   const int sms = sm_count();
