@@ -311,15 +311,21 @@ constexpr int kTcMaxUnits = 8;        // unit buffers of scales
 struct TcPiece {
   int tile, rt, kb0, kb1;
 };
+// The CTA's steps [x0, x1) unit by unit.  One division at the start: three
+// 64-bit ones a unit took a role longer than the three stages of a K of 768.
 template <typename F>
-__device__ __forceinline__ void tc_pieces(int64_t x0, int64_t x1, int n_st, int RT, F f) {
-  for (int64_t x = x0; x < x1;) {
-    const int64_t u = x / n_st;
-    const int kb0 = (int)(x - u * n_st);
-    const int kb1 = (int)min((int64_t)n_st, kb0 + (x1 - x));
-    const TcPiece pc{(int)(u / RT), (int)(u % RT), kb0, kb1};
+__device__ __forceinline__ void tc_pieces(int x0, int x1, int n_st, int RT, F f) {
+  const int u = x0 / n_st;
+  TcPiece pc{u / RT, u % RT, x0 - u * n_st, 0};
+  for (int left = x1 - x0; left > 0;) {
+    pc.kb1 = min(n_st, pc.kb0 + left);
     if (!f(pc)) return;
-    x += kb1 - kb0;
+    left -= pc.kb1 - pc.kb0;
+    pc.kb0 = 0;
+    if (++pc.rt == RT) {
+      pc.rt = 0;
+      ++pc.tile;
+    }
   }
 }
 
@@ -407,8 +413,9 @@ __global__ void __launch_bounds__(kTcThreads + (kTma ? 0 : 32 * kTcLoaderWarps),
   const int64_t S = (int64_t)s_tab.tile[p.E] * RT * n_st;
   const int64_t G = tc_ctas(S, gridDim.x);
   const bool works = blockIdx.x < G;
-  const int64_t x0 = works ? tc_bound(S, blockIdx.x, G) : 0;
-  const int64_t x1 = works ? tc_bound(S, blockIdx.x + 1, G) : 0;
+  // at most 1024 tiles x 512 row tiles x 128 stages
+  const int x0 = works ? (int)tc_bound(S, blockIdx.x, G) : 0;
+  const int x1 = works ? (int)tc_bound(S, blockIdx.x + 1, G) : 0;
   // a tile is looked up once: its units follow one another
   int known = -1;
   TcTile tile{};
