@@ -33,15 +33,19 @@
 
 namespace nvfp4 {
 
-constexpr int kPieces = 8;                  // columns of a pair
-constexpr int kPiecesBf16 = 6;              // of them used for a bf16 result
+constexpr int kPieces = 8;                  // columns of a pair for an fp32 result
+constexpr int kPiecesBf16 = 6;              // ... for a bf16 one
 constexpr int kTcMaxExperts = NVFP4_MOE_MAX_EXPERTS;
 constexpr int kTcMaxK = 64;                 // slots of a token
 constexpr uint32_t kTcAStage = 128 * 128;   // 128 rows x 256 codes
 constexpr uint32_t kTcSfStage = 4 * 512;    // 4 atoms of 128 rows x 4 blocks
-constexpr uint32_t kTcPairStage = kPieces * 128;
+constexpr uint32_t kTcRow = 128;            // bytes of a piece in a stage
 constexpr int kTcMaxRing = 8;
-constexpr size_t kTcSmem = 220 << 10;       // dynamic shared memory of a product's CTA
+// Dynamic shared memory of a product's CTA: what lets a CTA of the prep kernel
+// share its SM where tiles are small (64 of 152 CTAs began 5 us late without),
+// else what there is.
+constexpr size_t kTcSmem = 205 << 10, kTcSmemLarge = 220 << 10;
+constexpr int kTcMaxCap = 20;               // pairs of a tile
 constexpr int64_t kTcMaxUnitK = 4096;       // largest K whose 128 rows of scales are loaded at once
 constexpr int kTcSfCols = 32;               // TMEM columns of a stage's scales: A 16 + B 16
 
@@ -53,31 +57,39 @@ struct __align__(16) TcPlace {
 // The routing as every CTA of a product derives it: pairs and tiles before
 // each expert.
 struct TcTables {
-  int cnt[kTcMaxExperts], off[kTcMaxExperts], tile[kTcMaxExperts + 1];
+  int cnt[kTcMaxExperts];
+  uint16_t off[kTcMaxExperts], tile[kTcMaxExperts + 1];  // at most 4096
 };
 
 struct TcTile {
   int expert, first, n;  // pairs first .. first + n - 1 in sorted order
 };
 
-__device__ __forceinline__ void tc_tables(const int32_t* ids, int P, int E, int cap, TcTables& s) {
-  const int tid = threadIdx.x, lane = tid & 31;
+// Named barrier `bar` of n threads.
+__device__ __forceinline__ void tc_sync(int bar, int n) {
+  asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(n) : "memory");
+}
+
+// By the n threads tid = 0 .. n - 1 (whole warps) that meet at barrier `bar`.
+__device__ __forceinline__ void tc_tables(const int32_t* ids, int P, int E, int cap, TcTables& s,
+                                          int tid, int n, int bar) {
+  const int lane = tid & 31;
   const int mine = tid < P ? __ldg(ids + tid) : -1;  // under way while the counts are cleared
-  for (int e = tid; e < E; e += blockDim.x) s.cnt[e] = 0;
-  __syncthreads();
+  for (int e = tid; e < E; e += n) s.cnt[e] = 0;
+  tc_sync(bar, n);
   if (mine >= 0 && mine < E) atomicAdd(&s.cnt[mine], 1);
-  for (int i = tid + blockDim.x; i < P; i += blockDim.x) {
+  for (int i = tid + n; i < P; i += n) {
     const int e = __ldg(ids + i);
     if (e >= 0 && e < E) atomicAdd(&s.cnt[e], 1);
   }
-  __syncthreads();
+  tc_sync(bar, n);
   if (tid < 32) {
     // lane l takes `per` consecutive experts
     const int per = (E + 31) / 32, e0 = min(lane * per, E), e1 = min(e0 + per, E);
     int both = 0;  // pairs | tiles << 16: at most 4096 of either
     for (int e = e0; e < e1; ++e) {
-      const int n = s.cnt[e];
-      both += n | ((n + cap - 1) / cap) << 16;
+      const int c = s.cnt[e];
+      both += c | ((c + cap - 1) / cap) << 16;
     }
     int incl = both;
 #pragma unroll
@@ -87,15 +99,15 @@ __device__ __forceinline__ void tc_tables(const int32_t* ids, int P, int E, int 
     }
     int off = (incl - both) & 0xFFFF, tiles = (incl - both) >> 16;
     for (int e = e0; e < e1; ++e) {
-      const int n = s.cnt[e];
-      s.off[e] = off;
-      s.tile[e] = tiles;
-      off += n;
-      tiles += (n + cap - 1) / cap;
+      const int c = s.cnt[e];
+      s.off[e] = (uint16_t)off;
+      s.tile[e] = (uint16_t)tiles;
+      off += c;
+      tiles += (c + cap - 1) / cap;
     }
-    if (lane == 31) s.tile[E] = tiles;
+    if (lane == 31) s.tile[E] = (uint16_t)tiles;
   }
-  __syncthreads();
+  tc_sync(bar, n);
 }
 
 __device__ __forceinline__ TcTile tc_tile(const TcTables& s, int E, int cap, int t) {
@@ -143,63 +155,66 @@ __host__ __device__ __forceinline__ int tc_owner(int64_t S, int64_t x, int64_t G
 __device__ __forceinline__ int tc_slot(int b, bool opened) { return 2 * b + (opened ? 1 : 0); }
 
 // ------------------------------------------------------------ pieces
-// One warp: the pieces of 8 x 32 consecutive values v (this lane: 8 lane ..,
-// already times the row's power of two) of one stage, to the pairs dst[0, n).
-// They are gathered in the warp's kSplitBytes of shared memory and written
-// from there in 16-byte pieces; the loop is kept rolled, because this runs
-// once and cold (unrolled, instruction fetch took longer than the work).
-constexpr int kSplitBytes = kTcPairStage + kPieces * 16;
+// A stage of a row, split: kSplitBytes of a warp's shared memory, [piece][128
+// bytes of codes] and [piece][16 scales].  The loop is kept rolled, because
+// this runs once and cold (unrolled, instruction fetch took longer than the
+// work).  v: this lane's values 8 lane .. of the stage, already times the row's
+// power of two.
+constexpr int kSplitBytes = kPieces * (kTcRow + 16);
 
-__device__ __forceinline__ void tc_split(float (&v)[8], int stage, const TcPlace* dst, int n,
-                                         int pieces, int P, int tiles_max, uint8_t* act,
-                                         uint8_t* sf, uint8_t* buf) {
+__device__ __forceinline__ void tc_split(float (&v)[8], int pieces, uint8_t* buf) {
   const int lane = threadIdx.x & 31;
-  uint8_t* scales = buf + kTcPairStage;  // [piece][16 blocks]
-  __syncwarp();
+  uint8_t* scales = buf + kPieces * kTcRow;
 #pragma unroll 1
-  for (int p = 0; p < kPieces; ++p) {
-    uint32_t w = 0u, s8 = 0u;
-    if (p < pieces) {
-      float a = fmaxf(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))),
-                      fmaxf(fmaxf(fabsf(v[4]), fabsf(v[5])), fmaxf(fabsf(v[6]), fabsf(v[7]))));
-      a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1));  // the block's other half
-      s8 = __nv_cvt_float_to_fp8(a * (1.0f / 6.0f), __NV_SATFINITE, __NV_E4M3);
-      const float s =
-          __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)s8, __NV_E4M3)));
-      // a quotient one ulp off may take the neighbouring code: its error is
-      // in the residual like any other
-      const float inv = s == 0.0f ? 0.0f : __fdividef(1.0f, s);
-      float q[8];
+  for (int p = 0; p < pieces; ++p) {
+    float a = fmaxf(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))),
+                    fmaxf(fmaxf(fabsf(v[4]), fabsf(v[5])), fmaxf(fabsf(v[6]), fabsf(v[7]))));
+    a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1));  // the block's other half
+    const uint32_t s8 = __nv_cvt_float_to_fp8(a * (1.0f / 6.0f), __NV_SATFINITE, __NV_E4M3);
+    const float s =
+        __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)s8, __NV_E4M3)));
+    // a quotient one ulp off may take the neighbouring code: its error is in
+    // the residual like any other
+    const float inv = s == 0.0f ? 0.0f : __fdividef(1.0f, s);
+    float q[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] = v[i] * inv;
-      w = cvt_e2m1x8_signed(q);
-      uint32_t h[4];
-      e2m1x8_to_f16(w, h);
+    for (int i = 0; i < 8; ++i) q[i] = v[i] * inv;
+    const uint32_t w = cvt_e2m1x8_signed(q);
+    uint32_t h[4];
+    e2m1x8_to_f16(w, h);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-        v[2 * i] = __fmaf_rn(-f.x, s, v[2 * i]);
-        v[2 * i + 1] = __fmaf_rn(-f.y, s, v[2 * i + 1]);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+      v[2 * i] = __fmaf_rn(-f.x, s, v[2 * i]);
+      v[2 * i + 1] = __fmaf_rn(-f.y, s, v[2 * i + 1]);
     }
-    // rows of 128 bytes, 16-byte pieces swizzled by the row
-    *reinterpret_cast<uint32_t*>(buf + p * 128 + (((lane >> 2) ^ p) << 4) + ((lane & 3) << 2)) = w;
+    reinterpret_cast<uint32_t*>(buf + p * kTcRow)[lane] = w;
     if ((lane & 1) == 0) scales[p * 16 + (lane >> 1)] = (uint8_t)s8;
   }
   __syncwarp();
-  const uint4 lo = reinterpret_cast<const uint4*>(buf)[lane];
-  const uint4 hi = reinterpret_cast<const uint4*>(buf)[lane + 32];
-  const uint32_t sw = reinterpret_cast<const uint32_t*>(scales)[(lane & 7) * 4 + (lane >> 3)];
-  for (int j = 0; j < n; ++j) {
-    const TcPlace d = dst[j];
-    uint4* to = reinterpret_cast<uint4*>(act + ((int64_t)stage * P + d.place) * kTcPairStage) + lane;
-    to[0] = lo;
-    to[32] = hi;
-    // atom lane / 8, the tile's rows 8 d.col ..: row 32 a + b at b 16 + a 4
-    *reinterpret_cast<uint32_t*>(sf + ((int64_t)stage * tiles_max + d.tile) * kTcSfStage +
-                                 (lane >> 3) * 512 + ((d.col & 3) * 8 + (lane & 7)) * 16 +
-                                 (d.col >> 2) * 4) = sw;
+}
+
+// One warp: a split stage to where the products read it, for the pair at d.
+// Row n = pieces x d.col + p of the tile: 128 bytes in 16-byte pieces swizzled
+// by the row (the MMA's 128-byte layout); its scales, row 32 a + b of atom j,
+// at byte b 16 + a 4 of the atom.
+__device__ __forceinline__ void tc_place(const uint8_t* buf, int pieces, int stage, const TcPlace& d,
+                                         int P, int tiles_max, uint8_t* act, uint8_t* sf) {
+  const int lane = threadIdx.x & 31;
+  const int n0 = pieces * d.col;
+  uint8_t* to = act + ((int64_t)stage * P + d.place) * pieces * kTcRow;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {  // eight lanes a row, four rows at a time
+    const int p = 4 * i + (lane >> 3), c = lane & 7;
+    if (p < pieces)
+      *reinterpret_cast<uint4*>(to + p * kTcRow + ((c ^ ((n0 + p) & 7)) << 4)) =
+          *reinterpret_cast<const uint4*>(buf + p * kTcRow + c * 16);
   }
+  const int p = lane & 7, n = n0 + p;
+  if (p < pieces)
+    *reinterpret_cast<uint32_t*>(sf + ((int64_t)stage * tiles_max + d.tile) * kTcSfStage +
+                                 (lane >> 3) * 512 + (n & 31) * 16 + (n >> 5) * 4) =
+        reinterpret_cast<const uint32_t*>(buf + kPieces * kTcRow)[p * 4 + (lane >> 3)];
 }
 
 // The power of two that takes a row's largest magnitude (bits mx) to 2^10 ..,
@@ -211,70 +226,30 @@ __device__ __forceinline__ float tc_scale(uint32_t mx, float& undo) {
 }
 
 // ------------------------------------------------------------ prep
-constexpr int kPrepThreads = 256;
+// Half of the CTA splits the token's row while the other half finds where its
+// pairs go.
+constexpr int kPrepHalf = 256;
 
-__global__ void __launch_bounds__(kPrepThreads) moe_prep_kernel(const TcArgs p) {
+__global__ void __launch_bounds__(2 * kPrepHalf) moe_prep_kernel(const TcArgs p) {
+  constexpr int kWarps = kPrepHalf / 32;
   __shared__ TcTables s_tab;
+  __shared__ __align__(16) uint8_t s_buf[kWarps][kSplitBytes];
   __shared__ TcPlace s_dst[kTcMaxK];
-  __shared__ __align__(16) uint8_t s_buf[kPrepThreads / 32][kSplitBytes];
   __shared__ int s_n;
   __shared__ uint32_t s_max;
   grid_dependency_wait();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int m = blockIdx.x, n_stages = (p.H + 255) / 256;
-  if (tid == 0) {
-    s_n = 0;
-    s_max = 0u;
-  }
-  // the row's largest magnitude: this warp's stages warp, warp + 8, ..
-  constexpr int kWarps = kPrepThreads / 32;
+  const int lane = threadIdx.x & 31, m = blockIdx.x;
+  const bool splits = threadIdx.x < kPrepHalf;
+  const int tid = splits ? threadIdx.x : threadIdx.x - kPrepHalf, warp = tid >> 5;
+  const int n_stages = (p.H + 255) / 256;
   const uint4* row = reinterpret_cast<const uint4*>(p.x + (int64_t)m * p.H);
   auto load = [&](int s) {
     const int i = 32 * s + lane;
     return i < p.H / 8 ? __ldg(row + i) : make_uint4(0u, 0u, 0u, 0u);
   };
-  uint32_t mx = 0;
-  for (int s = warp; s < n_stages; s += kWarps) {
-    const uint4 r = load(s);
-    const uint32_t c = __vmaxu2(__vmaxu2(r.x & 0x7FFF7FFFu, r.y & 0x7FFF7FFFu),
-                                __vmaxu2(r.z & 0x7FFF7FFFu, r.w & 0x7FFF7FFFu));
-    mx = max(mx, max(c & 0xFFFFu, c >> 16));
-  }
-  // the place of pair i is its rank among its expert's; this warp's slots are
-  // j = warp, warp + 8, .., lane j / 8 keeping slot j's
-  int my_e = -1, my_rank = 0;
-  for (int j = warp; j < p.k; j += kWarps) {
-    const int i = m * p.k + j, e = __ldg(p.ids + i);
-    int rank = 0;
-    for (int b = lane; b < i; b += 32) rank += __ldg(p.ids + b) == e ? 1 : 0;
-    rank = __reduce_add_sync(0xFFFFFFFFu, rank);
-    if (lane == j / kWarps) {
-      my_e = e;
-      my_rank = rank;
-    }
-  }
-  tc_tables(p.ids, p.P, p.E, p.cap, s_tab);
-  mx = __reduce_max_sync(0xFFFFFFFFu, mx);
-  if (lane == 0) atomicMax(&s_max, mx << 16);
-  if (m == 0 && tid == 0) {
-    *p.status = NVFP4_OK;
-    *p.counts = make_int2(s_tab.off[p.E - 1] + s_tab.cnt[p.E - 1], s_tab.tile[p.E]);
-  }
-  if (warp + kWarps * lane < p.k) {
-    TcPlace d{0, 0, 0, -1};
-    if (my_e >= 0 && my_e < p.E) {
-      d = {my_e, s_tab.tile[my_e] + my_rank / p.cap, my_rank % p.cap, s_tab.off[my_e] + my_rank};
-      p.by_place[d.place] = d;
-      s_dst[atomicAdd(&s_n, 1)] = d;
-    }
-    p.by_pair[m * p.k + warp + kWarps * lane] = d;
-  }
-  __syncthreads();
-  float undo;
-  const float up = tc_scale(s_max, undo);
-  if (tid < s_n) p.mul1[s_dst[tid].place] = undo;
-  for (int s = warp; s < n_stages; s += kWarps) {
+  float up = 0.0f, undo = 0.0f;
+  auto split = [&](int s) {
     const uint4 r = load(s);
     const uint32_t u[4] = {r.x, r.y, r.z, r.w};
     float v[8];
@@ -283,7 +258,67 @@ __global__ void __launch_bounds__(kPrepThreads) moe_prep_kernel(const TcArgs p) 
       v[2 * q] = __uint_as_float(u[q] << 16) * up;
       v[2 * q + 1] = __uint_as_float(u[q] & 0xFFFF0000u) * up;
     }
-    tc_split(v, s, s_dst, s_n, p.pieces, p.P, p.tiles_max, p.act1, p.sf1, s_buf[warp]);
+    tc_split(v, p.pieces, s_buf[warp]);
+  };
+  if (splits) {
+    // stages warp, warp + 8, ..; the first of them is split ahead of the places
+    uint32_t mx = 0;
+    for (int s = warp; s < n_stages; s += kWarps) {
+      const uint4 r = load(s);
+      const uint32_t c = __vmaxu2(__vmaxu2(r.x & 0x7FFF7FFFu, r.y & 0x7FFF7FFFu),
+                                  __vmaxu2(r.z & 0x7FFF7FFFu, r.w & 0x7FFF7FFFu));
+      mx = max(mx, max(c & 0xFFFFu, c >> 16));
+    }
+    mx = __reduce_max_sync(0xFFFFFFFFu, mx);
+    if (tid == 0) s_max = 0u;
+    tc_sync(1, kPrepHalf);
+    if (lane == 0) atomicMax(&s_max, mx << 16);
+    tc_sync(1, kPrepHalf);
+    up = tc_scale(s_max, undo);
+    if (warp < n_stages) split(warp);
+  } else {
+    if (tid == 0) s_n = 0;
+    // the place of pair i is its rank among its expert's; this warp's slots are
+    // j = warp, warp + 8, .., lane j / 8 keeping slot j's
+    int my_e = -1, my_rank = 0;
+    for (int j = warp; j < p.k; j += kWarps) {
+      const int i = m * p.k + j, e = __ldg(p.ids + i);
+      int rank = 0;
+      for (int b = lane; b < i; b += 32) rank += __ldg(p.ids + b) == e ? 1 : 0;
+      rank = __reduce_add_sync(0xFFFFFFFFu, rank);
+      if (lane == j / kWarps) {
+        my_e = e;
+        my_rank = rank;
+      }
+    }
+    tc_tables(p.ids, p.P, p.E, p.cap, s_tab, tid, kPrepHalf, 2);
+    if (m == 0 && tid == 0) {
+      *p.status = NVFP4_OK;
+      *p.counts = make_int2(s_tab.off[p.E - 1] + s_tab.cnt[p.E - 1], s_tab.tile[p.E]);
+    }
+    if (warp + kWarps * lane < p.k) {
+      TcPlace d{0, 0, 0, -1};
+      if (my_e >= 0 && my_e < p.E) {
+        d = {my_e, s_tab.tile[my_e] + my_rank / p.cap, my_rank % p.cap, s_tab.off[my_e] + my_rank};
+        p.by_place[d.place] = d;
+        s_dst[atomicAdd(&s_n, 1)] = d;
+      }
+      p.by_pair[m * p.k + warp + kWarps * lane] = d;
+    }
+  }
+  __syncthreads();
+  // every warp places: the halves take alternate pairs of a split stage
+  const int n_dst = s_n, first = splits ? 0 : 1;
+  if (splits && tid < n_dst) p.mul1[s_dst[tid].place] = undo;
+  for (int s = warp; s - warp < n_stages; s += kWarps) {
+    if (s < n_stages)
+      for (int j = first; j < n_dst; j += 2)
+        tc_place(s_buf[warp], p.pieces, s, s_dst[j], p.P, p.tiles_max, p.act1, p.sf1);
+    if (s - warp + kWarps < n_stages) {  // the next round (block-uniform)
+      __syncthreads();
+      if (splits && s + kWarps < n_stages) split(s + kWarps);
+      __syncthreads();
+    }
   }
 }
 
@@ -292,7 +327,7 @@ struct TcGemm {
   const int32_t* ids;
   const uint8_t *codes, *scales;
   int64_t rows;  // E N: rows of the whole tensor
-  int N, K, E, cap, ring, P, tiles_max;
+  int N, K, E, cap, pieces, ring, P, tiles_max;
   int unit_scales;  // buffers for the scales of a unit's 128 rows; 0: a stage's at a time
   const uint8_t *act, *sf;
   const float* mul;
@@ -304,7 +339,7 @@ struct TcGemm {
 // 3 activations, 4-7 epilogue, 8-11 scale layout, then the code loaders.
 constexpr int kTcScaleWarps = 4;
 constexpr int kTcThreads = 32 * (8 + kTcScaleWarps);
-constexpr int kTcLoaderWarps = 8;     // where TMA cannot read the code rows
+constexpr int kTcLoaderWarps = 4;     // where TMA cannot read the code rows
 constexpr int kTcLoaderDepth = 3;     // stages a loader keeps in flight (the ring has 4 or more)
 constexpr int kTcMaxUnits = 8;        // unit buffers of scales
 
@@ -352,19 +387,59 @@ __device__ __forceinline__ uint4 tc_lds16(uint32_t addr, int valid, bool aligned
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// The MMA's columns of a tile of n pairs (16 are its step), and the bytes of
+// a full tile's stage (whole 8-row swizzle atoms).
+__host__ __device__ __forceinline__ uint32_t tc_cols(int n, int pieces) {
+  return (uint32_t)(n * pieces + 15) / 16 * 16;
+}
+__host__ __device__ __forceinline__ uint32_t tc_b_stage(int cap, int pieces) {
+  return tc_cols(cap, pieces) * kTcRow;
+}
+
 __host__ __device__ __forceinline__ uint32_t tc_unit_bytes(int K) {
   return (uint32_t)align_up((size_t)128 * (K / 16) + 16, 128);
 }
 
+// An epilogue thread's row of a tile's n pairs, four at a time:
+// out[c stride] = the sum of pair c's kNp columns, from the smallest
+// piece up, times its multiplier (lane c's mul).
+template <int kNp>
+__device__ __forceinline__ void tc_drain(uint32_t taddr, int n, float mul, bool store, float* out,
+                                         int64_t stride) {
+  constexpr int kAt = 4, kLoads = kAt * kNp / 8;
+  static_assert(kAt * kNp % 8 == 0, "whole 8-column loads");
+  for (int c = 0; c < n; c += kAt) {
+    uint32_t v[kLoads][8];
+    const int cols = min(kAt, n - c) * kNp;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      if (8 * i < cols) tmem_ld8(taddr + c * kNp + 8 * i, v[i]);
+    tc_wait_ld();
+#pragma unroll
+    for (int h = 0; h < kAt; ++h) {
+      const float m = __shfl_sync(0xFFFFFFFFu, mul, (c + h) & 31);
+      if (c + h < n && store) {
+        float sum = __uint_as_float(v[(h * kNp + kNp - 1) / 8][(h * kNp + kNp - 1) % 8]);
+#pragma unroll
+        for (int q = kNp - 2; q >= 0; --q)
+          sum += __uint_as_float(v[(h * kNp + q) / 8][(h * kNp + q) % 8]);
+        out[(c + h) * stride] = sum * m;
+      }
+    }
+  }
+}
+
+// Registers: at most 112, so that a CTA of the prep kernel fits beside one of
+// a product (the bound names more threads than there are).
 template <bool kTma>
-__global__ void __launch_bounds__(kTcThreads + (kTma ? 0 : 32 * kTcLoaderWarps), 1)
+__global__ void __launch_bounds__(576, 1)
     moe_tc_kernel(const __grid_constant__ CUtensorMap tm_w,
                   const __grid_constant__ CUtensorMap tm_s, const TcGemm p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   const int ring = p.ring;
-  const uint32_t b_stage = (uint32_t)p.cap * kTcPairStage;
+  const uint32_t b_stage = tc_b_stage(p.cap, p.pieces);
   uint8_t* s_a = smem;
   uint8_t* s_b = s_a + ring * kTcAStage;
   uint8_t* s_sfa = s_b + ring * b_stage;
@@ -404,7 +479,7 @@ __global__ void __launch_bounds__(kTcThreads + (kTma ? 0 : 32 * kTcLoaderWarps),
   }
   // The expert ids were complete before the kernel ahead of this one let it
   // start; its own results are waited for where they are read.
-  tc_tables(p.ids, p.P, p.E, p.cap, s_tab);
+  tc_tables(p.ids, p.P, p.E, p.cap, s_tab, threadIdx.x, blockDim.x, 0);
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, tmem_slot, 0);
   const WaitCtl wc{p.status, abort_flag, kWaitLimitNs};
@@ -466,9 +541,9 @@ __global__ void __launch_bounds__(kTcThreads + (kTma ? 0 : 32 * kTcLoaderWarps),
         const uint32_t st = issued % ring, ph = (issued / ring) & 1;
         if (!warp_wait(&empty[st], ph ^ 1, wc)) return false;
         if (elect_one()) {
-          const uint32_t bytes = (uint32_t)t.n * kTcPairStage;
+          const uint32_t bytes = (uint32_t)t.n * p.pieces * kTcRow;
           mbar_arrive_expect_tx(&full[st], bytes + kTcSfStage);
-          bulk_load(s_b + st * b_stage, p.act + ((int64_t)kb * p.P + t.first) * kTcPairStage, bytes,
+          bulk_load(s_b + st * b_stage, p.act + ((int64_t)kb * p.P + t.first) * p.pieces * kTcRow, bytes,
                     &full[st], keep);
           bulk_load(s_sfb + st * kTcSfStage, p.sf + ((int64_t)kb * p.tiles_max + pc.tile) * kTcSfStage,
                     kTcSfStage, &full[st], keep);
@@ -501,15 +576,15 @@ __global__ void __launch_bounds__(kTcThreads + (kTma ? 0 : 32 * kTcLoaderWarps),
   } else if (warp == 1) {
     // ---------------- scales into TMEM, then one MMA per 64 k
     const uint64_t ad0 = smem_desc_sw128(smem_u32(s_a)), bd0 = smem_desc_sw128(smem_u32(s_b));
-    const uint32_t n_cols = (uint32_t)p.cap * kPieces;
+    const uint32_t n_cols = tc_cols(p.cap, p.pieces);
     const uint32_t sf_base = tmem + 2 * n_cols;
     uint32_t g = 0;
     int i = 0;
     tc_pieces(x0, x1, n_st, RT, [&](const TcPiece& pc) {
       const TcTile t = tile_at(pc.tile);
-      // 16 columns are the MMA's step: an odd pair count computes 8 that
-      // nobody reads
-      const uint32_t idesc = idesc_e2m1_bs((uint32_t)((t.n * kPieces + 15) / 16 * 16));
+      // (columns past the tile's are computed from what the slot held before,
+      // and read by nobody)
+      const uint32_t idesc = idesc_e2m1_bs(tc_cols(t.n, p.pieces));
       const uint32_t buf = i & 1, dph = (i >> 1) & 1;
       ++i;
       if (!warp_wait(&d_empty[buf], dph ^ 1, wc)) return false;
@@ -577,24 +652,11 @@ __global__ void __launch_bounds__(kTcThreads + (kTma ? 0 : 32 * kTcLoaderWarps),
         out = p.part + (int64_t)tc_slot(blockIdx.x, pc.kb0 == 0) * p.cap * 128 + row;
         stride = 128;
       }
-      const uint32_t d = tmem + buf * (uint32_t)p.cap * kPieces + lane_off;
-      for (int c = 0; c < t.n; c += 4) {
-        uint32_t v[2][16];
-        tmem_ld16(d + c * kPieces, v[0]);
-        if (c + 2 < t.n) tmem_ld16(d + (c + 2) * kPieces, v[1]);
-        tc_wait_ld();
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const float m = __shfl_sync(0xFFFFFFFFu, mul, (c + h) & 31);
-          if (c + h < t.n && n < p.N) {
-            // the pieces from the smallest up
-            float sum = __uint_as_float(v[h >> 1][8 * (h & 1) + 7]);
-#pragma unroll
-            for (int q = 6; q >= 0; --q) sum += __uint_as_float(v[h >> 1][8 * (h & 1) + q]);
-            out[(c + h) * stride] = sum * m;
-          }
-        }
-      }
+      const uint32_t d = tmem + buf * tc_cols(p.cap, p.pieces) + lane_off;
+      if (p.pieces == kPiecesBf16)
+        tc_drain<kPiecesBf16>(d, t.n, mul, n < p.N, out, stride);
+      else
+        tc_drain<kPieces>(d, t.n, mul, n < p.N, out, stride);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&d_empty[buf]);
@@ -780,13 +842,15 @@ __global__ void __launch_bounds__(kActMaxThreads) moe_act_kernel(const TcArgs p)
   const float up = tc_scale(s_max, undo);
   if (tid == 0) p.mul2[q] = undo;
   const int stages = (p.I + 255) / 256;
+  uint8_t* buf = s_act_mem + warp * kSplitBytes;
   for (int s = warp; s < stages; s += n_threads / 32) {
     const int k0 = 256 * s + 8 * lane;
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = k0 < p.I ? s_h[k0 + i] * up : 0.0f;
-    tc_split(v, s, &s_dst, 1, p.pieces, p.P, p.tiles_max, p.act2, p.sf2,
-             s_act_mem + warp * kSplitBytes);
+    __syncwarp();
+    tc_split(v, p.pieces, buf);
+    tc_place(buf, p.pieces, s, s_dst, p.P, p.tiles_max, p.act2, p.sf2);
   }
 }
 
@@ -871,16 +935,19 @@ struct TcLayout {
   int tiles_max;
 };
 
-// Pairs of a tile: 8 (the MMA's columns: 64) where no expert can have more
-// without repeating a token, else 16.
-static int tc_cap(int64_t M) { return M <= 8 ? 8 : 16; }
+// Pairs of a tile: 8 where no expert has more (unless a token names it
+// twice), 16 where few do, else what 128 columns hold: a second tile of an
+// expert reads its weights again, from L2, but in as many steps as the first.
+static int tc_cap(int64_t P, int64_t M, int64_t E, int pieces) {
+  return M <= 8 ? 8 : P <= 6 * E ? 16 : std::min(128 / pieces, kTcMaxCap);
+}
 
 static TcLayout tc_layout(int64_t M, int64_t k, int64_t H, int64_t I, int sms) {
-  const int64_t P = M * k, cap = tc_cap(M);
+  const int64_t P = M * k, cap = kTcMaxCap;  // either size of tile
   const int64_t st1 = (H + 255) / 256, st2 = (I + 255) / 256;
   TcLayout L;
   // every tile but one per expert is full
-  L.tiles_max = (int)(std::min<int64_t>(P, kTcMaxExperts) + P / cap);
+  L.tiles_max = (int)(std::min<int64_t>(P, kTcMaxExperts) + P / 8);
   size_t at = kWsHeader;
   auto put = [&](size_t bytes) {
     const size_t here = at;
@@ -894,8 +961,8 @@ static TcLayout tc_layout(int64_t M, int64_t k, int64_t H, int64_t I, int sms) {
   L.mul2 = put((size_t)P * 4);
   L.sf1 = put((size_t)st1 * L.tiles_max * kTcSfStage);
   L.sf2 = put((size_t)st2 * L.tiles_max * kTcSfStage);
-  L.act1 = put((size_t)st1 * P * kTcPairStage);
-  L.act2 = put((size_t)st2 * P * kTcPairStage);
+  L.act1 = put((size_t)st1 * P * kPieces * kTcRow);
+  L.act2 = put((size_t)st2 * P * kPieces * kTcRow);
   L.gu = put((size_t)P * 2 * I * 4);
   L.y = put((size_t)P * H * 4);
   L.part1 = put((size_t)2 * sms * cap * 128 * 4);
@@ -915,6 +982,21 @@ bool moe_tc_takes(int64_t k, int64_t H, int64_t I) {
   return k <= kTcMaxK && tc_k_ok(H) && tc_k_ok(I);
 }
 
+// The small kernels ask for the shared-memory split of the products: an SM
+// changes its split only when it is idle, so a product's CTA could not start
+// beside one of them, or had to wait for the change.
+static cudaError_t tc_carveout_once(std::atomic<uint64_t>& done, const void* kern) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                           cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess && bit) done.fetch_or(bit, std::memory_order_acq_rel);
+  return e;
+}
+
 static cudaError_t tc_gemm_launch(TcGemm g, int grid, cudaStream_t stream) {
   CUtensorMap tm = {}, tm_s = {};
   const bool tma = g.K % 32 == 0;  // the code rows' stride for TMA
@@ -930,16 +1012,17 @@ static cudaError_t tc_gemm_launch(TcGemm g, int grid, cudaStream_t stream) {
       !encode_2d(&tm_s, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.scales, (uint64_t)g.K / 16,
                  (uint64_t)g.rows, (uint64_t)g.K / 16, 16, 128, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorUnknown;
-  // 28 to 38 KB a stage beside two units' scales: 4 to 7 stages
-  const size_t stage = kTcAStage + (size_t)g.cap * kTcPairStage +
-                       (g.unit_scales ? 2 : 3) * (size_t)kTcSfStage;
+  // 26 to 38 KB a stage beside the units' scales: 4 to 7 stages
+  const size_t stage =
+      kTcAStage + tc_b_stage(g.cap, g.pieces) + (g.unit_scales ? 2 : 3) * (size_t)kTcSfStage;
+  const size_t budget = g.cap <= 16 ? kTcSmem : kTcSmemLarge;
   const size_t units = g.unit_scales * (size_t)tc_unit_bytes(g.K);
-  g.ring = (int)std::min<size_t>((kTcSmem - 1024 - units) / stage, kTcMaxRing);
+  g.ring = (int)std::min<size_t>((budget - 1024 - units) / stage, kTcMaxRing);
   const size_t smem = 1024 + units + (size_t)g.ring * stage;
   static std::atomic<uint64_t> limit_set[2];
   auto kern = tma ? moe_tc_kernel<true> : moe_tc_kernel<false>;
   const cudaError_t err =
-      smem_limit_once(limit_set[tma], reinterpret_cast<const void*>(kern), kTcSmem);
+      smem_limit_once(limit_set[tma], reinterpret_cast<const void*>(kern), kTcSmemLarge);
   if (err != cudaSuccess) return err;
   PdlLaunch l(dim3((unsigned)grid), dim3(kTcThreads + (tma ? 0 : 32 * kTcLoaderWarps)), smem, stream);
   return cudaLaunchKernelEx(&l.cfg, kern, tm, tm_s, g);
@@ -967,10 +1050,10 @@ nvfp4_status moe_tc_launch(const void* x, int64_t M, int64_t k, int64_t H, int64
   a.I = (int)I;
   a.E = (int)E;
   a.P = (int)(M * k);
-  a.cap = tc_cap(M);
   a.tiles_max = L.tiles_max;
   a.grid = sms;
   a.pieces = out_dtype == NVFP4_OUT_BF16 ? kPiecesBf16 : kPieces;
+  a.cap = tc_cap(M * k, M, E, a.pieces);
   a.counts = reinterpret_cast<int2*>(ws + L.counts);
   a.by_pair = reinterpret_cast<TcPlace*>(ws + L.by_pair);
   a.by_place = reinterpret_cast<TcPlace*>(ws + L.by_place);
@@ -988,6 +1071,7 @@ nvfp4_status moe_tc_launch(const void* x, int64_t M, int64_t k, int64_t H, int64
 
   TcGemm g = {};
   g.cap = a.cap;
+  g.pieces = a.pieces;
   g.ids = ids;
   g.E = a.E;
   g.P = a.P;
@@ -1017,8 +1101,10 @@ nvfp4_status moe_tc_launch(const void* x, int64_t M, int64_t k, int64_t H, int64
 
   cudaError_t err;
   {
-    PdlLaunch l(dim3((unsigned)M), dim3(kPrepThreads), 0, stream);
-    err = cudaLaunchKernelEx(&l.cfg, moe_prep_kernel, a);
+    static std::atomic<uint64_t> split_set{0};
+    err = tc_carveout_once(split_set, reinterpret_cast<const void*>(moe_prep_kernel));
+    PdlLaunch l(dim3((unsigned)M), dim3(2 * kPrepHalf), 0, stream);
+    if (err == cudaSuccess) err = cudaLaunchKernelEx(&l.cfg, moe_prep_kernel, a);
   }
   if (err == cudaSuccess) err = tc_gemm_launch(g1, sms, stream);
   if (err == cudaSuccess) {
@@ -1030,6 +1116,9 @@ nvfp4_status moe_tc_launch(const void* x, int64_t M, int64_t k, int64_t H, int64
     static std::atomic<uint64_t> limit_set{0};
     err = smem_limit_once(limit_set, reinterpret_cast<const void*>(moe_act_kernel),
                           bytes(NVFP4_MOE_MAX_DIM));
+    static std::atomic<uint64_t> split_set{0};
+    if (err == cudaSuccess)
+      err = tc_carveout_once(split_set, reinterpret_cast<const void*>(moe_act_kernel));
     if (err == cudaSuccess) {
       PdlLaunch l(dim3((unsigned)a.P), dim3(act_threads(I)), smem, stream);
       err = cudaLaunchKernelEx(&l.cfg, moe_act_kernel, a);
@@ -1038,9 +1127,12 @@ nvfp4_status moe_tc_launch(const void* x, int64_t M, int64_t k, int64_t H, int64
   if (err == cudaSuccess) err = tc_gemm_launch(g2a, sms, stream);
   if (err == cudaSuccess) {
     const int RT = (int)((H + 127) / 128);
+    const bool bf16 = out_dtype == NVFP4_OUT_BF16;
+    auto kern = bf16 ? moe_tc_combine_kernel<true> : moe_tc_combine_kernel<false>;
+    static std::atomic<uint64_t> split_set[2];
+    err = tc_carveout_once(split_set[bf16], reinterpret_cast<const void*>(kern));
     PdlLaunch l(dim3((unsigned)((RT + 7) / 8), (unsigned)M), dim3(256), 0, stream);
-    err = out_dtype == NVFP4_OUT_BF16 ? cudaLaunchKernelEx(&l.cfg, moe_tc_combine_kernel<true>, a)
-                                      : cudaLaunchKernelEx(&l.cfg, moe_tc_combine_kernel<false>, a);
+    if (err == cudaSuccess) err = cudaLaunchKernelEx(&l.cfg, kern, a);
   }
   return err == cudaSuccess && cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
