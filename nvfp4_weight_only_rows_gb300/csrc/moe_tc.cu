@@ -340,7 +340,6 @@ struct TcGemm {
 constexpr int kTcScaleWarps = 4;
 constexpr int kTcThreads = 32 * (8 + kTcScaleWarps);
 constexpr int kTcLoaderWarps = 4;     // where TMA cannot read the code rows
-constexpr int kTcLoaderDepth = 3;     // stages a loader keeps in flight (the ring has 4 or more)
 constexpr int kTcMaxUnits = 8;        // unit buffers of scales
 
 struct TcPiece {
@@ -704,7 +703,7 @@ __global__ void __launch_bounds__(576, 1)
       raise_status(p.status, NVFP4_ERR_NONFINITE);
   } else if constexpr (!kTma) {
     // ---------------- weight codes in 8-byte pieces (rows that are not a
-    // 16-byte multiple), kTcLoaderDepth stages in flight
+    // 16-byte multiple)
     constexpr int kRowsAt = kTcLoaderWarps * 2;  // rows of one round: 16 lanes a row
     const int tid = threadIdx.x - kTcThreads;
     const int64_t rb = p.K / 2;
@@ -737,9 +736,16 @@ __global__ void __launch_bounds__(576, 1)
                        : "memory");
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-        if (it + 1 >= (uint32_t)kTcLoaderDepth) {
-          asm volatile("cp.async.wait_group %0;" ::"n"(kTcLoaderDepth - 1) : "memory");
-          land();
+        // all but one of the ring's stages stay in flight (it has 4 or more)
+        if (ring >= 6) {
+          asm volatile("cp.async.wait_group 4;" ::: "memory");
+          if (it >= 4) land();
+        } else if (ring == 5) {
+          asm volatile("cp.async.wait_group 3;" ::: "memory");
+          if (it >= 3) land();
+        } else {
+          asm volatile("cp.async.wait_group 2;" ::: "memory");
+          if (it >= 2) land();
         }
       }
       return true;
@@ -770,6 +776,11 @@ __device__ __forceinline__ TcSpan tc_span(int64_t S, int grid, int n_st, int RT,
 // one round trip.
 constexpr int kActMaxThreads = 768;
 static int act_threads(int64_t I) { return I <= 1024 ? 256 : I <= 2048 ? 512 : kActMaxThreads; }
+// The warps that split the pair's stages.
+__host__ __device__ __forceinline__ int act_split_warps(int64_t I, int threads) {
+  const int64_t stages = (I + 255) / 256;
+  return (int)(stages < threads / 32 ? stages : threads / 32);
+}
 
 __global__ void __launch_bounds__(kActMaxThreads) moe_act_kernel(const TcArgs p) {
   // a split buffer a warp, I values, the spans of the 2I / 128 row tiles
@@ -779,7 +790,7 @@ __global__ void __launch_bounds__(kActMaxThreads) moe_act_kernel(const TcArgs p)
   const int n_threads = blockDim.x;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int N = 2 * p.I, RT = (N + 127) / 128, n_st = (p.H + 255) / 256;
-  float* s_h = reinterpret_cast<float*>(s_act_mem + (n_threads / 32) * kSplitBytes);
+  float* s_h = reinterpret_cast<float*>(s_act_mem + act_split_warps(p.I, n_threads) * kSplitBytes);
   TcSpan* s_span = reinterpret_cast<TcSpan*>(s_h + p.I);
   // where the pair and its sums lie: written by the prep kernel, which was
   // complete before the product this kernel waits for began
@@ -797,6 +808,7 @@ __global__ void __launch_bounds__(kActMaxThreads) moe_act_kernel(const TcArgs p)
   }
   __syncthreads();
   grid_dependency_wait();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!present) return;
   const float g13 = __ldg(p.g13 + at.x);
   // four values in flight per thread; a unit that was cut has its other parts
@@ -836,8 +848,6 @@ __global__ void __launch_bounds__(kActMaxThreads) moe_act_kernel(const TcArgs p)
   mx = __reduce_max_sync(0xFFFFFFFFu, mx);
   if (lane == 0) atomicMax(&s_max, mx);
   __syncthreads();
-  // the next product's CTAs take a whole SM each: not before the loads
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   float undo;
   const float up = tc_scale(s_max, undo);
   if (tid == 0) p.mul2[q] = undo;
@@ -1000,11 +1010,11 @@ static cudaError_t tc_carveout_once(std::atomic<uint64_t>& done, const void* ker
 static cudaError_t tc_gemm_launch(TcGemm g, int grid, cudaStream_t stream) {
   CUtensorMap tm = {}, tm_s = {};
   const bool tma = g.K % 32 == 0;  // the code rows' stride for TMA
-  // two units' scales, or as many as 32 KB hold: the next unit's are asked for
+  // two units' scales, or as many as 20 KB hold: the next unit's are asked for
   // one buffer round ahead (K = 768, 64 tokens: 23 us with two)
   g.unit_scales = g.K > kTcMaxUnitK
                       ? 0
-                      : std::max(2, std::min(kTcMaxUnits, (int)((32 << 10) / tc_unit_bytes(g.K))));
+                      : std::max(2, std::min(kTcMaxUnits, (int)((20 << 10) / tc_unit_bytes(g.K))));
   if (tma && !encode_2d(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.codes, (uint64_t)g.K / 2,
                         (uint64_t)g.rows, (uint64_t)g.K / 2, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorUnknown;
@@ -1109,7 +1119,7 @@ nvfp4_status moe_tc_launch(const void* x, int64_t M, int64_t k, int64_t H, int64
   if (err == cudaSuccess) err = tc_gemm_launch(g1, sms, stream);
   if (err == cudaSuccess) {
     auto bytes = [](int64_t I) {
-      return (size_t)(act_threads(I) / 32) * kSplitBytes + (size_t)I * 4 +
+      return (size_t)act_split_warps(I, act_threads(I)) * kSplitBytes + (size_t)I * 4 +
              (size_t)((2 * I + 127) / 128) * sizeof(TcSpan);
     };
     const size_t smem = bytes(I);
