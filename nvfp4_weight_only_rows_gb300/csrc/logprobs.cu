@@ -1,12 +1,16 @@
 // logprobs.cu -- log probabilities of given tokens from a matrix of logits,
 // with entropy, rank and the top alternatives, and their gradient.
 //
-// With z = s l (s the inverse temperature) and, over the rows's N logits,
-//   S = sum exp(z - m),  T = sum (z - m) exp(z - m),   m the row maximum:
-//   lse = m + log S,  log p(t) = z_t - lse,  entropy = log S - T / S.
-// S and T merge under a new maximum m' as S' = S e, T' = e (T + (m - m') S),
-// e = exp(m - m'), so one pass over the logits keeps them per thread (fp32)
-// and a row is joined over threads, warps and the CTAs of a cluster.
+// With s the inverse temperature, c = s log2 e, m the largest of the row's
+// logits l and z = c (l - m), a power of two,
+//   S = sum 2^z,  T = sum z 2^z:   lse = s m + ln2 log2 S,
+//   log p(t) = s (l_t - m) - ln2 log2 S,  entropy = ln2 (log2 S - T / S).
+// S and T merge under a new maximum m' as S' = S e, T' = e (T + d S), d =
+// c (m - m'), e = 2^d, so one pass over the logits keeps them per thread (fp32)
+// and a row is joined over threads, warps and the CTAs of a cluster.  The
+// pass is bound by instruction issue before HBM where the logits are bf16
+// (11 instructions an element fit the copy rate): maxima and comparisons on
+// bf16 pairs, sums on fp32 pairs.
 //
 // The top k come out of the same pass: each thread also keeps the largest
 // logit it saw.  The k-th largest of those maxima bounds the row's k-th
@@ -14,6 +18,8 @@
 // can hold a logit that does, so a second look (from L2) covers about k
 // threads' shares of the row and yields a few more than k keys
 // (order key << 32 | ~index: distinct, lower index first on ties).
+#include <cuda_bf16.h>
+
 #include "gemm_common.cuh"
 
 namespace nvfp4 {
@@ -34,7 +40,7 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // exp(d) for d <= 0; a result below 2^-126 is zero
 __device__ __forceinline__ float exp_neg(float d) { return ex2(d * kLog2e); }
@@ -113,30 +119,38 @@ __device__ __forceinline__ float2 unpack2f(uint64_t v) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
   return r;
 }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
+// Two logits (bits) into the sums: z = c (x - m), S += 2^z, T += z 2^z, for
+// both at once.  m2: -m.
+__device__ __forceinline__ void lp_pair(uint32_t x0, uint32_t x1, uint64_t c2, uint64_t m2,
+                                        uint64_t& S, uint64_t& T) {
+  asm("{\n\t.reg .b64 x, d, e;\n\t.reg .f32 a, b;\n\t"
+      "mov.b64 x, {%2, %3};\n\t"
+      "add.rn.f32x2 d, x, %5;\n\t"
+      "mul.rn.f32x2 d, d, %4;\n\t"
+      "mov.b64 {a, b}, d;\n\t"
+      "ex2.approx.ftz.f32 a, a;\n\t"
+      "ex2.approx.ftz.f32 b, b;\n\t"
+      "mov.b64 e, {a, b};\n\t"
+      "add.rn.f32x2 %0, %0, e;\n\t"
+      "fma.rn.f32x2 %1, d, e, %1;\n\t}"
+      : "+l"(S), "+l"(T)
+      : "r"(x0), "r"(x1), "l"(c2), "l"(m2));
 }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 
-// Softmax state of a part of a row relative to the maximum m (scaled).
+// Softmax state of a part of a row relative to its largest logit m.
 struct LpStats {
   float m, S, T;
 };
 // ... seen from a maximum m >= a.m.  A part that vanishes adds nothing (the
 // product d S may have overflowed).
-__device__ __forceinline__ LpStats lp_shift(const LpStats& a, float m) {
-  const float d = a.m - m, e = exp_neg(d);
+__device__ __forceinline__ LpStats lp_shift(const LpStats& a, float m, float c) {
+  const float d = c * (a.m - m), e = ex2(d);
   return {m, a.S * e, e == 0.0f ? 0.0f : e * __fmaf_rn(d, a.S, a.T)};
 }
 
@@ -144,7 +158,7 @@ struct LpArgs {
   const void* logits;
   int64_t N, ld;
   const int64_t* tokens;
-  float s;
+  float s, c;  // the inverse temperature, and times log2 e
   int k;
   float *logprob, *entropy, *lse, *top_lp;
   int64_t *rank, *top_ids;
@@ -189,7 +203,7 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, unsigned long long v) 
 // (-inf) has a finite d and 0 d = 0.  What is held there has to vanish against
 // the largest logit; where it does not (a share with nothing else left, an
 // extreme temperature) the share is looked at again without the floor.
-constexpr float kFloor = -1e25f;
+constexpr float kFloor = -0x1p83f;  // also a bf16
 constexpr float kMaxScale = 1e12f;  // times the floor: finite
 
 // T: float, or uint16_t for bf16 bits; kT threads.
@@ -239,44 +253,67 @@ __global__ void __launch_bounds__(kT, 1024 / kT) logprobs_kernel(const LpArgs p)
   const float x_tok = has ? Vec<T>::load(row + tok) : __int_as_float(0x7F800000);
 
   // ---- one pass: softmax state, the largest logit, logits above the token's
-  float xmax = kFloor;
-  LpStats st{kFloor * p.s, 0.0f, 0.0f};
+  LpStats st{kFloor, 0.0f, 0.0f};
   uint64_t S2 = 0ull, T2 = 0ull;
-  const uint64_t s2 = pack2f(p.s, p.s), l2 = pack2f(kLog2e, kLog2e);
+  const uint64_t c2 = pack2f(p.c, p.c);
   uint32_t above = 0;
   auto raise = [&](float bm) {  // a new largest logit
-    xmax = max_nan(xmax, bm);
-    const float m = p.s * xmax;
-    const float d = st.m - m, e = exp_neg(d);
+    const float m = max_nan(st.m, bm);
+    const float d = p.c * (st.m - m), e = ex2(d);
     const float2 S = unpack2f(S2), t = unpack2f(T2);
     T2 = e == 0.0f ? 0ull : pack2f(e * __fmaf_rn(d, S.x, t.x), e * __fmaf_rn(d, S.y, t.y));
     S2 = pack2f(S.x * e, S.y * e);
     st.m = m;
   };
   while (v < v1) {
-    float x[kU * kV];
+    constexpr int kWords = 4 * kU;
+    uint32_t x[kWords];
 #pragma unroll
-    for (int u = 0; u < kU; ++u) Vec<T>::unpack(raw[u], x + u * kV);
+    for (int u = 0; u < kU; ++u) {
+      x[4 * u] = raw[u].x;
+      x[4 * u + 1] = raw[u].y;
+      x[4 * u + 2] = raw[u].z;
+      x[4 * u + 3] = raw[u].w;
+    }
     v += kU * kT;
     if (v < v1) fetch(v);
-    float bm = x[0];
+    float bm;
+    if constexpr (sizeof(T) == 2) {
+      uint32_t b2 = x[0];
 #pragma unroll
-    for (int i = 1; i < kU * kV; ++i) bm = max_nan(bm, x[i]);
-    if (!(bm <= x_tok)) {
+      for (int i = 1; i < kWords; ++i) b2 = max2_nan(b2, x[i]);
+      bm = max_nan(__uint_as_float(b2 << 16), __uint_as_float(b2 & 0xFFFF0000u));
+      if (!(bm <= x_tok)) {
+        const __nv_bfloat162 t2 = __float2bfloat162_rn(x_tok);  // a bf16 (or +inf) as it is
+        __nv_bfloat162 n2 = __float2bfloat162_rn(0.0f);  // counts of at most 16: exact
 #pragma unroll
-      for (int i = 0; i < kU * kV; ++i) above += x[i] > x_tok ? 1u : 0u;
+        for (int i = 0; i < kWords; ++i)
+          n2 = __hadd2(n2, __hgt2(*reinterpret_cast<const __nv_bfloat162*>(&x[i]), t2));
+        above += (uint32_t)(__low2float(n2) + __high2float(n2));
+      }
+      const uint32_t f2 = __float_as_uint(kFloor) >> 16 | (__float_as_uint(kFloor) & 0xFFFF0000u);
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) x[i] = max2_nan(x[i], f2);
+    } else {
+      bm = __uint_as_float(x[0]);
+#pragma unroll
+      for (int i = 1; i < kWords; ++i) bm = max_nan(bm, __uint_as_float(x[i]));
+      if (!(bm <= x_tok)) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) above += __uint_as_float(x[i]) > x_tok ? 1u : 0u;
+      }
+#pragma unroll
+      for (int i = 0; i < kWords; ++i)
+        x[i] = __float_as_uint(max_nan(__uint_as_float(x[i]), kFloor));
     }
-#pragma unroll
-    for (int i = 0; i < kU * kV; ++i) x[i] = max_nan(x[i], kFloor);
-    if (!(bm <= xmax)) raise(bm);
+    if (!(bm <= st.m)) raise(bm);
     const uint64_t m2 = pack2f(-st.m, -st.m);
+    if constexpr (sizeof(T) == 2) {
 #pragma unroll
-    for (int i = 0; i < kU * kV; i += 2) {
-      const uint64_t d = fma2(pack2f(x[i], x[i + 1]), s2, m2);
-      const float2 a = unpack2f(mul2(d, l2));
-      const uint64_t e = pack2f(ex2(a.x), ex2(a.y));
-      S2 = add2(S2, e);
-      T2 = fma2(d, e, T2);
+      for (int i = 0; i < kWords; ++i) lp_pair(x[i] << 16, x[i] & 0xFFFF0000u, c2, m2, S2, T2);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 2) lp_pair(x[i], x[i + 1], c2, m2, S2, T2);
     }
   }
   float single = __int_as_float(0xFF800000);
@@ -284,20 +321,20 @@ __global__ void __launch_bounds__(kT, 1024 / kT) logprobs_kernel(const LpArgs p)
     single = Vec<T>::load(row + single_at(tid));
     above += single > x_tok ? 1u : 0u;
     const float x = max_nan(single, kFloor);
-    if (!(x <= xmax)) raise(x);
-    const float d = __fmaf_rn(x, p.s, -st.m), e = exp_neg(d);
-    S2 = add2(S2, pack2f(e, 0.0f));
-    T2 = fma2(pack2f(d, 0.0f), pack2f(e, 0.0f), T2);
+    if (!(x <= st.m)) raise(x);
+    const float d = p.c * (x - st.m), e = ex2(d);
+    st.S = e;
+    st.T = d * e;
   }
   {
     const float2 S = unpack2f(S2), t = unpack2f(T2);
-    st.S = S.x + S.y;
-    st.T = t.x + t.y;
+    st.S += S.x + S.y;
+    st.T += t.x + t.y;
   }
 
   // ---- over the block: the largest logit first, then plain sums
   const bool any = v0 + tid < v1 || tid < singles;
-  const uint32_t key = any ? lp_key(xmax) : 0u;
+  const uint32_t key = any ? lp_key(st.m) : 0u;
   {
     const uint32_t c = __reduce_add_sync(0xFFFFFFFFu, above);
     const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, key);
@@ -315,11 +352,11 @@ __global__ void __launch_bounds__(kT, 1024 / kT) logprobs_kernel(const LpArgs p)
   const int n_any = __syncthreads_count(any);
   const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, lane < kW ? s_hi[lane] : 0u);
   const uint32_t lo = __reduce_min_sync(0xFFFFFFFFu, lane < kW ? s_lo[lane] : 0xFFFFFFFFu);
-  float m_blk = p.s * key_value(hi);
+  float m_blk = key_value(hi);
   // (block-uniform)
-  const bool plain = !(m_blk - p.s * kFloor >= 1000.0f) || p.s > kMaxScale;
+  const bool plain = !(p.c * (m_blk - kFloor) >= 1500.0f) || p.c > kMaxScale;
   if (!plain) {
-    st = lp_shift(st, m_blk);
+    st = lp_shift(st, m_blk, p.c);
   } else {
     const int64_t n_el = (v1 - v0) * kV;
     auto at = [&](int64_t i) {
@@ -331,11 +368,10 @@ __global__ void __launch_bounds__(kT, 1024 / kT) logprobs_kernel(const LpArgs p)
     __syncthreads();
     if (lane == 0) s_hi[warp] = wk;
     __syncthreads();
-    m_blk = max_nan(p.s * key_value(__reduce_max_sync(0xFFFFFFFFu, lane < kW ? s_hi[lane] : 0u)),
-                    kLowest);
+    m_blk = max_nan(key_value(__reduce_max_sync(0xFFFFFFFFu, lane < kW ? s_hi[lane] : 0u)), kLowest);
     st = {m_blk, 0.0f, 0.0f};
     for (int64_t i = tid; i < n_el + singles; i += kT) {
-      const float d = max_nan(__fmaf_rn(at(i), p.s, -m_blk), -1e30f), e = exp_neg(d);
+      const float d = max_nan(p.c * (at(i) - m_blk), -1e30f), e = ex2(d);
       st.S += e;
       st.T = __fmaf_rn(d, e, st.T);
     }
@@ -564,17 +600,17 @@ __global__ void __launch_bounds__(kT, 1024 / kT) logprobs_kernel(const LpArgs p)
 #pragma unroll
   for (int o = kLpMaxCluster / 2; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
   m = __shfl_sync(0xFFFFFFFFu, m, 0);
-  const LpStats a = lp_shift({part.x, part.y, part.z}, m);
+  const LpStats a = lp_shift({part.x, part.y, part.z}, m, p.c);
   const float S = warp_sum(a.S), t = warp_sum(a.T);
   const bool empty = S == 0.0f;  // every logit is -inf
-  const float logS = empty ? __int_as_float(0xFF800000) : logf(S);
-  auto logp = [&](float x) { return empty ? logS : __fmaf_rn(x, p.s, -m) - logS; };
+  const float logS = empty ? __int_as_float(0xFF800000) : kLn2 * log2f(S);
+  auto logp = [&](float x) { return empty ? logS : __fmaf_rn(p.s, x - m, -logS); };
   if (warp == 0) {
     const uint32_t c = __reduce_add_sync(0xFFFFFFFFu, lane < C ? __float_as_uint(part.w) : 0u);
     if (lane == 0) {
       p.logprob[m_row] = has ? logp(x_tok) : 0.0f;
-      p.entropy[m_row] = empty ? 0.0f : logS - t / S;
-      p.lse[m_row] = empty ? logS : m + logS;
+      p.entropy[m_row] = empty ? 0.0f : logS - kLn2 * (t / S);
+      p.lse[m_row] = empty ? logS : __fmaf_rn(p.s, m, logS);
       p.rank[m_row] = has ? (int64_t)c + 1 : 0;
     }
   }
@@ -698,7 +734,7 @@ nvfp4_status logprobs_launch(const void* logits, int dtype, int64_t M, int64_t N
                              cudaStream_t stream) {
   const int sms = sm_count();
   if (sms <= 0) return NVFP4_ERR_CUDA;
-  const LpArgs a{logits, N, ld, tokens, s, k, logprob, entropy, lse, top_lp, rank, top_ids};
+  const LpArgs a{logits, N, ld, tokens, s, (float)(s * 1.4426950408889634), k, logprob, entropy, lse, top_lp, rank, top_ids};
   const int c = lp_cluster(M, N, sms);
   const bool wide = N / c > kLpWideShare;
   const cudaError_t err =
