@@ -206,13 +206,13 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, unsigned long long v) 
 constexpr float kFloor = -0x1p83f;  // also a bf16
 constexpr float kMaxScale = 1e12f;  // times the floor: finite
 
-// T: float, or uint16_t for bf16 bits; kT threads.
-template <typename T, int kT>
-__global__ void __launch_bounds__(kT, 1024 / kT) logprobs_kernel(const LpArgs p) {
+// T: float, or uint16_t for bf16 bits; kT threads; kU vectors of a batch, whose
+// loads are in flight together (4 let 1024 threads share an SM).
+template <typename T, int kT, int kU>
+__global__ void __launch_bounds__(kT, kU == 4 ? 1024 / kT : 1) logprobs_kernel(const LpArgs p) {
   grid_dependency_wait();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int kV = Vec<T>::kN;
-  constexpr int kU = 4;  // vectors of a batch: their loads are in flight together
   constexpr int kW = kT / 32;
   __shared__ unsigned long long s_cand[kLpCand];
   __shared__ unsigned long long s_top[NVFP4_TOPK_MAX];
@@ -706,11 +706,14 @@ static int lp_cluster(int64_t M, int64_t N, int sms) {
   return c;
 }
 
-// Shares above this take 512 threads, others 256: 256 rows of 128256 fp32
-// 23.5 against 29.1 us, 512 rows of 32000 bf16 11.2 against 9.2 us.
+// Shares above this take 512 threads while the grid is at most two CTAs an SM
+// or many alternatives are asked for, others 256: 256 rows of 128256 fp32 23.5
+// against 29.1 us, 512 rows of 32000 bf16 11.2 against 9.2 us, 2048 rows of
+// 128256 bf16 94.3 against 87.1 us (k = 20: 114 against 125).  A grid of one
+// CTA an SM loads twice as far ahead: 64 rows of 151936 fp32 15.0 -> 13.6 us.
 constexpr int64_t kLpWideShare = 32768;
 
-template <typename T, int kT>
+template <typename T, int kT, int kU>
 static cudaError_t lp_launch(const LpArgs& a, int64_t M, int c, cudaStream_t stream) {
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -725,7 +728,7 @@ static cudaError_t lp_launch(const LpArgs& a, int64_t M, int c, cudaStream_t str
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, kT>, a);
+  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, kT, kU>, a);
 }
 
 nvfp4_status logprobs_launch(const void* logits, int dtype, int64_t M, int64_t N, int64_t ld,
@@ -736,11 +739,13 @@ nvfp4_status logprobs_launch(const void* logits, int dtype, int64_t M, int64_t N
   if (sms <= 0) return NVFP4_ERR_CUDA;
   const LpArgs a{logits, N, ld, tokens, s, (float)(s * 1.4426950408889634), k, logprob, entropy, lse, top_lp, rank, top_ids};
   const int c = lp_cluster(M, N, sms);
-  const bool wide = N / c > kLpWideShare;
-  const cudaError_t err =
-      dtype == NVFP4_OUT_BF16
-          ? (wide ? lp_launch<uint16_t, 512>(a, M, c, stream) : lp_launch<uint16_t, 256>(a, M, c, stream))
-          : (wide ? lp_launch<float, 512>(a, M, c, stream) : lp_launch<float, 256>(a, M, c, stream));
+  const bool wide = N / c > kLpWideShare && (M * c <= 2 * sms || k >= 16);
+  auto launch = [&](auto type) {
+    using T = decltype(type);
+    if (!wide) return lp_launch<T, 256, 4>(a, M, c, stream);
+    return M * c <= sms ? lp_launch<T, 512, 8>(a, M, c, stream) : lp_launch<T, 512, 4>(a, M, c, stream);
+  };
+  const cudaError_t err = dtype == NVFP4_OUT_BF16 ? launch(uint16_t{}) : launch(float{});
   return err == cudaSuccess && cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 
