@@ -253,6 +253,7 @@ __global__ void __launch_bounds__(kT, kU == 4 ? 1024 / kT : 1) logprobs_kernel(c
   const float x_tok = has ? Vec<T>::load(row + tok) : __int_as_float(0x7F800000);
 
   // ---- one pass: softmax state, the largest logit, logits above the token's
+  float largest = __int_as_float(0xFF800000);  // without the floor
   LpStats st{kFloor, 0.0f, 0.0f};
   uint64_t S2 = 0ull, T2 = 0ull;
   const uint64_t c2 = pack2f(p.c, p.c);
@@ -306,6 +307,7 @@ __global__ void __launch_bounds__(kT, kU == 4 ? 1024 / kT : 1) logprobs_kernel(c
       for (int i = 0; i < kWords; ++i)
         x[i] = __float_as_uint(max_nan(__uint_as_float(x[i]), kFloor));
     }
+    largest = max_nan(largest, bm);
     if (!(bm <= st.m)) raise(bm);
     const uint64_t m2 = pack2f(-st.m, -st.m);
     if constexpr (sizeof(T) == 2) {
@@ -320,6 +322,7 @@ __global__ void __launch_bounds__(kT, kU == 4 ? 1024 / kT : 1) logprobs_kernel(c
   if (tid < singles) {
     single = Vec<T>::load(row + single_at(tid));
     above += single > x_tok ? 1u : 0u;
+    largest = max_nan(largest, single);
     const float x = max_nan(single, kFloor);
     if (!(x <= st.m)) raise(x);
     const float d = p.c * (x - st.m), e = ex2(d);
@@ -353,28 +356,43 @@ __global__ void __launch_bounds__(kT, kU == 4 ? 1024 / kT : 1) logprobs_kernel(c
   const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, lane < kW ? s_hi[lane] : 0u);
   const uint32_t lo = __reduce_min_sync(0xFFFFFFFFu, lane < kW ? s_lo[lane] : 0xFFFFFFFFu);
   float m_blk = key_value(hi);
+  // the share's vectors, four at a time per thread, and its singles: f of each
+  // logit
+  auto for_each = [&](auto f) {
+    constexpr int kB = 4;
+    for (int64_t i0 = v0 + tid; i0 < v1; i0 += kB * kT) {
+      uint4 r[kB];
+#pragma unroll
+      for (int u = 0; u < kB; ++u) r[u] = i0 + u * kT < v1 ? __ldg(vec + i0 + u * kT) : make_uint4(pad, pad, pad, pad);
+#pragma unroll 1
+      for (int u = 0; u < kB; ++u) {
+        float x[kV];
+        Vec<T>::unpack(r[u], x);
+        if (i0 + u * kT < v1)
+#pragma unroll
+          for (int q = 0; q < kV; ++q) f(x[q]);
+      }
+    }
+    if (tid < singles) f(single);
+  };
   // (block-uniform)
   const bool plain = !(p.c * (m_blk - kFloor) >= 1500.0f) || p.c > kMaxScale;
   if (!plain) {
     st = lp_shift(st, m_blk, p.c);
   } else {
-    const int64_t n_el = (v1 - v0) * kV;
-    auto at = [&](int64_t i) {
-      return Vec<T>::load(row + (i < n_el ? rs.head + v0 * kV + i : single_at(i - n_el)));
-    };
-    float bm = __int_as_float(0xFF800000);
-    for (int64_t i = tid; i < n_el + singles; i += kT) bm = max_nan(bm, at(i));
-    const uint32_t wk = __reduce_max_sync(0xFFFFFFFFu, lp_key(bm));
+    const uint32_t wk = __reduce_max_sync(0xFFFFFFFFu, lp_key(largest));
     __syncthreads();
     if (lane == 0) s_hi[warp] = wk;
     __syncthreads();
-    m_blk = max_nan(key_value(__reduce_max_sync(0xFFFFFFFFu, lane < kW ? s_hi[lane] : 0u)), kLowest);
+    const float top = key_value(__reduce_max_sync(0xFFFFFFFFu, lane < kW ? s_hi[lane] : 0u));
+    m_blk = max_nan(top, kLowest);
     st = {m_blk, 0.0f, 0.0f};
-    for (int64_t i = tid; i < n_el + singles; i += kT) {
-      const float d = max_nan(p.c * (at(i) - m_blk), -1e30f), e = ex2(d);
-      st.S += e;
-      st.T = __fmaf_rn(d, e, st.T);
-    }
+    if (!(top < kLowest))  // (all -inf: nothing)
+      for_each([&](float x) {
+        const float d = max_nan(p.c * (x - m_blk), -1e30f), e = ex2(d);
+        st.S += e;
+        st.T = __fmaf_rn(d, e, st.T);
+      });
   }
   {
     const float S = warp_sum(st.S), t = warp_sum(st.T);
@@ -532,10 +550,10 @@ __global__ void __launch_bounds__(kT, kU == 4 ? 1024 / kT : 1) logprobs_kernel(c
       uint32_t below = bound;
       while (left > 0) {
         uint32_t mx = 0u;
-        for (int64_t i = tid; i < mine; i += kT) {
-          const uint32_t kk = key_at(i);
+        for_each([&](float x) {
+          const uint32_t kk = lp_key(x);
           if (kk < below) mx = max(mx, kk);
-        }
+        });
         mx = __reduce_max_sync(0xFFFFFFFFu, mx);
         __syncthreads();
         if (lane == 0) s_eq[warp] = mx;
