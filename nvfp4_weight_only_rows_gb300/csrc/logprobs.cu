@@ -641,7 +641,12 @@ __global__ void __launch_bounds__(kT, kU == 4 ? 1024 / kT : 1) logprobs_kernel(c
 
 // dl_n = s (a (1[n = t] - p_n) - b p_n (log p_n + H)): one read and one write
 // of the row, p from the forward's log-sum-exp.
-constexpr int kGradThreads = 256;
+//
+// Bound by HBM.  kStream reads and writes past the caches' reuse (evict
+// first, both: neither alone helps), in CTAs of 512 threads: 2048 x 128256
+// bf16 177 -> 152 us (1.03 of the copy rate, which caches its writes), 64 x
+// 128256 bf16 8.0 -> 7.5 us.  Below 32 MB a gradient stays for its reader, in
+// CTAs of 256: 19 x 50257 fp32 2.9 against 3.2 us.
 constexpr int kGradVecs = 4;  // vectors per thread
 
 struct LpGradArgs {
@@ -653,8 +658,8 @@ struct LpGradArgs {
   void* out;
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const LpGradArgs p) {
+template <typename T, int kT, bool kStream>
+__global__ void __launch_bounds__(kT) logprobs_grad_kernel(const LpGradArgs p) {
   grid_dependency_wait();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int kV = Vec<T>::kN;
@@ -677,16 +682,16 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const LpGra
   // the output's rows may start elsewhere against a 16-byte boundary
   const bool vec_out = ((reinterpret_cast<uintptr_t>(out + rs.head)) & 15) == 0;
   const uint4* src = reinterpret_cast<const uint4*>(row + rs.head);
-  const int64_t v0 = (int64_t)blockIdx.x * kGradThreads * kGradVecs + threadIdx.x;
+  const int64_t v0 = (int64_t)blockIdx.x * kT * kGradVecs + threadIdx.x;
   uint4 raw[kGradVecs];
 #pragma unroll
   for (int u = 0; u < kGradVecs; ++u) {
-    const int64_t v = v0 + u * kGradThreads;
-    if (v < rs.nv) raw[u] = src[v];
+    const int64_t v = v0 + u * kT;
+    if (v < rs.nv) raw[u] = kStream ? __ldcs(src + v) : src[v];
   }
 #pragma unroll
   for (int u = 0; u < kGradVecs; ++u) {
-    const int64_t v = v0 + u * kGradThreads;
+    const int64_t v = v0 + u * kT;
     if (v >= rs.nv) continue;
     float x[kV];
     Vec<T>::unpack(raw[u], x);
@@ -699,7 +704,8 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const LpGra
         if (n0 + i == tok) x[i] += a;
     }
     if (vec_out) {
-      *reinterpret_cast<uint4*>(out + n0) = Vec<T>::pack(x);
+      if constexpr (kStream) __stcs(reinterpret_cast<uint4*>(out + n0), Vec<T>::pack(x));
+      else *reinterpret_cast<uint4*>(out + n0) = Vec<T>::pack(x);
     } else {
 #pragma unroll
       for (int i = 0; i < kV; ++i) Vec<T>::store(out + n0 + i, x[i]);
@@ -771,11 +777,13 @@ nvfp4_status logprobs_grad_launch(const void* logits, int dtype, int64_t M, int6
                                   const int64_t* tokens, float s, const float* lse,
                                   const float* entropy, const float* g_lp, const float* g_ent,
                                   void* out, int64_t ld_out, cudaStream_t stream) {
-  const int64_t per = kGradThreads * kGradVecs * (dtype == NVFP4_OUT_BF16 ? 8 : 4);
+  const size_t es = dtype == NVFP4_OUT_BF16 ? 2 : 4;
+  const bool stream_it = 2 * (double)M * (double)N * (double)es >= (double)(32 << 20);
+  const int threads = stream_it ? 512 : 256;
+  const int64_t per = threads * kGradVecs * (16 / (int64_t)es);
   // rows beyond the grid's y limit go to further launches
   for (int64_t m0 = 0; m0 < M; m0 += 65535) {
     const int64_t rows = M - m0 < 65535 ? M - m0 : 65535;
-    const size_t es = dtype == NVFP4_OUT_BF16 ? 2 : 4;
     const LpGradArgs a{static_cast<const uint8_t*>(logits) + m0 * ld * es,
                        N,
                        ld,
@@ -787,12 +795,14 @@ nvfp4_status logprobs_grad_launch(const void* logits, int dtype, int64_t M, int6
                        g_lp + m0,
                        g_ent ? g_ent + m0 : nullptr,
                        static_cast<uint8_t*>(out) + m0 * ld_out * es};
-    PdlLaunch l(dim3((unsigned)((N + per - 1) / per), (unsigned)rows), dim3(kGradThreads), 0,
+    PdlLaunch l(dim3((unsigned)((N + per - 1) / per), (unsigned)rows), dim3((unsigned)threads), 0,
                 stream);
-    const cudaError_t err =
-        dtype == NVFP4_OUT_BF16
-            ? cudaLaunchKernelEx(&l.cfg, logprobs_grad_kernel<uint16_t>, a)
-            : cudaLaunchKernelEx(&l.cfg, logprobs_grad_kernel<float>, a);
+    auto kern = dtype == NVFP4_OUT_BF16
+                    ? (stream_it ? logprobs_grad_kernel<uint16_t, 512, true>
+                                 : logprobs_grad_kernel<uint16_t, 256, false>)
+                    : (stream_it ? logprobs_grad_kernel<float, 512, true>
+                                 : logprobs_grad_kernel<float, 256, false>);
+    const cudaError_t err = cudaLaunchKernelEx(&l.cfg, kern, a);
     if (err != cudaSuccess) return NVFP4_ERR_CUDA;
   }
   return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;

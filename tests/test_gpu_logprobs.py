@@ -193,6 +193,25 @@ def test_gradient_against_the_formula(M, N, dtype, s):
     check_grad(got, x, tok, s, lse.cpu(), ent.cpu(), a, torch.zeros(M))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("pad", [0, 3])
+def test_large_gradient(dtype, pad):
+    """Logits and gradient of more than 32 MB together, rows on and off
+    16-byte boundaries, into a new tensor and in place."""
+    M, N = 75, 120001
+    x, tok = make(M, N, dtype, seed=9, pad=pad)
+    tok[4] = -1
+    x[7, 1::2] = -INF
+    tok[7] = 0
+    dev = x.cuda() if pad == 0 else torch.empty(M, N + pad, dtype=dtype, device="cuda")[:, :N].copy_(x)
+    g = torch.Generator().manual_seed(8)
+    a, b = torch.randn(M, generator=g), torch.randn(M, generator=g) * 0.1
+    _, ent, lse, *_ = nv.token_logprobs(dev, tok.cuda())
+    args = (tok.cuda(), lse, ent, a.cuda(), b.cuda())
+    check_grad(nv.token_logprobs_backward(dev, *args), x, tok, 1.0, lse.cpu(), ent.cpu(), a, b)
+    check_grad(nv.token_logprobs_backward(dev, *args, out=dev), x, tok, 1.0, lse.cpu(), ent.cpu(), a, b)
+
+
 def test_gradient_against_differences():
     """Directional differences of f = sum a logprob + b entropy in 64 bits:
     central differences of step 1e-4 are off by about 1e-8 of f's third
