@@ -14,6 +14,7 @@
 #include <initializer_list>
 #include <stdexcept>
 #include <string>
+#include <utility>
 
 #include "../../include/nvfp4_lm_head.h"
 
@@ -59,6 +60,48 @@ at::Tensor result(PyObject* o, at::ScalarType dtype, const char* name,
   check(t, dtype, name, shape);
   return t;
 }
+
+// The results of one call, cut from one allocation at 256-byte steps: the six
+// of token_logprobs, allocated one by one, took the host 10.5 us a call, more
+// than the kernel takes for one row; this way a call is 5 us.
+class Results {
+ public:
+  at::Tensor* add(at::ScalarType dtype, std::initializer_list<int64_t> shape) {
+    Part& p = parts_[n_++];
+    int64_t bytes = (int64_t)c10::elementSize(dtype);
+    p.dtype = dtype;
+    p.dims = 0;
+    for (const int64_t d : shape) {
+      p.shape[p.dims++] = d;
+      bytes *= d;
+    }
+    p.at = total_;
+    total_ += (bytes + 255) / 256 * 256;
+    return &p.t;
+  }
+  void allocate(const at::Tensor& like) {
+    const at::Tensor base = at::empty({total_}, like.options().dtype(at::kByte));
+    for (int i = 0; i < n_; ++i) {
+      Part& p = parts_[i];
+      p.t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(base.storage()),
+                                                     c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                                     c10::scalarTypeToTypeMeta(p.dtype));
+      p.t.unsafeGetTensorImpl()->set_storage_offset(p.at / (int64_t)c10::elementSize(p.dtype));
+      p.t.unsafeGetTensorImpl()->set_sizes_contiguous({p.shape, (size_t)p.dims});
+    }
+  }
+
+ private:
+  struct Part {
+    at::ScalarType dtype;
+    int64_t shape[2], at;
+    int dims;
+    at::Tensor t;
+  };
+  Part parts_[6];
+  int n_ = 0;
+  int64_t total_ = 0;
+};
 
 const void* optional_f32(PyObject* o, const char* name, int64_t n) {
   if (o == Py_None) return nullptr;
@@ -154,8 +197,17 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t M = x.size(0), E = x.size(1), k = integer(a[1]), kk = std::max<int64_t>(k, 0);
     check(x, x.scalar_type(), "router_logits", {M, E});
     const void* bias = optional_f32(a[4], "bias", E);
-    const at::Tensor ids = result(a[6], at::kInt, "expert_ids", {M, kk}, x);
-    const at::Tensor w = result(a[7], at::kFloat, "weights", {M, kk}, x);
+    at::Tensor ids, w;
+    if (a[6] == Py_None && a[7] == Py_None) {
+      Results r;
+      at::Tensor &ri = *r.add(at::kInt, {M, kk}), &rw = *r.add(at::kFloat, {M, kk});
+      r.allocate(x);
+      ids = std::move(ri);
+      w = std::move(rw);
+    } else {
+      ids = result(a[6], at::kInt, "expert_ids", {M, kk}, x);
+      w = result(a[7], at::kFloat, "weights", {M, kk}, x);
+    }
     done(moe_route(x.data_ptr(), code, M, E, k, (int)integer(a[3]), (int)integer(a[2]),
                    static_cast<const float*>(bias), number(a[5]),
                    static_cast<int32_t*>(ids.data_ptr()), static_cast<float*>(w.data_ptr()),
@@ -231,10 +283,11 @@ PyObject* logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor &x = tensor(a[0], "logits"), &tok = tensor(a[1], "token_ids");
     const Logits l = logits_args(x, tok);
     const int64_t k = integer(a[2]), kk = std::max<int64_t>(k, 0);
-    const auto f = x.options().dtype(at::kFloat), i = x.options().dtype(at::kLong);
-    const at::Tensor lp = at::empty({l.M}, f), ent = at::empty({l.M}, f), lse = at::empty({l.M}, f);
-    const at::Tensor ranks = at::empty({l.M}, i), ids = at::empty({l.M, kk}, i);
-    const at::Tensor top = at::empty({l.M, kk}, f);
+    Results r;
+    at::Tensor &ranks = *r.add(at::kLong, {l.M}), &ids = *r.add(at::kLong, {l.M, kk});
+    at::Tensor &lp = *r.add(at::kFloat, {l.M}), &ent = *r.add(at::kFloat, {l.M});
+    at::Tensor &lse = *r.add(at::kFloat, {l.M}), &top = *r.add(at::kFloat, {l.M, kk});
+    r.allocate(x);
     auto pf = [](const at::Tensor& t) { return static_cast<float*>(t.data_ptr()); };
     auto pi = [](const at::Tensor& t) { return static_cast<int64_t*>(t.data_ptr()); };
     done(token_logprobs(x.data_ptr(), l.code, l.M, l.N, l.ld, pi(tok), number(a[3]), k, pf(lp),
