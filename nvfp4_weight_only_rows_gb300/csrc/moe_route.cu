@@ -7,15 +7,20 @@
 // A candidate is one word: the upper bits of its 32-bit order key above the
 // complement of its expert, so that one integer maximum over the warp picks
 // the largest key and, of equal ones, the lowest expert.  Each lane sorts its
-// words once; a round then is that maximum and a shift in the lane that held
-// it.  bf16 logits fit their words whole.  For fp32 keys k + 1 rounds show
-// whether two neighbours of the order share all the bits kept (values within
-// 2^-14 of each other): only then the token is done again by whole keys, two
-// reductions a round.  All sums are fp32.
+// words once and leaves them in shared memory; a round then is that maximum
+// and a step of the lane that held it (shifting them in registers: 16384 x 256
+// fp32 10.3 against 8.2 us).  bf16 logits fit their words whole.  For fp32
+// keys k + 1 rounds show whether two neighbours of the order share all the
+// bits kept (values within 2^-14 of each other): only then the token is done
+// again by whole keys, two reductions a round.  All sums are fp32.
 //
-// A call reads M E logits once and writes 8 M k bytes: a prompt of 16384
-// tokens and 256 experts is 18 MB (2.7 us at the copy rate), and bound by
-// instruction issue (about 250 a token).
+// A call reads M E logits once and writes 8 M k bytes: 16384 x 256 fp32 is 18
+// MB, 2.7 us at the copy rate, and takes 8.2 us; 65536 x 256 20.2 us.  One
+// token 1.9 us.  Bound by instruction issue (70% of its rate; a round 9 cycles
+// of an SM quarter, of about 285 a token) and, below some 10^5 tokens, by the
+// start of one CTA per four tokens.  Four tokens a warp with their rounds side
+// by side took 8.2 us too; CTAs of 8 or 16 tokens 8.4; a grid of resident CTAs
+// that loop 10.7 or more.
 #include "gemm_common.cuh"
 
 namespace nvfp4 {
@@ -57,169 +62,210 @@ __device__ __forceinline__ float route_logit(const uint16_t* p) {
   return __uint_as_float((uint32_t)__ldg(p) << 16);
 }
 
+struct RouteArgs {
+  const void* logits;
+  int64_t M;
+  int E, k, scoring, renorm;
+  const float* bias;
+  float scale;
+  int32_t* ids;
+  float* weights;
+  bool vec;  // rows are whole aligned 16-byte vectors
+};
+
+constexpr float kNegInf = -__builtin_huge_valf();
+
+// The row's logits e0 .. e0 + kR - 1, -inf past its end.
+template <int kR, typename T>
+__device__ __forceinline__ void route_load(const T* row, int e0, int E, bool vec, float (&x)[kR]) {
+  constexpr int kVec = 16 / sizeof(T);
+  if constexpr (kR % kVec == 0) {
+    if (vec) {
+#pragma unroll
+      for (int r = 0; r < kR; r += kVec) {
+        uint4 v;
+        const bool in = e0 + r < E;
+        if (in) v = __ldg(reinterpret_cast<const uint4*>(row + e0 + r));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (sizeof(T) == 4) {
+            x[r + i] = in ? __uint_as_float(w[i]) : kNegInf;
+          } else {
+            x[r + 2 * i] = in ? __uint_as_float(w[i] << 16) : kNegInf;
+            x[r + 2 * i + 1] = in ? __uint_as_float(w[i] & 0xFFFF0000u) : kNegInf;
+          }
+        }
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kR; ++r) x[r] = e0 + r < E ? route_logit(row + e0 + r) : kNegInf;
+}
+
+// A token's maximum and sum where scores themselves are needed: a bias is
+// added to them, or they are returned as they are.
+struct RouteSoftmax {
+  float top, total;
+};
+
+template <int kR>
+__device__ __forceinline__ RouteSoftmax route_softmax(const float (&x)[kR], int e0, int E) {
+  float top = x[0], total = 0.0f;
+#pragma unroll
+  for (int r = 1; r < kR; ++r) top = fmaxf(top, x[r]);
+  // (a NaN is not in this maximum; it reaches every score through the sum,
+  // or through its own)
+  top = key_value(__reduce_max_sync(0xFFFFFFFFu, route_key(top)));
+#pragma unroll
+  for (int r = 0; r < kR; ++r)
+    if (e0 + r < E) total += expf(x[r] - top);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+  return {top, total};
+}
+
+__device__ __forceinline__ float route_score(float v, bool softmax, RouteSoftmax s) {
+  // a token whose logits are all -inf has no expert: every score is zero
+  if (softmax) return s.top == kNegInf && v == v ? 0.0f : expf(v - s.top) / s.total;
+  return 1.0f / (1.0f + expf(-v));
+}
+
+// Selection keys, kTaken past the row's end.
+template <int kR>
+__device__ __forceinline__ void route_keys(const float (&x)[kR], int e0, const RouteArgs& p,
+                                           RouteSoftmax s, uint32_t (&key)[kR]) {
+  float v[kR];
+#pragma unroll
+  for (int r = 0; r < kR; ++r) v[r] = x[r];
+  if (p.bias != nullptr) {
+    const bool softmax = p.scoring == NVFP4_ROUTE_SOFTMAX;
+#pragma unroll
+    for (int r = 0; r < kR; ++r)
+      if (e0 + r < p.E) v[r] = route_score(x[r], softmax, s) + __ldg(p.bias + e0 + r);
+  }
+  if (e0 + kR <= p.E) {
+#pragma unroll
+    for (int r = 0; r < kR; ++r) key[r] = route_key(v[r]);
+  } else {
+#pragma unroll
+    for (int r = 0; r < kR; ++r) key[r] = e0 + r < p.E ? route_key(v[r]) : kTaken;
+  }
+}
+
 // kR: logits per lane (E <= 32 kR).  T: float, or uint16_t for bf16 bits.
 template <int kR, typename T>
-__global__ void __launch_bounds__(32 * kRouteWarps) moe_route_kernel(
-    const T* __restrict__ logits, int64_t M, int E, int k, int scoring, int renorm,
-    const float* __restrict__ bias, float scale, int32_t* __restrict__ ids,
-    float* __restrict__ weights) {
+__global__ void __launch_bounds__(32 * kRouteWarps) moe_route_kernel(const RouteArgs p) {
   grid_dependency_wait();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr uint32_t kIdMask = 32 * kR - 1;
-  constexpr float kNegInf = -__builtin_huge_valf();
-  const int lane = threadIdx.x & 31;
-  const int64_t m = (int64_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
-  if (m >= M) return;
-  const bool softmax = scoring == NVFP4_ROUTE_SOFTMAX;
-  const T* row = logits + m * E;
+  __shared__ uint32_t s_word[kRouteWarps][kR + 2][32];  // a lane's words in order
+  __shared__ uint32_t s_best[kRouteWarps][33];  // the words picked, in order
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t m = (int64_t)blockIdx.x * kRouteWarps + warp;
+  if (m >= p.M) return;
+  const bool softmax = p.scoring == NVFP4_ROUTE_SOFTMAX;
+  const bool sums = softmax && (p.bias != nullptr || !p.renorm);
+  const bool whole = sizeof(T) == 2 && p.bias == nullptr;  // the words hold the keys
+  const int rounds = p.k + (whole ? 0 : 1);
+  const T* row = static_cast<const T*>(p.logits) + m * p.E;
   const int e0 = lane * kR;  // this lane's experts e0 .. e0 + kR - 1
+
   float x[kR];
-  constexpr int kVec = 16 / sizeof(T);
-  bool vec = false;
-  if constexpr (kR % kVec == 0)
-    vec = E % kVec == 0 && (reinterpret_cast<uintptr_t>(logits) & 15) == 0;
-  if constexpr (kR % kVec == 0) {
-    if (vec) {  // whole vectors inside the row
+  route_load(row, e0, p.E, p.vec, x);
+  RouteSoftmax soft = {0.0f, 1.0f};
+  if (sums) soft = route_softmax(x, e0, p.E);
+  uint32_t key[kR];
+  route_keys(x, e0, p, soft, key);
+  {
+    uint32_t word[kR];
+    if (e0 + kR <= p.E) {
 #pragma unroll
-      for (int r = 0; r < kR; r += kVec) {
-        if (e0 + r < E) {
-          const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + e0 + r));
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      for (int r = 0; r < kR; ++r) word[r] = (key[r] | kIdMask) - (uint32_t)(e0 + r);
+    } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if constexpr (sizeof(T) == 4) {
-              x[r + i] = __uint_as_float(w[i]);
-            } else {
-              x[r + 2 * i] = __uint_as_float(w[i] << 16);
-              x[r + 2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-            }
-          }
-        } else {
+      for (int r = 0; r < kR; ++r)
+        word[r] = e0 + r < p.E ? (key[r] | kIdMask) - (uint32_t)(e0 + r) : kTaken;
+    }
+    sort_desc(word);
+    // the last round may find every expert taken: one more row to read
 #pragma unroll
-          for (int i = 0; i < kVec; ++i) x[r + i] = kNegInf;
-        }
+    for (int r = 1; r < kR; ++r) s_word[warp][r][lane] = word[r];
+    s_word[warp][kR][lane] = s_word[warp][kR + 1][lane] = kTaken;
+    uint32_t head = word[0];
+    const uint32_t* at = &s_word[warp][0][lane];
+#pragma unroll 1
+    for (int j = 0; j < rounds; ++j) {
+      const uint32_t mx = __reduce_max_sync(0xFFFFFFFFu, head);
+      if (head == mx) {
+        s_best[warp][j] = mx;
+        at += 32;
+        head = *at;
       }
     }
   }
-  if (!vec) {
-#pragma unroll
-    for (int r = 0; r < kR; ++r) x[r] = e0 + r < E ? route_logit(row + e0 + r) : kNegInf;
-  }
-  // the softmax's maximum and sum: needed where a score itself is (a bias
-  // is added to it, or it is returned as it is)
-  float top = 0.0f, total = 1.0f;
-  if (softmax) {
-    top = x[0];
-#pragma unroll
-    for (int r = 1; r < kR; ++r) top = fmaxf(top, x[r]);
-    // (a NaN is not in this maximum; it reaches every score through the sum,
-    // or through its own)
-    const uint32_t t = __reduce_max_sync(0xFFFFFFFFu, route_key(top));
-    top = key_value(t);
-    if (bias != nullptr || !renorm) {
-      total = 0.0f;
-#pragma unroll
-      for (int r = 0; r < kR; ++r)
-        if (e0 + r < E) total += expf(x[r] - top);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
-    }
-  }
-  auto score = [&](float v) {
-    // a token whose logits are all -inf has no expert: every score is zero
-    if (softmax) return top == kNegInf && v == v ? 0.0f : expf(v - top) / total;
-    return 1.0f / (1.0f + expf(-v));
-  };
-  uint32_t key[kR];
-#pragma unroll
-  for (int r = 0; r < kR; ++r)
-    key[r] = e0 + r >= E ? kTaken
-                         : route_key(bias != nullptr ? score(x[r]) + __ldg(bias + e0 + r) : x[r]);
+  __syncwarp();
 
-  int my_id = 0;
-  bool near = false;
-  {
-    uint32_t word[kR];
+  const bool on = lane < p.k;
+  const uint32_t mine = on ? s_best[warp][lane] : kTaken;
+  int id = on ? (int)(~mine & kIdMask) : 0;
+  if (__any_sync(0xFFFFFFFFu,
+                 !whole && on && ((mine ^ s_best[warp][lane + 1]) & ~kIdMask) == 0u)) {
+    uint32_t most = kTaken;
 #pragma unroll
-    for (int r = 0; r < kR; ++r)
-      word[r] = key[r] == kTaken ? kTaken : (key[r] & ~kIdMask) | (~(uint32_t)(e0 + r) & kIdMask);
-    sort_desc(word);
-    const bool whole = sizeof(T) == 2 && bias == nullptr;  // the words hold the keys
-    uint32_t mine = kTaken;  // lane j: the word of round j
-    const int rounds = k + (whole ? 0 : 1);
-#pragma unroll 2
-    for (int j = 0; j < rounds; ++j) {
-      const uint32_t mx = __reduce_max_sync(0xFFFFFFFFu, word[0]);
-      const bool pop = word[0] == mx;
-#pragma unroll
-      for (int r = 0; r + 1 < kR; ++r) word[r] = pop ? word[r + 1] : word[r];
-      word[kR - 1] = pop ? kTaken : word[kR - 1];
-      mine = lane == j ? mx : mine;
-    }
-    my_id = (int)(~mine & kIdMask);
-    if (!whole) {
-      // round 32 (k of 32) is in no lane: such tokens go by whole keys
-      const uint32_t before = __shfl_up_sync(0xFFFFFFFFu, mine, 1);
-      near = rounds > 32 || __any_sync(0xFFFFFFFFu, lane > 0 && lane < rounds &&
-                                                        ((mine ^ before) & ~kIdMask) == 0u);
-    }
-  }
-  if (near) {  // warp-uniform
-    uint32_t best = kTaken;
-#pragma unroll
-    for (int r = 0; r < kR; ++r) best = max(best, key[r]);
-    for (int j = 0; j < k; ++j) {
-      const uint32_t mx = __reduce_max_sync(0xFFFFFFFFu, best);
+    for (int r = 0; r < kR; ++r) most = max(most, key[r]);
+    for (int j = 0; j < p.k; ++j) {
+      const uint32_t mx = __reduce_max_sync(0xFFFFFFFFu, most);
       uint32_t e = 0xFFFFFFFFu;
 #pragma unroll
       for (int r = kR - 1; r >= 0; --r)
         if (key[r] == mx) e = e0 + r;
       e = __reduce_min_sync(0xFFFFFFFFu, e);
-      best = kTaken;
+      most = kTaken;
 #pragma unroll
       for (int r = 0; r < kR; ++r) {
         if ((uint32_t)(e0 + r) == e) key[r] = kTaken;
-        best = max(best, key[r]);
+        most = max(most, key[r]);
       }
-      if (lane == j) my_id = (int)e;
+      if (lane == j) id = (int)e;
     }
   }
-  float w = lane < k ? score(route_logit(row + min(my_id, E - 1))) : 0.0f;
-  if (renorm) {
+  const float v = on ? route_logit(row + min(id, p.E - 1)) : 0.0f;
+  // without sums the choice is by logits, and the first is their maximum
+  if (!sums) soft.top = __shfl_sync(0xFFFFFFFFu, v, 0);
+  float w = on ? route_score(v, softmax, soft) : 0.0f;
+  if (p.renorm) {
     float sum = w;
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     w = sum == 0.0f ? 0.0f : w / sum;
   }
-  if (lane < k) {
-    ids[m * k + lane] = my_id;
-    weights[m * k + lane] = w * scale;
+  if (on) {
+    p.ids[m * p.k + lane] = id;
+    p.weights[m * p.k + lane] = w * p.scale;
   }
 }
 
 template <typename T>
-static cudaError_t route_dispatch(const T* logits, int64_t M, int E, int k, int scoring,
-                                  int renorm, const float* bias, float scale, int32_t* ids,
-                                  float* weights, cudaStream_t stream) {
-  PdlLaunch l(dim3((unsigned)((M + kRouteWarps - 1) / kRouteWarps)), dim3(32 * kRouteWarps), 0,
+static cudaError_t route_dispatch(const RouteArgs& p, cudaStream_t stream) {
+  PdlLaunch l(dim3((unsigned)((p.M + kRouteWarps - 1) / kRouteWarps)), dim3(32 * kRouteWarps), 0,
               stream);
-  auto kern = E <= 64    ? moe_route_kernel<2, T>
-              : E <= 128 ? moe_route_kernel<4, T>
-              : E <= 256 ? moe_route_kernel<8, T>
-                         : moe_route_kernel<16, T>;
-  return cudaLaunchKernelEx(&l.cfg, kern, logits, M, E, k, scoring, renorm, bias, scale, ids,
-                            weights);
+  auto kern = p.E <= 64    ? moe_route_kernel<2, T>
+              : p.E <= 128 ? moe_route_kernel<4, T>
+              : p.E <= 256 ? moe_route_kernel<8, T>
+                           : moe_route_kernel<16, T>;
+  return cudaLaunchKernelEx(&l.cfg, kern, p);
 }
 
 nvfp4_status moe_route_launch(const void* logits, int dtype, int64_t M, int E, int k, int scoring,
                               int renorm, const float* bias, float scale, int32_t* ids,
                               float* weights, cudaStream_t stream) {
-  const cudaError_t err =
-      dtype == NVFP4_OUT_BF16
-          ? route_dispatch(static_cast<const uint16_t*>(logits), M, E, k, scoring, renorm, bias,
-                           scale, ids, weights, stream)
-          : route_dispatch(static_cast<const float*>(logits), M, E, k, scoring, renorm, bias,
-                           scale, ids, weights, stream);
+  const int per = dtype == NVFP4_OUT_BF16 ? 8 : 4;
+  const RouteArgs p{logits, M, E, k, scoring, renorm, bias, scale, ids, weights,
+                    E % per == 0 && (reinterpret_cast<uintptr_t>(logits) & 15) == 0};
+  const cudaError_t err = dtype == NVFP4_OUT_BF16 ? route_dispatch<uint16_t>(p, stream)
+                                                  : route_dispatch<float>(p, stream);
   return err == cudaSuccess && cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 
