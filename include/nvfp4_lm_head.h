@@ -593,14 +593,20 @@ size_t w4a16_moe_workspace_bytes(int64_t M, int64_t k, int64_t H, int64_t I);
  *   out          [M, H] bf16 (NVFP4_OUT_BF16) or fp32 (NVFP4_OUT_F32), device,
  *                16-byte aligned.
  *   workspace    >= w4a16_moe_workspace_bytes(M, k, H, I), 256-byte aligned.
- * Each weight of the experts in use is read once per 8 to 32 pairs; rows of
- * a K that is a multiple of 64 (and bases on 32 bytes) are read in 32-byte
- * pieces, others in 8-byte pieces.  Sums are fp32 in a fixed order (the
- * result does not depend on the schedule); each product x * w is exact, h is
+ * Two routes, by the sizes: with few pairs an expert's weights are read once
+ * per 8 to 32 pairs and multiplied as fp16, each product x * w exact, h
  * rounded to 11 bits for a bf16 result and to 22 for an fp32 one (values far
- * below the largest of 256 of them keep an absolute 2^-40 of it).  A NaN
- * block scale in a weight that was read raises NVFP4_ERR_NONFINITE in the
- * workspace status word.
+ * below the largest of 256 of them keep an absolute 2^-40 of it).  With more
+ * (M * k * H * I >= 2^26 or M * k >= 6 E; k <= 64, and H and I at most 4096 or
+ * multiples of 256) the FP4 tensor cores read the weights as they are, once
+ * per 8 to 20 pairs, and x and h are given to them as sums of NVFP4 values:
+ * to 3e-5 of the largest of 16 of them for a bf16 result and to 1e-6 for an
+ * fp32 one, or to 2e-6 of the largest of their row where that is more.  Block
+ * scales must not be negative (no quantizer of this library writes such a
+ * byte; the tensor cores' scales have no sign).  Sums are fp32 in a fixed
+ * order (the result does not depend on the schedule).  An Inf or NaN in a token's x makes that token's result NaN or
+ * Inf, no other's.  A NaN block scale in a weight that was read raises
+ * NVFP4_ERR_NONFINITE in the workspace status word.
  */
 nvfp4_status w4a16_moe(const void *x, int64_t M, int64_t k, int64_t H, int64_t I, int64_t E,
                        const int32_t *expert_ids, const float *weights, const uint8_t *w13_packed,
@@ -637,8 +643,8 @@ nvfp4_status w4a16_moe(const void *x, int64_t M, int64_t k, int64_t H, int64_t I
  *   k             0 <= k <= min(N, NVFP4_TOPK_MAX).
  *   logprobs, entropy, lse  fp32 [M]; ranks int64 [M]; device.  Written.
  *   top_ids       int64 [M, k], top_logprobs fp32 [M, k]; may be NULL if k == 0.
- * One kernel, one read of the logits (a second look at about k / 512 of a
- * row for the alternatives), no workspace, sums in fp32.
+ * One kernel, one read of the logits (and, for the alternatives, a second
+ * look at what about k of 256 to 512 threads read), no workspace, sums in fp32.
  */
 nvfp4_status token_logprobs(const void *logits, int dtype, int64_t M, int64_t N, int64_t ld,
                             const int64_t *token_ids, float inv_temperature, int64_t k,

@@ -1,9 +1,11 @@
-"""Online NVFP4 lm_head for GB300 (sm_103a): a thin ctypes binding.
+"""Online NVFP4 lm_head for GB300 (sm_103a): a thin Python binding.
 
 Every step of the path runs in the CUDA kernels of ``libnvfp4_lm_head.so``
 (see ``include/nvfp4_lm_head.h``); this module only checks tensor metadata,
 allocates outputs and workspaces with PyTorch when the caller gives none,
-and passes device pointers plus the current CUDA stream through the C ABI.
+and passes device pointers plus the current CUDA stream through the C ABI:
+with ctypes, or, for the router, the expert layer and the log probabilities,
+whose kernels are shorter than that, in the compiled module ``_calls``.
 There is no CPU or PyTorch fallback: if the library is missing, every call
 raises.
 

@@ -33,6 +33,10 @@
 // Work: the items (expert segment, 16-row tile) are split evenly over the
 // CTAs, and inside a CTA the (tile, stage) steps of a segment evenly over its
 // warps; a tile cut between warps is joined in shared memory in warp order.
+//
+// Measured: 1 token of H 2048, I 768, top 8 of 128 (21 MB, 3.2 us at the copy
+// rate) 14.4 us, most of it the latency of three dependent kernels' first
+// loads and of the boundaries between them.
 #include <cuda_fp16.h>
 
 #include <type_traits>

@@ -26,6 +26,13 @@
 //   moe_tc_combine      out = sum over a token's slots, in slot order
 // The products derive the tiles from the expert ids themselves, so that
 // their weight loads start while the kernel before them still runs.
+//
+// Measured (bf16 result, H 2048, I 768, top 8 of 128): 64 tokens, 335 MB, 74.6
+// us, 6.9 TB/s between a product's first and last MMA, about 20 us of prep, h,
+// combine, kernel boundaries and first loads around them.  5 tokens of H = I =
+// 2880, top 4 of 32, 221 MB: 57.8 us.  193 tokens of 64 experts with I 720 and
+// half the pairs elsewhere, 159 MB: 74.3 us, bound by the ring's latency (12
+// pairs an expert, K % 32 != 0 in the second product).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
