@@ -78,17 +78,24 @@ __device__ __forceinline__ void tc_sync(int bar, int n) {
 }
 
 // By the n threads tid = 0 .. n - 1 (whole warps) that meet at barrier `bar`.
+// seen(i, e): pair i has expert e, or kTcNoExpert; meanwhile(): by the warps
+// but the first, once every id was seen.
+constexpr int kTcNoExpert = 0xFFFF;
+template <typename Seen, typename Meanwhile>
 __device__ __forceinline__ void tc_tables(const int32_t* ids, int P, int E, int cap, TcTables& s,
-                                          int tid, int n, int bar) {
+                                          int tid, int n, int bar, Seen seen, Meanwhile meanwhile) {
   const int lane = tid & 31;
   const int mine = tid < P ? __ldg(ids + tid) : -1;  // under way while the counts are cleared
   for (int e = tid; e < E; e += n) s.cnt[e] = 0;
   tc_sync(bar, n);
-  if (mine >= 0 && mine < E) atomicAdd(&s.cnt[mine], 1);
-  for (int i = tid + n; i < P; i += n) {
-    const int e = __ldg(ids + i);
-    if (e >= 0 && e < E) atomicAdd(&s.cnt[e], 1);
-  }
+  auto count = [&](int i, int e) {
+    const bool in = e >= 0 && e < E;
+    if (in) atomicAdd(&s.cnt[e], 1);
+    seen(i, in ? e : kTcNoExpert);
+  };
+  if (tid < P) count(tid, mine);
+#pragma unroll 4
+  for (int i = tid + n; i < P; i += n) count(i, __ldg(ids + i));
   tc_sync(bar, n);
   if (tid < 32) {
     // lane l takes `per` consecutive experts
@@ -113,6 +120,8 @@ __device__ __forceinline__ void tc_tables(const int32_t* ids, int P, int E, int 
       tiles += (c + cap - 1) / cap;
     }
     if (lane == 31) s.tile[E] = (uint16_t)tiles;
+  } else {
+    meanwhile();
   }
   tc_sync(bar, n);
 }
@@ -244,6 +253,8 @@ __global__ void __launch_bounds__(2 * kPrepHalf) moe_prep_kernel(const TcArgs p)
   __shared__ TcPlace s_dst[kTcMaxK];
   __shared__ int s_n;
   __shared__ uint32_t s_max;
+  extern __shared__ __align__(16) uint8_t s_prep_mem[];
+  uint16_t* s_ids = reinterpret_cast<uint16_t*>(s_prep_mem);  // of all pairs, whole 16 bytes
   grid_dependency_wait();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31, m = blockIdx.x;
@@ -256,6 +267,7 @@ __global__ void __launch_bounds__(2 * kPrepHalf) moe_prep_kernel(const TcArgs p)
     return i < p.H / 8 ? __ldg(row + i) : make_uint4(0u, 0u, 0u, 0u);
   };
   float up = 0.0f, undo = 0.0f;
+  int my_e = kTcNoExpert, my_rank = 0;
   auto split = [&](int s) {
     const uint4 r = load(s);
     const uint32_t u[4] = {r.x, r.y, r.z, r.w};
@@ -284,33 +296,48 @@ __global__ void __launch_bounds__(2 * kPrepHalf) moe_prep_kernel(const TcArgs p)
     up = tc_scale(s_max, undo);
     if (warp < n_stages) split(warp);
   } else {
+    // The place of pair i is its rank among its expert's pairs, counted from
+    // the ids in shared memory (from global memory, one pair's after another:
+    // 193 tokens of 8 2 us more).  Slot j is warp 1 + j % 7's, whose lane j / 7
+    // keeps it.
     if (tid == 0) s_n = 0;
-    // the place of pair i is its rank among its expert's; this warp's slots are
-    // j = warp, warp + 8, .., lane j / 8 keeping slot j's
-    int my_e = -1, my_rank = 0;
-    for (int j = warp; j < p.k; j += kWarps) {
-      const int i = m * p.k + j, e = __ldg(p.ids + i);
-      int rank = 0;
-      for (int b = lane; b < i; b += 32) rank += __ldg(p.ids + b) == e ? 1 : 0;
-      rank = __reduce_add_sync(0xFFFFFFFFu, rank);
-      if (lane == j / kWarps) {
-        my_e = e;
-        my_rank = rank;
-      }
-    }
-    tc_tables(p.ids, p.P, p.E, p.cap, s_tab, tid, kPrepHalf, 2);
+    tc_tables(p.ids, p.P, p.E, p.cap, s_tab, tid, kPrepHalf, 2,
+              [&](int i, int e) { s_ids[i] = (uint16_t)e; },
+              [&] {
+                for (int j = warp - 1; j < p.k; j += kWarps - 1) {
+                  const int i = m * p.k + j, e = s_ids[i];
+                  const uint32_t ee = (uint32_t)e | (uint32_t)e << 16;
+                  int bits = 0;
+                  for (int b = 8 * lane; b < i; b += 256) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(s_ids + b);
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                      const int left = i - (b + 2 * q);  // ids of this word before i
+                      const uint32_t same = __vcmpeq2(w[q], ee);
+                      bits += __popc(left >= 2 ? same : left == 1 ? same & 0xFFFFu : 0u);
+                    }
+                  }
+                  const int rank = __reduce_add_sync(0xFFFFFFFFu, bits) >> 4;
+                  if (lane == j / (kWarps - 1)) {
+                    my_e = e;
+                    my_rank = rank;
+                  }
+                }
+              });
     if (m == 0 && tid == 0) {
       *p.status = NVFP4_OK;
       *p.counts = make_int2(s_tab.off[p.E - 1] + s_tab.cnt[p.E - 1], s_tab.tile[p.E]);
     }
-    if (warp + kWarps * lane < p.k) {
+    const int slot = warp - 1 + (kWarps - 1) * lane;
+    if (warp > 0 && slot < p.k) {
       TcPlace d{0, 0, 0, -1};
-      if (my_e >= 0 && my_e < p.E) {
+      if (my_e != kTcNoExpert) {
         d = {my_e, s_tab.tile[my_e] + my_rank / p.cap, my_rank % p.cap, s_tab.off[my_e] + my_rank};
         p.by_place[d.place] = d;
         s_dst[atomicAdd(&s_n, 1)] = d;
       }
-      p.by_pair[m * p.k + warp + kWarps * lane] = d;
+      p.by_pair[m * p.k + slot] = d;
     }
   }
   __syncthreads();
@@ -485,7 +512,7 @@ __global__ void __launch_bounds__(576, 1)
   }
   // The expert ids were complete before the kernel ahead of this one let it
   // start; its own results are waited for where they are read.
-  tc_tables(p.ids, p.P, p.E, p.cap, s_tab, threadIdx.x, blockDim.x, 0);
+  tc_tables(p.ids, p.P, p.E, p.cap, s_tab, threadIdx.x, blockDim.x, 0, [](int, int) {}, [] {});
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, tmem_slot, 0);
   const WaitCtl wc{p.status, abort_flag, kWaitLimitNs};
@@ -1120,7 +1147,7 @@ nvfp4_status moe_tc_launch(const void* x, int64_t M, int64_t k, int64_t H, int64
   {
     static std::atomic<uint64_t> split_set{0};
     err = tc_carveout_once(split_set, reinterpret_cast<const void*>(moe_prep_kernel));
-    PdlLaunch l(dim3((unsigned)M), dim3(2 * kPrepHalf), 0, stream);
+    PdlLaunch l(dim3((unsigned)M), dim3(2 * kPrepHalf), align_up((size_t)a.P * 2, 16), stream);
     if (err == cudaSuccess) err = cudaLaunchKernelEx(&l.cfg, moe_prep_kernel, a);
   }
   if (err == cudaSuccess) err = tc_gemm_launch(g1, sms, stream);
