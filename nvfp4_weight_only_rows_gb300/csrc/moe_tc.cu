@@ -806,78 +806,94 @@ __device__ __forceinline__ TcSpan tc_span(int64_t S, int grid, int n_st, int RT,
   return {tc_owner(S, x, G), tc_owner(S, x + n_st - 1, G)};
 }
 
-// Threads by the pair's length: a quarter of its values, so that its loads are
-// one round trip.
-constexpr int kActMaxThreads = 768;
-static int act_threads(int64_t I) { return I <= 1024 ? 256 : I <= 2048 ? 512 : kActMaxThreads; }
-// The warps that split the pair's stages.
-__host__ __device__ __forceinline__ int act_split_warps(int64_t I, int threads) {
-  const int64_t stages = (I + 255) / 256;
-  return (int)(stages < threads / 32 ? stages : threads / 32);
+// Eight consecutive values of h a thread, so that a warp's are the stage it
+// splits and stay in its registers (beyond 1024 threads they are computed
+// again once the row's maximum is known).  CTAs this small (I of 768: 96
+// threads) leave the next product's CTAs room beside them, whose weights are
+// then under way while h is computed: 64 tokens 72.4 against 74.1 us with 256
+// threads and h in shared memory.  Where there are more pairs than fit at once
+// they start late (193 tokens of 8); a grid of what fits, looping, took 4% longer.
+constexpr int kActMaxThreads = 1024;
+static int act_threads(int64_t I) {
+  return (int)std::min<int64_t>((I / 8 + 31) / 32 * 32, kActMaxThreads);
 }
 
 __global__ void __launch_bounds__(kActMaxThreads) moe_act_kernel(const TcArgs p) {
-  // a split buffer a warp, I values, the spans of the 2I / 128 row tiles
+  // a split buffer a warp, the spans of the 2I / 128 row tiles
   extern __shared__ __align__(16) uint8_t s_act_mem[];
   __shared__ uint32_t s_max;
-  __shared__ TcPlace s_dst;
   const int n_threads = blockDim.x;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int N = 2 * p.I, RT = (N + 127) / 128, n_st = (p.H + 255) / 256;
-  float* s_h = reinterpret_cast<float*>(s_act_mem + act_split_warps(p.I, n_threads) * kSplitBytes);
-  TcSpan* s_span = reinterpret_cast<TcSpan*>(s_h + p.I);
-  // where the pair and its sums lie: written by the prep kernel, which was
+  uint8_t* buf = s_act_mem + warp * kSplitBytes;
+  TcSpan* s_span = reinterpret_cast<TcSpan*>(s_act_mem + n_threads / 32 * kSplitBytes);
+  // where a pair and its sums lie: written by the prep kernel, which was
   // complete before the product this kernel waits for began
-  const int q = blockIdx.x;
   const int2 counts = __ldcg(p.counts);
-  const int4 at = __ldcg(reinterpret_cast<const int4*>(p.by_place) + q);  // not set past counts.x
-  const bool present = q < counts.x;
-  const int tile = at.y, col = at.z;
   const int64_t S = (int64_t)counts.y * RT * n_st;
-  if (present)
-    for (int r = tid; r < RT; r += n_threads) s_span[r] = tc_span(S, p.grid, n_st, RT, tile, r);
-  if (tid == 0) {
-    s_max = 0u;
-    s_dst = {at.x, tile, col, q};
+  const int64_t slot = (int64_t)p.cap * 128;
+  const int q = blockIdx.x;
+  const bool present = q < counts.x;
+  TcPlace at{};
+  if (present) {
+    const int4 v = __ldcg(reinterpret_cast<const int4*>(p.by_place) + q);
+    at = {v.x, v.y, v.z, q};
+    for (int r = tid; r < RT; r += n_threads) s_span[r] = tc_span(S, p.grid, n_st, RT, at.tile, r);
   }
+  if (tid == 0) s_max = 0u;
   __syncthreads();
   grid_dependency_wait();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!present) return;
-  const float g13 = __ldg(p.g13 + at.x);
-  // four values in flight per thread; a unit that was cut has its other parts
-  // added in order
-  const int64_t slot = (int64_t)p.cap * 128;
-  auto first = [&](int n) {
-    const TcSpan sp = s_span[n >> 7];
-    return __ldcg(sp.b0 == sp.b1 ? p.gu + (int64_t)q * N + n
-                                 : p.part1 + tc_slot(sp.b0, true) * slot + (int64_t)col * 128 + (n & 127));
+  const float g13 = __ldg(p.g13 + at.expert);
+  // columns n .. n + 3 of gu: a unit that was cut has its parts added in order
+  auto first = [&](int n, TcSpan sp) {
+    return __ldcg(reinterpret_cast<const float4*>(
+        sp.b0 == sp.b1 ? p.gu + (int64_t)q * N + n
+                       : p.part1 + tc_slot(sp.b0, true) * slot + at.col * 128 + (n & 127)));
   };
-  auto rest = [&](int n, float sum) {
-    const TcSpan sp = s_span[n >> 7];
-    for (int b = sp.b0 + 1; b <= sp.b1; ++b)
-      sum += __ldcg(p.part1 + tc_slot(b, false) * slot + (int64_t)col * 128 + (n & 127));
-    return sum;
+  auto part = [&](int n, int b) {
+    return __ldcg(reinterpret_cast<const float4*>(p.part1 + tc_slot(b, false) * slot +
+                                                  at.col * 128 + (n & 127)));
   };
-  constexpr int kAhead = 4;
+  auto values = [&](int i, float (&h)[8]) {
+    float4 v[4];
+    TcSpan sp[4];
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {  // gate, up; i, i + 4
+      const int n = (a & 1) * p.I + i + (a >> 1) * 4;
+      sp[a] = s_span[n >> 7];
+      v[a] = first(n, sp[a]);
+    }
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      const int n = (a & 1) * p.I + i + (a >> 1) * 4;
+      for (int b = sp[a].b0 + 1; b <= sp[a].b1; ++b) {
+        const float4 o = part(n, b);
+        v[a].x += o.x;
+        v[a].y += o.y;
+        v[a].z += o.z;
+        v[a].w += o.w;
+      }
+    }
+    auto act = [&](float g, float u) {
+      g *= g13;
+      return g / (1.0f + __expf(-g)) * (u * g13);
+    };
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+      h[4 * a] = act(v[2 * a].x, v[2 * a + 1].x);
+      h[4 * a + 1] = act(v[2 * a].y, v[2 * a + 1].y);
+      h[4 * a + 2] = act(v[2 * a].z, v[2 * a + 1].z);
+      h[4 * a + 3] = act(v[2 * a].w, v[2 * a + 1].w);
+    }
+  };
+  float h[8];
   uint32_t mx = 0;
-  for (int i0 = tid; i0 < p.I; i0 += kAhead * n_threads) {
-    float g[kAhead], u[kAhead];
+  for (int i = 8 * tid; i < p.I; i += 8 * n_threads) {
+    values(i, h);
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      const int i = i0 + a * n_threads;
-      g[a] = i < p.I ? first(i) : 0.0f;
-      u[a] = i < p.I ? first(p.I + i) : 0.0f;
-    }
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      const int i = i0 + a * n_threads;
-      if (i >= p.I) break;
-      const float gv = rest(i, g[a]) * g13, uv = rest(p.I + i, u[a]) * g13;
-      const float h = gv / (1.0f + __expf(-gv)) * uv;
-      s_h[i] = h;
-      mx = max(mx, __float_as_uint(h) & 0x7FFFFFFFu);
-    }
+    for (int a = 0; a < 8; ++a) mx = max(mx, __float_as_uint(h[a]) & 0x7FFFFFFFu);
   }
   mx = __reduce_max_sync(0xFFFFFFFFu, mx);
   if (lane == 0) atomicMax(&s_max, mx);
@@ -886,15 +902,14 @@ __global__ void __launch_bounds__(kActMaxThreads) moe_act_kernel(const TcArgs p)
   const float up = tc_scale(s_max, undo);
   if (tid == 0) p.mul2[q] = undo;
   const int stages = (p.I + 255) / 256;
-  uint8_t* buf = s_act_mem + warp * kSplitBytes;
   for (int s = warp; s < stages; s += n_threads / 32) {
-    const int k0 = 256 * s + 8 * lane;
-    float v[8];
+    const int i = 256 * s + 8 * lane;
+    if (stages > n_threads / 32 && i < p.I) values(i, h);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = k0 < p.I ? s_h[k0 + i] * up : 0.0f;
+    for (int a = 0; a < 8; ++a) h[a] = i < p.I ? h[a] * up : 0.0f;
     __syncwarp();
-    tc_split(v, p.pieces, buf);
-    tc_place(buf, p.pieces, s, s_dst, p.P, p.tiles_max, p.act2, p.sf2);
+    tc_split(h, p.pieces, buf);
+    tc_place(buf, p.pieces, s, at, p.P, p.tiles_max, p.act2, p.sf2);
   }
 }
 
@@ -1152,19 +1167,13 @@ nvfp4_status moe_tc_launch(const void* x, int64_t M, int64_t k, int64_t H, int64
   }
   if (err == cudaSuccess) err = tc_gemm_launch(g1, sms, stream);
   if (err == cudaSuccess) {
-    auto bytes = [](int64_t I) {
-      return (size_t)act_split_warps(I, act_threads(I)) * kSplitBytes + (size_t)I * 4 +
-             (size_t)((2 * I + 127) / 128) * sizeof(TcSpan);
-    };
-    const size_t smem = bytes(I);
-    static std::atomic<uint64_t> limit_set{0};
-    err = smem_limit_once(limit_set, reinterpret_cast<const void*>(moe_act_kernel),
-                          bytes(NVFP4_MOE_MAX_DIM));
+    const int threads = act_threads(I);
+    const size_t smem =
+        (size_t)threads / 32 * kSplitBytes + (size_t)((2 * I + 127) / 128) * sizeof(TcSpan);
     static std::atomic<uint64_t> split_set{0};
-    if (err == cudaSuccess)
-      err = tc_carveout_once(split_set, reinterpret_cast<const void*>(moe_act_kernel));
+    err = tc_carveout_once(split_set, reinterpret_cast<const void*>(moe_act_kernel));
     if (err == cudaSuccess) {
-      PdlLaunch l(dim3((unsigned)a.P), dim3(act_threads(I)), smem, stream);
+      PdlLaunch l(dim3((unsigned)a.P), dim3(threads), smem, stream);
       err = cudaLaunchKernelEx(&l.cfg, moe_act_kernel, a);
     }
   }
