@@ -369,11 +369,23 @@ struct TcGemm {
   int32_t* status;
 };
 
+// Where K / 2 bytes are no 16-byte multiple (K % 32 != 0), TMA cannot step
+// from a row of codes to the next, but from one to the next but one: a stage's
+// rows come as the even ones, which land where the MMA reads them (rows 0 to 63
+// of the tile), and the odd ones, 8 bytes early, which four warps copy into
+// place (rows 64 to 127).  193 tokens of 64 experts, I 720: 68.4 against 73.3
+// us with 8-byte cp.async by those warps instead.
+__device__ __forceinline__ int tc_row(bool tma, int r) {  // of tile row r, in memory
+  return tma ? r : r < 64 ? 2 * r : 2 * r - 127;
+}
+constexpr uint32_t kTcOddRow = 128 + 16;              // bytes of an odd row, 8 before it among them
+constexpr uint32_t kTcOddStage = 64 * kTcOddRow;
+
 // Warps: 0 weight codes (and, per stage, scales), 1 MMA, 2 scales per unit,
-// 3 activations, 4-7 epilogue, 8-11 scale layout, then the code loaders.
+// 3 activations, 4-7 epilogue, 8-11 scale layout, then the odd rows' copiers.
 constexpr int kTcScaleWarps = 4;
 constexpr int kTcThreads = 32 * (8 + kTcScaleWarps);
-constexpr int kTcLoaderWarps = 4;     // where TMA cannot read the code rows
+constexpr int kTcOddWarps = 4;
 constexpr int kTcMaxUnits = 8;        // unit buffers of scales
 
 struct TcPiece {
@@ -466,8 +478,9 @@ __device__ __forceinline__ void tc_drain(uint32_t taddr, int n, float mul, bool 
 // a product (the bound names more threads than there are).
 template <bool kTma>
 __global__ void __launch_bounds__(576, 1)
-    moe_tc_kernel(const __grid_constant__ CUtensorMap tm_w,
-                  const __grid_constant__ CUtensorMap tm_s, const TcGemm p) {
+    moe_tc_kernel(const __grid_constant__ CUtensorMap tm_w,  // codes, or their even rows
+                  const __grid_constant__ CUtensorMap tm_2,  // scales, or the odd rows
+                  const TcGemm p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -477,10 +490,11 @@ __global__ void __launch_bounds__(576, 1)
   uint8_t* s_b = s_a + ring * kTcAStage;
   uint8_t* s_sfa = s_b + ring * b_stage;
   uint8_t* s_sfb = s_sfa + ring * kTcSfStage;
-  uint8_t* s_raw = s_sfb + ring * kTcSfStage;  // scales as stored: a slot a stage, or whole units
+  uint8_t* s_odd = s_sfb + ring * kTcSfStage;
+  uint8_t* s_raw = s_odd + (kTma ? 0 : ring * kTcOddStage);  // scales as stored: a slot a stage, or whole units
   __shared__ TcTables s_tab;
   __shared__ uint64_t full[kTcMaxRing], empty[kTcMaxRing], raw_full[kTcMaxRing], raw_empty[kTcMaxUnits];
-  __shared__ uint64_t d_full[2], d_empty[2], done_bar;
+  __shared__ uint64_t odd_full[kTcMaxRing], d_full[2], d_empty[2], done_bar;
   __shared__ uint32_t tmem_slot;
   __shared__ int32_t s_abort;
   volatile int32_t* abort_flag = &s_abort;
@@ -488,8 +502,9 @@ __global__ void __launch_bounds__(576, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < ring; ++i) {
-      mbar_init(&full[i], 1 + kTcScaleWarps + (kTma ? 1 : kTcLoaderWarps));
+      mbar_init(&full[i], 2 + kTcScaleWarps + (kTma ? 0 : kTcOddWarps));
       mbar_init(&empty[i], 1);
+      mbar_init(&odd_full[i], 1);
     }
     for (int i = 0; i < kTcMaxUnits; ++i) {
       mbar_init(&raw_full[i], 1);
@@ -503,8 +518,8 @@ __global__ void __launch_bounds__(576, 1)
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    if (kTma) tma_prefetch_desc(&tm_w);
-    if (!p.unit_scales) tma_prefetch_desc(&tm_s);
+    tma_prefetch_desc(&tm_w);
+    if (!kTma || !p.unit_scales) tma_prefetch_desc(&tm_2);
   }
   if (warp == 1) {
     tmem_alloc(&tmem_slot, 512);
@@ -539,30 +554,35 @@ __global__ void __launch_bounds__(576, 1)
     // ---------------- weight codes, and scales where they come per stage
     const uint64_t once = policy_evict_first();
     uint32_t issued = 0;
-    if (kTma || !p.unit_scales)
-      tc_pieces(x0, x1, n_st, RT, [&](const TcPiece& pc) {
-        const int r0 = tile_at(pc.tile).expert * p.N + pc.rt * 128;
-        for (int kb = pc.kb0; kb < pc.kb1; ++kb, ++issued) {
-          const uint32_t st = issued % ring, ph = (issued / ring) & 1;
-          if (!warp_wait(&empty[st], ph ^ 1, wc)) return false;
-          if (elect_one()) {
+    tc_pieces(x0, x1, n_st, RT, [&](const TcPiece& pc) {
+      const int r0 = tile_at(pc.tile).expert * p.N + pc.rt * 128;
+      for (int kb = pc.kb0; kb < pc.kb1; ++kb, ++issued) {
+        const uint32_t st = issued % ring, ph = (issued / ring) & 1;
+        if (!warp_wait(&empty[st], ph ^ 1, wc)) return false;
+        if (elect_one()) {
+          if constexpr (kTma) {
             if (!p.unit_scales) {
               mbar_arrive_expect_tx(&raw_full[st], kTcSfStage);
-              tma_load_2d_hint(s_raw + st * kTcSfStage, &tm_s, kb * 16, r0, &raw_full[st], once);
+              tma_load_2d_hint(s_raw + st * kTcSfStage, &tm_2, kb * 16, r0, &raw_full[st], once);
             }
-            if (kTma) {
-              mbar_arrive_expect_tx(&full[st], kTcAStage);
-              tma_load_2d_hint(s_a + st * kTcAStage, &tm_w, kb * 128, r0, &full[st], once);
-            }
+            mbar_arrive_expect_tx(&full[st], kTcAStage);
+            tma_load_2d_hint(s_a + st * kTcAStage, &tm_w, kb * 128, r0, &full[st], once);
+          } else {
+            mbar_arrive_expect_tx(&odd_full[st], kTcOddStage);
+            tma_load_2d_hint(s_odd + st * kTcOddStage, &tm_2, kb * 128, r0 / 2, &odd_full[st], once);
+            mbar_arrive_expect_tx(&full[st], kTcAStage / 2);
+            tma_load_2d_hint(s_a + st * kTcAStage, &tm_w, kb * 128, r0 / 2, &full[st], once);
           }
-          __syncwarp();
         }
-        return true;
-      });
-    if (!p.unit_scales) drain_loads(raw_full, ring, issued, 0, p.status);
+        __syncwarp();
+      }
+      return true;
+    });
+    if (!kTma) drain_loads(odd_full, ring, issued, 0, p.status);
+    else if (!p.unit_scales) drain_loads(raw_full, ring, issued, 0, p.status);
     // codes and activations of a stage land on one barrier, which the MMA
     // warp waits for; what an aborted call left in flight lands here
-    if (*abort_flag && kTma) drain_loads(full, ring, issued, 0, p.status);
+    if (*abort_flag) drain_loads(full, ring, issued, 0, p.status);
   } else if (warp == 3) {
     // ---------------- the pairs' pieces and their scales
     grid_dependency_wait();
@@ -660,7 +680,7 @@ __global__ void __launch_bounds__(576, 1)
   } else if (warp < 8) {
     // ---------------- epilogue: a row a thread; a pair's pieces are summed
     grid_dependency_wait();  // the multipliers
-    const int row = (warp & 3) * 32 + lane;
+    const int row = tc_row(kTma, (warp & 3) * 32 + lane);
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     int i = 0, mul_of = -1;
     float mul = 0.0f;
@@ -700,7 +720,7 @@ __global__ void __launch_bounds__(576, 1)
     // one tcgen05.cp reads (atom j, row 32 a + b: byte b 16 + a 4 of atom j);
     // warp a takes rows 32 a ..: one warp for all four took 1480 cycles a
     // stage where rows are not 16-byte multiples
-    const int a = warp - 8, r = 32 * a + lane;
+    const int a = warp - 8, r = tc_row(kTma, 32 * a + lane);
     const bool aligned = !p.unit_scales || nb % 16 == 0;
     uint32_t nan_bits = 0, it = 0, units = 0;
     tc_pieces(x0, x1, n_st, RT, [&](const TcPiece& pc) {
@@ -736,56 +756,37 @@ __global__ void __launch_bounds__(576, 1)
     if (__any_sync(0xFFFFFFFFu, (nan_bits & 0x80808080u) != 0u) && lane == 0)
       raise_status(p.status, NVFP4_ERR_NONFINITE);
   } else if constexpr (!kTma) {
-    // ---------------- weight codes in 8-byte pieces (rows that are not a
-    // 16-byte multiple)
-    constexpr int kRowsAt = kTcLoaderWarps * 2;  // rows of one round: 16 lanes a row
-    const int tid = threadIdx.x - kTcThreads;
-    const int64_t rb = p.K / 2;
-    const int r_in = tid >> 4, o = (tid & 15) * 8;
-    const uint32_t to = r_in * 128 + (((o >> 4) ^ (r_in & 7)) << 4) + (o & 8);
-    uint32_t it = 0, landed = 0;
-    bool ok = true;
-    auto land = [&]() {
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&full[landed % ring]);
-      ++landed;
-    };
+    // ---------------- the odd rows into place: eight lanes a row
+    const int tid = threadIdx.x - kTcThreads, row = tid >> 3, c = tid & 7;
+    uint32_t it = 0;
     tc_pieces(x0, x1, n_st, RT, [&](const TcPiece& pc) {
-      const int64_t r0 = (int64_t)tile_at(pc.tile).expert * p.N + pc.rt * 128 + r_in;
-      const int rows = (int)min((int64_t)128, p.rows - r0);  // from r0 on
-      const uint8_t* src = p.codes + r0 * rb + o;
       for (int kb = pc.kb0; kb < pc.kb1; ++kb, ++it) {
         const uint32_t st = it % ring, ph = (it / ring) & 1;
-        ok = warp_wait(&empty[st], ph ^ 1, wc);
-        if (!ok) return false;
-        const uint32_t dst = smem_u32(s_a + st * kTcAStage) + to;
-        const int64_t c = (int64_t)kb * 128;
-        const bool in_row = c + o < rb;
+        if (!warp_wait(&empty[st], ph ^ 1, wc) || !warp_wait(&odd_full[st], ph, wc)) return false;
+        const uint32_t from = smem_u32(s_odd + st * kTcOddStage) + row * kTcOddRow + 8 + 16 * c;
+        const uint32_t to = smem_u32(s_a + st * kTcAStage) + kTcAStage / 2 + row * 128 +
+                            ((c ^ (row & 7)) << 4);
+        uint32_t v[4][4];
 #pragma unroll
-        for (int q = 0; q < 128 / kRowsAt; ++q) {
-          const bool in = in_row && q * kRowsAt < rows;
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst + q * kRowsAt * 128),
-                       "l"(in ? src + c + q * kRowsAt * rb : p.codes), "r"(in ? 8 : 0)
+        for (int q = 0; q < 4; ++q) {  // 16 rows at a time
+          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                       : "=r"(v[q][0]), "=r"(v[q][1])
+                       : "r"(from + q * 16 * kTcOddRow));
+          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                       : "=r"(v[q][2]), "=r"(v[q][3])
+                       : "r"(from + q * 16 * kTcOddRow + 8));
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + q * 16 * 128),
+                       "r"(v[q][0]), "r"(v[q][1]), "r"(v[q][2]), "r"(v[q][3])
                        : "memory");
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        // all but one of the ring's stages stay in flight (it has 4 or more)
-        if (ring >= 6) {
-          asm volatile("cp.async.wait_group 4;" ::: "memory");
-          if (it >= 4) land();
-        } else if (ring == 5) {
-          asm volatile("cp.async.wait_group 3;" ::: "memory");
-          if (it >= 3) land();
-        } else {
-          asm volatile("cp.async.wait_group 2;" ::: "memory");
-          if (it >= 2) land();
-        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[st]);
       }
       return true;
     });
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    while (ok && landed < it) land();
   }
 
   __syncthreads();
@@ -1057,23 +1058,31 @@ static cudaError_t tc_carveout_once(std::atomic<uint64_t>& done, const void* ker
 }
 
 static cudaError_t tc_gemm_launch(TcGemm g, int grid, cudaStream_t stream) {
-  CUtensorMap tm = {}, tm_s = {};
-  const bool tma = g.K % 32 == 0;  // the code rows' stride for TMA
+  CUtensorMap tm = {}, tm_2 = {};
+  const bool tma = g.K % 32 == 0;  // TMA steps from row to row
   // two units' scales, or as many as 20 KB hold: the next unit's are asked for
   // one buffer round ahead (K = 768, 64 tokens: 23 us with two)
   g.unit_scales = g.K > kTcMaxUnitK
                       ? 0
                       : std::max(2, std::min(kTcMaxUnits, (int)((20 << 10) / tc_unit_bytes(g.K))));
-  if (tma && !encode_2d(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.codes, (uint64_t)g.K / 2,
-                        (uint64_t)g.rows, (uint64_t)g.K / 2, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+  const uint64_t row = (uint64_t)g.K / 2;
+  if (tma ? !encode_2d(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.codes, row, (uint64_t)g.rows, row, 128,
+                       128, CU_TENSOR_MAP_SWIZZLE_128B)
+          // (an even number of rows: N is a multiple of 16)
+          : !encode_2d(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.codes, row, (uint64_t)g.rows / 2,
+                       2 * row, 128, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+                !encode_2d(&tm_2, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.codes + row - 8, row + 8,
+                           (uint64_t)g.rows / 2, 2 * row, kTcOddRow, 64,
+                           CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorUnknown;
-  if (!g.unit_scales &&
-      !encode_2d(&tm_s, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.scales, (uint64_t)g.K / 16,
+  if (!g.unit_scales &&  // (K % 256 == 0)
+      !encode_2d(&tm_2, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.scales, (uint64_t)g.K / 16,
                  (uint64_t)g.rows, (uint64_t)g.K / 16, 16, 128, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorUnknown;
-  // 26 to 38 KB a stage beside the units' scales: 4 to 7 stages
+  // 26 to 47 KB a stage beside the units' scales: 4 to 7 stages
   const size_t stage =
-      kTcAStage + tc_b_stage(g.cap, g.pieces) + (g.unit_scales ? 2 : 3) * (size_t)kTcSfStage;
+      kTcAStage + tc_b_stage(g.cap, g.pieces) + (g.unit_scales ? 2 : 3) * (size_t)kTcSfStage +
+      (tma ? 0 : kTcOddStage);
   const size_t budget = g.cap <= 16 ? kTcSmem : kTcSmemLarge;
   const size_t units = g.unit_scales * (size_t)tc_unit_bytes(g.K);
   g.ring = (int)std::min<size_t>((budget - 1024 - units) / stage, kTcMaxRing);
@@ -1083,8 +1092,8 @@ static cudaError_t tc_gemm_launch(TcGemm g, int grid, cudaStream_t stream) {
   const cudaError_t err =
       smem_limit_once(limit_set[tma], reinterpret_cast<const void*>(kern), kTcSmemLarge);
   if (err != cudaSuccess) return err;
-  PdlLaunch l(dim3((unsigned)grid), dim3(kTcThreads + (tma ? 0 : 32 * kTcLoaderWarps)), smem, stream);
-  return cudaLaunchKernelEx(&l.cfg, kern, tm, tm_s, g);
+  PdlLaunch l(dim3((unsigned)grid), dim3(kTcThreads + (tma ? 0 : 32 * kTcOddWarps)), smem, stream);
+  return cudaLaunchKernelEx(&l.cfg, kern, tm, tm_2, g);
 }
 
 nvfp4_status moe_tc_launch(const void* x, int64_t M, int64_t k, int64_t H, int64_t I, int64_t E,
