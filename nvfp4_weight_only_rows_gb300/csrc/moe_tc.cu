@@ -49,9 +49,9 @@ constexpr uint32_t kTcSfStage = 4 * 512;    // 4 atoms of 128 rows x 4 blocks
 constexpr uint32_t kTcRow = 128;            // bytes of a piece in a stage
 constexpr int kTcMaxRing = 8;
 // Dynamic shared memory of a product's CTA: what lets a CTA of the prep kernel
-// share its SM where tiles are small (64 of 152 CTAs began 5 us late without),
-// else what there is.
-constexpr size_t kTcSmem = 205 << 10, kTcSmemLarge = 220 << 10;
+// share its SM (64 of 152 CTAs began 5 us late without; 193 tokens: 67.7 us
+// against 68.7 with 220 KB and one stage more).
+constexpr size_t kTcSmem = 205 << 10;
 constexpr int kTcMaxCap = 20;               // pairs of a tile
 constexpr int64_t kTcMaxUnitK = 4096;       // largest K whose 128 rows of scales are loaded at once
 constexpr int kTcSfCols = 32;               // TMEM columns of a stage's scales: A 16 + B 16
@@ -1079,18 +1079,17 @@ static cudaError_t tc_gemm_launch(TcGemm g, int grid, cudaStream_t stream) {
       !encode_2d(&tm_2, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.scales, (uint64_t)g.K / 16,
                  (uint64_t)g.rows, (uint64_t)g.K / 16, 16, 128, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorUnknown;
-  // 26 to 47 KB a stage beside the units' scales: 4 to 7 stages
+  // 24 to 47 KB a stage beside the units' scales: 3 to 7 stages
   const size_t stage =
       kTcAStage + tc_b_stage(g.cap, g.pieces) + (g.unit_scales ? 2 : 3) * (size_t)kTcSfStage +
       (tma ? 0 : kTcOddStage);
-  const size_t budget = g.cap <= 16 ? kTcSmem : kTcSmemLarge;
   const size_t units = g.unit_scales * (size_t)tc_unit_bytes(g.K);
-  g.ring = (int)std::min<size_t>((budget - 1024 - units) / stage, kTcMaxRing);
+  g.ring = (int)std::min<size_t>((kTcSmem - 1024 - units) / stage, kTcMaxRing);
   const size_t smem = 1024 + units + (size_t)g.ring * stage;
   static std::atomic<uint64_t> limit_set[2];
   auto kern = tma ? moe_tc_kernel<true> : moe_tc_kernel<false>;
   const cudaError_t err =
-      smem_limit_once(limit_set[tma], reinterpret_cast<const void*>(kern), kTcSmemLarge);
+      smem_limit_once(limit_set[tma], reinterpret_cast<const void*>(kern), kTcSmem);
   if (err != cudaSuccess) return err;
   PdlLaunch l(dim3((unsigned)grid), dim3(kTcThreads + (tma ? 0 : 32 * kTcOddWarps)), smem, stream);
   return cudaLaunchKernelEx(&l.cfg, kern, tm, tm_2, g);
