@@ -516,10 +516,21 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_gemm_kernel(const MoeArgs 
 }
 
 // out[m, :] = sum over the slots j of w[m, j] G2[e] y[m k + j, :], four
-// columns a thread.
+// columns a thread; the row of CTAs past the tokens reads the flags.
 template <bool kBf16>
 __global__ void __launch_bounds__(256) moe_combine_kernel(const MoeArgs p, int n_flags) {
   const int m = blockIdx.y, c = blockIdx.x * blockDim.x + threadIdx.x;
+  if (m == p.M) {
+    grid_dependency_wait();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (blockIdx.x != 0) return;
+    int bad = 0;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < n_flags; i += blockDim.x) bad |= __ldcg(p.nan_flags + i);
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0) *p.status = bad ? NVFP4_ERR_NONFINITE : NVFP4_OK;
+    return;
+  }
   constexpr int kAt = 8;  // slots whose loads are in flight together
   float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   bool waited = false;
@@ -563,12 +574,6 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const MoeArgs p, int n
     } else {
       reinterpret_cast<float4*>(p.out)[at] = sum;
     }
-  }
-  if (blockIdx.x == 0 && blockIdx.y == 0) {
-    int bad = 0;
-    for (int i = threadIdx.x; i < n_flags; i += blockDim.x) bad |= __ldcg(p.nan_flags + i);
-    bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0) *p.status = bad ? NVFP4_ERR_NONFINITE : NVFP4_OK;
   }
 }
 
@@ -687,7 +692,7 @@ nvfp4_status moe_launch(const void* x, int64_t M, int64_t k, int64_t H, int64_t 
     err = split ? moe_gemm_launch<2, true>(a, wide(p2, s2, I), grid, stream)
                 : moe_gemm_launch<2, false>(a, wide(p2, s2, I), grid, stream);
   if (err == cudaSuccess) {
-    PdlLaunch l(dim3((unsigned)((H / 4 + 255) / 256), (unsigned)M), dim3(256), 0, stream);
+    PdlLaunch l(dim3((unsigned)((H / 4 + 255) / 256), (unsigned)M + 1), dim3(256), 0, stream);
     err = out_dtype == NVFP4_OUT_BF16
               ? cudaLaunchKernelEx(&l.cfg, moe_combine_kernel<true>, a, 2 * grid)
               : cudaLaunchKernelEx(&l.cfg, moe_combine_kernel<false>, a, 2 * grid);
