@@ -597,7 +597,7 @@ size_t w4a16_moe_workspace_bytes(int64_t M, int64_t k, int64_t H, int64_t I);
  * per 8 to 32 pairs and multiplied as fp16, each product x * w exact, h
  * rounded to 11 bits for a bf16 result and to 22 for an fp32 one (values far
  * below the largest of 256 of them keep an absolute 2^-40 of it).  With more
- * (M * k * H * I >= 2^26 or M * k >= 6 E; k <= 64, and H and I at most 4096 or
+ * (M * k * H * I >= 48 * 2^20 or M * k >= 6 E; k <= 64, and H and I at most 4096 or
  * multiples of 256) the FP4 tensor cores read the weights as they are, once
  * per 8 to 20 pairs, and x and h are given to them as sums of NVFP4 values:
  * to 3e-5 of the largest of 16 of them for a bf16 result and to 1e-6 for an

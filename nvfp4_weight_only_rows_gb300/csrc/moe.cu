@@ -35,7 +35,7 @@
 // warps; a tile cut between warps is joined in shared memory in warp order.
 //
 // Measured: 1 token of H 2048, I 768, top 8 of 128 (21 MB, 3.2 us at the copy
-// rate) 14.4 us, most of it the latency of three dependent kernels' first
+// rate) 14.3 us, most of it the latency of three dependent kernels' first
 // loads and of the boundaries between them.
 #include <cuda_fp16.h>
 
@@ -599,15 +599,16 @@ nvfp4_status moe_tc_launch(const void* x, int64_t M, int64_t k, int64_t H, int64
                            const uint8_t* s2, const float* g2, void* out, int out_dtype,
                            void* workspace, cudaStream_t stream);
 
-// The FP4 tensor-core route (moe_tc.cu: five kernels instead of three, but 6
-// TB/s between them) is taken for more weight than about 113 MB counted once
+// The FP4 tensor-core route (moe_tc.cu: five kernels instead of three, but 7
+// TB/s between them) is taken for more weight than about 85 MB counted once
 // per pair (27/16 byte per element of an H x I matrix), or for 6 pairs an
 // expert, where the products here turn from bandwidth to issue bound.
-// Measured (here / there): 1 token of H 2048, I 768, top 8 of 128 14.8 / 28.9
-// us, 4 tokens 33.5 / 37.8, 8 tokens 46.9 / 45.8, 16 tokens 64.0 / 54.9; H 1024,
-// I 512, top 2 of 64: 32 tokens 23.3 / 27.0, 64 tokens 32.5 / 30.2; H 512, I
-// 256, top 2 of 16: 32 tokens 16.6 / 17.5, 128 tokens 31.6 / 22.4.
-constexpr int64_t kMoeFewWork = 64 << 20;
+// Measured (here / there): H 2048, I 768, top 8 of 128: 1 token 13.9 / 24.1 us,
+// 3 tokens 28.2 / 30.2, 4 tokens 32.0 / 32.3, 6 tokens 40.2 / 36.6; H = I = 2880,
+// top 4 of 32: 1 token 26.3 / 30.6, 2 tokens 40.2 / 36.0; H 1024, I 512, top 2 of
+// 64: 32 tokens 23.0 / 23.3, 48 tokens 27.6 / 24.8; H 512, I 256, top 2 of 16:
+// 32 tokens 16.2 / 17.1, 48 tokens 18.3 / 17.8, 128 tokens 30.1 / 21.0.
+constexpr int64_t kMoeFewWork = 48 << 20;
 constexpr int64_t kMoeFewPairs = 6;
 static bool moe_use_tc(int64_t M, int64_t k, int64_t H, int64_t I, int64_t E) {
   const int64_t P = M * k;
