@@ -27,12 +27,13 @@
 // The products derive the tiles from the expert ids themselves, so that
 // their weight loads start while the kernel before them still runs.
 //
-// Measured (bf16 result, H 2048, I 768, top 8 of 128): 64 tokens, 335 MB, 74.6
-// us, 6.9 TB/s between a product's first and last MMA, about 20 us of prep, h,
-// combine, kernel boundaries and first loads around them.  5 tokens of H = I =
-// 2880, top 4 of 32, 221 MB: 57.8 us.  193 tokens of 64 experts with I 720 and
-// half the pairs elsewhere, 159 MB: 74.3 us, bound by the ring's latency (12
-// pairs an expert, K % 32 != 0 in the second product).
+// Measured (bf16 result, H 2048, I 768, top 8 of 128): 64 tokens, 112 experts
+// in use, 297 MB, 72.1 us, 6.9 and 6.0 TB/s between the products' first and last MMA,
+// about 25 us of prep, h, combine, kernel boundaries and first loads around
+// them.  5 tokens of H = I = 2880, top 4 of 32, 224 MB: 56.3 us.  193 tokens of
+// 64 experts with I 720 and half the pairs elsewhere, 144 MB: 67.7 us; the 14
+// second tiles of experts with more than 20 pairs cost as much time as first
+// ones, although they find their weights in L2.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -491,9 +492,11 @@ __global__ void __launch_bounds__(576, 1)
   uint8_t* s_sfa = s_b + ring * b_stage;
   uint8_t* s_sfb = s_sfa + ring * kTcSfStage;
   uint8_t* s_odd = s_sfb + ring * kTcSfStage;
-  uint8_t* s_raw = s_odd + (kTma ? 0 : ring * kTcOddStage);  // scales as stored: a slot a stage, or whole units
+  // scales as stored: a slot a stage, or whole units
+  uint8_t* s_raw = s_odd + (kTma ? 0 : ring * kTcOddStage);
   __shared__ TcTables s_tab;
-  __shared__ uint64_t full[kTcMaxRing], empty[kTcMaxRing], raw_full[kTcMaxRing], raw_empty[kTcMaxUnits];
+  __shared__ uint64_t full[kTcMaxRing], empty[kTcMaxRing];
+  __shared__ uint64_t raw_full[kTcMaxRing], raw_empty[kTcMaxUnits];
   __shared__ uint64_t odd_full[kTcMaxRing], d_full[2], d_empty[2], done_bar;
   __shared__ uint32_t tmem_slot;
   __shared__ int32_t s_abort;
@@ -569,7 +572,8 @@ __global__ void __launch_bounds__(576, 1)
             tma_load_2d_hint(s_a + st * kTcAStage, &tm_w, kb * 128, r0, &full[st], once);
           } else {
             mbar_arrive_expect_tx(&odd_full[st], kTcOddStage);
-            tma_load_2d_hint(s_odd + st * kTcOddStage, &tm_2, kb * 128, r0 / 2, &odd_full[st], once);
+            tma_load_2d_hint(s_odd + st * kTcOddStage, &tm_2, kb * 128, r0 / 2, &odd_full[st],
+                             once);
             mbar_arrive_expect_tx(&full[st], kTcAStage / 2);
             tma_load_2d_hint(s_a + st * kTcAStage, &tm_w, kb * 128, r0 / 2, &full[st], once);
           }

@@ -173,6 +173,15 @@ def test_moe_wide(M, E, k, H, I, out_dtype):
     check(nv.w4a16_moe(*on_gpu(*args), out_dtype=out_dtype), args)
 
 
+# rows of an odd number of 8-byte pieces, at the longest and the shortest
+@pytest.mark.parametrize("M,E,k,H,I", [(16, 8, 4, 4080, 2864), (24, 4, 2, 48, 4080),
+                                       (32, 5, 1, 16, 16), (60, 9, 3, 1008, 176)])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+def test_moe_wide_odd_rows(M, E, k, H, I, out_dtype):
+    args = make(M, E, k, H, I, seed=2 * H + I)
+    check(nv.w4a16_moe(*on_gpu(*args), out_dtype=out_dtype), args)
+
+
 def test_moe_wide_absent_repeated_special_and_dirty():
     x, ids, w, w13, w2 = make(64, 16, 8, 512, 256, seed=15, absent=0.4)
     ids[0] = -1
