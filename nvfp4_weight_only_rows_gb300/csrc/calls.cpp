@@ -135,6 +135,15 @@ void* stream_of(PyObject* o) {
   return s;
 }
 
+// A tensor allocated here, by the current stream's order, that kernels of
+// another stream use: its memory is not given out again before they are done.
+void used_on(const at::Tensor& t, void* stream, PyObject* given) {
+  if (given == Py_None) return;  // the current stream
+  const auto s = static_cast<cudaStream_t>(stream);
+  if (s != c10::cuda::getCurrentCUDAStream().stream())
+    t.record_stream(c10::cuda::getStreamFromExternal(s, t.get_device()).unwrap());
+}
+
 // The package's own exception for a status that is not NVFP4_OK.
 void done(nvfp4_status st, const char* where) {
   if (st == NVFP4_OK) return;
@@ -208,11 +217,14 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
       ids = result(a[6], at::kInt, "expert_ids", {M, kk}, x);
       w = result(a[7], at::kFloat, "weights", {M, kk}, x);
     }
+    void* stream = stream_of(a[8]);
     done(moe_route(x.data_ptr(), code, M, E, k, (int)integer(a[3]), (int)integer(a[2]),
                    static_cast<const float*>(bias), number(a[5]),
                    static_cast<int32_t*>(ids.data_ptr()), static_cast<float*>(w.data_ptr()),
-                   stream_of(a[8])),
+                   stream),
          "moe_route");
+    if (a[6] == Py_None) used_on(ids, stream, a[8]);
+    if (a[7] == Py_None) used_on(w, stream, a[8]);
     return tuple({ids, w});
   });
 }
@@ -250,13 +262,16 @@ PyObject* moe(PyObject*, PyObject* const* a, Py_ssize_t n) {
                         x.options().dtype(at::kByte))
             : tensor(a[11], "workspace");
     if (!ws.is_cuda()) throw ValueError("workspace must be a CUDA tensor");
+    void* stream = stream_of(a[12]);
     using u8 = const uint8_t*;
     using f32 = const float*;
     done(w4a16_moe(x.data_ptr(), M, k, H, I, E, static_cast<const int32_t*>(ids.data_ptr()),
                    f32(w.data_ptr()), u8(p13.data_ptr()), u8(s13.data_ptr()), f32(g13.data_ptr()),
                    u8(p2.data_ptr()), u8(s2.data_ptr()), f32(g2.data_ptr()), out.data_ptr(), code,
-                   ws.data_ptr(), (size_t)ws.numel() * ws.element_size(), stream_of(a[12])),
+                   ws.data_ptr(), (size_t)ws.numel() * ws.element_size(), stream),
          "w4a16_moe");
+    if (a[9] == Py_None) used_on(out, stream, a[12]);
+    if (a[11] == Py_None) used_on(ws, stream, a[12]);
     return THPVariable_Wrap(out);
   });
 }
@@ -288,11 +303,13 @@ PyObject* logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
     at::Tensor &lp = *r.add(at::kFloat, {l.M}), &ent = *r.add(at::kFloat, {l.M});
     at::Tensor &lse = *r.add(at::kFloat, {l.M}), &top = *r.add(at::kFloat, {l.M, kk});
     r.allocate(x);
+    void* stream = stream_of(a[4]);
     auto pf = [](const at::Tensor& t) { return static_cast<float*>(t.data_ptr()); };
     auto pi = [](const at::Tensor& t) { return static_cast<int64_t*>(t.data_ptr()); };
     done(token_logprobs(x.data_ptr(), l.code, l.M, l.N, l.ld, pi(tok), number(a[3]), k, pf(lp),
-                        pf(ent), pf(lse), pi(ranks), pi(ids), pf(top), stream_of(a[4])),
+                        pf(ent), pf(lse), pi(ranks), pi(ids), pf(top), stream),
          "token_logprobs");
+    used_on(lp, stream, a[4]);  // all six: one allocation
     return tuple({lp, ent, lse, ranks, ids, top});
   });
 }
@@ -317,12 +334,14 @@ PyObject* logprobs_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
           (l.N > 1 && out.stride(1) != 1))
         throw ValueError("out must be a CUDA tensor of the logits' shape and dtype, rows contiguous");
     }
+    void* stream = stream_of(a[8]);
     using f32 = const float*;
     done(token_logprobs_backward(x.data_ptr(), l.code, l.M, l.N, l.ld,
                                  static_cast<const int64_t*>(tok.data_ptr()), number(a[6]),
                                  f32(lse.data_ptr()), f32(ent), f32(g.data_ptr()), f32(ge),
-                                 out.data_ptr(), l.M > 1 ? out.stride(0) : l.N, stream_of(a[8])),
+                                 out.data_ptr(), l.M > 1 ? out.stride(0) : l.N, stream),
          "token_logprobs_backward");
+    if (a[7] == Py_None) used_on(out, stream, a[8]);
     return THPVariable_Wrap(out);
   });
 }

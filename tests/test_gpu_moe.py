@@ -369,3 +369,27 @@ def test_moe_empty_batch_and_refusals():
         nv.moe_route(torch.zeros(2, 8, device="cuda"), 2, scoring="relu")
     with pytest.raises(nv.NVFP4Error):
         nv.moe_route(torch.zeros(2, 8, device="cuda"), 9)
+
+
+def test_memory_of_a_call_on_another_stream_is_not_given_out_early():
+    args = make(64, 16, 4, 512, 256, seed=21)
+    dev = on_gpu(*args)
+    logits = torch.randn(64, 16, device="cuda")
+    n = nv.w4a16_moe_workspace_bytes(64, 4, 512, 256)
+
+    def fill():
+        return [torch.full((b,), 255, dtype=torch.uint8, device="cuda") for b in (n, n, 4096, 4096)]
+
+    nv.w4a16_moe(*dev)  # every kernel is loaded before the clock runs
+    nv.moe_route(logits, 4)
+    assert all(bool((j == 255).all()) for j in fill())
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(40_000_000)  # the calls below wait for some 20 ms
+    out = nv.w4a16_moe(*dev, stream=s)
+    nv.moe_route(logits, 4, stream=s)
+    junk = fill()
+    torch.cuda.synchronize()
+    assert all(bool((j == 255).all()) for j in junk)
+    check(out, args)
