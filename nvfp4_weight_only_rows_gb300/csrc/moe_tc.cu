@@ -675,6 +675,9 @@ __global__ void __launch_bounds__(576, 1)
       __syncwarp();
       return true;
     });
+    // What comes next reads the prep kernel's places ahead of its own wait: a
+    // CTA without work lets it start no sooner than that kernel is complete.
+    grid_dependency_wait();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (elect_one()) tc_commit(&done_bar);
     __syncwarp();
@@ -757,8 +760,10 @@ __global__ void __launch_bounds__(576, 1)
       return true;
     });
     // a block scale that is NaN (0x7F or 0xFF: never loaded)
-    if (__any_sync(0xFFFFFFFFu, (nan_bits & 0x80808080u) != 0u) && lane == 0)
-      raise_status(p.status, NVFP4_ERR_NONFINITE);
+    if (__any_sync(0xFFFFFFFFu, (nan_bits & 0x80808080u) != 0u)) {
+      grid_dependency_wait();  // the prep kernel clears the status
+      if (lane == 0) raise_status(p.status, NVFP4_ERR_NONFINITE);
+    }
   } else if constexpr (!kTma) {
     // ---------------- the odd rows into place: eight lanes a row
     const int tid = threadIdx.x - kTcThreads, row = tid >> 3, c = tid & 7;

@@ -393,3 +393,14 @@ def test_memory_of_a_call_on_another_stream_is_not_given_out_early():
     torch.cuda.synchronize()
     assert all(bool((j == 255).all()) for j in junk)
     check(out, args)
+
+
+@pytest.mark.parametrize("M,k", [(300, 8), (2048, 2)])
+def test_moe_wide_without_any_expert(M, k):
+    """Nothing for either product, places of an earlier use in the workspace."""
+    x, ids, w, *weights = on_gpu(*make(M, 8, k, 256, 144, seed=31))
+    ws = torch.empty(nv.w4a16_moe_workspace_bytes(M, k, 256, 144), dtype=torch.uint8, device="cuda")
+    none = torch.full_like(ids, -1)
+    for fill in (0, 1, 127, 255) * 5:
+        ws.fill_(fill)
+        assert bool((nv.w4a16_moe(x, none, w, *weights, workspace=ws) == 0).all())
