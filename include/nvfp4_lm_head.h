@@ -594,9 +594,9 @@ size_t w4a16_moe_workspace_bytes(int64_t M, int64_t k, int64_t H, int64_t I);
  *                16-byte aligned.
  *   workspace    >= w4a16_moe_workspace_bytes(M, k, H, I), 256-byte aligned.
  * Two routes, by the sizes: with few pairs an expert's weights are read once
- * per 8 to 32 pairs and multiplied as fp16, each product x * w exact, h
- * rounded to 11 bits for a bf16 result and to 22 for an fp32 one (values far
- * below the largest of 256 of them keep an absolute 2^-40 of it).  With more
+ * per 8 to 32 pairs and multiplied as fp16, each product x * w exact, h held
+ * to 22 bits (values of x and h far below the largest of 256 of them keep an
+ * absolute 2^-39 of it).  With more
  * (M * k * H * I >= 48 * 2^20 or M * k >= 6 E; k <= 64, and H and I at most 4096 or
  * multiples of 256) the FP4 tensor cores read the weights as they are, once
  * per 8 to 20 pairs, and x and h are given to them as sums of NVFP4 values:

@@ -26,16 +26,16 @@
 // Activations: a stage (256 k of a pair) is carried as fp16 after a
 // power-of-two rescale by the stage's largest magnitude (exact for bf16 x
 // within 2^28 of that maximum), built by each CTA in shared memory.  h, an
-// fp32 value, is rounded to fp16's 11 bits for a bf16 result (an eighth of
-// that result's own rounding); for an fp32 result it is carried as two fp16,
-// 22 bits, at twice the MMAs of the second product.
+// fp32 value, is carried as two fp16, 22 bits, at twice the MMAs of the second
+// product.  (One fp16 moved a bf16 result by 9e-4 of it, half of that result's
+// own rounding, and saved 0.7 us at one token.)
 //
 // Work: the items (expert segment, 16-row tile) are split evenly over the
 // CTAs, and inside a CTA the (tile, stage) steps of a segment evenly over its
 // warps; a tile cut between warps is joined in shared memory in warp order.
 //
 // Measured: 1 token of H 2048, I 768, top 8 of 128 (21 MB, 3.2 us at the copy
-// rate) 14.3 us, most of it the latency of three dependent kernels' first
+// rate) 14.9 us, most of it the latency of three dependent kernels' first
 // loads and of the boundaries between them.
 #include <cuda_fp16.h>
 
@@ -333,8 +333,9 @@ __device__ __forceinline__ void moe_steps(MoeStream<kWide>& in, int N, int n_sta
   if (s != 0) flush(false);
 }
 
-template <int kStep, bool kWide, bool kSplit>
+template <int kStep, bool kWide>
 __global__ void __launch_bounds__(kMoeThreads, 2) moe_gemm_kernel(const MoeArgs p) {
+  constexpr bool kSplit = kStep == 2;  // h; x is exact
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int s_cnt[kMoeMaxExperts];
   __shared__ int s_exp[kMoeMaxExperts];   // active experts
@@ -621,27 +622,30 @@ size_t moe_workspace_bytes(int64_t M, int64_t k, int64_t H, int64_t I) {
   return moe_tc_takes(k, H, I) ? std::max(few, moe_tc_workspace_bytes(M, k, H, I)) : few;
 }
 
+// Bytes of a pair's activations in a stage: x as one fp16, h as two.
+static int64_t moe_stage_bytes(int step) { return step == 1 ? 512 : 1024; }
+
 // Pairs of a segment: what fits the activation budget, in whole tiles of 8
 // where more than one does, but never more than an expert can have.
-static int moe_segment(int64_t K, int64_t pairs, bool split) {
-  const int64_t row = (K + 255) / 256 * (split ? 1024 : 512);
+static int moe_segment(int64_t K, int64_t pairs, int step) {
+  const int64_t row = (K + 255) / 256 * moe_stage_bytes(step);
   int64_t n = (int64_t)kMoeActBytes / row;
   n = n >= 8 ? std::min<int64_t>(n / 8 * 8, 8 * kMoeTileN) : std::max<int64_t>(n, 1);
   return (int)(n >= 8 ? n : std::min(n, pairs));
 }
 
-static size_t moe_smem(int64_t K, int seg, bool split) {
+static size_t moe_smem(int64_t K, int seg, int step) {
   const int64_t stages = (K + 255) / 256;
-  return (size_t)stages * (kMoeMulStride * sizeof(float) + (size_t)seg * (split ? 1024 : 512));
+  return (size_t)stages * (kMoeMulStride * sizeof(float) + (size_t)seg * moe_stage_bytes(step));
 }
 
-template <int kStep, bool kSplit>
+template <int kStep>
 static cudaError_t moe_gemm_launch(const MoeArgs& a, bool wide, int grid, cudaStream_t stream) {
-  const size_t smem = moe_smem(kStep == 1 ? a.H : a.I, kStep == 1 ? a.seg1 : a.seg2, kSplit);
-  auto kern = wide ? moe_gemm_kernel<kStep, true, kSplit> : moe_gemm_kernel<kStep, false, kSplit>;
+  const size_t smem = moe_smem(kStep == 1 ? a.H : a.I, kStep == 1 ? a.seg1 : a.seg2, kStep);
+  auto kern = wide ? moe_gemm_kernel<kStep, true> : moe_gemm_kernel<kStep, false>;
   static std::atomic<uint64_t> limit_set[2];
   const cudaError_t err = smem_limit_once(limit_set[wide], reinterpret_cast<const void*>(kern),
-                                          moe_smem(NVFP4_MOE_MAX_DIM, 1, true));
+                                          moe_smem(NVFP4_MOE_MAX_DIM, 1, 2));
   if (err != cudaSuccess) return err;
   PdlLaunch l(dim3((unsigned)grid), dim3(kMoeThreads), smem, stream);
   return cudaLaunchKernelEx(&l.cfg, kern, a);
@@ -679,19 +683,16 @@ nvfp4_status moe_launch(const void* x, int64_t M, int64_t k, int64_t H, int64_t 
   a.H = (int)H;
   a.I = (int)I;
   a.E = (int)E;
-  const bool split = out_dtype == NVFP4_OUT_F32;
-  a.seg1 = moe_segment(H, M * k, false);
-  a.seg2 = moe_segment(I, M * k, split);
+  a.seg1 = moe_segment(H, M * k, 1);
+  a.seg2 = moe_segment(I, M * k, 2);
   // whole 32-byte pieces of every row
   auto wide = [](const uint8_t* codes, const uint8_t* scales, int64_t K) {
     return K % 64 == 0 && reinterpret_cast<uintptr_t>(codes) % 32 == 0 &&
            reinterpret_cast<uintptr_t>(scales) % 4 == 0;
   };
   const int grid = 2 * sms;
-  cudaError_t err = moe_gemm_launch<1, false>(a, wide(p13, s13, H), grid, stream);
-  if (err == cudaSuccess)
-    err = split ? moe_gemm_launch<2, true>(a, wide(p2, s2, I), grid, stream)
-                : moe_gemm_launch<2, false>(a, wide(p2, s2, I), grid, stream);
+  cudaError_t err = moe_gemm_launch<1>(a, wide(p13, s13, H), grid, stream);
+  if (err == cudaSuccess) err = moe_gemm_launch<2>(a, wide(p2, s2, I), grid, stream);
   if (err == cudaSuccess) {
     PdlLaunch l(dim3((unsigned)((H / 4 + 255) / 256), (unsigned)M + 1), dim3(256), 0, stream);
     err = out_dtype == NVFP4_OUT_BF16
