@@ -600,8 +600,8 @@ size_t w4a16_moe_workspace_bytes(int64_t M, int64_t k, int64_t H, int64_t I);
  * (M * k * H * I >= 48 * 2^20 or M * k >= 6 E; k <= 64, and H and I at most 4096 or
  * multiples of 256) the FP4 tensor cores read the weights as they are, once
  * per 8 to 20 pairs, and x and h are given to them as sums of NVFP4 values:
- * to 3e-5 of the largest of 16 of them for a bf16 result and to 1e-6 for an
- * fp32 one, or to 2e-6 of the largest of their row where that is more.  Block
+ * to 3e-5 of the largest of 16 of them plus 2e-8 of the largest of their row
+ * for a bf16 result, to 1e-6 plus 2e-9 for an fp32 one.  Block
  * scales must not be negative (no quantizer of this library writes such a
  * byte; the tensor cores' scales have no sign).  Sums are fp32 in a fixed
  * order (the result does not depend on the schedule).  An Inf or NaN in a token's x makes that token's result NaN or

@@ -5,12 +5,18 @@
 //
 // A row v (a token's x, a pair's h) times a power of two that takes its
 // largest magnitude to 2^10 .. 2^11 is split per 16 values into NVFP4 blocks,
-// r_0 = v: s_i = e4m3(max|r_i| / 6), q_i = e2m1(r_i / s_i), r_{i+1} = r_i - s_i q_i.
-// The largest error of a code is its scale, so a piece leaves at most 0.177
-// of the block's maximum: six of them 3e-5 (for a bf16 result, whose own
-// rounding is 2e-3), eight 1e-6 (for an fp32 result), or 2e-6 of the row's
-// maximum where the scales reach the E4M3 subnormals.  The pieces of a pair
-// are columns of the MMA's N side; their products, each exact, sum in fp32.
+// r_0 = v: s_i = e4m3(max|r_i| / 6), q_i = e2m1(r_i / s_i),
+// r_{i+1} = 4 (r_i - s_i q_i).  The largest error of a code is its scale, so a
+// piece leaves at most 0.177 of the block's maximum: six of them 3e-5 (for a
+// bf16 result: 6e-7 rms, which moves it by 3e-5 of itself where fp32 sums in
+// another order move it by 2e-5), eight 1e-6 (for an fp32 result).  The factor
+// 4 keeps the residuals' scales off the E4M3 subnormals, and a block far below
+// its row's maximum gets its first codes in a later piece: what is lost below
+// the subnormals is 2e-8 of the row's maximum after six pieces, 1.3e-9 after
+// eight (without it 6e-6, which one outlier channel of 3000 in a normal row
+// turned into 3e-3 of the product).  The pieces of a pair are columns of the
+// MMA's N side; their products, each exact, sum in fp32, and piece i's sum
+// counts 4^-i.
 //
 // The layer is bound by HBM (9/16 byte a weight), and this way the SMs only
 // move bytes: a 256-k stage of 128 weight rows is 18 KB, 800 cycles at the
@@ -177,6 +183,7 @@ __device__ __forceinline__ int tc_slot(int b, bool opened) { return 2 * b + (ope
 // this runs once and cold (unrolled, instruction fetch took longer than the
 // work).  v: this lane's values 8 lane .. of the stage, already times the row's
 // power of two.
+constexpr float kResidualUp = 4.0f;  // a residual's factor before the next piece
 constexpr int kSplitBytes = kPieces * (kTcRow + 16);
 
 __device__ __forceinline__ void tc_split(float (&v)[8], int pieces, uint8_t* buf) {
@@ -202,8 +209,8 @@ __device__ __forceinline__ void tc_split(float (&v)[8], int pieces, uint8_t* buf
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-      v[2 * i] = __fmaf_rn(-f.x, s, v[2 * i]);
-      v[2 * i + 1] = __fmaf_rn(-f.y, s, v[2 * i + 1]);
+      v[2 * i] = kResidualUp * __fmaf_rn(-f.x, s, v[2 * i]);
+      v[2 * i + 1] = kResidualUp * __fmaf_rn(-f.y, s, v[2 * i + 1]);
     }
     reinterpret_cast<uint32_t*>(buf + p * kTcRow)[lane] = w;
     if ((lane & 1) == 0) scales[p * 16 + (lane >> 1)] = (uint8_t)s8;
@@ -447,8 +454,8 @@ __host__ __device__ __forceinline__ uint32_t tc_unit_bytes(int K) {
 }
 
 // An epilogue thread's row of a tile's n pairs, four at a time:
-// out[c stride] = the sum of pair c's kNp columns, from the smallest
-// piece up, times its multiplier (lane c's mul).
+// out[c stride] = the sum of pair c's kNp columns, column q times 4^-q, from
+// the smallest piece up, times its multiplier (lane c's mul).
 template <int kNp>
 __device__ __forceinline__ void tc_drain(uint32_t taddr, int n, float mul, bool store, float* out,
                                          int64_t stride) {
@@ -468,7 +475,8 @@ __device__ __forceinline__ void tc_drain(uint32_t taddr, int n, float mul, bool 
         float sum = __uint_as_float(v[(h * kNp + kNp - 1) / 8][(h * kNp + kNp - 1) % 8]);
 #pragma unroll
         for (int q = kNp - 2; q >= 0; --q)
-          sum += __uint_as_float(v[(h * kNp + q) / 8][(h * kNp + q) % 8]);
+          sum = __fmaf_rn(sum, 1.0f / kResidualUp,
+                          __uint_as_float(v[(h * kNp + q) / 8][(h * kNp + q) % 8]));
         out[(c + h) * stride] = sum * m;
       }
     }

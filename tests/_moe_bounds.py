@@ -27,6 +27,18 @@ def held_two_fp16(v):
     return 2.0 ** -22 * v.abs() + 2.0 ** -39 * blocks_max(v, 256)
 
 
+def held_pieces(pieces):
+    """x and h on the FP4 route: at most 0.177 of a block of 16 is left by
+    each NVFP4 piece.  The residual is multiplied by 4 before the next, on a
+    row whose largest value is 2^10 .. 2^11; a scale below the E4M3 normals is
+    off by 2^-10, that is 6 2^-10 of a value, at 4^-q of the row's scale in
+    piece q.  Summed over the pieces that is below 3.5 times the last one's."""
+    def bound(v):
+        return 1.001 * 0.1771 ** pieces * blocks_max(v, 16) + \
+            3.5 * 6 * 2.0 ** -20 * 4.0 ** (1 - pieces) * v.abs().amax(1, keepdim=True)
+    return bound
+
+
 def layer(x, ids, weights, w13, w2, held_x, held_h, steps=16, hold=None):
     """(out, tolerance of an fp32 result), float64 [M, H].  hold(h): h as a route
     would hold it, for `out` (for tests of the bound itself).
@@ -65,6 +77,32 @@ def layer(x, ids, weights, w13, w2, held_x, held_h, steps=16, hold=None):
 
 
 # ------------------------------------------------- what the bounds tell apart
+_GRID = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def _e2m1(q):
+    """To the nearest code, ties to the even one."""
+    a = q.abs().clamp(max=6.0)
+    mid = (_GRID[1:] + _GRID[:-1]) / 2
+    i = torch.searchsorted(mid, a)
+    i = torch.where((i < 7) & (a == mid[i.clamp(max=6)]) & (i % 2 == 1), i + 1, i)
+    return torch.sign(q) * _GRID[i]
+
+
+def pieces_of(v, pieces, grow=4.0):
+    """v [rows, K] as `pieces` NVFP4 values, the residual times `grow` before each next."""
+    up = 2.0 ** (10 - torch.floor(torch.log2(v.abs().amax(1, keepdim=True))))
+    r = (v * up).float().unflatten(1, (-1, 16))
+    total, f = torch.zeros(r.shape, dtype=torch.float64), 1.0
+    for _ in range(pieces):
+        s = (r.abs().amax(2, keepdim=True) * (1 / 6)).clamp(max=448.0).to(torch.float8_e4m3fn).float()
+        q = _e2m1(torch.where(s == 0, 0.0, r / s))
+        total += (q * s).double() * f
+        r = (r - q * s) * grow
+        f /= grow
+    return total.flatten(1) / up.double()
+
+
 def one_fp16(v):
     up = 2.0 ** (14 - torch.floor(torch.log2(blocks_max(v, 256))))
     return (v * up).half().double() / up

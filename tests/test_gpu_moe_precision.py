@@ -51,3 +51,20 @@ def check(args, out_dtype, steps, held_x, held_h):
 def test_few_pairs(M, E, k, H, I, out_dtype, outlier):
     args = layer_args(M, E, k, H, I, outlier, seed=M + I)
     check(args, out_dtype, 8, mb.held_fp16, mb.held_two_fp16)
+
+
+@pytest.mark.parametrize("M,E,k,H,I", [(16, 4, 2, 256, 256), (40, 5, 3, 512, 128), (30, 4, 4, 336, 272)])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("outlier", [0, 30.0, 3000.0, 30000.0])
+def test_fp4_route(M, E, k, H, I, out_dtype, outlier):
+    args = layer_args(M, E, k, H, I, outlier, seed=M + I)
+    held = mb.held_pieces(6 if out_dtype == torch.bfloat16 else 8)
+    check(args, out_dtype, 16, held, held)
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("outlier", [3000.0, 30000.0])
+def test_fp4_route_beside_an_ignored_block(out_dtype, outlier):
+    args = layer_args(64, 4, 2, 2048, 32, outlier, seed=2, block=True)
+    held = mb.held_pieces(6 if out_dtype == torch.bfloat16 else 8)
+    check(args, out_dtype, 16, held, held)

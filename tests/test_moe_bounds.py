@@ -14,6 +14,29 @@ def rows(outlier, seed=0):
     return v.double()
 
 
+@pytest.mark.parametrize("outlier", [1.0, 30.0, 3000.0, 30000.0])
+@pytest.mark.parametrize("pieces", [6, 8])
+def test_pieces(outlier, pieces):
+    v = rows(outlier)
+    bound = mb.held_pieces(pieces)(v)
+    assert bool(((mb.pieces_of(v.float(), pieces) - v.float().double()).abs() <= bound).all())
+    # two pieces less, or all of a row on one scale (6e-6 of its largest: less
+    # than six pieces of a block leave, unless the block is far below the row)
+    if outlier >= 30.0 or pieces == 8:
+        flat = (mb.pieces_of(v.float(), pieces, 1.0) - v.float().double()).abs()
+        assert not bool((flat <= bound).all())
+    fewer = (mb.pieces_of(v.float(), pieces - 2) - v.float().double()).abs()
+    assert not bool((fewer <= bound).all())
+
+
+@pytest.mark.parametrize("at", [1e-3, 1e-5, 1e-7])
+def test_blocks_far_below_the_row(at):
+    v = rows(1.0)
+    v[:, 512:] *= at
+    v = v.float()
+    assert bool(((mb.pieces_of(v, 8) - v.double()).abs() <= mb.held_pieces(8)(v.double())).all())
+
+
 def test_two_fp16():
     v = rows(30.0).float().double()
     assert bool(((mb.two_fp16(v) - v).abs() <= mb.held_two_fp16(v)).all())
