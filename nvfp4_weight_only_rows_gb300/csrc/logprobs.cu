@@ -201,10 +201,12 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, unsigned long long v) 
 
 // Logits are held at or above this in the main pass, so that a masked one
 // (-inf) has a finite d and 0 d = 0.  What is held there has to vanish against
-// the largest logit; where it does not (a share with nothing else left, an
-// extreme temperature) the share is looked at again without the floor.
+// the largest logit, and its d to stay finite; where it does not (a share with
+// nothing else left, an extreme temperature, a largest logit near fp32's own)
+// the share is looked at again without the floor, with d held at -1e30.
 constexpr float kFloor = -0x1p83f;  // also a bf16
 constexpr float kMaxScale = 1e12f;  // times the floor: finite
+constexpr float kMinDrop = 1500.0f, kMaxDrop = 1e38f;  // -d of what is held there
 
 // T: float, or uint16_t for bf16 bits; kT threads; kU vectors of a batch, whose
 // loads are in flight together (4 let 1024 threads share an SM).
@@ -376,7 +378,8 @@ __global__ void __launch_bounds__(kT, kU == 4 ? 1024 / kT : 1) logprobs_kernel(c
     if (tid < singles) f(single);
   };
   // (block-uniform)
-  const bool plain = !(p.c * (m_blk - kFloor) >= 1500.0f) || p.c > kMaxScale;
+  const float drop = p.c * (m_blk - kFloor);
+  const bool plain = !(drop >= kMinDrop && drop <= kMaxDrop) || p.c > kMaxScale;
   if (!plain) {
     st = lp_shift(st, m_blk, p.c);
   } else {

@@ -1,0 +1,40 @@
+"""Token log probabilities at the ends of fp32's range: the largest finite
+logits."""
+import pytest
+import torch
+
+import nvfp4_weight_only_rows_gb300 as nv
+from tests.test_gpu_logprobs import check, make
+
+pytestmark = pytest.mark.gpu
+INF = float("inf")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__
+
+    __graft_entry__.build()
+    assert torch.cuda.is_available()
+
+
+def dominated(M, N, dtype, value):
+    """Rows of ordinary logits in which one is `value` (and in every other row
+    half of the others are masked)."""
+    x, tok = make(M, N, dtype, seed=N)
+    x[1::2, ::2] = -INF
+    x[torch.arange(M), torch.arange(M) * 7 % N] = value
+    tok[:2] = torch.arange(2) * 7 % N
+    return x, tok
+
+
+@pytest.mark.parametrize("M,N", [(3, 61), (6, 5003), (2, 70001), (130, 36001)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("s,value", [(1.0, None), (0.25, None), (0.75, 3.0e38), (100.0, 3.0e36),
+                                     (1.0e6, 1.0e31)])
+def test_a_logit_near_the_largest_number(M, N, dtype, s, value):
+    x, tok = dominated(M, N, dtype, torch.finfo(dtype).max if value is None else value)
+    s = float(torch.tensor(s, dtype=torch.float32))
+    got = nv.token_logprobs(x.cuda(), tok.cuda(), 3, inv_temperature=s)
+    check(got, x, tok, 3, s)
+    assert bool((got[1] == 0).all())
