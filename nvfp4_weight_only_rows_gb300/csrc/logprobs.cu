@@ -143,17 +143,6 @@ __device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Softmax state of a part of a row relative to its largest logit m.
-struct LpStats {
-  float m, S, T;
-};
-// ... seen from a maximum m >= a.m.  A part that vanishes adds nothing (the
-// product d S may have overflowed).
-__device__ __forceinline__ LpStats lp_shift(const LpStats& a, float m, float c) {
-  const float d = c * (a.m - m), e = ex2(d);
-  return {m, a.S * e, e == 0.0f ? 0.0f : e * __fmaf_rn(d, a.S, a.T)};
-}
-
 struct LpArgs {
   const void* logits;
   int64_t N, ld;
@@ -163,6 +152,25 @@ struct LpArgs {
   float *logprob, *entropy, *lse, *top_lp;
   int64_t *rank, *top_ids;
 };
+
+constexpr float kMaxScale = 1e12f;  // c in the main pass: times the floor below it is finite
+
+// c times a difference of logits; c itself is beyond fp32 for the largest
+// inverse temperatures.
+__device__ __forceinline__ float lp_scaled(const LpArgs& p, float d) {
+  return p.c <= kMaxScale ? p.c * d : kLog2e * (p.s * d);
+}
+
+// Softmax state of a part of a row relative to its largest logit m.
+struct LpStats {
+  float m, S, T;
+};
+// ... seen from a maximum m >= a.m.  A part that vanishes adds nothing (the
+// product d S may have overflowed).
+__device__ __forceinline__ LpStats lp_shift(const LpStats& a, float m, const LpArgs& p) {
+  const float d = lp_scaled(p, a.m - m), e = ex2(d);
+  return {m, a.S * e, e == 0.0f ? 0.0f : e * __fmaf_rn(d, a.S, a.T)};
+}
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -205,7 +213,6 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, unsigned long long v) 
 // nothing else left, an extreme temperature, a largest logit near fp32's own)
 // the share is looked at again without the floor, with d held at -1e30.
 constexpr float kFloor = -0x1p83f;  // also a bf16
-constexpr float kMaxScale = 1e12f;  // times the floor: finite
 constexpr float kMinDrop = 1500.0f, kMaxDrop = 1e38f;  // -d of what is held there
 
 // T: float, or uint16_t for bf16 bits; kT threads; kU vectors of a batch, whose
@@ -381,7 +388,7 @@ __global__ void __launch_bounds__(kT, kU == 4 ? 1024 / kT : 1) logprobs_kernel(c
   const float drop = p.c * (m_blk - kFloor);
   const bool plain = !(drop >= kMinDrop && drop <= kMaxDrop) || p.c > kMaxScale;
   if (!plain) {
-    st = lp_shift(st, m_blk, p.c);
+    st = lp_shift(st, m_blk, p);
   } else {
     const uint32_t wk = __reduce_max_sync(0xFFFFFFFFu, lp_key(largest));
     __syncthreads();
@@ -392,7 +399,7 @@ __global__ void __launch_bounds__(kT, kU == 4 ? 1024 / kT : 1) logprobs_kernel(c
     st = {m_blk, 0.0f, 0.0f};
     if (!(top < kLowest))  // (all -inf: nothing)
       for_each([&](float x) {
-        const float d = max_nan(p.c * (x - m_blk), -1e30f), e = ex2(d);
+        const float d = max_nan(lp_scaled(p, x - m_blk), -1e30f), e = ex2(d);
         st.S += e;
         st.T = __fmaf_rn(d, e, st.T);
       });
@@ -625,7 +632,7 @@ __global__ void __launch_bounds__(kT, kU == 4 ? 1024 / kT : 1) logprobs_kernel(c
 #pragma unroll
   for (int o = kLpMaxCluster / 2; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
   m = __shfl_sync(0xFFFFFFFFu, m, 0);
-  const LpStats a = lp_shift({part.x, part.y, part.z}, m, p.c);
+  const LpStats a = lp_shift({part.x, part.y, part.z}, m, p);
   const float S = warp_sum(a.S), t = warp_sum(a.T);
   const bool empty = S == 0.0f;  // every logit is -inf
   const float logS = empty ? __int_as_float(0xFF800000) : kLn2 * log2f(S);

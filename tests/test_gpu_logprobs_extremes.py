@@ -1,5 +1,5 @@
 """Token log probabilities at the ends of fp32's range: the largest finite
-logits."""
+logits, and temperatures near 2^-128."""
 import pytest
 import torch
 
@@ -38,3 +38,15 @@ def test_a_logit_near_the_largest_number(M, N, dtype, s, value):
     got = nv.token_logprobs(x.cuda(), tok.cuda(), 3, inv_temperature=s)
     check(got, x, tok, 3, s)
     assert bool((got[1] == 0).all())
+
+
+@pytest.mark.parametrize("N", [9, 5003, 70001])
+@pytest.mark.parametrize("s", [1.0e38, 2.5e38, 3.3e38])
+def test_temperature_near_zero(N, s):
+    g = torch.Generator().manual_seed(N)
+    x = torch.randn(4, N, generator=g) * 2e-38
+    x[1, ::2] = -INF
+    tok = torch.randint(0, N, (4,), generator=g)
+    tok[1] = 1
+    s = float(torch.tensor(s, dtype=torch.float32))
+    check(nv.token_logprobs(x.cuda(), tok.cuda(), 3, inv_temperature=s), x, tok, 3, s)
