@@ -688,8 +688,9 @@ __global__ void __launch_bounds__(kT) logprobs_grad_kernel(const LpGradArgs p) {
   const float c0 = b != 0.0f ? -(a + b * p.entropy[m]) : -a, c1 = -b;
   const bool empty = lse == __int_as_float(0xFF800000);  // no logit of the row is finite
   auto grad = [&](float x) {
-    // p log p = 0 at a logit of -inf: log p is held finite
-    const float lp = max_nan(__fmaf_rn(x, p.s, -lse), -1e30f);
+    // p log p = 0 at a logit of -inf: log p is held where p is zero already, and
+    // low enough that no gradient b of the entropy takes b log p to infinity
+    const float lp = max_nan(__fmaf_rn(x, p.s, -lse), -100.0f);
     return empty ? 0.0f : exp_neg(lp) * __fmaf_rn(c1, lp, c0);
   };
   const RowSplit rs = split_row(row, p.N);

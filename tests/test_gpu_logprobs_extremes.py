@@ -1,5 +1,5 @@
-"""Token log probabilities at the ends of fp32's range: the largest finite
-logits, and temperatures near 2^-128."""
+"""Token log probabilities and their gradient at the ends of fp32's range: the
+largest finite logits, temperatures near 2^-128, and large gradient weights."""
 import pytest
 import torch
 
@@ -50,3 +50,19 @@ def test_temperature_near_zero(N, s):
     tok[1] = 1
     s = float(torch.tensor(s, dtype=torch.float32))
     check(nv.token_logprobs(x.cuda(), tok.cuda(), 3, inv_temperature=s), x, tok, 3, s)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("b", [1e9, 1e30])
+def test_gradient_of_masked_columns_with_a_large_weight(dtype, b):
+    """p log p is 0 at a masked column whatever the entropy's gradient is."""
+    x, tok = make(5, 4099, dtype, seed=1)
+    x[:, ::2] = -INF
+    tok[:] = 1
+    _, ent, lse, *_ = nv.token_logprobs(x.cuda(), tok.cuda())
+    g = nv.token_logprobs_backward(x.cuda(), tok.cuda(), lse, ent, torch.zeros(5).cuda(),
+                                   torch.full((5,), b).cuda())
+    assert bool((g[:, ::2] == 0).all()) and bool(torch.isfinite(g).all())
+    one = nv.token_logprobs_backward(x.cuda(), tok.cuda(), lse, ent, torch.zeros(5).cuda(),
+                                     torch.ones(5).cuda())
+    assert bool(((g.double() / b - one.double()).abs() <= 2.0 ** -7 * one.double().abs() + 1e-30).all())
