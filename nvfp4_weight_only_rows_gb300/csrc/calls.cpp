@@ -9,6 +9,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
 #include <initializer_list>
@@ -122,10 +123,8 @@ float number(PyObject* o) {
   return (float)v;
 }
 
-// stream: None (the current device's current stream), a torch stream or an
-// integer handle.
+// A torch stream or an integer handle.
 void* stream_of(PyObject* o) {
-  if (o == Py_None) return c10::cuda::getCurrentCUDAStream().stream();
   PyObject* h = PyObject_HasAttrString(o, "cuda_stream") ? PyObject_GetAttrString(o, "cuda_stream")
                                                          : PyNumber_Long(o);
   if (!h) throw PyFailure();
@@ -135,14 +134,29 @@ void* stream_of(PyObject* o) {
   return s;
 }
 
-// A tensor allocated here, by the current stream's order, that kernels of
-// another stream use: its memory is not given out again before they are done.
-void used_on(const at::Tensor& t, void* stream, PyObject* given) {
-  if (given == Py_None) return;  // the current stream
-  const auto s = static_cast<cudaStream_t>(stream);
-  if (s != c10::cuda::getCurrentCUDAStream().stream())
-    t.record_stream(c10::cuda::getStreamFromExternal(s, t.get_device()).unwrap());
-}
+// The stream of a call: `given`, or the current one.  While this lives, memory
+// is allocated in the order of that stream, so that a block whose last use is
+// still queued on another stream is not given out to the call's kernels.
+class OnStream {
+ public:
+  OnStream(PyObject* given, const at::Tensor& like)
+      : caller_(c10::cuda::getCurrentCUDAStream()), handle_(caller_.stream()) {
+    if (given == Py_None) return;
+    handle_ = static_cast<cudaStream_t>(stream_of(given));
+    if (handle_ != caller_.stream())
+      guard_.reset_stream(c10::cuda::getStreamFromExternal(handle_, like.get_device()));
+  }
+  void* handle() const { return handle_; }
+  // A result allocated here: the caller's stream uses it next.
+  void result(const at::Tensor& t) const {
+    if (handle_ != caller_.stream()) t.record_stream(caller_.unwrap());
+  }
+
+ private:
+  const c10::cuda::CUDAStream caller_;
+  cudaStream_t handle_;
+  c10::cuda::OptionalCUDAStreamGuard guard_;
+};
 
 // The package's own exception for a status that is not NVFP4_OK.
 void done(nvfp4_status st, const char* where) {
@@ -206,6 +220,7 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t M = x.size(0), E = x.size(1), k = integer(a[1]), kk = std::max<int64_t>(k, 0);
     check(x, x.scalar_type(), "router_logits", {M, E});
     const void* bias = optional_f32(a[4], "bias", E);
+    const OnStream on(a[8], x);
     at::Tensor ids, w;
     if (a[6] == Py_None && a[7] == Py_None) {
       Results r;
@@ -217,14 +232,13 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
       ids = result(a[6], at::kInt, "expert_ids", {M, kk}, x);
       w = result(a[7], at::kFloat, "weights", {M, kk}, x);
     }
-    void* stream = stream_of(a[8]);
     done(moe_route(x.data_ptr(), code, M, E, k, (int)integer(a[3]), (int)integer(a[2]),
                    static_cast<const float*>(bias), number(a[5]),
                    static_cast<int32_t*>(ids.data_ptr()), static_cast<float*>(w.data_ptr()),
-                   stream),
+                   on.handle()),
          "moe_route");
-    if (a[6] == Py_None) used_on(ids, stream, a[8]);
-    if (a[7] == Py_None) used_on(w, stream, a[8]);
+    if (a[6] == Py_None) on.result(ids);
+    if (a[7] == Py_None) on.result(w);
     return tuple({ids, w});
   });
 }
@@ -254,6 +268,7 @@ PyObject* moe(PyObject*, PyObject* const* a, Py_ssize_t n) {
     check(g2, at::kFloat, "w2_global", {E});
     at::ScalarType dt = integer(a[10]) ? at::kBFloat16 : at::kFloat;
     if (a[9] != Py_None) dt = tensor(a[9], "out").scalar_type();
+    const OnStream on(a[12], x);
     const at::Tensor out = result(a[9], dt, "out", {M, H}, x);
     const int code = dtype_code(out, "out must be float32 or bfloat16");
     const at::Tensor ws =
@@ -262,16 +277,14 @@ PyObject* moe(PyObject*, PyObject* const* a, Py_ssize_t n) {
                         x.options().dtype(at::kByte))
             : tensor(a[11], "workspace");
     if (!ws.is_cuda()) throw ValueError("workspace must be a CUDA tensor");
-    void* stream = stream_of(a[12]);
     using u8 = const uint8_t*;
     using f32 = const float*;
     done(w4a16_moe(x.data_ptr(), M, k, H, I, E, static_cast<const int32_t*>(ids.data_ptr()),
                    f32(w.data_ptr()), u8(p13.data_ptr()), u8(s13.data_ptr()), f32(g13.data_ptr()),
                    u8(p2.data_ptr()), u8(s2.data_ptr()), f32(g2.data_ptr()), out.data_ptr(), code,
-                   ws.data_ptr(), (size_t)ws.numel() * ws.element_size(), stream),
+                   ws.data_ptr(), (size_t)ws.numel() * ws.element_size(), on.handle()),
          "w4a16_moe");
-    if (a[9] == Py_None) used_on(out, stream, a[12]);
-    if (a[11] == Py_None) used_on(ws, stream, a[12]);
+    if (a[9] == Py_None) on.result(out);
     return THPVariable_Wrap(out);
   });
 }
@@ -298,18 +311,18 @@ PyObject* logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor &x = tensor(a[0], "logits"), &tok = tensor(a[1], "token_ids");
     const Logits l = logits_args(x, tok);
     const int64_t k = integer(a[2]), kk = std::max<int64_t>(k, 0);
+    const OnStream on(a[4], x);
     Results r;
     at::Tensor &ranks = *r.add(at::kLong, {l.M}), &ids = *r.add(at::kLong, {l.M, kk});
     at::Tensor &lp = *r.add(at::kFloat, {l.M}), &ent = *r.add(at::kFloat, {l.M});
     at::Tensor &lse = *r.add(at::kFloat, {l.M}), &top = *r.add(at::kFloat, {l.M, kk});
     r.allocate(x);
-    void* stream = stream_of(a[4]);
     auto pf = [](const at::Tensor& t) { return static_cast<float*>(t.data_ptr()); };
     auto pi = [](const at::Tensor& t) { return static_cast<int64_t*>(t.data_ptr()); };
     done(token_logprobs(x.data_ptr(), l.code, l.M, l.N, l.ld, pi(tok), number(a[3]), k, pf(lp),
-                        pf(ent), pf(lse), pi(ranks), pi(ids), pf(top), stream),
+                        pf(ent), pf(lse), pi(ranks), pi(ids), pf(top), on.handle()),
          "token_logprobs");
-    used_on(lp, stream, a[4]);  // all six: one allocation
+    on.result(lp);  // all six: one allocation
     return tuple({lp, ent, lse, ranks, ids, top});
   });
 }
@@ -325,6 +338,7 @@ PyObject* logprobs_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const void* ent = optional_f32(a[3], "entropy", l.M);
     const void* ge = optional_f32(a[5], "grad_entropy", l.M);
     if (a[5] != Py_None && a[3] == Py_None) throw ValueError("grad_entropy needs the forward's entropy");
+    const OnStream on(a[8], x);
     at::Tensor out;
     if (a[7] == Py_None) {
       out = at::empty({l.M, l.N}, x.options());
@@ -334,14 +348,13 @@ PyObject* logprobs_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
           (l.N > 1 && out.stride(1) != 1))
         throw ValueError("out must be a CUDA tensor of the logits' shape and dtype, rows contiguous");
     }
-    void* stream = stream_of(a[8]);
     using f32 = const float*;
     done(token_logprobs_backward(x.data_ptr(), l.code, l.M, l.N, l.ld,
                                  static_cast<const int64_t*>(tok.data_ptr()), number(a[6]),
                                  f32(lse.data_ptr()), f32(ent), f32(g.data_ptr()), f32(ge),
-                                 out.data_ptr(), l.M > 1 ? out.stride(0) : l.N, stream),
+                                 out.data_ptr(), l.M > 1 ? out.stride(0) : l.N, on.handle()),
          "token_logprobs_backward");
-    if (a[7] == Py_None) used_on(out, stream, a[8]);
+    if (a[7] == Py_None) on.result(out);
     return THPVariable_Wrap(out);
   });
 }

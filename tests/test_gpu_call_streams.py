@@ -1,0 +1,76 @@
+"""Calls given a stream other than the current one: their results and
+workspaces are not memory whose last use is still queued on the current
+stream."""
+import pytest
+import torch
+
+import nvfp4_weight_only_rows_gb300 as nv
+from tests.test_gpu_logprobs import check as check_logprobs
+from tests.test_gpu_logprobs import make as make_logits
+from tests.test_gpu_moe import check, make, on_gpu
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__
+
+    __graft_entry__.build()
+    assert torch.cuda.is_available()
+
+
+def test_memory_still_in_use_on_the_current_stream_is_not_reused():
+    args = make(64, 16, 4, 512, 256, seed=21)
+    dev = on_gpu(*args)
+    logits = torch.randn(64, 16, device="cuda")
+    big, tok = make_logits(40, 5001, torch.float32, seed=3)
+    bd, td = big.cuda(), tok.cuda()
+    n = nv.w4a16_moe_workspace_bytes(64, 4, 512, 256)
+    sizes = (n, n, 64 * 512 * 2, 4096, 8192, 16384, 40 * 5001 * 4)
+    grads = torch.randn(40, device="cuda")
+    lse = torch.logsumexp(bd, 1)
+    ent = torch.ones(40, device="cuda")
+
+    def calls(stream):
+        return [nv.w4a16_moe(*dev, stream=stream), *nv.moe_route(logits, 4, stream=stream),
+                *nv.token_logprobs(bd, td, 5, stream=stream),
+                nv.token_logprobs_backward(bd, td, lse, ent, grads, stream=stream)]
+
+    want = [t.cpu() for t in calls(None)]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    free = [torch.empty(b, dtype=torch.uint8, device="cuda") for b in sizes for _ in range(3)]
+    torch.cuda._sleep(40_000_000)  # what the current stream does below waits for some 20 ms
+    for t in free:
+        t.fill_(255)
+    del t, free
+    got = calls(s)
+    s.synchronize()
+    with torch.cuda.stream(s):
+        early = [t.cpu() for t in got]
+    torch.cuda.synchronize()
+    for now, a, b in zip(early, got, want):
+        assert torch.equal(now, b) and torch.equal(a.cpu(), b)
+    check(got[0], args)
+    check_logprobs(got[3:9], big, tok, 5)
+
+
+def test_results_used_by_the_current_stream_are_not_given_out_on_the_other():
+    """Freed while the current stream still has to read them."""
+    logits, tok = (t.cuda() for t in make_logits(64, 40001, torch.float32, seed=5))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    want = nv.token_logprobs(logits, tok, 20)[5].clone()
+    out = torch.empty_like(want)
+    torch.cuda.synchronize()
+    held = nv.token_logprobs(logits, tok, 20, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda._sleep(40_000_000)
+    out.copy_(held[5])
+    del held
+    with torch.cuda.stream(s):
+        junk = [torch.zeros(64 * 20 * 12 + 4096, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    assert all(bool((j == 0).all()) for j in junk)
