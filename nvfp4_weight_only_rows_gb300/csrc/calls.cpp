@@ -39,9 +39,17 @@ const at::Tensor& tensor(PyObject* o, const char* name) {
   return THPVariable_Unpack(o);
 }
 
-void check(const at::Tensor& t, at::ScalarType dtype, const char* name,
-           std::initializer_list<int64_t> shape) {
+// On the GPU of `first`, the call's first tensor.
+void check_device(const at::Tensor& t, const char* name, const at::Tensor& first) {
   if (!t.is_cuda()) throw ValueError(std::string(name) + " must be a CUDA tensor");
+  if (t.device() != first.device())
+    throw ValueError(std::string(name) + " is on " + t.device().str() + ", not on " +
+                     first.device().str());
+}
+
+void check(const at::Tensor& t, at::ScalarType dtype, const char* name,
+           std::initializer_list<int64_t> shape, const at::Tensor& first) {
+  check_device(t, name, first);
   if (t.scalar_type() != dtype)
     throw ValueError(std::string(name) + " must be " + c10::toString(dtype) + ", got " +
                      c10::toString(t.scalar_type()));
@@ -52,13 +60,12 @@ void check(const at::Tensor& t, at::ScalarType dtype, const char* name,
                      shape_text(t.sizes()));
 }
 
-// The tensor of `o`, checked; a new one where it is None.
-at::Tensor result(PyObject* o, at::ScalarType dtype, const char* name,
-                  std::initializer_list<int64_t> shape, const at::Tensor& like) {
-  if (o == Py_None)
-    return at::empty(at::IntArrayRef(shape.begin(), shape.size()), like.options().dtype(dtype));
+// The tensor of `o`, checked; none where it is None.
+at::Tensor optional(PyObject* o, at::ScalarType dtype, const char* name,
+                    std::initializer_list<int64_t> shape, const at::Tensor& first) {
+  if (o == Py_None) return {};
   const at::Tensor& t = tensor(o, name);
-  check(t, dtype, name, shape);
+  check(t, dtype, name, shape, first);
   return t;
 }
 
@@ -104,10 +111,10 @@ class Results {
   int64_t total_ = 0;
 };
 
-const void* optional_f32(PyObject* o, const char* name, int64_t n) {
+const void* optional_f32(PyObject* o, const char* name, int64_t n, const at::Tensor& first) {
   if (o == Py_None) return nullptr;
   const at::Tensor& t = tensor(o, name);
-  check(t, at::kFloat, name, {n});
+  check(t, at::kFloat, name, {n}, first);
   return t.data_ptr();
 }
 
@@ -141,6 +148,10 @@ class OnStream {
  public:
   OnStream(PyObject* given, const at::Tensor& like)
       : caller_(c10::cuda::getCurrentCUDAStream()), handle_(caller_.stream()) {
+    // the kernels run on the current device, whose streams these are
+    if (like.device() != caller_.device())
+      throw ValueError("the tensors are on " + like.device().str() + ", the current device is " +
+                       caller_.device().str());
     if (given == Py_None) return;
     handle_ = static_cast<cudaStream_t>(stream_of(given));
     if (handle_ != caller_.stream())
@@ -218,19 +229,20 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int code = dtype_code(x, "router_logits must be float32 or bfloat16 [M, E]");
     if (x.dim() != 2) throw ValueError("router_logits must be float32 or bfloat16 [M, E]");
     const int64_t M = x.size(0), E = x.size(1), k = integer(a[1]), kk = std::max<int64_t>(k, 0);
-    check(x, x.scalar_type(), "router_logits", {M, E});
-    const void* bias = optional_f32(a[4], "bias", E);
+    check(x, x.scalar_type(), "router_logits", {M, E}, x);
+    const void* bias = optional_f32(a[4], "bias", E, x);
+    at::Tensor ids = optional(a[6], at::kInt, "expert_ids", {M, kk}, x);
+    at::Tensor w = optional(a[7], at::kFloat, "weights", {M, kk}, x);
     const OnStream on(a[8], x);
-    at::Tensor ids, w;
-    if (a[6] == Py_None && a[7] == Py_None) {
+    if (!ids.defined() && !w.defined()) {
       Results r;
       at::Tensor &ri = *r.add(at::kInt, {M, kk}), &rw = *r.add(at::kFloat, {M, kk});
       r.allocate(x);
       ids = std::move(ri);
       w = std::move(rw);
     } else {
-      ids = result(a[6], at::kInt, "expert_ids", {M, kk}, x);
-      w = result(a[7], at::kFloat, "weights", {M, kk}, x);
+      if (!ids.defined()) ids = at::empty({M, kk}, x.options().dtype(at::kInt));
+      if (!w.defined()) w = at::empty({M, kk}, x.options().dtype(at::kFloat));
     }
     done(moe_route(x.data_ptr(), code, M, E, k, (int)integer(a[3]), (int)integer(a[2]),
                    static_cast<const float*>(bias), number(a[5]),
@@ -255,28 +267,32 @@ PyObject* moe(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (ids.dim() != 2) throw ValueError("expert_ids must be 2-D [M, k]");
     if (p2.dim() != 3) throw ValueError("w2_packed must be 3-D [E, H, I/2]");
     const int64_t M = x.size(0), H = x.size(1), k = ids.size(1), E = p2.size(0), I = p2.size(2) * 2;
-    check(x, at::kBFloat16, "x", {M, H});
-    check(ids, at::kInt, "expert_ids", {M, k});
-    check(w, at::kFloat, "weights", {M, k});
+    check(x, at::kBFloat16, "x", {M, H}, x);
+    check(ids, at::kInt, "expert_ids", {M, k}, x);
+    check(w, at::kFloat, "weights", {M, k}, x);
     if (s13.element_size() != 1 || s2.element_size() != 1)
       throw ValueError("scales must be float8_e4m3fn (or uint8 bit patterns)");
-    check(p13, at::kByte, "w13_packed", {E, 2 * I, H / 2});
-    check(s13, s13.scalar_type(), "w13_scales", {E, 2 * I, H / 16});
-    check(g13, at::kFloat, "w13_global", {E});
-    check(p2, at::kByte, "w2_packed", {E, H, I / 2});
-    check(s2, s2.scalar_type(), "w2_scales", {E, H, I / 16});
-    check(g2, at::kFloat, "w2_global", {E});
+    check(p13, at::kByte, "w13_packed", {E, 2 * I, H / 2}, x);
+    check(s13, s13.scalar_type(), "w13_scales", {E, 2 * I, H / 16}, x);
+    check(g13, at::kFloat, "w13_global", {E}, x);
+    check(p2, at::kByte, "w2_packed", {E, H, I / 2}, x);
+    check(s2, s2.scalar_type(), "w2_scales", {E, H, I / 16}, x);
+    check(g2, at::kFloat, "w2_global", {E}, x);
     at::ScalarType dt = integer(a[10]) ? at::kBFloat16 : at::kFloat;
     if (a[9] != Py_None) dt = tensor(a[9], "out").scalar_type();
+    at::Tensor out = optional(a[9], dt, "out", {M, H}, x), ws;
+    if (a[11] != Py_None) {
+      ws = tensor(a[11], "workspace");
+      check_device(ws, "workspace", x);
+      // (an expanded or strided view has more elements than bytes of its own)
+      if (!ws.is_contiguous()) throw ValueError("workspace must be contiguous");
+    }
     const OnStream on(a[12], x);
-    const at::Tensor out = result(a[9], dt, "out", {M, H}, x);
+    if (!out.defined()) out = at::empty({M, H}, x.options().dtype(dt));
     const int code = dtype_code(out, "out must be float32 or bfloat16");
-    const at::Tensor ws =
-        a[11] == Py_None
-            ? at::empty({std::max<int64_t>((int64_t)w4a16_moe_workspace_bytes(M, k, H, I), 256)},
-                        x.options().dtype(at::kByte))
-            : tensor(a[11], "workspace");
-    if (!ws.is_cuda()) throw ValueError("workspace must be a CUDA tensor");
+    if (!ws.defined())
+      ws = at::empty({std::max<int64_t>((int64_t)w4a16_moe_workspace_bytes(M, k, H, I), 256)},
+                     x.options().dtype(at::kByte));
     using u8 = const uint8_t*;
     using f32 = const float*;
     done(w4a16_moe(x.data_ptr(), M, k, H, I, E, static_cast<const int32_t*>(ids.data_ptr()),
@@ -301,7 +317,7 @@ Logits logits_args(const at::Tensor& x, const at::Tensor& tokens) {
   const int64_t M = x.size(0), N = x.size(1), ld = M > 1 ? x.stride(0) : N;
   if (N > 1 && x.stride(1) != 1) throw ValueError("the logits of a row must be contiguous");
   if (ld < N) throw ValueError("the rows of logits overlap");
-  check(tokens, at::kLong, "token_ids", {M});
+  check(tokens, at::kLong, "token_ids", {M}, x);
   return {code, M, N, ld};
 }
 
@@ -333,21 +349,21 @@ PyObject* logprobs_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor &x = tensor(a[0], "logits"), &tok = tensor(a[1], "token_ids");
     const Logits l = logits_args(x, tok);
     const at::Tensor &lse = tensor(a[2], "lse"), &g = tensor(a[4], "grad_logprobs");
-    check(lse, at::kFloat, "lse", {l.M});
-    check(g, at::kFloat, "grad_logprobs", {l.M});
-    const void* ent = optional_f32(a[3], "entropy", l.M);
-    const void* ge = optional_f32(a[5], "grad_entropy", l.M);
+    check(lse, at::kFloat, "lse", {l.M}, x);
+    check(g, at::kFloat, "grad_logprobs", {l.M}, x);
+    const void* ent = optional_f32(a[3], "entropy", l.M, x);
+    const void* ge = optional_f32(a[5], "grad_entropy", l.M, x);
     if (a[5] != Py_None && a[3] == Py_None) throw ValueError("grad_entropy needs the forward's entropy");
-    const OnStream on(a[8], x);
     at::Tensor out;
-    if (a[7] == Py_None) {
-      out = at::empty({l.M, l.N}, x.options());
-    } else {
+    if (a[7] != Py_None) {
       out = tensor(a[7], "out");
-      if (!out.is_cuda() || out.scalar_type() != x.scalar_type() || out.sizes() != x.sizes() ||
+      check_device(out, "out", x);
+      if (out.scalar_type() != x.scalar_type() || out.sizes() != x.sizes() ||
           (l.N > 1 && out.stride(1) != 1))
         throw ValueError("out must be a CUDA tensor of the logits' shape and dtype, rows contiguous");
     }
+    const OnStream on(a[8], x);
+    if (!out.defined()) out = at::empty({l.M, l.N}, x.options());
     using f32 = const float*;
     done(token_logprobs_backward(x.data_ptr(), l.code, l.M, l.N, l.ld,
                                  static_cast<const int64_t*>(tok.data_ptr()), number(a[6]),

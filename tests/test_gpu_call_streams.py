@@ -1,4 +1,4 @@
-"""Calls given a stream other than the current one: their results and
+"""The memory of the compiled calls.  Given a stream other than the current one, their results and
 workspaces are not memory whose last use is still queued on the current
 stream."""
 import pytest
@@ -74,3 +74,15 @@ def test_results_used_by_the_current_stream_are_not_given_out_on_the_other():
     torch.cuda.synchronize()
     assert torch.equal(out, want)
     assert all(bool((j == 0).all()) for j in junk)
+
+
+def test_workspace_has_its_bytes():
+    """A view with enough elements over a small storage is refused."""
+    dev = on_gpu(*make(3, 4, 2, 64, 32, seed=1))
+    n = nv.w4a16_moe_workspace_bytes(3, 2, 64, 32)
+    small = torch.zeros(1, dtype=torch.uint8, device="cuda")
+    for view in (small.expand(n), torch.zeros(2 * n, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError, match="workspace must be contiguous"):
+            nv.w4a16_moe(*dev, workspace=view)
+    with pytest.raises(ValueError, match="workspace must be a CUDA tensor"):
+        nv.w4a16_moe(*dev, workspace=torch.zeros(n, dtype=torch.uint8))
