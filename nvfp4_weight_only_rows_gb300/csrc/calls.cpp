@@ -203,6 +203,15 @@ PyObject* tuple(std::initializer_list<at::Tensor> ts) {
   return t;
 }
 
+// The exception class torch raises where its allocator has no memory left.
+void set_out_of_memory(const char* what) {
+  PyObject* torch = PyImport_ImportModule("torch");
+  PyObject* type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+  if (type) PyErr_SetString(type, what);
+  Py_XDECREF(type);
+  Py_XDECREF(torch);
+}
+
 template <int64_t kArgs, typename F>
 PyObject* guarded(Py_ssize_t n, F f) {
   try {
@@ -214,6 +223,10 @@ PyObject* guarded(Py_ssize_t n, F f) {
   } catch (const PyFailure&) {
   } catch (const ValueError& e) {
     PyErr_SetString(PyExc_ValueError, e.what());
+  } catch (const c10::OutOfMemoryError& e) {
+    set_out_of_memory(e.what_without_backtrace());
+  } catch (const c10::Error& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
   } catch (...) {

@@ -86,3 +86,31 @@ def test_workspace_has_its_bytes():
             nv.w4a16_moe(*dev, workspace=view)
     with pytest.raises(ValueError, match="workspace must be a CUDA tensor"):
         nv.w4a16_moe(*dev, workspace=torch.zeros(n, dtype=torch.uint8))
+
+
+def test_out_of_memory_is_torchs_own_exception():
+    """As the calls that allocate through torch.empty raise it; the allocator
+    is told that it has no memory left."""
+    logits = torch.randn(300, 40001, device="cuda")
+    tok = torch.zeros(300, dtype=torch.int64, device="cuda")
+    vec = torch.zeros(300, device="cuda")
+    dev = on_gpu(*make(512, 8, 8, 1024, 512, seed=1))
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    torch.cuda.set_per_process_memory_fraction(torch.cuda.memory_reserved() /
+                                               torch.cuda.get_device_properties(0).total_memory)
+    held = []
+    try:
+        with pytest.raises(torch.OutOfMemoryError):  # what is free of the memory held already
+            while True:
+                held.append(torch.empty(16 << 20, dtype=torch.uint8, device="cuda"))
+        for call in (lambda: torch.empty_like(logits),
+                     lambda: nv.token_logprobs_backward(logits, tok, vec, vec, vec),
+                     lambda: nv.w4a16_moe(*dev)):
+            with pytest.raises(torch.OutOfMemoryError):
+                call()
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+        held.clear()
+    nv.w4a16_moe(*dev)
+    torch.cuda.synchronize()
