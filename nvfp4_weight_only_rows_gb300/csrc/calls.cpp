@@ -12,6 +12,7 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
+#include <algorithm>
 #include <initializer_list>
 #include <stdexcept>
 #include <string>
@@ -212,6 +213,12 @@ void set_out_of_memory(const char* what) {
   Py_XDECREF(torch);
 }
 
+// k as results are allocated for it: one out of range is refused by the C ABI
+// call, not by an allocation of its size.
+int64_t within(int64_t k, int64_t n, int64_t most) {
+  return std::max<int64_t>(0, std::min(k, std::min(n, most)));
+}
+
 template <int64_t kArgs, typename F>
 PyObject* guarded(Py_ssize_t n, F f) {
   try {
@@ -242,6 +249,7 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int code = dtype_code(x, "router_logits must be float32 or bfloat16 [M, E]");
     if (x.dim() != 2) throw ValueError("router_logits must be float32 or bfloat16 [M, E]");
     const int64_t M = x.size(0), E = x.size(1), k = integer(a[1]), kk = std::max<int64_t>(k, 0);
+    const int64_t fit = within(k, E, NVFP4_ROUTE_MAX_K);
     check(x, x.scalar_type(), "router_logits", {M, E}, x);
     const void* bias = optional_f32(a[4], "bias", E, x);
     at::Tensor ids = optional(a[6], at::kInt, "expert_ids", {M, kk}, x);
@@ -249,13 +257,13 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const OnStream on(a[8], x);
     if (!ids.defined() && !w.defined()) {
       Results r;
-      at::Tensor &ri = *r.add(at::kInt, {M, kk}), &rw = *r.add(at::kFloat, {M, kk});
+      at::Tensor &ri = *r.add(at::kInt, {M, fit}), &rw = *r.add(at::kFloat, {M, fit});
       r.allocate(x);
       ids = std::move(ri);
       w = std::move(rw);
     } else {
-      if (!ids.defined()) ids = at::empty({M, kk}, x.options().dtype(at::kInt));
-      if (!w.defined()) w = at::empty({M, kk}, x.options().dtype(at::kFloat));
+      if (!ids.defined()) ids = at::empty({M, fit}, x.options().dtype(at::kInt));
+      if (!w.defined()) w = at::empty({M, fit}, x.options().dtype(at::kFloat));
     }
     done(moe_route(x.data_ptr(), code, M, E, k, (int)integer(a[3]), (int)integer(a[2]),
                    static_cast<const float*>(bias), number(a[5]),
@@ -339,7 +347,7 @@ PyObject* logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded<5>(n, [&]() -> PyObject* {
     const at::Tensor &x = tensor(a[0], "logits"), &tok = tensor(a[1], "token_ids");
     const Logits l = logits_args(x, tok);
-    const int64_t k = integer(a[2]), kk = std::max<int64_t>(k, 0);
+    const int64_t k = integer(a[2]), kk = within(k, l.N, NVFP4_TOPK_MAX);
     const OnStream on(a[4], x);
     Results r;
     at::Tensor &ranks = *r.add(at::kLong, {l.M}), &ids = *r.add(at::kLong, {l.M, kk});

@@ -114,3 +114,15 @@ def test_out_of_memory_is_torchs_own_exception():
         held.clear()
     nv.w4a16_moe(*dev)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("k", [-1, 11, 1000, 1 << 40, (1 << 62) + 3])
+def test_k_out_of_range_is_a_shape_error_of_any_size(k):
+    x = torch.zeros(4, 10, device="cuda")
+    tok = torch.zeros(4, dtype=torch.int64, device="cuda")
+    for call in (lambda: nv.token_logprobs(x, tok, k), lambda: nv.moe_route(x, k),
+                 lambda: nv.moe_route(x, k, expert_ids=torch.zeros(4, max(k, 0), dtype=torch.int32, device="cuda")
+                                      if k < 2000 else None)):
+        with pytest.raises(nv.NVFP4Error) as err:
+            call()
+        assert err.value.status == nv.Status.ERR_SHAPE
