@@ -724,13 +724,47 @@ def w4a16_moe(x: torch.Tensor, expert_ids: torch.Tensor, weights: torch.Tensor,
         w2_global, out, out_dtype is torch.bfloat16, workspace, stream)
 
 
+class _TokenLogprobs(torch.autograd.Function):
+    """token_logprobs in an autograd graph: token_logprobs_backward is the
+    gradient of logprobs and entropy."""
+
+    @staticmethod
+    def forward(ctx, logits, token_ids, k, inv_temperature, stream):
+        out = _native.token_logprobs(logits, token_ids, k, inv_temperature, stream)
+        logprobs, entropy, lse, ranks, top_ids, _ = out
+        ctx.save_for_backward(logits, token_ids, lse, entropy)
+        ctx.inv_temperature = inv_temperature
+        ctx.mark_non_differentiable(ranks, top_ids)
+        ctx.set_materialize_grads(False)
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_logprobs, grad_entropy, grad_lse, grad_ranks, grad_ids, grad_top):
+        if grad_lse is not None or grad_top is not None:
+            raise RuntimeError("token_logprobs has gradients of logprobs and entropy only, "
+                               "not of lse or top_logprobs")
+        if grad_logprobs is None and grad_entropy is None:
+            return None, None, None, None, None
+        logits, token_ids, lse, entropy = ctx.saved_tensors
+        grad = token_logprobs_backward(
+            logits, token_ids, lse, entropy,
+            torch.zeros_like(lse) if grad_logprobs is None else grad_logprobs.contiguous(),
+            None if grad_entropy is None else grad_entropy.contiguous(), ctx.inv_temperature)
+        return grad, None, None, None, None
+
+
 def token_logprobs(logits: torch.Tensor, token_ids: torch.Tensor, k: int = 0,
                    inv_temperature: float = 1.0, stream=None):
     """Log probabilities of token_ids i64[M] under softmax(inv_temperature *
     logits) for logits f32 or bf16 [M, N] (rows may be strided), and the k
     most likely tokens of each row: (logprobs f32[M], entropy f32[M], lse
-    f32[M], ranks i64[M], top_ids i64[M, k], top_logprobs f32[M, k])."""
-    return (_native or _load_native()).token_logprobs(logits, token_ids, k, inv_temperature, stream)
+    f32[M], ranks i64[M], top_ids i64[M, k], top_logprobs f32[M, k]).  Where
+    logits require a gradient, logprobs and entropy carry it."""
+    native = _native or _load_native()
+    if isinstance(logits, torch.Tensor) and logits.requires_grad and torch.is_grad_enabled():
+        return _TokenLogprobs.apply(logits, token_ids, k, inv_temperature, stream)
+    return native.token_logprobs(logits, token_ids, k, inv_temperature, stream)
 
 
 def token_logprobs_backward(logits: torch.Tensor, token_ids: torch.Tensor, lse: torch.Tensor,
