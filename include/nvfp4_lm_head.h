@@ -73,7 +73,8 @@ typedef enum {
   NVFP4_ERR_DTYPE = 5,      /* unknown output dtype code */
   NVFP4_ERR_CUDA = 6,       /* a CUDA runtime/driver call failed */
   NVFP4_ERR_NONFINITE = 7,  /* device status: W held an Inf or NaN (quantizer), or a block
-                               scale read by a W4A16 product is NaN (an unloaded scale) */
+                               scale read by a W4A16 product is NaN (an unloaded scale; in
+                               w4a16_moe also a negative one) */
   NVFP4_ERR_TIMEOUT = 8,    /* device status: a pipeline wait ran out of time */
   NVFP4_ERR_UNSUPPORTED = 9, /* no sm_103a device / kernel image for it */
   NVFP4_ERR_SCRATCH_LIMIT = 10 /* w4a16_lm_head_noalloc: M*K needs more than its fixed scratch */
@@ -601,12 +602,13 @@ size_t w4a16_moe_workspace_bytes(int64_t M, int64_t k, int64_t H, int64_t I);
  * multiples of 256) the FP4 tensor cores read the weights as they are, once
  * per 8 to 20 pairs, and x and h are given to them as sums of NVFP4 values:
  * to 3e-5 of the largest of 16 of them plus 2e-8 of the largest of their row
- * for a bf16 result, to 1e-6 plus 2e-9 for an fp32 one.  Block
- * scales must not be negative (no quantizer of this library writes such a
- * byte; the tensor cores' scales have no sign).  Sums are fp32 in a fixed
- * order (the result does not depend on the schedule).  An Inf or NaN in a token's x makes that token's result NaN or
- * Inf, no other's.  A NaN block scale in a weight that was read raises
- * NVFP4_ERR_NONFINITE in the workspace status word.
+ * for a bf16 result, to 1e-6 plus 2e-9 for an fp32 one.   Sums
+ * are fp32 in a fixed order (the result does not depend on the schedule).  An
+ * Inf or NaN in a token's x makes that token's result NaN or Inf, no other's.
+ * Block scales must not be NaN or negative (no quantizer of this library
+ * writes such a byte; the tensor cores' scales have no sign): on either route
+ * one in a weight that was read raises NVFP4_ERR_NONFINITE in the workspace
+ * status word, and the results that it enters are unspecified.
  */
 nvfp4_status w4a16_moe(const void *x, int64_t M, int64_t k, int64_t H, int64_t I, int64_t E,
                        const int32_t *expert_ids, const float *weights, const uint8_t *w13_packed,

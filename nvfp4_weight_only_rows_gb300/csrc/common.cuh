@@ -188,6 +188,14 @@ __device__ __forceinline__ void scales4_to_f16(uint32_t s, uint32_t& s01, uint32
       : "r"(s));
 }
 
+// Sign bits (of each byte) set where one of 4 E4M3 scale bytes is no scale:
+// NaN (0x7F or 0xFF: never loaded) or negative (an unsigned scale operand
+// drops the sign); -0 is a zero.
+__device__ __forceinline__ uint32_t bad_scales4(uint32_t s) {
+  const uint32_t m = s & 0x7F7F7F7Fu;
+  return ((m + 0x01010101u) | (s & (m + 0x7F7F7F7Fu))) & 0x80808080u;
+}
+
 __device__ __forceinline__ uint32_t dup_lo(uint32_t v) { return __byte_perm(v, 0, 0x1010); }
 __device__ __forceinline__ uint32_t dup_hi(uint32_t v) { return __byte_perm(v, 0, 0x3232); }
 

@@ -61,7 +61,7 @@ struct MoeArgs {
   const float *g13, *g2;
   void* out;
   float *gu, *y;
-  int32_t *status, *nan_flags;  // nan_flags: one word per CTA of each product
+  int32_t *status, *bad_flags;  // bad_flags: one word per CTA of each product
   int M, k, H, I, E;
   int seg1, seg2;  // pairs of a segment in either product
 };
@@ -235,7 +235,7 @@ template <int kNT, bool kWide, bool kSplit>
 __device__ __forceinline__ void moe_steps(MoeStream<kWide>& in, int N, int n_stages, int q0, int f0,
                                           int f1, int T, const int* list, const uint8_t* s_act,
                                           size_t lo_off, const float* s_mul, float* dst,
-                                          float4* part, uint32_t& nan_bits) {
+                                          float4* part, uint32_t& bad_scales) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   float acc[kNT][4];
 #pragma unroll
@@ -283,7 +283,7 @@ __device__ __forceinline__ void moe_steps(MoeStream<kWide>& in, int N, int n_sta
     uint32_t sf[2][2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      nan_bits |= (a.s[h] & 0x7F7F7F7Fu) + 0x01010101u;
+      bad_scales |= bad_scales4(a.s[h]);
       scales4_to_f16(a.s[h], sf[h][0], sf[h][1]);
     }
     const uint8_t* act = s_act + (size_t)s * T * 512;
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_gemm_kernel(const MoeArgs 
   int64_t it = total * blockIdx.x / gridDim.x;
   const int64_t end = total * (blockIdx.x + 1) / gridDim.x;
   bool waited = kStep == 1;  // step 2 waits for gu with its first weights under way
-  uint32_t nan_bits = 0;
+  uint32_t bad_scales = 0;
   while (it < end) {
     const int sg = (int)(it / RT), q0 = (int)(it % RT);
     const int nq = (int)min((int64_t)(RT - q0), end - it);
@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_gemm_kernel(const MoeArgs 
     if (f0 < f1) {
       auto go = [&](auto nt) {
         moe_steps<decltype(nt)::value, kWide, kSplit>(in, N, n_stages, q0, f0, f1, T, s_list, s_act,
-                                                      lo_off, s_mul, dst, s_part[warp], nan_bits);
+                                                      lo_off, s_mul, dst, s_part[warp], bad_scales);
       };
       if (T <= 8) go(std::integral_constant<int, 1>{});
       else if (T <= 16) go(std::integral_constant<int, 2>{});
@@ -511,9 +511,8 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_gemm_kernel(const MoeArgs 
     grid_dependency_wait();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   }
-  // a block scale that is NaN (0x7F or 0xFF: never loaded)
-  const int bad = __syncthreads_or((nan_bits & 0x80808080u) != 0u);
-  if (tid == 0) p.nan_flags[(kStep - 1) * gridDim.x + blockIdx.x] = bad;
+  const int bad = __syncthreads_or(bad_scales != 0u);
+  if (tid == 0) p.bad_flags[(kStep - 1) * gridDim.x + blockIdx.x] = bad;
 }
 
 // out[m, :] = sum over the slots j of w[m, j] G2[e] y[m k + j, :], four
@@ -527,7 +526,7 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const MoeArgs p, int n
     if (blockIdx.x != 0) return;
     int bad = 0;
 #pragma unroll 4
-    for (int i = threadIdx.x; i < n_flags; i += blockDim.x) bad |= __ldcg(p.nan_flags + i);
+    for (int i = threadIdx.x; i < n_flags; i += blockDim.x) bad |= __ldcg(p.bad_flags + i);
     bad = __syncthreads_or(bad);
     if (threadIdx.x == 0) *p.status = bad ? NVFP4_ERR_NONFINITE : NVFP4_OK;
     return;
@@ -677,7 +676,7 @@ nvfp4_status moe_launch(const void* x, int64_t M, int64_t k, int64_t H, int64_t 
   a.gu = reinterpret_cast<float*>(ws + L.gu);
   a.y = reinterpret_cast<float*>(ws + L.y);
   a.status = reinterpret_cast<int32_t*>(ws);
-  a.nan_flags = reinterpret_cast<int32_t*>(ws + L.flags);
+  a.bad_flags = reinterpret_cast<int32_t*>(ws + L.flags);
   a.M = (int)M;
   a.k = (int)k;
   a.H = (int)H;

@@ -737,7 +737,7 @@ __global__ void __launch_bounds__(576, 1)
     // stage where rows are not 16-byte multiples
     const int a = warp - 8, r = tc_row(kTma, 32 * a + lane);
     const bool aligned = !p.unit_scales || nb % 16 == 0;
-    uint32_t nan_bits = 0, it = 0, units = 0;
+    uint32_t bad = 0, it = 0, units = 0;
     tc_pieces(x0, x1, n_st, RT, [&](const TcPiece& pc) {
       const bool live = r < p.N - pc.rt * 128;  // a row of the unit
       const uint32_t buf = p.unit_scales ? units % p.unit_scales : 0;
@@ -759,16 +759,14 @@ __global__ void __launch_bounds__(576, 1)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[st]);
-        nan_bits |= ((v.x & 0x7F7F7F7Fu) + 0x01010101u) | ((v.y & 0x7F7F7F7Fu) + 0x01010101u) |
-                    ((v.z & 0x7F7F7F7Fu) + 0x01010101u) | ((v.w & 0x7F7F7F7Fu) + 0x01010101u);
+        bad |= bad_scales4(v.x) | bad_scales4(v.y) | bad_scales4(v.z) | bad_scales4(v.w);
       }
       ++units;
       __syncwarp();
       if (p.unit_scales && lane == 0) mbar_arrive(&raw_empty[buf]);
       return true;
     });
-    // a block scale that is NaN (0x7F or 0xFF: never loaded)
-    if (__any_sync(0xFFFFFFFFu, (nan_bits & 0x80808080u) != 0u)) {
+    if (__any_sync(0xFFFFFFFFu, bad != 0u)) {
       grid_dependency_wait();  // the prep kernel clears the status
       if (lane == 0) raise_status(p.status, NVFP4_ERR_NONFINITE);
     }
