@@ -4,7 +4,8 @@ Each translation unit is compiled by nvcc in parallel, then linked into one
 shared library next to this file.  The library links the CUDA runtime
 dynamically, so inside a PyTorch process it shares torch's runtime instance.
 calls.cpp, the Python side of some calls, is compiled beside them against the
-installed torch's headers into _calls.so, which links that library.
+installed torch's headers into _calls.so, which links that library.  A C
+caller who has no torch runs this file, which builds the library alone.
 """
 from __future__ import annotations
 
@@ -60,8 +61,9 @@ def _compile_calls(obj_dir: str):
     return obj, ["-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
 
 
-def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    if not force and not _stale(SOURCES, LIB) and not _stale(SOURCES, CALLS):
+def build_library(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
+    """libnvfp4_lm_head.so alone: nvcc, no torch."""
+    if not force and not _stale(SOURCES, LIB):
         return LIB
     obj_dir = os.path.join(HERE, "_build")
     os.makedirs(obj_dir, exist_ok=True)
@@ -77,10 +79,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
-        calls = ex.submit(_compile_calls, obj_dir)
+    with cf.ThreadPoolExecutor(len(SOURCES)) as ex:
         results = list(ex.map(compile_one, SOURCES))
-        calls_obj, calls_libs = calls.result()
     if verbose:
         for _, log in results:
             print(log)
@@ -91,6 +91,20 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    return LIB
+
+
+def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
+    """The library, and _calls.so against the installed torch.  A failure of the
+    second is raised once the library is in place."""
+    if not force and not _stale(SOURCES, LIB) and not _stale(SOURCES, CALLS):
+        return LIB
+    obj_dir = os.path.join(HERE, "_build")
+    os.makedirs(obj_dir, exist_ok=True)
+    with cf.ThreadPoolExecutor(1) as ex:
+        calls = ex.submit(_compile_calls, obj_dir)
+        build_library(force, verbose, ptxas_info)
+        calls_obj, calls_libs = calls.result()
     tmp = CALLS + f".tmp{os.getpid()}"
     cmd = ["g++", "-shared", "-o", tmp, calls_obj, "-L" + HERE, "-l:" + os.path.basename(LIB),
            "-Wl,-rpath,$ORIGIN", *calls_libs]
@@ -101,5 +115,5 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     return LIB
 
 
-if __name__ == "__main__":
-    print(build(force=True, verbose=True, ptxas_info=True))
+if __name__ == "__main__":  # a C caller's build
+    print(build_library(force=True, verbose=True, ptxas_info=True))
