@@ -22,6 +22,7 @@ CALLS = os.path.join(HERE, "_calls.so")
 SOURCES = ("quantize.cu", "lm_head.cu", "fp8.cu", "w4a4.cu", "topk.cu", "api.cu", "noalloc.cu",
            "selftest.cu", "moe_route.cu", "moe.cu", "moe_tc.cu",
            "logprobs.cu")
+CALLS_SOURCES = ("calls.cpp",)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr"]
@@ -35,12 +36,31 @@ def nvcc() -> str:
 
 
 def _stale(sources, target) -> bool:
+    """Whether target is older than its sources, a header or this file."""
     if not os.path.exists(target):
         return True
     t = os.path.getmtime(target)
-    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    deps.append(os.path.join(HERE, "..", "include", "nvfp4_lm_head.h"))
+    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f in sources or f.endswith(".cuh")]
+    deps += [os.path.join(HERE, "..", "include", "nvfp4_lm_head.h"), __file__]
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
+
+
+def _torch_id() -> str:
+    """What a build of calls.cpp fits: this torch in this Python."""
+    import torch
+
+    return f"torch {torch.__version__} at {os.path.dirname(torch.__file__)}, " \
+           f"{sysconfig.get_config_var('SOABI')}"
+
+
+def _calls_stale() -> bool:
+    if _stale(CALLS_SOURCES, CALLS):
+        return True
+    try:
+        with open(CALLS + ".for") as f:
+            return f.read() != _torch_id()
+    except OSError:
+        return True
 
 
 def _compile_calls(obj_dir: str):
@@ -97,14 +117,15 @@ def build_library(force: bool = False, verbose: bool = False, ptxas_info: bool =
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     """The library, and _calls.so against the installed torch.  A failure of the
     second is raised once the library is in place."""
-    if not force and not _stale(SOURCES, LIB) and not _stale(SOURCES, CALLS):
-        return LIB
     obj_dir = os.path.join(HERE, "_build")
     os.makedirs(obj_dir, exist_ok=True)
     with cf.ThreadPoolExecutor(1) as ex:
-        calls = ex.submit(_compile_calls, obj_dir)
+        calls = ex.submit(lambda: _compile_calls(obj_dir) if force or _calls_stale() else None)
         build_library(force, verbose, ptxas_info)
-        calls_obj, calls_libs = calls.result()
+        compiled = calls.result()
+    if compiled is None:
+        return LIB
+    calls_obj, calls_libs = compiled
     tmp = CALLS + f".tmp{os.getpid()}"
     cmd = ["g++", "-shared", "-o", tmp, calls_obj, "-L" + HERE, "-l:" + os.path.basename(LIB),
            "-Wl,-rpath,$ORIGIN", *calls_libs]
@@ -112,6 +133,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if r.returncode != 0:
         raise RuntimeError(f"link of _calls.so failed:\n{r.stderr}")
     os.replace(tmp, CALLS)
+    with open(CALLS + ".for", "w") as f:
+        f.write(_torch_id())
     return LIB
 
 

@@ -48,6 +48,9 @@ def tree(tmp_path, monkeypatch):
         def break_(self, compiler):
             (fail / compiler).write_text("")
 
+        def mend(self, compiler):
+            (fail / compiler).unlink()
+
         def ran(self):
             """The compilers run since the last look."""
             lines = log.read_text().splitlines()
@@ -79,3 +82,39 @@ def test_the_file_runs_alone():
     code = ("import sys, runpy; sys.modules['torch'] = None; "
             f"m = runpy.run_path({_build.__file__!r}); assert callable(m['build_library'])")
     subprocess.run([sys.executable, "-c", code], check=True)
+
+
+def test_what_is_built_again(tree, monkeypatch):
+    def later(path):  # a source edited after the last build
+        os.utime(path, (os.path.getmtime(path) + 1e6,) * 2)
+
+    _build.build()
+    assert {"nvcc", "g++"} == set(tree.ran())
+    _build.build()
+    assert tree.ran() == []
+    monkeypatch.setattr("torch.__version__", "2.0.1+another")
+    _build.build()
+    assert set(tree.ran()) == {"g++"}  # against the torch there is now
+    _build.build()
+    assert tree.ran() == []
+    later(tree.csrc / "calls.cpp")
+    _build.build()
+    assert set(tree.ran()) == {"g++"}
+    os.utime(tree.csrc / "calls.cpp", (0, 0))
+    later(tree.csrc / "moe.cu")
+    _build.build_library()
+    assert set(tree.ran()) == {"nvcc"}
+    os.utime(tree.csrc / "moe.cu", (0, 0))
+    later(tree.csrc / "common.cuh")
+    _build.build_library()
+    assert set(tree.ran()) == {"nvcc"}
+
+
+def test_the_python_side_after_a_failed_build(tree):
+    tree.break_("g++")
+    with pytest.raises(RuntimeError):
+        _build.build()
+    tree.ran()
+    tree.mend("g++")
+    _build.build()
+    assert set(tree.ran()) == {"g++"} and tree.calls.exists()
