@@ -660,7 +660,8 @@ nvfp4_status token_logprobs(const void *logits, int dtype, int64_t M, int64_t N,
  *   grad[m, n] = inv_temperature *
  *       (a[m] (1[n == t] - p[n]) - b[m] p[n] (z[n] - lse[m] + entropy[m])).
  * Where the token id lies outside [0, N), a[m] counts as 0; a row that was
- * all -inf (lse -inf) gets zeros; a masked column gets 0.
+ * all -inf (lse -inf) gets zeros; a masked column (p = 0) gets 0, or
+ * inv_temperature a[m] where it is the token's.
  *   logits, token_ids, inv_temperature  as given to token_logprobs.
  *   lse, entropy        fp32 [M] as it wrote them (entropy may be NULL when
  *                       grad_entropy is).

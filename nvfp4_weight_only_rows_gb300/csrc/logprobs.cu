@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kT, kU == 4 ? 1024 / kT : 1) logprobs_kernel(c
       bm = max_nan(__uint_as_float(b2 << 16), __uint_as_float(b2 & 0xFFFF0000u));
       if (!(bm <= x_tok)) {
         const __nv_bfloat162 t2 = __float2bfloat162_rn(x_tok);  // a bf16 (or +inf) as it is
-        __nv_bfloat162 n2 = __float2bfloat162_rn(0.0f);  // counts of at most 16: exact
+        __nv_bfloat162 n2 = __float2bfloat162_rn(0.0f);  // counts of at most 4 kU: exact
 #pragma unroll
         for (int i = 0; i < kWords; ++i)
           n2 = __hadd2(n2, __hgt2(*reinterpret_cast<const __nv_bfloat162*>(&x[i]), t2));

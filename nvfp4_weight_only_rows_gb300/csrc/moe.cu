@@ -603,11 +603,12 @@ nvfp4_status moe_tc_launch(const void* x, int64_t M, int64_t k, int64_t H, int64
 // TB/s between them) is taken for more weight than about 85 MB counted once
 // per pair (27/16 byte per element of an H x I matrix), or for 6 pairs an
 // expert, where the products here turn from bandwidth to issue bound.
-// Measured (here / there): H 2048, I 768, top 8 of 128: 1 token 13.9 / 24.1 us,
-// 3 tokens 28.2 / 30.2, 4 tokens 32.0 / 32.3, 6 tokens 40.2 / 36.6; H = I = 2880,
-// top 4 of 32: 1 token 26.3 / 30.6, 2 tokens 40.2 / 36.0; H 1024, I 512, top 2 of
-// 64: 32 tokens 23.0 / 23.3, 48 tokens 27.6 / 24.8; H 512, I 256, top 2 of 16:
-// 32 tokens 16.2 / 17.1, 48 tokens 18.3 / 17.8, 128 tokens 30.1 / 21.0.
+// Measured (here / there): H 2048, I 768, top 8 of 128: 1 token 14.9 / 23.7 us,
+// 3 tokens 30.4 / 30.0, 4 tokens 34.7 / 33.0, 6 tokens 43.0 / 37.2; H = I = 2880,
+// top 4 of 32: 1 token 29.4 / 30.6, 2 tokens 46.5 / 37.6; H 1024, I 512, top 2 of
+// 64: 16 tokens 18.3 / 20.8, 32 tokens 24.3 / 23.3, 48 tokens 29.8 / 25.4; H 512,
+// I 256, top 2 of 16: 32 tokens 16.6 / 17.1, 48 tokens 17.6 / 17.7, 128 tokens
+// 33.7 / 21.0.  With P H I from 32M to the threshold the routes are within 5%.
 constexpr int64_t kMoeFewWork = 48 << 20;
 constexpr int64_t kMoeFewPairs = 6;
 static bool moe_use_tc(int64_t M, int64_t k, int64_t H, int64_t I, int64_t E) {

@@ -15,12 +15,14 @@
 // again by whole keys, two reductions a round.  All sums are fp32.
 //
 // A call reads M E logits once and writes 8 M k bytes: 16384 x 256 fp32 is 18
-// MB, 2.7 us at the copy rate, and takes 8.2 us; 65536 x 256 20.2 us.  One
-// token 1.9 us.  Bound by instruction issue (70% of its rate; a round 9 cycles
-// of an SM quarter, of about 285 a token) and, below some 10^5 tokens, by the
-// start of one CTA per four tokens.  Four tokens a warp with their rounds side
-// by side took 8.2 us too; CTAs of 8 or 16 tokens 8.4; a grid of resident CTAs
-// that loop 10.7 or more.
+// MB, 2.7 us at the copy rate, and takes 8.2 us; 65536 x 256 28.7 us, 262144 x
+// 256 106 us.  bf16 logits take 2% less, a bias 12.5 us (sigmoid, 16384 x 256;
+// 384 experts 29.7 us: 16 words a lane).  One token 2.0 us.  Bound by
+// instruction issue: 415 warp instructions a token, 240 ns of an SM quarter in
+// the long runs, which is 6.5 of the 8.2 us; the rest is the launch and the
+// first loads.  Four tokens a warp with their rounds side by side took 8.2 us
+// too; CTAs of 8 or 16 tokens 8.4; a grid of resident CTAs that loop 10.7 or
+// more.
 #include "gemm_common.cuh"
 
 namespace nvfp4 {

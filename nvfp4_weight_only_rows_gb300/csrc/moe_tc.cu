@@ -34,10 +34,11 @@
 // their weight loads start while the kernel before them still runs.
 //
 // Measured (bf16 result, H 2048, I 768, top 8 of 128): 64 tokens, 112 experts
-// in use, 297 MB, 72.1 us, 6.9 and 6.0 TB/s between the products' first and last MMA,
+// in use, 297 MB, 72.2 us (fp32 result 72.9), 6.9 and 6.0 TB/s between the products' first and last MMA,
 // about 25 us of prep, h, combine, kernel boundaries and first loads around
-// them.  5 tokens of H = I = 2880, top 4 of 32, 224 MB: 56.3 us.  193 tokens of
-// 64 experts with I 720 and half the pairs elsewhere, 144 MB: 67.7 us; the 14
+// them.  5 tokens of H = I = 2880, top 4 of 32, 224 MB: 56.4 us.  193 tokens of
+// 64 experts with I 720 and half the pairs elsewhere, 144 MB: 67.6 us (fp32
+// result, tiles of 16 pairs, 71.5); the 14
 // second tiles of experts with more than 20 pairs cost as much time as first
 // ones, although they find their weights in L2.
 #include <cuda_fp16.h>
