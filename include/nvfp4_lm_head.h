@@ -677,6 +677,38 @@ nvfp4_status token_logprobs_backward(const void *logits, int dtype, int64_t M, i
                                      const float *grad_logprobs, const float *grad_entropy,
                                      void *grad, int64_t ld_grad, void *stream);
 
+/* --------------------------- gradients through frozen NVFP4 weights */
+
+/* Workspace bytes of w4a16_lm_head_backward; 0 for rejected shapes. */
+size_t w4a16_lm_head_backward_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/*
+ * The gradient of w4a16_lm_head in its activations, for a weight that is not
+ * trained (the codes have no gradient):
+ *   dx[m, k] = global * sum_n grad[m, n] * e2m1(code[n, k]) * f32(scale[n, k/16]).
+ *   grad         [M, N] fp32 (dtype NVFP4_OUT_F32) or bf16 (NVFP4_OUT_BF16),
+ *                the gradient of the logits, device, 16-byte aligned.
+ *   M, N, K      M >= 0, N >= 0 (M == 0 is a no-op, N == 0 writes zeros),
+ *                K >= 16 and K % 16 == 0.
+ *   packed, scales, global_scale  as given to w4a16_lm_head.
+ *   dx           [M, K], bf16 (out_dtype NVFP4_OUT_BF16) or fp32, device,
+ *                16-byte aligned.
+ *   workspace    >= w4a16_lm_head_backward_workspace_bytes(M, N, K), 256-byte
+ *                aligned.
+ * The gradient enters the tensor cores as fp16 after an exact power of two
+ * per token: a bf16 one exactly down to 2^-28 of the token's largest value,
+ * an fp32 one rounded by at most 2^-12 of each value (2^-39 of the largest
+ * where that is more).  Products are exact, sums fp32 in a fixed order (the
+ * result does not depend on the schedule).  A token whose gradient holds an
+ * Inf or NaN gets Inf or NaN, no other does.  A NaN block scale raises
+ * NVFP4_ERR_NONFINITE in the workspace status word.  Up to 256 MiB of fp16
+ * gradient are held at a time: more tokens are worked on in pieces.
+ */
+nvfp4_status w4a16_lm_head_backward(const void *grad, int dtype, int64_t M, int64_t N,
+                                    const uint8_t *packed, const uint8_t *scales,
+                                    const float *global_scale, int64_t K, void *dx, int out_dtype,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+
 /* ------------------------------------------- allocation-free variant */
 
 /* Size of the fixed device scratch array behind w4a16_lm_head_noalloc. */

@@ -68,7 +68,7 @@ __all__ = [
     "w4a16_lm_head_topk_workspace_bytes", "TOPK_MAX", "w8a8_lm_head_topk",
     "w8a8_lm_head_topk_workspace_bytes", "w4a4_lm_head_topk", "w4a4_lm_head_topk_workspace_bytes",
     "moe_route", "w4a16_moe", "w4a16_moe_workspace_bytes", "token_logprobs",
-    "token_logprobs_backward",
+    "token_logprobs_backward", "w4a16_lm_head_backward", "w4a16_lm_head_backward_workspace_bytes",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -193,6 +193,11 @@ def load_library() -> ctypes.CDLL:
     lib.token_logprobs_backward.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, ctypes.c_float,
                                             vp, vp, vp, vp, vp, i64, vp]
     lib.token_logprobs_backward.restype = st
+    lib.w4a16_lm_head_backward_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.w4a16_lm_head_backward_workspace_bytes.restype = sz
+    lib.w4a16_lm_head_backward.argtypes = [vp, ctypes.c_int, i64, i64, vp, vp, vp, i64, vp,
+                                           ctypes.c_int, vp, sz, vp]
+    lib.w4a16_lm_head_backward.restype = st
     lib.w4a16_lm_head_noalloc.argtypes = [vp, i64, i64, vp, vp, vp, i64, vp, ctypes.c_int, vp]
     lib.w4a16_lm_head_noalloc.restype = st
     lib.w4a16_lm_head_noalloc_status.argtypes = [ctypes.POINTER(ctypes.c_int32), vp]
@@ -776,6 +781,23 @@ def token_logprobs_backward(logits: torch.Tensor, token_ids: torch.Tensor, lse: 
     the logits, in their dtype; `out` may be the logits themselves."""
     return (_native or _load_native()).token_logprobs_backward(
         logits, token_ids, lse, entropy, grad_logprobs, grad_entropy, inv_temperature, out, stream)
+
+
+def w4a16_lm_head_backward_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(load_library().w4a16_lm_head_backward_workspace_bytes(M, N, K))
+
+
+def w4a16_lm_head_backward(grad_logits: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,
+                           global_scale: torch.Tensor, out: torch.Tensor | None = None,
+                           out_dtype: torch.dtype = torch.bfloat16,
+                           workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The gradient of w4a16_lm_head in x: dx[M, K] = grad_logits . dequant(W)
+    for grad_logits f32 or bf16 [M, N] (the packed weight is not trained)."""
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
+        raise ValueError("out must be float32 or bfloat16")
+    return (_native or _load_native()).w4a16_lm_head_backward(
+        grad_logits, packed, scales, global_scale, out, out_dtype is torch.bfloat16, workspace,
+        stream)
 
 
 def w4a16_lm_head_noalloc(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,

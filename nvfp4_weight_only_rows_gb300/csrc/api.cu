@@ -73,6 +73,12 @@ nvfp4_status logprobs_grad_launch(const void* logits, int dtype, int64_t M, int6
                                   const float* entropy, const float* g_lp, const float* g_ent,
                                   void* out, int64_t ld_out, cudaStream_t stream);
 
+size_t lm_head_back_workspace_bytes(int64_t M, int64_t N, int64_t K);
+nvfp4_status lm_head_back_launch(const void* dy, int dtype, int64_t M, int64_t N,
+                                 const uint8_t* packed, const uint8_t* scales, const float* global,
+                                 int64_t K, void* dx, int out_dtype, void* workspace,
+                                 cudaStream_t stream);
+
 static bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // The kernels are built for sm_103a only; refuse other devices up front.
@@ -608,6 +614,45 @@ nvfp4_status token_logprobs_backward(const void* logits, int dtype, int64_t M, i
   return logprobs_grad_launch(logits, dtype, M, N, ld, token_ids, inv_temperature, lse, entropy,
                               grad_logprobs, grad_entropy, grad, ld_grad,
                               static_cast<cudaStream_t>(stream));
+}
+
+static bool float_code(int dtype) { return dtype == NVFP4_OUT_F32 || dtype == NVFP4_OUT_BF16; }
+
+// Sizes of the calls that train through a weight [N, K]: M tokens.
+static bool train_shape_ok(int64_t M, int64_t N, int64_t K) {
+  return M >= 0 && N >= 0 && K >= 16 && K % 16 == 0 && M < kMaxDim && N < kMaxDim && K < kMaxDim;
+}
+
+size_t w4a16_lm_head_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (!train_shape_ok(M, N, K)) return 0;
+  return M == 0 || N == 0 ? kWsHeader : lm_head_back_workspace_bytes(M, N, K);
+}
+
+nvfp4_status w4a16_lm_head_backward(const void* grad, int dtype, int64_t M, int64_t N,
+                                    const uint8_t* packed, const uint8_t* scales,
+                                    const float* global_scale, int64_t K, void* dx, int out_dtype,
+                                    void* workspace, size_t workspace_bytes, void* stream) {
+  if (!train_shape_ok(M, N, K)) return NVFP4_ERR_SHAPE;
+  if (!float_code(dtype) || !float_code(out_dtype)) return NVFP4_ERR_DTYPE;
+  if (M == 0) return NVFP4_OK;
+  if (!dx || (N > 0 && (!grad || !packed || !scales || !global_scale))) return NVFP4_ERR_NULL;
+  if (!workspace || workspace_bytes < w4a16_lm_head_backward_workspace_bytes(M, N, K))
+    return NVFP4_ERR_WORKSPACE;
+  if (!aligned(grad, 16) || !aligned(packed, 16) || !aligned(scales, 16) ||
+      !aligned(global_scale, 4) || !aligned(dx, 16) || !aligned(workspace, 256))
+    return NVFP4_ERR_ALIGN;
+  nvfp4_status st = check_device();
+  if (st != NVFP4_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (N == 0) {
+    const size_t bytes = (size_t)M * K * (out_dtype == NVFP4_OUT_BF16 ? 2 : 4);
+    return cudaMemsetAsync(dx, 0, bytes, s) == cudaSuccess &&
+                   cudaMemsetAsync(workspace, 0, 4, s) == cudaSuccess
+               ? NVFP4_OK
+               : NVFP4_ERR_CUDA;
+  }
+  return lm_head_back_launch(grad, dtype, M, N, packed, scales, global_scale, K, dx, out_dtype,
+                             workspace, s);
 }
 
 }  // extern "C"

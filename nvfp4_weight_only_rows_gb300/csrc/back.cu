@@ -1,0 +1,590 @@
+// back.cu -- the product back through an NVFP4 weight on sm_103a tensor cores:
+//   dx[m, k] = global * sum_n dy[m, n] * e2m1(code[n, k]) * f32(scale[n, k/16]),
+// the gradient of w4a16_lm_head in its activations, and the second half of the
+// gradients of cross_entropy.cu and glu.cu.
+//
+// The contraction runs over the weight's rows, along which the packed codes
+// are not contiguous.  The MMA keeps the forward product's orientation, D[k,
+// token] = A . B^T with A = W^T in tensor memory, one lane per weight column,
+// and B = dy in shared memory, so each 256-row stage of 128 columns has to be
+// turned as it is dequantized.  That costs no extra pass and no second copy of
+// the weight: `ldmatrix.trans` on 16-bit units of four codes hands each lane
+// the codes of rows n and n + 1 for four neighbouring columns; two byte
+// permutes and four logic operations per 16 codes make bytes whose nibbles are
+// rows n and n + 1 of one column, which the e2m1 conversion turns into fp16
+// pairs along the contraction; and `tcgen05.st.16x128b`, whose fragment gives
+// a lane one column pair of TMEM in two lanes' rows, writes them where the MMA
+// wants them.  The four columns of a lane land 8 TMEM lanes apart: TMEM lane p
+// of a quadrant is column 4 (p & 7) + (p >> 3), which the epilogue undoes.  A
+// lane's four columns share a scale; a stage's scales are converted once per
+// warp to fp16 rows in that order in shared memory.
+//
+// dy enters as fp16 after an exact power of two per token (as x does in the
+// forward product), products are exact, sums fp32 in a fixed order.
+#include "back.cuh"
+#include "w4a16_tc.cuh"
+
+namespace nvfp4 {
+
+constexpr uint32_t kBackPacked = 256 * 64;  // bytes: 256 rows x 128 columns of codes
+constexpr uint32_t kBackScales = 256 * 16;  // 256 rows x the 16 scales of 256 columns
+constexpr uint32_t kBackScratch = 2 * 256 * 2;  // a warp's scales: 2 column groups x 256 rows, fp16
+
+struct BackArgs {
+  uint32_t n_ft;         // 128-column tiles
+  const float* factor;   // [M]
+  void* out;             // [M, K], or one of these per split
+  int64_t split_stride;  // elements between the splits' results
+  int bf16;
+};
+
+// Unit u: token tile (fastest), column tile, split of the weight's rows.
+struct BackUnit {
+  int64_t t0;
+  uint32_t ft, split;
+};
+__device__ __forceinline__ BackUnit back_unit(const GemmArgs& p, uint32_t n_ft, uint32_t u) {
+  const uint32_t r = u / (uint32_t)p.n_ttiles;
+  return {(int64_t)(u - r * (uint32_t)p.n_ttiles) * p.BN, r % n_ft, r / n_ft};
+}
+
+struct BackEpilogue {
+  static constexpr int kWarpBytes = kMaxBN * 4;
+  struct Unit {
+    int64_t at;    // element of (t0, k)
+    int64_t live;  // tokens from t0 on
+    bool valid;    // k < K
+  };
+  BackArgs b;
+  __device__ Unit begin(const GemmArgs& p, uint32_t u, int q, int lane, uint8_t* s) const {
+    const BackUnit g = back_unit(p, b.n_ft, u);
+    float* fac = reinterpret_cast<float*>(s);
+    for (int t = lane; t < p.BN; t += 32)
+      fac[t] = g.t0 + t < p.M ? __ldcg(b.factor + g.t0 + t) : 0.0f;
+    __syncwarp();
+    const int64_t k = (int64_t)g.ft * kRows + q * 32 + 4 * (lane & 7) + (lane >> 3);
+    return {g.split * b.split_stride + g.t0 * p.K + k, p.M - g.t0, k < p.K};
+  }
+  __device__ void chunk(const GemmArgs& p, const Unit& u, int c, const float (&v)[16], int,
+                        const uint8_t* s) const {
+    float fac[16];
+    lds_f32x16(reinterpret_cast<const float*>(s) + c, fac);
+    if (!u.valid) return;
+    const int64_t live = u.live - c;
+    if (b.bf16) {
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(b.out) + u.at + c * p.K;
+#pragma unroll
+      for (int t = 0; t < 16; ++t, o += p.K)
+        if (t < live) *o = __float2bfloat16_rn(v[t] * fac[t]);
+    } else {
+      float* o = static_cast<float*>(b.out) + u.at + c * p.K;
+#pragma unroll
+      for (int t = 0; t < 16; ++t, o += p.K)
+        if (t < live) *o = v[t] * fac[t];
+    }
+  }
+};
+
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// 16 TMEM lanes x 32 columns: register 2 j + h of lane (g, t) is lane g + 8 h,
+// column 4 j + t.
+__device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+      "r"(v[15])
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Warp roles as in w4a16_tc_kernel: 0 codes and scales, 1 dy, 2 MMA, then
+// kDq dequant warps a quadrant, then four epilogue warps.
+template <int kStages, int kPStages, int kDq>
+__global__ void __launch_bounds__((GemmShape<kStages, kPStages, kDq>::kThreads), 1)
+    w4a16_back_kernel(const __grid_constant__ CUtensorMap tm_packed,
+                      const __grid_constant__ CUtensorMap tm_scales,
+                      const __grid_constant__ CUtensorMap tm_d, const GemmArgs p,
+                      const BackEpilogue epi) {
+  using Shape = GemmShape<kStages, kPStages, kDq>;
+  constexpr int kFirstEpiWarp = Shape::kFirstEpiWarp;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const int BN = p.BN;
+  const uint32_t box_bytes = (uint32_t)BN * 128;
+  const uint32_t d_stage_bytes = (kKB / 64) * box_bytes;
+  uint8_t* s_packed = smem;
+  uint8_t* s_d = s_packed + kPStages * kBackPacked;
+  uint8_t* s_scales = s_d + kStages * d_stage_bytes;
+  uint8_t* s_scratch = s_scales + kPStages * kBackScales;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_scratch + Shape::kDqWarps * kBackScratch);
+  uint64_t* p_full = bars;
+  uint64_t* p_empty = p_full + kPStages;
+  uint64_t* s_full = p_empty + kPStages;
+  uint64_t* s_empty = s_full + kStages;
+  uint64_t* d_full = s_empty + kStages;
+  uint64_t* d_empty = d_full + 4;
+  uint64_t* done_bar = d_empty + 4;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
+  volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(tmem_slot + 1);
+  uint8_t* s_epi = reinterpret_cast<uint8_t*>(bars + 32);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kPStages; ++i) {
+      mbar_init(&p_full[i], 1);
+      mbar_init(&p_empty[i], 4);
+    }
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&s_full[i], 4 + 1);
+      mbar_init(&s_empty[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&d_full[i], 1);
+      mbar_init(&d_empty[i], 4);
+    }
+    mbar_init(done_bar, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tm_packed);
+    tma_prefetch_desc(&tm_scales);
+    tma_prefetch_desc(&tm_d);
+  }
+  if (warp == 2) {
+    tmem_alloc(tmem_slot, p.tmem_cols);
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
+  const uint32_t tmem_a = tmem_base + ((uint32_t)BN << p.dbuf_log2);
+  const WaitCtl wc{p.status, abort_flag, kWaitLimitNs};
+  const Sched sc = plain_sched(p);
+  const uint32_t n_kb = (uint32_t)p.n_kb;
+  const uint32_t n_ft = epi.b.n_ft;
+
+  if (warp == 0) {
+    uint32_t issued = 0;
+    for_each_piece(sc, n_kb, [&](const Piece& pc) {
+      const BackUnit g = back_unit(p, n_ft, pc.u);
+      for (uint32_t kb = pc.kb0; kb < pc.kb1; ++kb, ++issued) {
+        const uint32_t st = issued % kPStages, ph = (issued / kPStages) & 1;
+        if (!warp_wait(&p_empty[st], ph ^ 1, wc)) return false;
+        if (elect_one()) {
+          const int32_t n0 = (int32_t)((g.split * n_kb + kb) * kKB);
+          mbar_arrive_expect_tx(&p_full[st], kBackPacked + kBackScales);
+          tma_load_2d(s_packed + st * kBackPacked, &tm_packed, (int32_t)g.ft * (kRows / 2), n0,
+                      &p_full[st]);
+          tma_load_2d(s_scales + st * kBackScales, &tm_scales, (int32_t)(g.ft / 2) * 16, n0,
+                      &p_full[st]);
+        }
+        __syncwarp();
+      }
+      return true;
+    });
+    drain_loads(p_full, kPStages, issued, 1, p.status);
+  } else if (warp == 1) {
+    grid_dependency_wait();  // dy comes from the kernel before
+    uint32_t issued = 0;
+    for_each_piece(sc, n_kb, [&](const Piece& pc) {
+      const BackUnit g = back_unit(p, n_ft, pc.u);
+      for (uint32_t kb = pc.kb0; kb < pc.kb1; ++kb, ++issued) {
+        const uint32_t st = issued % kStages, ph = (issued / kStages) & 1;
+        if (!warp_wait(&s_empty[st], ph ^ 1, wc)) return false;
+        if (elect_one()) {
+          const int32_t n0 = (int32_t)((g.split * n_kb + kb) * kKB);
+          mbar_arrive_expect_tx(&s_full[st], d_stage_bytes);
+          uint8_t* dst = s_d + st * d_stage_bytes;
+#pragma unroll
+          for (int b = 0; b < kKB / 64; ++b)
+            tma_load_2d(dst + b * box_bytes, &tm_d, n0 + 64 * b, (int32_t)g.t0, &s_full[st]);
+        }
+        __syncwarp();
+      }
+      return true;
+    });
+    drain_loads(s_full, kStages, issued, 5, p.status);
+  } else if (warp == 2) {
+    const uint32_t idesc = idesc_f16_f32((uint32_t)BN);
+    const uint64_t desc0 = smem_desc_sw128(smem_u32(s_d));
+    const uint32_t box_desc = box_bytes >> 4;
+    uint32_t g = 0, i = 0;
+    for_each_piece(sc, n_kb, [&](const Piece& pc) {
+      const uint32_t buf = i & ((1u << p.dbuf_log2) - 1u);
+      const uint32_t dph = (i >> p.dbuf_log2) & 1u;
+      ++i;
+      if (!warp_wait(&d_empty[buf], dph ^ 1, wc)) return false;
+      tc_fence_after();
+      const uint32_t d_tmem = tmem_base + buf * BN;
+      for (uint32_t kb = pc.kb0; kb < pc.kb1; ++kb, ++g) {
+        const uint32_t st = g % kStages, ph = (g / kStages) & 1;
+        if (!warp_wait(&s_full[st], ph, wc)) return false;
+        tc_fence_after();
+        const uint64_t bdesc = desc0 + ((st * d_stage_bytes) >> 4);
+        const uint32_t a_t = tmem_a + st * (kKB / 2);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < kKB / 16; ++kk)
+            tc_mma_ts(d_tmem, a_t + kk * 8, bdesc + (kk >> 2) * box_desc + 2 * (kk & 3), idesc,
+                      (kb != pc.kb0) || (kk != 0));
+          tc_commit(&s_empty[st]);
+        }
+        __syncwarp();
+      }
+      if (elect_one()) tc_commit(&d_full[buf]);
+      __syncwarp();
+      return true;
+    });
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (elect_one()) tc_commit(done_bar);
+    __syncwarp();
+    volatile int32_t zero = 0;
+    const WaitCtl drain{p.status, &zero, 100000000ull};
+    mbar_wait(done_bar, 0, drain);
+  } else if (warp < kFirstEpiWarp) {
+    // Dequant and turn: quadrant q's 32 columns of a stage, 256 rows.
+    const int q = warp & 3;
+    const int r = (warp - kFirstDqWarp) >> 2;
+    const int t = lane & 3;
+    const uint32_t lane_off = (uint32_t)(q * 32) << 16;
+    uint8_t* scratch = s_scratch + (warp - kFirstDqWarp) * kBackScratch;
+    // where this lane's row of a 32-row block keeps its scale: the order in
+    // which a lane (., t) reads the rows 8 j + 2 t, 8 j + 2 t + 1, j = 0 .. 3
+    uint8_t* put = scratch + (((lane & 7) >> 1) * 8 + (lane >> 3) * 2 + (lane & 1)) * 2;
+    const uint8_t* get = scratch + (lane >> 4) * 512 + t * 16;  // column group (lane >> 2) >> 2
+    const uint32_t total = cta_stages(sc, n_kb);
+    const uint32_t swz = (uint32_t)((q ^ ((lane >> 1) & 3)) << 4) + lane * 64;
+    uint32_t nan_seen = 0;
+    bool ok = true;
+    uint32_t g = 0;  // stage of the CTA's sequence
+    for_each_piece(sc, n_kb, [&](const Piece& pc) {
+      const uint32_t ft = back_unit(p, n_ft, pc.u).ft;
+      for (uint32_t kb = pc.kb0; kb < pc.kb1; ++kb, ++g) {
+        if (g % kDq != (uint32_t)r) continue;
+        const uint32_t ps = g % kPStages, pph = (g / kPStages) & 1;
+        const uint32_t st = g % kStages, ph = (g / kStages) & 1;
+        if (!warp_wait(&p_full[ps], pph, wc)) return ok = false;
+        const uint8_t* srow = s_scales + ps * kBackScales + lane * 16 + (ft & 1) * 8 + q * 2;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t two = *reinterpret_cast<const uint16_t*>(srow + i * 512);
+          nan_seen |= (two & 0x7F7Fu) + 0x0101u;
+          uint32_t f, unused;
+          scales4_to_f16(two, f, unused);
+          *reinterpret_cast<uint16_t*>(put + i * 64) = (uint16_t)f;
+          *reinterpret_cast<uint16_t*>(put + i * 64 + 512) = (uint16_t)(f >> 16);
+        }
+        __syncwarp();
+        const uint32_t codes = smem_u32(s_packed + ps * kBackPacked) + swz;
+        const uint32_t ta = tmem_a + lane_off + st * (kKB / 2);
+#pragma unroll
+        for (int c4 = 0; c4 < kKB / 64; ++c4) {
+          uint32_t lo[16], hi[16];  // TMEM lanes 0-15 and 16-31 of the quadrant
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int b = c4 * 2 + half;
+            uint32_t w[4];
+            ldmatrix_x4_trans(codes + b * 32 * 64, w);
+            const uint4 s4 = *reinterpret_cast<const uint4*>(get + b * 64);
+            const uint32_t s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+              const uint32_t a = __byte_perm(w[j], w[j + 1], 0x5410);   // rows n
+              const uint32_t n1 = __byte_perm(w[j], w[j + 1], 0x7632);  // rows n + 1
+              const uint32_t even = (a & 0x0F0F0F0Fu) | ((n1 << 4) & 0xF0F0F0F0u);
+              const uint32_t odd = ((a >> 4) & 0x0F0F0F0Fu) | (n1 & 0xF0F0F0F0u);
+              uint32_t e[4], o[4];
+              e2m1x8_to_f16(even, e);
+              e2m1x8_to_f16(odd, o);
+              const int at = half * 8 + 2 * j;
+              lo[at] = mul_f16x2(e[0], s[j]);
+              lo[at + 1] = mul_f16x2(o[0], s[j]);
+              hi[at] = mul_f16x2(e[1], s[j]);
+              hi[at + 1] = mul_f16x2(o[1], s[j]);
+              lo[at + 2] = mul_f16x2(e[2], s[j + 1]);
+              lo[at + 3] = mul_f16x2(o[2], s[j + 1]);
+              hi[at + 2] = mul_f16x2(e[3], s[j + 1]);
+              hi[at + 3] = mul_f16x2(o[3], s[j + 1]);
+            }
+          }
+          if (c4 == 0 && !warp_wait(&s_empty[st], ph ^ 1, wc)) return ok = false;
+          tmem_st_16x128b_x8(ta + c4 * 32, lo);
+          tmem_st_16x128b_x8(ta + c4 * 32 + (16u << 16), hi);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_empty[ps]);
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_full[st]);
+      }
+      return true;
+    });
+    if (__any_sync(0xFFFFFFFFu, (nan_seen & 0x8080u) != 0u) && lane == 0)
+      raise_status(p.status, NVFP4_ERR_NONFINITE);
+  } else {
+    walk_epilogue(p, sc, epi, warp, lane, tmem_base, d_full, d_empty, wc,
+                  s_epi + (warp - kFirstEpiWarp) * BackEpilogue::kWarpBytes);
+  }
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, p.tmem_cols);
+  }
+}
+
+// ------------------------------------------------------------ splits joined
+// out[i] = sum over the splits, in their order.
+__global__ void __launch_bounds__(256) back_join_kernel(const float4* __restrict__ part,
+                                                        int64_t n4, int n_splits, void* out,
+                                                        int bf16) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n4;
+       i += (int64_t)gridDim.x * blockDim.x) {
+    float4 a = __ldcg(part + i);
+    for (int s = 1; s < n_splits; ++s) {
+      const float4 v = __ldcg(part + s * n4 + i);
+      a.x += v.x;
+      a.y += v.y;
+      a.z += v.z;
+      a.w += v.w;
+    }
+    if (bf16) {
+      const __nv_bfloat162 l = __floats2bfloat162_rn(a.x, a.y), h = __floats2bfloat162_rn(a.z, a.w);
+      static_cast<uint2*>(out)[i] = make_uint2(*reinterpret_cast<const uint32_t*>(&l),
+                                               *reinterpret_cast<const uint32_t*>(&h));
+    } else {
+      static_cast<float4*>(out)[i] = a;
+    }
+  }
+}
+
+// ------------------------------------------------------------ dy to fp16
+__device__ __forceinline__ float grad_value(const float* p) { return __ldg(p); }
+__device__ __forceinline__ float grad_value(const uint16_t* p) {
+  return __uint_as_float((uint32_t)__ldg(p) << 16);
+}
+
+// One CTA a token: its largest magnitude, then the row as fp16 after the
+// power of two that takes that to [2^14, 2^15).  bf16 gradients keep every
+// value down to 2^-28 of the largest; fp32 ones are rounded to 11 bits, 2^-12
+// of themselves, where a bf16 result is off by 2^-9 of itself.  The second
+// read finds the row in L2.
+template <typename T>
+__global__ void __launch_bounds__(512) back_prep_kernel(const T* __restrict__ dy, int64_t N,
+                                                        const float* __restrict__ global,
+                                                        __half* __restrict__ d16, int64_t stride,
+                                                        float* __restrict__ factor, int32_t* status,
+                                                        bool first, uint32_t* flags, int n_flags) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (blockIdx.x == 0) {
+    if (first && threadIdx.x == 0) *status = NVFP4_OK;
+    for (int i = threadIdx.x; i < n_flags; i += blockDim.x) flags[i] = 0;
+  }
+  const int64_t m = blockIdx.x;
+  const T* row = dy + m * N;
+  float mx = 0.0f;
+  bool bad = false;  // Inf or NaN: the row stays as it is
+#pragma unroll 8
+  for (int64_t n = threadIdx.x; n < N; n += blockDim.x) {
+    const float a = fabsf(grad_value(row + n));
+    mx = fmaxf(mx, a);
+    bad |= !(a <= 3.4028235e38f);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+  __shared__ float red[16];
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = mx;
+  bad = __syncthreads_or(bad);
+  mx = red[0];
+  for (int w = 1; w < (int)(blockDim.x >> 5); ++w) mx = fmaxf(mx, red[w]);
+  const int e = (mx > 0.0f && !bad) ? min(max(14 - ilogbf(mx), -126), 126) : 0;
+  if (threadIdx.x == 0) factor[m] = __fmul_rn(*global, __int_as_float((127 - e) << 23));
+  const float p2 = __int_as_float((127 + e) << 23);
+  __half* o = d16 + m * stride;
+#pragma unroll 4
+  for (int64_t n = 2 * (int64_t)threadIdx.x; n < N; n += 2 * blockDim.x) {
+    const float a = grad_value(row + n);
+    const float b = n + 1 < N ? grad_value(row + n + 1) : 0.0f;
+    *reinterpret_cast<__half2*>(o + n) = __floats2half2_rn(a * p2, b * p2);
+  }
+}
+
+// ------------------------------------------------------------ host side
+template <int kStages, int kPStages, int kDq>
+static size_t back_smem_bytes(int BN) {
+  return 1024 + kPStages * (size_t)(kBackPacked + kBackScales) + kStages * (size_t)BN * kKB * 2 +
+         GemmShape<kStages, kPStages, kDq>::kDqWarps * (size_t)kBackScratch + 256 +
+         4 * (size_t)BackEpilogue::kWarpBytes;
+}
+
+// Token tiles up to this take the deep ring (three stages of A and dy, six of
+// codes, three dequant warps a quadrant): its shared memory ends there.
+constexpr int kBackDeepBN = 48;
+
+BackLayout back_layout(int64_t M, int64_t N, int64_t K, int sms, size_t off) {
+  BackLayout l;
+  l.BN = lm_head_token_tile(M);
+  const int64_t tiles = ((K + kRows - 1) / kRows) * ((M + l.BN - 1) / l.BN);
+  const int64_t stages = (N + kKB - 1) / kKB;
+  // a unit for every SM: few tiles split the weight's rows between units
+  const int64_t want = std::min(stages, (sms + tiles - 1) / tiles);
+  l.n_kb = (int)((stages + want - 1) / want);
+  l.n_splits = (int)((stages + l.n_kb - 1) / l.n_kb);
+  l.grid = (int)std::min<int64_t>(sms, tiles * l.n_splits);
+  l.cnt = align_up(off, 256);
+  l.ready = l.cnt + align_up((size_t)l.grid * 4 * 4, 256);
+  l.part = l.ready + align_up((size_t)l.grid * 4 * 4, 256);
+  l.splits = l.part + align_up((size_t)l.grid * 4 * l.BN * 32 * 4, 256);
+  l.total = l.splits + (l.n_splits > 1 ? align_up((size_t)l.n_splits * M * K * 4, 256) : 0);
+  return l;
+}
+
+template <int kStages, int kPStages, int kDq>
+static cudaError_t back_gemm(const CUtensorMap& tm_packed, const CUtensorMap& tm_scales,
+                             const CUtensorMap& tm_d, const GemmArgs& a, const BackArgs& b,
+                             int grid, int max_bn, cudaStream_t stream) {
+  auto kern = w4a16_back_kernel<kStages, kPStages, kDq>;
+  static std::atomic<uint64_t> limit_set{0};
+  const cudaError_t e = smem_limit_once(limit_set, reinterpret_cast<const void*>(kern),
+                                        back_smem_bytes<kStages, kPStages, kDq>(max_bn));
+  if (e != cudaSuccess) return e;
+  PdlLaunch l(dim3((unsigned)grid), dim3(GemmShape<kStages, kPStages, kDq>::kThreads),
+              back_smem_bytes<kStages, kPStages, kDq>(a.BN), stream);
+  return cudaLaunchKernelEx(&l.cfg, kern, tm_packed, tm_scales, tm_d, a, BackEpilogue{b});
+}
+
+cudaError_t back_launch(const BackCall& c, const BackLayout& L, uint8_t* ws, cudaStream_t stream) {
+  const WeightStage& w = *c.stage;
+  const int64_t n_tt = (c.M + L.BN - 1) / L.BN;
+  CUtensorMap tm_packed, tm_scales, tm_d;
+  if (!encode_2d(&tm_packed, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.packed ? ws + w.packed_off : c.packed,
+                 (uint64_t)c.K / 2, (uint64_t)c.N, w.packed ? w.packed_stride : (uint64_t)c.K / 2,
+                 kRows / 2, kKB, CU_TENSOR_MAP_SWIZZLE_64B) ||
+      !encode_2d(&tm_scales, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.scales ? ws + w.scales_off : c.scales,
+                 (uint64_t)c.K / 16, (uint64_t)c.N, w.scales ? w.scales_stride : (uint64_t)c.K / 16,
+                 16, kKB, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !encode_2d(&tm_d, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, c.d, (uint64_t)c.N, (uint64_t)n_tt * L.BN,
+                 (uint64_t)c.d_stride * 2, 64, (uint32_t)L.BN, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  GemmArgs a = {};
+  a.M = c.M;
+  a.N = c.N;
+  a.K = c.K;
+  a.BN = L.BN;
+  a.n_ttiles = (int)n_tt;
+  a.n_kb = L.n_kb;
+  const int64_t n_ft = (c.K + kRows - 1) / kRows;
+  a.n_units = n_tt * n_ft * L.n_splits;
+  schedule_units(a, L.grid);
+  a.status = reinterpret_cast<int32_t*>(ws);
+  a.split_cnt = reinterpret_cast<uint32_t*>(ws + L.cnt);
+  a.split_ready = reinterpret_cast<uint32_t*>(ws + L.ready);
+  a.split_part = reinterpret_cast<float*>(ws + L.part);
+  const bool deep = L.BN <= kBackDeepBN;
+  const int stages = deep ? 3 : 2;
+  a.dbuf_log2 = (4 * L.BN + stages * (kKB / 2) <= 512) ? 2u : 1u;
+  a.tmem_cols = ((L.BN << a.dbuf_log2) + stages * (kKB / 2) <= 256) ? 256u : 512u;
+  const bool split = L.n_splits > 1;
+  const bool bf16 = c.out_dtype == NVFP4_OUT_BF16;
+  const BackArgs b{(uint32_t)n_ft, c.factor, split ? ws + L.splits : c.out, c.M * c.K,
+                   !split && bf16};
+  cudaError_t e =
+      deep ? back_gemm<3, 6, 3>(tm_packed, tm_scales, tm_d, a, b, L.grid, kBackDeepBN, stream)
+           : back_gemm<2, 4, 2>(tm_packed, tm_scales, tm_d, a, b, L.grid, kMaxBN, stream);
+  if (e != cudaSuccess || !split) return e;
+  const int64_t n4 = c.M * c.K / 4;
+  PdlLaunch l(dim3((unsigned)std::min<int64_t>((n4 + 255) / 256, 4096)), dim3(256), 0, stream);
+  return cudaLaunchKernelEx(&l.cfg, back_join_kernel, reinterpret_cast<const float4*>(ws + L.splits),
+                            n4, L.n_splits, c.out, (int)bf16);
+}
+
+// ------------------------------------------------------------ the call
+// Workspace: [status header][fp16 dy of a chunk of tokens][factors][the
+// product's own regions][staged weight rows].
+struct LmHeadBackLayout {
+  size_t d16, factor;
+  int64_t chunk, stride;
+  BackLayout back;
+  WeightStage stage;
+};
+
+static LmHeadBackLayout lm_head_back_layout(int64_t M, int64_t N, int64_t K, int sms) {
+  LmHeadBackLayout l;
+  l.stride = (N + 7) / 8 * 8;
+  l.chunk = chunk_tokens(M, l.stride * 2);
+  const int BN = lm_head_token_tile(l.chunk);
+  const int64_t rows = (l.chunk + BN - 1) / BN * BN;
+  l.d16 = kWsHeader;
+  l.factor = l.d16 + align_up((size_t)rows * l.stride * 2, 1024);
+  const size_t own = l.factor + align_up((size_t)rows * 4, 256);
+  l.back = back_layout(l.chunk, N, K, sms, own);
+  // a last chunk of fewer tokens may be split further
+  size_t end = l.back.total;
+  if (l.chunk > 0 && M % l.chunk != 0)
+    end = std::max(end, back_layout(M % l.chunk, N, K, sms, own).total);
+  l.stage = weight_stage(N, K, end, true);
+  return l;
+}
+
+size_t lm_head_back_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  return lm_head_back_layout(M, N, K, std::max(sm_count(), 1)).stage.total;
+}
+
+nvfp4_status lm_head_back_launch(const void* dy, int dtype, int64_t M, int64_t N,
+                                 const uint8_t* packed, const uint8_t* scales, const float* global,
+                                 int64_t K, void* dx, int out_dtype, void* workspace,
+                                 cudaStream_t stream) {
+  const int sms = sm_count();
+  if (sms <= 0) return NVFP4_ERR_CUDA;
+  const LmHeadBackLayout L = lm_head_back_layout(M, N, K, sms);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  __half* d16 = reinterpret_cast<__half*>(ws + L.d16);
+  float* factor = reinterpret_cast<float*>(ws + L.factor);
+  if (stage_weights(L.stage, packed, scales, N, K, ws, stream) != cudaSuccess)
+    return NVFP4_ERR_CUDA;
+  const size_t out_size = out_dtype == NVFP4_OUT_BF16 ? 2 : 4;
+  const size_t in_size = dtype == NVFP4_OUT_BF16 ? 2 : 4;
+  for (int64_t m = 0; m < M; m += L.chunk) {
+    const int64_t rows = std::min(L.chunk, M - m);
+    const void* src = static_cast<const uint8_t*>(dy) + (size_t)m * N * in_size;
+    const BackLayout back = back_layout(rows, N, K, sms, L.back.cnt);
+    uint32_t* flags = reinterpret_cast<uint32_t*>(ws + back.cnt);
+    PdlLaunch l(dim3((unsigned)rows), dim3(512), 0, stream);
+    int32_t* status = reinterpret_cast<int32_t*>(ws);
+    cudaError_t e =
+        dtype == NVFP4_OUT_BF16
+            ? cudaLaunchKernelEx(&l.cfg, back_prep_kernel<uint16_t>,
+                                 static_cast<const uint16_t*>(src), N, global, d16, L.stride,
+                                 factor, status, m == 0, flags, back.n_flags())
+            : cudaLaunchKernelEx(&l.cfg, back_prep_kernel<float>, static_cast<const float*>(src), N,
+                                 global, d16, L.stride, factor, status, m == 0, flags,
+                                 back.n_flags());
+    if (e != cudaSuccess) return NVFP4_ERR_CUDA;
+    const BackCall c{rows, N, K, d16, L.stride, packed, scales, &L.stage, factor,
+                     static_cast<uint8_t*>(dx) + (size_t)m * K * out_size, out_dtype};
+    if (back_launch(c, back, ws, stream) != cudaSuccess) return NVFP4_ERR_CUDA;
+  }
+  return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+}
+
+}  // namespace nvfp4

@@ -1,0 +1,42 @@
+// back.cuh -- the product back through a packed weight (back.cu) as the
+// gradients use it: out[m, k] = factor[m] sum_n d[m, n] W[n, k].
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "gemm_common.cuh"
+
+namespace nvfp4 {
+
+// Workspace of one product after `off`: the counters and flags of cut units
+// (zeroed by the kernel before it), their partials, and, where the weight's
+// rows are split over several units, fp32 results per split.
+struct BackLayout {
+  size_t cnt, ready, part, splits, total;
+  int grid, BN, n_splits, n_kb;
+  int n_flags() const { return (int)((part - cnt) / 4); }
+};
+BackLayout back_layout(int64_t M, int64_t N, int64_t K, int sms, size_t off);
+
+struct BackCall {
+  int64_t M, N, K;
+  const __half* d;      // [tokens rounded up to BN, stride]: rows past M hold anything
+  int64_t d_stride;     // elements, a multiple of 8, >= N
+  const uint8_t *packed, *scales;  // as in the call; `stage` says where TMA reads them
+  const WeightStage* stage;
+  const float* factor;  // [M]
+  void* out;            // [M, K]
+  int out_dtype;
+};
+// Two kernels at most, programmatic dependents of the kernel before.
+cudaError_t back_launch(const BackCall& c, const BackLayout& L, uint8_t* ws, cudaStream_t stream);
+
+// Tokens of a call that are worked on at a time, so that a fp16 row of
+// `row_bytes` for each fits `kChunkBytes`: whole tiles of 128.
+constexpr int64_t kChunkBytes = (int64_t)256 << 20;
+static inline int64_t chunk_tokens(int64_t M, int64_t row_bytes) {
+  const int64_t fit = kChunkBytes / row_bytes / kMaxBN * kMaxBN;
+  return M < kMaxBN ? M : std::min(M, std::max<int64_t>(fit, kMaxBN));
+}
+
+}  // namespace nvfp4

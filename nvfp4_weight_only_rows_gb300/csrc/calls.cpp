@@ -396,7 +396,72 @@ PyObject* logprobs_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// A packed NVFP4 weight's three tensors: codes u8[N, K/2], block scales
+// [N, K/16], global scale f32[1].
+struct Weight {
+  int64_t N, K;
+  const uint8_t *packed, *scales;
+  const float* global;
+};
+
+Weight weight_args(PyObject* packed, PyObject* scales, PyObject* global, const at::Tensor& first) {
+  const at::Tensor &p = tensor(packed, "packed"), &s = tensor(scales, "scales");
+  const at::Tensor& g = tensor(global, "global_scale");
+  if (p.dim() != 2) throw ValueError("packed must be 2-D [N, K/2]");
+  const int64_t N = p.size(0), K = p.size(1) * 2;
+  check(p, at::kByte, "packed", {N, K / 2}, first);
+  if (s.element_size() != 1)
+    throw ValueError("scales must be float8_e4m3fn (or uint8 bit patterns)");
+  check(s, s.scalar_type(), "scales", {N, K / 16}, first);
+  check(g, at::kFloat, "global_scale", {1}, first);
+  return {N, K, static_cast<const uint8_t*>(p.data_ptr()), static_cast<const uint8_t*>(s.data_ptr()),
+          static_cast<const float*>(g.data_ptr())};
+}
+
+// The given workspace, or one of `bytes`.
+at::Tensor workspace_arg(PyObject* o, size_t bytes, const at::Tensor& first) {
+  if (o == Py_None)
+    return at::empty({std::max<int64_t>((int64_t)bytes, 256)}, first.options().dtype(at::kByte));
+  return tensor(o, "workspace");
+}
+
+void check_workspace(PyObject* o, const at::Tensor& first) {
+  if (o == Py_None) return;
+  const at::Tensor& ws = tensor(o, "workspace");
+  check_device(ws, "workspace", first);
+  if (!ws.is_contiguous()) throw ValueError("workspace must be contiguous");
+}
+
+size_t bytes_of(const at::Tensor& ws) { return (size_t)ws.numel() * ws.element_size(); }
+
+// grad_logits, packed, scales, global_scale, out, bf16 out (if out is None), workspace, stream
+PyObject* lm_head_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded<8>(n, [&]() -> PyObject* {
+    const at::Tensor& dy = tensor(a[0], "grad_logits");
+    const int code = dtype_code(dy, "grad_logits must be float32 or bfloat16 [M, N]");
+    if (dy.dim() != 2) throw ValueError("grad_logits must be float32 or bfloat16 [M, N]");
+    const int64_t M = dy.size(0);
+    const Weight w = weight_args(a[1], a[2], a[3], dy);
+    check(dy, dy.scalar_type(), "grad_logits", {M, w.N}, dy);
+    at::ScalarType dt = integer(a[5]) ? at::kBFloat16 : at::kFloat;
+    if (a[4] != Py_None) dt = tensor(a[4], "out").scalar_type();
+    at::Tensor out = optional(a[4], dt, "out", {M, w.K}, dy);
+    check_workspace(a[6], dy);
+    const OnStream on(a[7], dy);
+    if (!out.defined()) out = at::empty({M, w.K}, dy.options().dtype(dt));
+    const int out_code = dtype_code(out, "out must be float32 or bfloat16");
+    const at::Tensor ws =
+        workspace_arg(a[6], w4a16_lm_head_backward_workspace_bytes(M, w.N, w.K), dy);
+    done(w4a16_lm_head_backward(dy.data_ptr(), code, M, w.N, w.packed, w.scales, w.global, w.K,
+                                out.data_ptr(), out_code, ws.data_ptr(), bytes_of(ws), on.handle()),
+         "w4a16_lm_head_backward");
+    if (a[4] == Py_None) on.result(out);
+    return THPVariable_Wrap(out);
+  });
+}
+
 PyMethodDef kMethods[] = {
+    {"w4a16_lm_head_backward", (PyCFunction)(void (*)())lm_head_backward, METH_FASTCALL, nullptr},
     {"moe_route", (PyCFunction)(void (*)())route, METH_FASTCALL, nullptr},
     {"w4a16_moe", (PyCFunction)(void (*)())moe, METH_FASTCALL, nullptr},
     {"token_logprobs", (PyCFunction)(void (*)())logprobs, METH_FASTCALL, nullptr},

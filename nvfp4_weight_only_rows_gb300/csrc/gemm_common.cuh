@@ -830,6 +830,73 @@ __device__ __forceinline__ void epilogue_role(const GemmArgs& p, const Sched& sc
   });
 }
 
+// The same walk for an epilogue of a call's own: E::begin per unit, before its
+// accumulator is ready (what the unit's tokens need, into the warp's E::kWarpBytes
+// of shared memory; it ends with a __syncwarp), E::chunk per 16 tokens of the
+// finished unit, a value of each for this lane's row.
+template <class E>
+__device__ __forceinline__ void walk_epilogue(const GemmArgs& p, const Sched& sc, const E& own,
+                                              int warp, int lane, uint32_t tmem_base,
+                                              uint64_t* d_full, uint64_t* d_empty,
+                                              const WaitCtl& wc, uint8_t* s_warp) {
+  grid_dependency_wait();  // what the units read, and the split flags, come from the kernel before
+  const int BN = p.BN;
+  const int q = warp & 3;
+  const uint32_t lane_off = (uint32_t)(q * 32) << 16;
+  uint32_t i = 0;
+  for_each_piece(sc, (uint32_t)p.n_kb, [&](const Piece& pc) {
+    const uint32_t buf = i & ((1u << p.dbuf_log2) - 1u);
+    const uint32_t dph = (i >> p.dbuf_log2) & 1u;
+    ++i;
+    const typename E::Unit unit = own.begin(p, pc.u, q, lane, s_warp);
+    if (!warp_wait(&d_full[buf], dph, wc)) return false;
+    tc_fence_after();
+    // a unit cut by a range boundary, as in epilogue_role
+    const bool whole = pc.kb0 == 0 && pc.kb1 == (uint32_t)p.n_kb;
+    bool finish = true;
+    float* part = nullptr;
+    uint32_t slot = 0;
+    if (!whole) {
+      slot = (pc.kb0 == 0 ? blockIdx.x + 1 : blockIdx.x) * 4 + q;
+      part = p.split_part + (size_t)slot * BN * 32;
+      uint32_t first = 0;
+      if (lane == 0) first = atomicAdd(p.split_cnt + slot, 1u) == 0u;
+      finish = __shfl_sync(0xFFFFFFFFu, first, 0) == 0u;
+      if (finish && !spin_until_set(p.split_ready + slot, wc)) return false;
+    }
+    for (int c = 0; c < BN; c += 16) {
+      uint32_t v[16];
+      tmem_ld16(tmem_base + lane_off + buf * BN + c, v);
+      tc_wait_ld();
+      float val[16];
+#pragma unroll
+      for (int t = 0; t < 16; ++t) val[t] = __uint_as_float(v[t]);
+      if (!finish) {
+#pragma unroll
+        for (int t = 0; t < 16; ++t) part[(c + t) * 32 + lane] = val[t];
+        continue;
+      }
+      if (!whole) {
+        float other[16];
+#pragma unroll
+        for (int t = 0; t < 16; ++t) other[t] = __ldcg(part + (c + t) * 32 + lane);
+#pragma unroll
+        for (int t = 0; t < 16; ++t) val[t] = __fadd_rn(val[t], other[t]);
+      }
+      own.chunk(p, unit, c, val, lane, s_warp);
+    }
+    if (!finish) {
+      __threadfence();  // the partial is visible before the flag
+      __syncwarp();
+      if (lane == 0) atomicExch(p.split_ready + slot, 1u);
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&d_empty[buf]);
+    return true;
+  });
+}
+
 // After every role of the CTA is done (call from all threads, after the
 // block barrier that follows the roles): the last CTA to finish turns the
 // per-token maxima into rows and values.
