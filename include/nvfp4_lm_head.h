@@ -28,8 +28,10 @@
  * all experts of an NVFP4 MoE layer; the W4A4 NVFP4 product of
  * `CompressedTensorsW4A4Fp4`; the router and the whole expert layer of an
  * NVFP4 MoE model for a few tokens; log probabilities of given tokens from
- * the logits, with their gradient; an allocation-free variant of the W4A16
- * product; and two self-tests.
+ * the logits, with their gradient; gradients through frozen NVFP4 weights
+ * (the product back, the cross entropy over the lm_head, the gated
+ * feed-forward block); an allocation-free variant of the W4A16 product; and
+ * two self-tests.
  *
  * Conventions for every call:
  *  - All tensor pointers are DEVICE pointers on the current CUDA device,
@@ -708,6 +710,109 @@ nvfp4_status w4a16_lm_head_backward(const void *grad, int dtype, int64_t M, int6
                                     const uint8_t *packed, const uint8_t *scales,
                                     const float *global_scale, int64_t K, void *dx, int out_dtype,
                                     void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of w4a16_cross_entropy without and with `mean`; 0 for
+ * rejected shapes. */
+size_t w4a16_cross_entropy_workspace_bytes(int64_t M, int64_t N, int64_t K, int with_mean);
+
+/*
+ * Softmax cross entropy over the rows of an lm_head, without its logits in
+ * memory: with z[m, n] the logits of w4a16_lm_head and t = targets[m],
+ *   lse[m]  = log sum_n exp(z[m, n])
+ *   loss[m] = lse[m] - z[m, t]
+ *   mean[m, :] = sum_{n != t} exp(z[m, n] - lse[m]) W[n, :]
+ * where W is the dequantized weight.  `mean` is what the gradient needs
+ * (w4a16_cross_entropy_backward); without it (NULL) the call costs one
+ * product, with it two: the logits are not computed again.
+ * A target outside [0, N) (a prompt or padding position) gives loss 0, and
+ * mean over every row; lse does not depend on it.
+ *   x, M, K, packed, scales, global_scale  as given to w4a16_lm_head.
+ *   N            1 <= N < 2^31.
+ *   targets      int64 [M], device.
+ *   loss, lse    fp32 [M], device.  Written.
+ *   mean         fp32 [M, K], device, 16-byte aligned, or NULL.  Written.
+ *   workspace    >= w4a16_cross_entropy_workspace_bytes(M, N, K, mean != NULL),
+ *                256-byte aligned.
+ * Sums are fp32.  The loss keeps its relative accuracy where the target is
+ * nearly certain: it is log(1 + the others' share), not a difference.  In
+ * `mean` each probability is an fp16 number (off by 2^-12 of itself, or by
+ * 2^-40 of the largest but the target's).  Results do not depend on the
+ * schedule.  A token whose x holds an Inf or NaN gets NaN, no other does.
+ * A NaN block scale raises NVFP4_ERR_NONFINITE in the workspace status word.
+ * Of probabilities, 256 MiB are held at a time: more tokens are worked on in
+ * pieces of at least 128.
+ */
+nvfp4_status w4a16_cross_entropy(const void *x, int64_t M, int64_t K, const uint8_t *packed,
+                                 const uint8_t *scales, const float *global_scale, int64_t N,
+                                 const int64_t *targets, float *loss, float *lse, float *mean,
+                                 void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The gradient of w4a16_cross_entropy in x, from the gradients a of loss and
+ * b of lse, with p = exp(-loss[m]):
+ *   dx[m, :] = (a + b) mean[m, :] + (b p - a (1 - p)) W[t, :].
+ * Where the target lies outside [0, N), a counts as 0 and the second term
+ * falls away; a token with a + b = 0 reads no `mean`.
+ *   mean, targets, loss, packed, scales, global_scale, N, K  of the forward call.
+ *   grad_loss    fp32 [M];  grad_lse fp32 [M], or NULL (zero).
+ *   dx           [M, K], bf16 (NVFP4_OUT_BF16) or fp32, device, 16-byte aligned.
+ * One kernel, one read of `mean` and of the targets' rows, no workspace.
+ */
+nvfp4_status w4a16_cross_entropy_backward(const float *mean, int64_t M, int64_t K,
+                                          const uint8_t *packed, const uint8_t *scales,
+                                          const float *global_scale, int64_t N,
+                                          const int64_t *targets, const float *loss,
+                                          const float *grad_loss, const float *grad_lse, void *dx,
+                                          int out_dtype, void *stream);
+
+/* Activation codes of w4a16_glu. */
+#define NVFP4_ACT_SILU 0      /* v / (1 + exp(-v)) */
+#define NVFP4_ACT_GELU_TANH 1 /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2 */
+
+/* Workspace bytes of w4a16_glu and w4a16_glu_backward; 0 for rejected shapes. */
+size_t w4a16_glu_workspace_bytes(int64_t M, int64_t I, int64_t K);
+size_t w4a16_glu_backward_workspace_bytes(int64_t M, int64_t I, int64_t K);
+
+/*
+ * The gated half of a feed-forward block in one product kernel:
+ *   g = W13[0:I] x[m],  u = W13[I:2I] x[m],  out[m] = act(g) * u,
+ * W13 dequantized as in w4a16_lm_head, gate rows first as in w4a16_moe.
+ *   x            bf16 [M, K], device, 16-byte aligned.
+ *   M, I, K      M >= 0 and I >= 0 (no-ops where 0), K >= 16 and K % 16 == 0;
+ *                2 I < 2^31.
+ *   w13_packed, w13_scales, w13_global
+ *                u8 [2I, K/2], u8 (e4m3) [2I, K/16], f32 [1], as
+ *                nvfp4_quantize_rows writes them for W13[2I, K].
+ *   activation   NVFP4_ACT_SILU or NVFP4_ACT_GELU_TANH, else NVFP4_ERR_DTYPE.
+ *   out          [M, I], bf16 (NVFP4_OUT_BF16) or fp32, device, 16-byte aligned.
+ *   workspace    >= w4a16_glu_workspace_bytes(M, I, K), 256-byte aligned.
+ * Accuracy, status word and determinism are those of w4a16_lm_head; g and u
+ * are fp32 and are not written to memory.
+ */
+nvfp4_status w4a16_glu(const void *x, int64_t M, int64_t K, const uint8_t *w13_packed,
+                       const uint8_t *w13_scales, const float *w13_global, int64_t I,
+                       int activation, void *out, int out_dtype, void *workspace,
+                       size_t workspace_bytes, void *stream);
+
+/*
+ * The gradient of w4a16_glu in x (the packed weight is not trained):
+ *   dx[m] = W13[0:I]^T (grad u act'(g)) + W13[I:2I]^T (grad act(g)).
+ * g and u are computed again.
+ *   grad         [M, I] fp32 (dtype NVFP4_OUT_F32) or bf16, device, 16-byte aligned.
+ *   x, M, K, w13_*, I, activation  as given to w4a16_glu.
+ *   dx           [M, K], bf16 (out_dtype NVFP4_OUT_BF16) or fp32, device,
+ *                16-byte aligned; zeros for I == 0.
+ *   workspace    >= w4a16_glu_backward_workspace_bytes(M, I, K), 256-byte aligned.
+ * The gradients of g and u enter the second product as fp16 times a power of
+ * two per token from a bound on their size, 1.13 max|grad| sum|x| 2688 global:
+ * off by 2^-12 of each, or by 2^-40 of that bound where this is more.  A token
+ * whose x or gradient holds an Inf or NaN gets Inf or NaN, no other does.
+ */
+nvfp4_status w4a16_glu_backward(const void *grad, int dtype, const void *x, int64_t M, int64_t K,
+                                const uint8_t *w13_packed, const uint8_t *w13_scales,
+                                const float *w13_global, int64_t I, int activation, void *dx,
+                                int out_dtype, void *workspace, size_t workspace_bytes,
+                                void *stream);
 
 /* ------------------------------------------- allocation-free variant */
 

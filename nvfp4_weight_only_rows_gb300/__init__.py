@@ -69,6 +69,9 @@ __all__ = [
     "w8a8_lm_head_topk_workspace_bytes", "w4a4_lm_head_topk", "w4a4_lm_head_topk_workspace_bytes",
     "moe_route", "w4a16_moe", "w4a16_moe_workspace_bytes", "token_logprobs",
     "token_logprobs_backward", "w4a16_lm_head_backward", "w4a16_lm_head_backward_workspace_bytes",
+    "w4a16_cross_entropy", "w4a16_cross_entropy_backward", "w4a16_cross_entropy_workspace_bytes",
+    "w4a16_glu", "w4a16_glu_backward", "w4a16_glu_workspace_bytes",
+    "w4a16_glu_backward_workspace_bytes",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -198,6 +201,23 @@ def load_library() -> ctypes.CDLL:
     lib.w4a16_lm_head_backward.argtypes = [vp, ctypes.c_int, i64, i64, vp, vp, vp, i64, vp,
                                            ctypes.c_int, vp, sz, vp]
     lib.w4a16_lm_head_backward.restype = st
+    lib.w4a16_cross_entropy_workspace_bytes.argtypes = [i64, i64, i64, ctypes.c_int]
+    lib.w4a16_cross_entropy_workspace_bytes.restype = sz
+    lib.w4a16_cross_entropy.argtypes = [vp, i64, i64, vp, vp, vp, i64, vp, vp, vp, vp, vp, sz, vp]
+    lib.w4a16_cross_entropy.restype = st
+    lib.w4a16_cross_entropy_backward.argtypes = [vp, i64, i64, vp, vp, vp, i64, vp, vp, vp, vp, vp,
+                                                 ctypes.c_int, vp]
+    lib.w4a16_cross_entropy_backward.restype = st
+    for name in ("w4a16_glu_workspace_bytes", "w4a16_glu_backward_workspace_bytes"):
+        f = getattr(lib, name)
+        f.argtypes = [i64, i64, i64]
+        f.restype = sz
+    lib.w4a16_glu.argtypes = [vp, i64, i64, vp, vp, vp, i64, ctypes.c_int, vp, ctypes.c_int, vp, sz,
+                              vp]
+    lib.w4a16_glu.restype = st
+    lib.w4a16_glu_backward.argtypes = [vp, ctypes.c_int, vp, i64, i64, vp, vp, vp, i64,
+                                       ctypes.c_int, vp, ctypes.c_int, vp, sz, vp]
+    lib.w4a16_glu_backward.restype = st
     lib.w4a16_lm_head_noalloc.argtypes = [vp, i64, i64, vp, vp, vp, i64, vp, ctypes.c_int, vp]
     lib.w4a16_lm_head_noalloc.restype = st
     lib.w4a16_lm_head_noalloc_status.argtypes = [ctypes.POINTER(ctypes.c_int32), vp]
@@ -299,11 +319,30 @@ def _quantize_into(fn, where, W, packed, scales, global_scale, workspace, stream
     _check(rc, where)
 
 
+class _LmHead(torch.autograd.Function):
+    """w4a16_lm_head in an autograd graph: w4a16_lm_head_backward is the
+    gradient in x (the packed weight is not trained)."""
+
+    @staticmethod
+    def forward(ctx, x, packed, scales, global_scale, out_dtype, workspace, stream):
+        ctx.save_for_backward(packed, scales, global_scale)
+        return w4a16_lm_head(x, packed, scales, global_scale, None, out_dtype, workspace, stream)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad):
+        dx = w4a16_lm_head_backward(grad.contiguous(), *ctx.saved_tensors)
+        return dx, None, None, None, None, None, None
+
+
 def w4a16_lm_head(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,
                   global_scale: torch.Tensor, out: torch.Tensor | None = None,
                   out_dtype: torch.dtype = torch.float32,
                   workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """logits[M, N] = x . dequant(W)^T for x bf16[M, K] and the packed NVFP4 weight."""
+    """logits[M, N] = x . dequant(W)^T for x bf16[M, K] and the packed NVFP4 weight.
+    Where x requires a gradient and `out` is not given, the logits carry it."""
+    if out is None and isinstance(x, torch.Tensor) and x.requires_grad and torch.is_grad_enabled():
+        return _LmHead.apply(x, packed, scales, global_scale, out_dtype, workspace, stream)
     lib = load_library()
     _need(x, torch.bfloat16, "x")
     M, K = x.shape
@@ -798,6 +837,134 @@ def w4a16_lm_head_backward(grad_logits: torch.Tensor, packed: torch.Tensor, scal
     return (_native or _load_native()).w4a16_lm_head_backward(
         grad_logits, packed, scales, global_scale, out, out_dtype is torch.bfloat16, workspace,
         stream)
+
+
+def w4a16_cross_entropy_workspace_bytes(M: int, N: int, K: int, with_mean: bool = False) -> int:
+    return int(load_library().w4a16_cross_entropy_workspace_bytes(M, N, K, int(with_mean)))
+
+
+class _CrossEntropy(torch.autograd.Function):
+    """w4a16_cross_entropy in an autograd graph: the forward pass also makes
+    `mean`, from which w4a16_cross_entropy_backward takes the gradient in x."""
+
+    @staticmethod
+    def forward(ctx, x, packed, scales, global_scale, targets, workspace, stream):
+        loss, lse, mean = _native.w4a16_cross_entropy(x, packed, scales, global_scale, targets, True,
+                                                      workspace, stream)
+        ctx.save_for_backward(mean, packed, scales, global_scale, targets, loss)
+        ctx.set_materialize_grads(False)
+        return loss, lse
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_loss, grad_lse):
+        if grad_loss is None and grad_lse is None:
+            return (None,) * 7
+        mean, packed, scales, global_scale, targets, loss = ctx.saved_tensors
+        dx = w4a16_cross_entropy_backward(
+            mean, packed, scales, global_scale, targets, loss,
+            torch.zeros_like(loss) if grad_loss is None else grad_loss.contiguous(),
+            None if grad_lse is None else grad_lse.contiguous())
+        return dx, None, None, None, None, None, None
+
+
+def w4a16_cross_entropy(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,
+                        global_scale: torch.Tensor, targets: torch.Tensor, with_mean: bool = False,
+                        workspace: torch.Tensor | None = None, stream=None):
+    """Softmax cross entropy of the logits w4a16_lm_head would give against
+    targets i64[M], without the logits: (loss f32[M], lse f32[M]).  A target
+    outside [0, N) gives loss 0.  Where x requires a gradient, both carry it.
+    With with_mean the third result is mean f32[M, K], the probability-weighted
+    sum of the other rows of the weight, for w4a16_cross_entropy_backward
+    (and no result is in a graph)."""
+    native = _native or _load_native()
+    if not with_mean and isinstance(x, torch.Tensor) and x.requires_grad and torch.is_grad_enabled():
+        return _CrossEntropy.apply(x, packed, scales, global_scale, targets, workspace, stream)
+    return native.w4a16_cross_entropy(x, packed, scales, global_scale, targets, with_mean, workspace,
+                                      stream)
+
+
+def w4a16_cross_entropy_backward(mean: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,
+                                 global_scale: torch.Tensor, targets: torch.Tensor,
+                                 loss: torch.Tensor, grad_loss: torch.Tensor,
+                                 grad_lse: torch.Tensor | None = None,
+                                 out: torch.Tensor | None = None,
+                                 out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """The gradient of w4a16_cross_entropy's loss and lse in x, [M, K], from
+    the mean and loss it returned."""
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
+        raise ValueError("out must be float32 or bfloat16")
+    return (_native or _load_native()).w4a16_cross_entropy_backward(
+        mean, packed, scales, global_scale, targets, loss, grad_loss, grad_lse, out,
+        out_dtype is torch.bfloat16, stream)
+
+
+_ACTIVATION = {"silu": 0, "gelu_tanh": 1}  # NVFP4_ACT_*
+
+
+def _activation_code(activation: str) -> int:
+    code = _ACTIVATION.get(activation)
+    if code is None:
+        raise ValueError(f"activation must be one of {sorted(_ACTIVATION)}, got {activation!r}")
+    return code
+
+
+def w4a16_glu_workspace_bytes(M: int, I: int, K: int) -> int:
+    return int(load_library().w4a16_glu_workspace_bytes(M, I, K))
+
+
+def w4a16_glu_backward_workspace_bytes(M: int, I: int, K: int) -> int:
+    return int(load_library().w4a16_glu_backward_workspace_bytes(M, I, K))
+
+
+class _Glu(torch.autograd.Function):
+    """w4a16_glu in an autograd graph; the backward pass computes gate and up again."""
+
+    @staticmethod
+    def forward(ctx, x, w13_packed, w13_scales, w13_global, activation, bf16, workspace, stream):
+        ctx.save_for_backward(x, w13_packed, w13_scales, w13_global)
+        ctx.activation = activation
+        return _native.w4a16_glu(x, w13_packed, w13_scales, w13_global, _ACTIVATION[activation], None,
+                                 bf16, workspace, stream)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad):
+        dx = w4a16_glu_backward(grad.contiguous(), *ctx.saved_tensors, activation=ctx.activation)
+        return dx, None, None, None, None, None, None, None
+
+
+def w4a16_glu(x: torch.Tensor, w13_packed: torch.Tensor, w13_scales: torch.Tensor,
+              w13_global: torch.Tensor, activation: str = "silu", out: torch.Tensor | None = None,
+              out_dtype: torch.dtype = torch.bfloat16, workspace: torch.Tensor | None = None,
+              stream=None) -> torch.Tensor:
+    """The gated half of a feed-forward block: act(gate) * up [M, I] for x
+    bf16[M, K] and W13 [2I, K], gate rows first; activation "silu" or
+    "gelu_tanh".  Where x requires a gradient and `out` is not given, the
+    result carries it."""
+    native = _native or _load_native()
+    code = _activation_code(activation)
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
+        raise ValueError("out must be float32 or bfloat16")
+    bf16 = out_dtype is torch.bfloat16
+    if out is None and isinstance(x, torch.Tensor) and x.requires_grad and torch.is_grad_enabled():
+        return _Glu.apply(x, w13_packed, w13_scales, w13_global, activation, bf16, workspace, stream)
+    return native.w4a16_glu(x, w13_packed, w13_scales, w13_global, code, out, bf16, workspace, stream)
+
+
+def w4a16_glu_backward(grad: torch.Tensor, x: torch.Tensor, w13_packed: torch.Tensor,
+                       w13_scales: torch.Tensor, w13_global: torch.Tensor,
+                       activation: str = "silu", out: torch.Tensor | None = None,
+                       out_dtype: torch.dtype = torch.bfloat16,
+                       workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The gradient of w4a16_glu in x, [M, K], from grad f32 or bf16 [M, I]
+    (gate and up are computed again; the packed weight is not trained)."""
+    native = _native or _load_native()
+    code = _activation_code(activation)
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
+        raise ValueError("out must be float32 or bfloat16")
+    return native.w4a16_glu_backward(grad, x, w13_packed, w13_scales, w13_global, code, out,
+                                     out_dtype is torch.bfloat16, workspace, stream)
 
 
 def w4a16_lm_head_noalloc(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,

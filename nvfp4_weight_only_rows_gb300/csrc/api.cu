@@ -79,6 +79,23 @@ nvfp4_status lm_head_back_launch(const void* dy, int dtype, int64_t M, int64_t N
                                  int64_t K, void* dx, int out_dtype, void* workspace,
                                  cudaStream_t stream);
 
+size_t cross_entropy_workspace_bytes(int64_t M, int64_t N, int64_t K, bool grad);
+nvfp4_status cross_entropy_launch(const void* x, int64_t M, int64_t K, const uint8_t* packed,
+                                  const uint8_t* scales, const float* global, int64_t N,
+                                  const int64_t* targets, float* loss, float* lse, float* mean,
+                                  void* workspace, cudaStream_t stream);
+nvfp4_status cross_entropy_back_launch(const float* mean, int64_t M, int64_t K,
+                                       const uint8_t* packed, const uint8_t* scales,
+                                       const float* global, int64_t N, const int64_t* targets,
+                                       const float* loss, const float* grad_loss,
+                                       const float* grad_lse, void* dx, int out_dtype,
+                                       cudaStream_t stream);
+size_t glu_workspace_bytes(int64_t M, int64_t I, int64_t K, bool grad);
+nvfp4_status glu_launch(const void* x, int64_t M, int64_t K, const uint8_t* packed,
+                        const uint8_t* scales, const float* global, int64_t I, int act,
+                        const void* dh, int dtype, void* out, int out_dtype, void* workspace,
+                        cudaStream_t stream);
+
 static bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // The kernels are built for sm_103a only; refuse other devices up front.
@@ -623,6 +640,16 @@ static bool train_shape_ok(int64_t M, int64_t N, int64_t K) {
   return M >= 0 && N >= 0 && K >= 16 && K % 16 == 0 && M < kMaxDim && N < kMaxDim && K < kMaxDim;
 }
 
+// An empty sum: zeros, and a clear status word.
+static nvfp4_status zero_result(void* out, int64_t n, int dtype, void* workspace, void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const size_t bytes = (size_t)n * (dtype == NVFP4_OUT_BF16 ? 2 : 4);
+  return cudaMemsetAsync(out, 0, bytes, s) == cudaSuccess &&
+                 cudaMemsetAsync(workspace, 0, sizeof(int32_t), s) == cudaSuccess
+             ? NVFP4_OK
+             : NVFP4_ERR_CUDA;
+}
+
 size_t w4a16_lm_head_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (!train_shape_ok(M, N, K)) return 0;
   return M == 0 || N == 0 ? kWsHeader : lm_head_back_workspace_bytes(M, N, K);
@@ -643,16 +670,114 @@ nvfp4_status w4a16_lm_head_backward(const void* grad, int dtype, int64_t M, int6
     return NVFP4_ERR_ALIGN;
   nvfp4_status st = check_device();
   if (st != NVFP4_OK) return st;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (N == 0) {
-    const size_t bytes = (size_t)M * K * (out_dtype == NVFP4_OUT_BF16 ? 2 : 4);
-    return cudaMemsetAsync(dx, 0, bytes, s) == cudaSuccess &&
-                   cudaMemsetAsync(workspace, 0, 4, s) == cudaSuccess
-               ? NVFP4_OK
-               : NVFP4_ERR_CUDA;
-  }
+  if (N == 0) return zero_result(dx, M * K, out_dtype, workspace, stream);
   return lm_head_back_launch(grad, dtype, M, N, packed, scales, global_scale, K, dx, out_dtype,
-                             workspace, s);
+                             workspace, static_cast<cudaStream_t>(stream));
+}
+
+size_t w4a16_cross_entropy_workspace_bytes(int64_t M, int64_t N, int64_t K, int with_mean) {
+  if (!train_shape_ok(M, N, K) || N == 0) return 0;
+  return M == 0 ? kWsHeader : cross_entropy_workspace_bytes(M, N, K, with_mean != 0);
+}
+
+nvfp4_status w4a16_cross_entropy(const void* x, int64_t M, int64_t K, const uint8_t* packed,
+                                 const uint8_t* scales, const float* global_scale, int64_t N,
+                                 const int64_t* targets, float* loss, float* lse, float* mean,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  if (!train_shape_ok(M, N, K) || N == 0) return NVFP4_ERR_SHAPE;
+  if (M == 0) return NVFP4_OK;
+  if (!x || !packed || !scales || !global_scale || !targets || !loss || !lse) return NVFP4_ERR_NULL;
+  if (!workspace || workspace_bytes < w4a16_cross_entropy_workspace_bytes(M, N, K, mean != nullptr))
+    return NVFP4_ERR_WORKSPACE;
+  if (!aligned(x, 16) || !aligned(packed, 16) || !aligned(scales, 16) ||
+      !aligned(global_scale, 4) || !aligned(targets, 8) || !aligned(loss, 4) || !aligned(lse, 4) ||
+      !aligned(mean, 16) || !aligned(workspace, 256))
+    return NVFP4_ERR_ALIGN;
+  nvfp4_status st = check_device();
+  if (st != NVFP4_OK) return st;
+  return cross_entropy_launch(x, M, K, packed, scales, global_scale, N, targets, loss, lse, mean,
+                              workspace, static_cast<cudaStream_t>(stream));
+}
+
+nvfp4_status w4a16_cross_entropy_backward(const float* mean, int64_t M, int64_t K,
+                                          const uint8_t* packed, const uint8_t* scales,
+                                          const float* global_scale, int64_t N,
+                                          const int64_t* targets, const float* loss,
+                                          const float* grad_loss, const float* grad_lse, void* dx,
+                                          int out_dtype, void* stream) {
+  if (!train_shape_ok(M, N, K) || N == 0) return NVFP4_ERR_SHAPE;
+  if (!float_code(out_dtype)) return NVFP4_ERR_DTYPE;
+  if (M == 0) return NVFP4_OK;
+  if (!mean || !packed || !scales || !global_scale || !targets || !loss || !grad_loss || !dx)
+    return NVFP4_ERR_NULL;
+  if (!aligned(mean, 16) || !aligned(packed, 16) || !aligned(scales, 16) ||
+      !aligned(global_scale, 4) || !aligned(targets, 8) || !aligned(loss, 4) ||
+      !aligned(grad_loss, 4) || !aligned(grad_lse, 4) || !aligned(dx, 16))
+    return NVFP4_ERR_ALIGN;
+  nvfp4_status st = check_device();
+  if (st != NVFP4_OK) return st;
+  return cross_entropy_back_launch(mean, M, K, packed, scales, global_scale, N, targets, loss,
+                                   grad_loss, grad_lse, dx, out_dtype,
+                                   static_cast<cudaStream_t>(stream));
+}
+
+static bool glu_shape_ok(int64_t M, int64_t I, int64_t K) {
+  return I >= 0 && I < kMaxDim / 2 && train_shape_ok(M, 2 * I, K);
+}
+
+static bool act_ok(int activation) {
+  return activation == NVFP4_ACT_SILU || activation == NVFP4_ACT_GELU_TANH;
+}
+
+size_t w4a16_glu_workspace_bytes(int64_t M, int64_t I, int64_t K) {
+  if (!glu_shape_ok(M, I, K)) return 0;
+  return M == 0 || I == 0 ? kWsHeader : glu_workspace_bytes(M, I, K, false);
+}
+
+size_t w4a16_glu_backward_workspace_bytes(int64_t M, int64_t I, int64_t K) {
+  if (!glu_shape_ok(M, I, K)) return 0;
+  return M == 0 || I == 0 ? kWsHeader : glu_workspace_bytes(M, I, K, true);
+}
+
+nvfp4_status w4a16_glu(const void* x, int64_t M, int64_t K, const uint8_t* w13_packed,
+                       const uint8_t* w13_scales, const float* w13_global, int64_t I,
+                       int activation, void* out, int out_dtype, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  if (!glu_shape_ok(M, I, K)) return NVFP4_ERR_SHAPE;
+  if (!float_code(out_dtype) || !act_ok(activation)) return NVFP4_ERR_DTYPE;
+  if (M == 0 || I == 0) return NVFP4_OK;
+  if (!x || !w13_packed || !w13_scales || !w13_global || !out) return NVFP4_ERR_NULL;
+  if (!workspace || workspace_bytes < w4a16_glu_workspace_bytes(M, I, K)) return NVFP4_ERR_WORKSPACE;
+  if (!aligned(x, 16) || !aligned(w13_packed, 16) || !aligned(w13_scales, 16) ||
+      !aligned(w13_global, 4) || !aligned(out, 16) || !aligned(workspace, 256))
+    return NVFP4_ERR_ALIGN;
+  nvfp4_status st = check_device();
+  if (st != NVFP4_OK) return st;
+  return glu_launch(x, M, K, w13_packed, w13_scales, w13_global, I, activation, nullptr, out_dtype,
+                    out, 0, workspace, static_cast<cudaStream_t>(stream));
+}
+
+nvfp4_status w4a16_glu_backward(const void* grad, int dtype, const void* x, int64_t M, int64_t K,
+                                const uint8_t* w13_packed, const uint8_t* w13_scales,
+                                const float* w13_global, int64_t I, int activation, void* dx,
+                                int out_dtype, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+  if (!glu_shape_ok(M, I, K)) return NVFP4_ERR_SHAPE;
+  if (!float_code(dtype) || !float_code(out_dtype) || !act_ok(activation)) return NVFP4_ERR_DTYPE;
+  if (M == 0) return NVFP4_OK;
+  if (!dx || (I > 0 && (!grad || !x || !w13_packed || !w13_scales || !w13_global)))
+    return NVFP4_ERR_NULL;
+  if (!workspace || workspace_bytes < w4a16_glu_backward_workspace_bytes(M, I, K))
+    return NVFP4_ERR_WORKSPACE;
+  if (!aligned(grad, 16) || !aligned(x, 16) || !aligned(w13_packed, 16) ||
+      !aligned(w13_scales, 16) || !aligned(w13_global, 4) || !aligned(dx, 16) ||
+      !aligned(workspace, 256))
+    return NVFP4_ERR_ALIGN;
+  nvfp4_status st = check_device();
+  if (st != NVFP4_OK) return st;
+  if (I == 0) return zero_result(dx, M * K, out_dtype, workspace, stream);
+  return glu_launch(x, M, K, w13_packed, w13_scales, w13_global, I, activation, grad, dtype, dx,
+                    out_dtype, workspace, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

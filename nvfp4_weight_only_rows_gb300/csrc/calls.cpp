@@ -1,5 +1,6 @@
-// calls.cpp -- the Python side of moe_route, w4a16_moe, token_logprobs and
-// token_logprobs_backward as a CPython module: metadata checks, allocation of
+// calls.cpp -- the Python side of moe_route, w4a16_moe, token_logprobs,
+// token_logprobs_backward, w4a16_lm_head_backward, w4a16_cross_entropy and
+// w4a16_glu with their gradients as a CPython module: metadata checks, allocation of
 // results and workspaces, the current stream, and the C ABI call.
 //
 // These kernels take 3 to 30 us at decode sizes, less than ctypes, the checks
@@ -404,16 +405,21 @@ struct Weight {
   const float* global;
 };
 
-Weight weight_args(PyObject* packed, PyObject* scales, PyObject* global, const at::Tensor& first) {
-  const at::Tensor &p = tensor(packed, "packed"), &s = tensor(scales, "scales");
-  const at::Tensor& g = tensor(global, "global_scale");
-  if (p.dim() != 2) throw ValueError("packed must be 2-D [N, K/2]");
+// `names`: of the three in the call.
+constexpr const char* kWeightNames[3] = {"packed", "scales", "global_scale"};
+constexpr const char* kW13Names[3] = {"w13_packed", "w13_scales", "w13_global"};
+
+Weight weight_args(PyObject* packed, PyObject* scales, PyObject* global, const at::Tensor& first,
+                   const char* const (&names)[3] = kWeightNames) {
+  const at::Tensor &p = tensor(packed, names[0]), &s = tensor(scales, names[1]);
+  const at::Tensor& g = tensor(global, names[2]);
+  if (p.dim() != 2) throw ValueError(std::string(names[0]) + " must be 2-D [N, K/2]");
   const int64_t N = p.size(0), K = p.size(1) * 2;
-  check(p, at::kByte, "packed", {N, K / 2}, first);
-  if (s.element_size() != 1)
-    throw ValueError("scales must be float8_e4m3fn (or uint8 bit patterns)");
-  check(s, s.scalar_type(), "scales", {N, K / 16}, first);
-  check(g, at::kFloat, "global_scale", {1}, first);
+  check(p, at::kByte, names[0], {N, K / 2}, first);
+  if (s.scalar_type() != at::kFloat8_e4m3fn && s.scalar_type() != at::kByte)
+    throw ValueError(std::string(names[1]) + " must be float8_e4m3fn (or uint8 bit patterns)");
+  check(s, s.scalar_type(), names[1], {N, K / 16}, first);
+  check(g, at::kFloat, names[2], {1}, first);
   return {N, K, static_cast<const uint8_t*>(p.data_ptr()), static_cast<const uint8_t*>(s.data_ptr()),
           static_cast<const float*>(g.data_ptr())};
 }
@@ -460,7 +466,139 @@ PyObject* lm_head_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// x, packed, scales, global_scale, targets, with_mean, workspace, stream
+PyObject* cross_entropy(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded<8>(n, [&]() -> PyObject* {
+    const at::Tensor &x = tensor(a[0], "x"), &targets = tensor(a[4], "targets");
+    if (x.dim() != 2) throw ValueError("x must be 2-D [M, K]");
+    const int64_t M = x.size(0);
+    const Weight w = weight_args(a[1], a[2], a[3], x);
+    check(x, at::kBFloat16, "x", {M, w.K}, x);
+    check(targets, at::kLong, "targets", {M}, x);
+    const bool with_mean = integer(a[5]) != 0;
+    check_workspace(a[6], x);
+    const OnStream on(a[7], x);
+    Results r;
+    at::Tensor &loss = *r.add(at::kFloat, {M}), &lse = *r.add(at::kFloat, {M});
+    r.allocate(x);
+    at::Tensor mean;  // memory of its own: it is dropped before the losses are
+    if (with_mean) mean = at::empty({M, w.K}, x.options().dtype(at::kFloat));
+    const at::Tensor ws = workspace_arg(
+        a[6], w4a16_cross_entropy_workspace_bytes(M, w.N, w.K, with_mean), x);
+    auto pf = [](const at::Tensor& t) { return static_cast<float*>(t.data_ptr()); };
+    done(w4a16_cross_entropy(x.data_ptr(), M, w.K, w.packed, w.scales, w.global, w.N,
+                             static_cast<const int64_t*>(targets.data_ptr()), pf(loss), pf(lse),
+                             with_mean ? pf(mean) : nullptr, ws.data_ptr(), bytes_of(ws),
+                             on.handle()),
+         "w4a16_cross_entropy");
+    on.result(loss);
+    if (!with_mean) return tuple({loss, lse});
+    on.result(mean);
+    return tuple({loss, lse, mean});
+  });
+}
+
+// mean, packed, scales, global_scale, targets, loss, grad_loss, grad_lse, out,
+// bf16 out (if out is None), stream
+PyObject* cross_entropy_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded<11>(n, [&]() -> PyObject* {
+    const at::Tensor &mean = tensor(a[0], "mean"), &targets = tensor(a[4], "targets");
+    const at::Tensor &loss = tensor(a[5], "loss"), &g = tensor(a[6], "grad_loss");
+    if (mean.dim() != 2) throw ValueError("mean must be 2-D [M, K]");
+    const int64_t M = mean.size(0);
+    const Weight w = weight_args(a[1], a[2], a[3], mean);
+    check(mean, at::kFloat, "mean", {M, w.K}, mean);
+    check(targets, at::kLong, "targets", {M}, mean);
+    check(loss, at::kFloat, "loss", {M}, mean);
+    check(g, at::kFloat, "grad_loss", {M}, mean);
+    const void* gz = optional_f32(a[7], "grad_lse", M, mean);
+    at::ScalarType dt = integer(a[9]) ? at::kBFloat16 : at::kFloat;
+    if (a[8] != Py_None) dt = tensor(a[8], "out").scalar_type();
+    at::Tensor out = optional(a[8], dt, "out", {M, w.K}, mean);
+    const OnStream on(a[10], mean);
+    if (!out.defined()) out = at::empty({M, w.K}, mean.options().dtype(dt));
+    using f32 = const float*;
+    done(w4a16_cross_entropy_backward(
+             f32(mean.data_ptr()), M, w.K, w.packed, w.scales, w.global, w.N,
+             static_cast<const int64_t*>(targets.data_ptr()), f32(loss.data_ptr()),
+             f32(g.data_ptr()), f32(gz), out.data_ptr(),
+             dtype_code(out, "out must be float32 or bfloat16"), on.handle()),
+         "w4a16_cross_entropy_backward");
+    if (a[8] == Py_None) on.result(out);
+    return THPVariable_Wrap(out);
+  });
+}
+
+// Sizes of a gated block's call: x [M, K] on w13 [2I, K].
+struct Glu {
+  Weight w;
+  int64_t M, I;
+};
+
+Glu glu_args(const at::Tensor& x, PyObject* packed, PyObject* scales, PyObject* global,
+             const at::Tensor& first) {
+  if (x.dim() != 2) throw ValueError("x must be 2-D [M, K]");
+  const Weight w = weight_args(packed, scales, global, first, kW13Names);
+  if (w.N % 2) throw ValueError("w13_packed must have gate and up rows: an even number");
+  check(x, at::kBFloat16, "x", {x.size(0), w.K}, first);
+  return {w, x.size(0), w.N / 2};
+}
+
+// x, w13_packed, w13_scales, w13_global, activation code, out, bf16 out (if out
+// is None), workspace, stream
+PyObject* glu(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded<9>(n, [&]() -> PyObject* {
+    const at::Tensor& x = tensor(a[0], "x");
+    const Glu g = glu_args(x, a[1], a[2], a[3], x);
+    at::ScalarType dt = integer(a[6]) ? at::kBFloat16 : at::kFloat;
+    if (a[5] != Py_None) dt = tensor(a[5], "out").scalar_type();
+    at::Tensor out = optional(a[5], dt, "out", {g.M, g.I}, x);
+    check_workspace(a[7], x);
+    const OnStream on(a[8], x);
+    if (!out.defined()) out = at::empty({g.M, g.I}, x.options().dtype(dt));
+    const int code = dtype_code(out, "out must be float32 or bfloat16");
+    const at::Tensor ws = workspace_arg(a[7], w4a16_glu_workspace_bytes(g.M, g.I, g.w.K), x);
+    done(w4a16_glu(x.data_ptr(), g.M, g.w.K, g.w.packed, g.w.scales, g.w.global, g.I,
+                   (int)integer(a[4]), out.data_ptr(), code, ws.data_ptr(), bytes_of(ws),
+                   on.handle()),
+         "w4a16_glu");
+    if (a[5] == Py_None) on.result(out);
+    return THPVariable_Wrap(out);
+  });
+}
+
+// grad, x, w13_packed, w13_scales, w13_global, activation code, out, bf16 out
+// (if out is None), workspace, stream
+PyObject* glu_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded<10>(n, [&]() -> PyObject* {
+    const at::Tensor &dh = tensor(a[0], "grad"), &x = tensor(a[1], "x");
+    const int code = dtype_code(dh, "grad must be float32 or bfloat16 [M, I]");
+    const Glu g = glu_args(x, a[2], a[3], a[4], dh);
+    check(dh, dh.scalar_type(), "grad", {g.M, g.I}, dh);
+    at::ScalarType dt = integer(a[7]) ? at::kBFloat16 : at::kFloat;
+    if (a[6] != Py_None) dt = tensor(a[6], "out").scalar_type();
+    at::Tensor out = optional(a[6], dt, "out", {g.M, g.w.K}, dh);
+    check_workspace(a[8], dh);
+    const OnStream on(a[9], dh);
+    if (!out.defined()) out = at::empty({g.M, g.w.K}, dh.options().dtype(dt));
+    const int out_code = dtype_code(out, "out must be float32 or bfloat16");
+    const at::Tensor ws =
+        workspace_arg(a[8], w4a16_glu_backward_workspace_bytes(g.M, g.I, g.w.K), dh);
+    done(w4a16_glu_backward(dh.data_ptr(), code, x.data_ptr(), g.M, g.w.K, g.w.packed, g.w.scales,
+                            g.w.global, g.I, (int)integer(a[5]), out.data_ptr(), out_code,
+                            ws.data_ptr(), bytes_of(ws), on.handle()),
+         "w4a16_glu_backward");
+    if (a[6] == Py_None) on.result(out);
+    return THPVariable_Wrap(out);
+  });
+}
+
 PyMethodDef kMethods[] = {
+    {"w4a16_cross_entropy", (PyCFunction)(void (*)())cross_entropy, METH_FASTCALL, nullptr},
+    {"w4a16_cross_entropy_backward", (PyCFunction)(void (*)())cross_entropy_backward, METH_FASTCALL,
+     nullptr},
+    {"w4a16_glu", (PyCFunction)(void (*)())glu, METH_FASTCALL, nullptr},
+    {"w4a16_glu_backward", (PyCFunction)(void (*)())glu_backward, METH_FASTCALL, nullptr},
     {"w4a16_lm_head_backward", (PyCFunction)(void (*)())lm_head_backward, METH_FASTCALL, nullptr},
     {"moe_route", (PyCFunction)(void (*)())route, METH_FASTCALL, nullptr},
     {"w4a16_moe", (PyCFunction)(void (*)())moe, METH_FASTCALL, nullptr},

@@ -1,0 +1,496 @@
+// cross_entropy.cu -- softmax cross entropy over the rows of an NVFP4 lm_head
+// without its logits, and its gradient in the hidden states.
+//
+// With z[m, n] the logits of w4a16_lm_head, y = z / ln 2 and t the target:
+//   lse = log sum_n exp z,  loss = lse - z_t,
+//   mean[m, :] = sum_{n != t} p[m, n] W[n, :],   p = exp(z - lse).
+// The gradient of a loss + b lse is (a + b) mean + (a (p_t - 1) + b p_t) W_t:
+// the backward pass is one row of W and one of `mean` per token, and the whole
+// of training costs the logits once (2 M N K) and the product back once.
+//
+// Per chunk of tokens, five kernels at most:
+//  1. w4a16_prep_x_kernel: x as fp16 (lm_head.cu).
+//  2. w4a16_tc_kernel with EntropyEpilogue: the logits of 128 rows x up to 128
+//     tokens at a time in tensor memory; per token and 32 rows an integer
+//     reference r >= max y and s = sum 2^(y - r); for the gradient also
+//     P = 2^(y - r) as fp16 in the workspace.
+//  3. entropy_rows_kernel: r and s joined per token, loss, lse, and P brought
+//     to the token's one reference where a group of rows used a lower one.
+//  4. w4a16_back_kernel: mean = factor P W (back.cu), fp32.
+//
+// The reference: a CTA meets a token's rows in no fixed order, so a group uses
+// the largest reference seen so far for the token, or its own maximum rounded
+// up where that is larger.  References are integers and e^z is formed as
+// 2^(y - round(y)) times a power of two, so another reference changes no bit
+// of the mantissa: the sums and P do not depend on the schedule.  (P is
+// rounded to 11 bits, then truncated where fp16 is subnormal, below 2^-29 of
+// the reference; truncations to coarser and coarser grids give the last one.)
+// After the first wave of units hardly a group raises its reference.
+//
+// The target's row is left out of r, s and P: where the model is sure of the
+// target, 1 - p_t and the pull of all other rows keep their relative accuracy
+// (a P of the target, rounded to 2^-12, would be larger than that pull).
+// P in fp16 is off by 2^-12 of each term, at random; the result is rounded to
+// bf16, 2^-9 of itself.
+#include "back.cuh"
+#include "w4a16_tc.cuh"
+
+namespace nvfp4 {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNoRef = -3.0e38f;       // the reference of a token without rows so far
+constexpr float kMagic = 12582912.0f;    // 1.5 * 2^23: x + it - it rounds |x| < 2^22 to an integer
+constexpr float kMagicLimit = 2097152.0f;
+constexpr int kPBits = 15;               // P is stored times 2^15
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// fp32 rounded to 11 bits, then to fp16 towards zero (which rounds only
+// subnormals).
+__device__ __forceinline__ uint16_t f16_canonical(float v) {
+  const float r = __uint_as_float((__float_as_uint(v) + 0x1000u) & 0xFFFFE000u);
+  return __half_as_ushort(__float2half_rz(r));
+}
+
+// A token's reference word: the low half of its line (see WsLayout keys),
+// order_key of the reference, 0 for none.
+__device__ __forceinline__ uint32_t* ref_word(const GemmArgs& p, int64_t tok) {
+  return reinterpret_cast<uint32_t*>(p.am_keys + tok * kKeyStride);
+}
+
+struct EntropyArgs {
+  const int64_t* targets;  // [M]
+  float* y_t;              // [M] the target's y
+  float2* part;            // [groups of 32 rows][M] {r, 2^15 s}
+  __half* P;               // [tokens rounded up to BN, stride]
+  int64_t stride;
+};
+
+template <bool kGrad>
+struct EntropyEpilogue {
+  static constexpr bool kOwn = true, kPaired = false;
+  static constexpr int kWarpBytes = 3 * kMaxBN * 4;  // multiplier, reference, target of a token
+  struct Unit {
+    int64_t t0;
+    uint32_t n_base;  // the warp's first row
+  };
+  EntropyArgs a;
+
+  __device__ Unit begin(const GemmArgs& p, uint32_t u, int q, int lane, uint8_t* s) const {
+    float* mul = reinterpret_cast<float*>(s);
+    float* ref = mul + kMaxBN;
+    int32_t* tgt = reinterpret_cast<int32_t*>(ref + kMaxBN);
+    const uint32_t tile = u / (uint32_t)p.n_ttiles;
+    const int64_t t0 = (int64_t)(u - tile * (uint32_t)p.n_ttiles) * p.BN;
+    for (int t = lane; t < p.BN; t += 32) {
+      const bool live = t0 + t < p.M;
+      mul[t] = live ? __ldcg(p.tok_scale + t0 + t) * kLog2e : 0.0f;
+      const uint32_t key = live ? __ldcg(ref_word(p, t0 + t)) : 0u;
+      ref[t] = key ? key_value(key) : (live ? kNoRef : 0.0f);
+      const int64_t want = live ? __ldg(a.targets + t0 + t) : -1;
+      tgt[t] = want >= 0 && want < p.N ? (int32_t)want : -1;
+    }
+    __syncwarp();
+    return {t0, tile * kRows + (uint32_t)q * 32u};
+  }
+
+  __device__ void chunk(const GemmArgs& p, const Unit& u, int c, const float (&v)[16], int lane,
+                        uint8_t* s) const {
+    if (u.n_base >= p.N) return;  // warp-uniform
+    float* ref = reinterpret_cast<float*>(s) + kMaxBN;
+    const int32_t* tgt = reinterpret_cast<const int32_t*>(ref + kMaxBN);
+    const int64_t tc = u.t0 + c, live = p.M - tc;
+    const bool valid = u.n_base + (uint32_t)lane < p.N;
+    const float none = __int_as_float(0xFF800000);
+    float mul[16], y[16], r[16];
+    lds_f32x16(reinterpret_cast<const float*>(s) + c, mul);
+#pragma unroll
+    for (int t = 0; t < 16; t += 2) {
+      const float2 w = __fmul2_rn(make_float2(v[t], v[t + 1]), make_float2(mul[t], mul[t + 1]));
+      y[t] = valid ? w.x : none;
+      y[t + 1] = valid ? w.y : none;
+    }
+    // targets among these 32 rows: their y is kept, and they count no further
+    const int32_t d = lane < 16 ? tgt[c + lane] - (int32_t)u.n_base : -1;
+    const bool has = lane < 16 && tgt[c + (lane & 15)] >= 0 && (uint32_t)d < 32u;
+    const uint32_t hits = __ballot_sync(0xFFFFFFFFu, has);
+    if (hits) {
+#pragma unroll
+      for (int t = 0; t < 16; ++t) {
+        if (!((hits >> t) & 1u)) continue;
+        if (lane == __shfl_sync(0xFFFFFFFFu, d, t)) {
+          a.y_t[tc + t] = y[t];
+          y[t] = none;
+        }
+      }
+    }
+    lds_f32x16(ref + c, r);
+    bool above = false;
+#pragma unroll
+    for (int t = 0; t < 16; ++t) above |= !(y[t] <= r[t]);
+    if (__any_sync(0xFFFFFFFFu, above)) {  // a reference rises (or a NaN becomes one)
+      __syncwarp();
+#pragma unroll
+      for (int t = 0; t < 16; ++t) {
+        if (!__any_sync(0xFFFFFFFFu, !(y[t] <= r[t]))) continue;
+        const float top = key_value(__reduce_max_sync(0xFFFFFFFFu, order_key(y[t])));
+        r[t] = ceilf(top);
+        if (lane == 0) {
+          ref[c + t] = r[t];
+          if (t < live) atomicMax(ref_word(p, tc + t), order_key(r[t]));
+        }
+      }
+      __syncwarp();
+    }
+    // 2^(y - r + 15): y is at most r; below r - 140 nothing is left of it
+    float e[16];
+    const bool far = __any_sync(0xFFFFFFFFu, !(fabsf(ref[c + (lane & 15)]) < kMagicLimit));
+    if (!far) {
+#pragma unroll
+      for (int t = 0; t < 16; ++t) {
+        const float x = fmaxf(y[t], r[t] - 140.0f);
+        const float whole = x + kMagic;
+        const int32_t shift = __float_as_int(whole) - __float_as_int(r[t] + kMagic);
+        e[t] = ex2(x - (whole - kMagic)) * __int_as_float((shift + 127 + kPBits) << 23);
+      }
+    } else {  // no reference yet, one that is no number, or logits in the millions
+#pragma unroll
+      for (int t = 0; t < 16; ++t) e[t] = ex2(y[t] - r[t]) * (float)(1 << kPBits);
+    }
+    if (kGrad && valid) {
+      uint16_t* o = reinterpret_cast<uint16_t*>(a.P) + tc * a.stride + u.n_base + lane;
+#pragma unroll
+      for (int t = 0; t < 16; ++t, o += a.stride) *o = f16_canonical(e[t]);
+    }
+    // sums over the warp's rows: as group_maxima, lanes 2 t and 2 t + 1 end with token t's
+#pragma unroll
+    for (int w = 8; w >= 1; w >>= 1) {
+      const bool upper = (lane & (2 * w)) != 0;
+#pragma unroll
+      for (int j = 0; j < w; ++j) {
+        const float mine = upper ? e[j + w] : e[j];
+        const float send = upper ? e[j] : e[j + w];
+        e[j] = mine + __shfl_xor_sync(0xFFFFFFFFu, send, 2 * w);
+      }
+    }
+    e[0] += __shfl_xor_sync(0xFFFFFFFFu, e[0], 1);
+    const int t = (lane >> 1) & 15;
+    if ((lane & 1) == 0 && t < live)
+      a.part[(int64_t)(u.n_base >> 5) * p.M + tc + t] = make_float2(ref[c + t], e[0]);
+  }
+};
+
+// ------------------------------------------------------------ rows joined
+// 2^d for an integer d <= 0 (0 below 2^-126).
+__device__ __forceinline__ float pow2_down(float d) {
+  return d > -127.0f ? __int_as_float((127 + (int)d) << 23) : 0.0f;
+}
+
+// {r, s} and {r', s'} as one.
+__device__ __forceinline__ float2 join(float2 a, float2 b) {
+  if (b.x != b.x) return b;
+  if (b.x > a.x) return make_float2(b.x, a.y * pow2_down(a.x - b.x) + b.y);
+  return make_float2(a.x, a.y + b.y * pow2_down(b.x - a.x));
+}
+
+constexpr int kJoinThreads = 1024;
+
+// A CTA takes TT (a power of two) neighbouring tokens, a thread every
+// (1024 / TT)-th group of one of them.
+template <bool kGrad>
+__global__ void __launch_bounds__(kJoinThreads)
+    entropy_rows_kernel(const float2* __restrict__ part, int64_t M, int64_t N, int tt_log2,
+                        const int64_t* __restrict__ targets, const float* __restrict__ y_t,
+                        const float* __restrict__ global, float* __restrict__ loss,
+                        float* __restrict__ lse, float* __restrict__ factor, __half* P,
+                        int64_t stride) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ float2 s_part[kJoinThreads];
+  const int TT = 1 << tt_log2;
+  const int slices = kJoinThreads >> tt_log2;
+  const int64_t m = (int64_t)blockIdx.x * TT + (threadIdx.x & (TT - 1));
+  const int slice = threadIdx.x >> tt_log2;
+  const int64_t groups = (N + 31) / 32;
+  float2 acc = make_float2(kNoRef, 0.0f);
+  if (m < M) {
+#pragma unroll 4
+    for (int64_t g = slice; g < groups; g += slices) acc = join(acc, __ldcg(part + g * M + m));
+  }
+  s_part[threadIdx.x] = acc;
+  for (int w = kJoinThreads / 2; w >= TT; w >>= 1) {
+    __syncthreads();
+    if ((int)threadIdx.x < w) s_part[threadIdx.x] = join(s_part[threadIdx.x], s_part[threadIdx.x + w]);
+  }
+  __syncthreads();
+  if (m >= M) return;
+  const float2 all = s_part[threadIdx.x & (TT - 1)];
+  const float r = all.x;
+  if (slice == 0) {
+    const float L = all.y * (1.0f / (1 << kPBits));  // the others' sum over 2^r
+    const float log2L = log2f(L);
+    const int64_t t = targets[m];
+    float f = __fdividef(1.0f, L), lo, ls;
+    if (t >= 0 && t < N) {
+      const float y = __ldcg(y_t + m);
+      const float ratio = log2L - (y - r);  // log2 of the others over the target
+      const float small = log1pf(exp2f(-fabsf(ratio)));
+      if (ratio < 0.0f) {
+        lo = small;
+        ls = fmaf(y, kLn2, small);
+      } else {  // (also NaN)
+        lo = fmaf(ratio, kLn2, small);
+        ls = fmaf(r + log2L, kLn2, small);
+      }
+      f = f / (1.0f + exp2f(-ratio));
+      if (L == 0.0f) f = 0.0f;
+    } else {
+      lo = 0.0f;
+      ls = (r + log2L) * kLn2;
+    }
+    f += r - r;  // NaN where the token's reference is none
+    loss[m] = lo;
+    lse[m] = ls;
+    if (kGrad) factor[m] = *global * f * (1.0f / (1 << kPBits));
+  }
+  if (!kGrad) return;
+  for (int64_t g = slice; g < groups; g += slices) {
+    const float rg = __ldcg(part + g * M + m).x;
+    if (!(rg < r) || rg == kNoRef) continue;  // at the reference, NaN, or nothing there
+    const float scale = pow2_down(rg - r);
+    uint4* v = reinterpret_cast<uint4*>(P + m * stride + g * 32);
+    const int n16 = (int)min((int64_t)4, (stride - g * 32) / 8);
+    for (int i = 0; i < n16; ++i) {
+      uint4 w = v[i];
+      uint32_t* h = &w.x;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f2 = __half22float2(*reinterpret_cast<const __half2*>(h + j));
+        h[j] = (uint32_t)__half_as_ushort(__float2half_rz(f2.x * scale)) |
+               ((uint32_t)__half_as_ushort(__float2half_rz(f2.y * scale)) << 16);
+      }
+      v[i] = w;
+    }
+  }
+}
+
+// ------------------------------------------------------------ backward pass
+// dx[m] = (a + b) mean[m] + (b p_t - a (1 - p_t)) W[t], one CTA a token.
+__global__ void __launch_bounds__(256)
+    entropy_back_kernel(const float* __restrict__ mean, int64_t N, int64_t K,
+                        const uint8_t* __restrict__ packed, const uint8_t* __restrict__ scales,
+                        const float* __restrict__ global, const int64_t* __restrict__ targets,
+                        const float* __restrict__ loss, const float* __restrict__ grad_loss,
+                        const float* __restrict__ grad_lse, void* dx, int bf16) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int64_t m = blockIdx.x;
+  const int64_t t = targets[m];
+  const bool has = t >= 0 && t < N;
+  const float a = has ? grad_loss[m] : 0.0f;
+  const float b = grad_lse ? grad_lse[m] : 0.0f;
+  const float others = has ? -expm1f(-loss[m]) : 0.0f;  // 1 - p_t
+  const float fm = a + b;
+  const float ft = has ? (b * (1.0f - others) - a * others) * *global : 0.0f;
+  const uint8_t* codes = packed + t * (K / 2);
+  const uint8_t* sf = scales + t * (K / 16);
+  for (int64_t k = (int64_t)threadIdx.x * 8; k < K; k += (int64_t)blockDim.x * 8) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      // a token that counts nowhere gets zeros whatever its hidden state holds
+      const float4 f = fm == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                                  : __ldg(reinterpret_cast<const float4*>(mean + m * K + k) + i);
+      v[4 * i] = fm * f.x;
+      v[4 * i + 1] = fm * f.y;
+      v[4 * i + 2] = fm * f.z;
+      v[4 * i + 3] = fm * f.w;
+    }
+    if (has) {
+      uint32_t h[4], s01, s23;
+      e2m1x8_to_f16(__ldg(reinterpret_cast<const uint32_t*>(codes + k / 2)), h);
+      scales4_to_f16(__ldg(sf + k / 16), s01, s23);
+      const float s = ft * __half2float(__ushort_as_half((unsigned short)s01));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 w = __half22float2(*reinterpret_cast<const __half2*>(h + i));
+        v[2 * i] = fmaf(s, w.x, v[2 * i]);
+        v[2 * i + 1] = fmaf(s, w.y, v[2 * i + 1]);
+      }
+    }
+    if (bf16) {
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        o[i] = *reinterpret_cast<const uint32_t*>(&p);
+      }
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(dx) + m * K + k) =
+          make_uint4(o[0], o[1], o[2], o[3]);
+    } else {
+      float4* o = reinterpret_cast<float4*>(static_cast<float*>(dx) + m * K + k);
+      o[0] = make_float4(v[0], v[1], v[2], v[3]);
+      o[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  }
+}
+
+// ------------------------------------------------------------ host side
+// Workspace: [status header][fp16 x][token multipliers][token lines][y of the
+// targets][factors][{r, s} per token and 32 rows][P][partials of the logits'
+// cut units][their counters and flags][the product back's own regions, whose
+// counters and flags come first][staged weight rows]; the prep kernel clears
+// the counters and flags of both products at once.
+struct EntropyLayout {
+  size_t x16, tok, keys, y_t, factor, part, P, split_part, cnt, ready, end;
+  int64_t stride;
+  int BN, grid;
+  BackLayout back;
+};
+
+static EntropyLayout entropy_layout(int64_t M, int64_t N, int64_t K, bool grad, int sms) {
+  EntropyLayout l;
+  l.BN = lm_head_token_tile(M);
+  const int64_t m_pad = (M + l.BN - 1) / l.BN * l.BN;
+  const int64_t units = ((N + kRows - 1) / kRows) * (m_pad / l.BN);
+  l.grid = (int)std::min<int64_t>(sms, units);
+  l.stride = (N + 7) / 8 * 8;
+  l.x16 = kWsHeader;
+  l.tok = l.x16 + align_up((size_t)m_pad * K * 2, 1024);
+  l.keys = l.tok + align_up((size_t)m_pad * 4, 256);
+  l.y_t = l.keys + (size_t)m_pad * kKeyStride * 8;
+  l.factor = l.y_t + align_up((size_t)M * 4, 256);
+  l.part = l.factor + align_up((size_t)M * 4, 256);
+  l.P = l.part + align_up((size_t)((N + 31) / 32) * M * 8, 256);
+  l.split_part = l.P + (grad ? align_up((size_t)m_pad * l.stride * 2, 256) : 0);
+  l.cnt = l.split_part + align_up((size_t)l.grid * 4 * l.BN * 32 * 4, 256);
+  l.ready = l.cnt + align_up((size_t)l.grid * 4 * 4, 256);
+  l.end = l.ready + align_up((size_t)l.grid * 4 * 4, 256);
+  l.back = {};
+  if (grad) {
+    l.back = back_layout(M, N, K, sms, l.end);
+    l.end = l.back.total;
+  }
+  return l;
+}
+
+static int64_t entropy_chunk(int64_t M, int64_t N, bool grad) {
+  return chunk_tokens(M, grad ? (N + 7) / 8 * 16 : (N + 31) / 32 * 8);
+}
+
+static WeightStage entropy_stage(int64_t M, int64_t N, int64_t K, bool grad, int sms) {
+  const int64_t chunk = entropy_chunk(M, N, grad);
+  size_t end = entropy_layout(chunk, N, K, grad, sms).end;
+  if (M % chunk) end = std::max(end, entropy_layout(M % chunk, N, K, grad, sms).end);
+  return weight_stage(N, K, end, true);
+}
+
+size_t cross_entropy_workspace_bytes(int64_t M, int64_t N, int64_t K, bool grad) {
+  return entropy_stage(M, N, K, grad, std::max(sm_count(), 1)).total;
+}
+
+template <bool kGrad>
+static nvfp4_status entropy_run(const void* x, int64_t M, int64_t K, const uint8_t* packed,
+                                const uint8_t* scales, const float* global, int64_t N,
+                                const int64_t* targets, float* loss, float* lse, float* mean,
+                                uint8_t* ws, cudaStream_t stream) {
+  const int sms = sm_count();
+  if (sms <= 0) return NVFP4_ERR_CUDA;
+  const WeightStage wst = entropy_stage(M, N, K, kGrad, sms);
+  if (stage_weights(wst, packed, scales, N, K, ws, stream) != cudaSuccess) return NVFP4_ERR_CUDA;
+  CUtensorMap tm_packed, tm_scales, tm_x;
+  if (!encode_weight_maps(&tm_packed, &tm_scales, wst, packed, scales, N, K, ws))
+    return NVFP4_ERR_CUDA;
+  const int64_t chunk = entropy_chunk(M, N, kGrad);
+  for (int64_t m0 = 0; m0 < M; m0 += chunk) {
+    const int64_t rows = std::min(chunk, M - m0);
+    const EntropyLayout L = entropy_layout(rows, N, K, kGrad, sms);
+    const int64_t n_tt = (rows + L.BN - 1) / L.BN;
+    __half* x16 = reinterpret_cast<__half*>(ws + L.x16);
+    float* tok = reinterpret_cast<float*>(ws + L.tok);
+    float* factor = reinterpret_cast<float*>(ws + L.factor);
+    unsigned long long* keys = reinterpret_cast<unsigned long long*>(ws + L.keys);
+    const size_t flags_end = kGrad ? L.back.part : L.end;
+    if (prep_x_launch(static_cast<const uint8_t*>(x) + (size_t)m0 * K * 2, rows, K, n_tt * L.BN,
+                      global, x16, tok, m0 == 0 ? reinterpret_cast<int32_t*>(ws) : nullptr,
+                      reinterpret_cast<uint32_t*>(ws + L.cnt), (int)((flags_end - L.cnt) / 4), keys,
+                      stream) != cudaSuccess)
+      return NVFP4_ERR_CUDA;
+    if (!encode_2d(&tm_x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x16, (uint64_t)K,
+                   (uint64_t)(n_tt * L.BN), (uint64_t)K * 2, 64, (uint32_t)L.BN,
+                   CU_TENSOR_MAP_SWIZZLE_128B))
+      return NVFP4_ERR_CUDA;
+    GemmArgs a = {};
+    a.M = rows;
+    a.N = N;
+    a.K = K;
+    a.BN = L.BN;
+    a.n_ttiles = (int)n_tt;
+    a.n_units = ((N + kRows - 1) / kRows) * n_tt;
+    a.n_kb = (int)((K + kKB - 1) / kKB);
+    schedule_units(a, L.grid);
+    a.tok_scale = tok;
+    a.status = reinterpret_cast<int32_t*>(ws);
+    a.split_cnt = reinterpret_cast<uint32_t*>(ws + L.cnt);
+    a.split_ready = reinterpret_cast<uint32_t*>(ws + L.ready);
+    a.split_part = reinterpret_cast<float*>(ws + L.split_part);
+    a.am_keys = keys;
+    const bool deep = L.BN <= 64;
+    const int stages = deep ? 3 : 2;
+    a.dbuf_log2 = (4 * L.BN + stages * (kKB / 2) <= 512) ? 2u : 1u;
+    a.tmem_cols = ((L.BN << a.dbuf_log2) + stages * (kKB / 2) <= 256) ? 256u : 512u;
+    const EntropyArgs ea{targets + m0, reinterpret_cast<float*>(ws + L.y_t),
+                         reinterpret_cast<float2*>(ws + L.part),
+                         kGrad ? reinterpret_cast<__half*>(ws + L.P) : nullptr, L.stride};
+    const EntropyEpilogue<kGrad> epi{ea};
+    cudaError_t e =
+        deep ? launch_gemm_with<3, 6, 3>(epi, tm_packed, tm_scales, tm_x, a, L.grid, stream)
+             : launch_gemm_with<2, 4, 2>(epi, tm_packed, tm_scales, tm_x, a, L.grid, stream);
+    if (e != cudaSuccess) return NVFP4_ERR_CUDA;
+    int tt_log2 = 0;
+    while (tt_log2 < 3 && (1 << (tt_log2 + 1)) <= rows) ++tt_log2;
+    PdlLaunch l(dim3((unsigned)((rows + (1 << tt_log2) - 1) >> tt_log2)), dim3(kJoinThreads), 0,
+                stream);
+    e = cudaLaunchKernelEx(&l.cfg, entropy_rows_kernel<kGrad>, (const float2*)ea.part, rows, N,
+                           tt_log2, ea.targets, (const float*)ea.y_t, global, loss + m0, lse + m0,
+                           factor, ea.P, L.stride);
+    if (e == cudaSuccess && kGrad) {
+      const BackCall c{rows, N, K, ea.P, L.stride, packed, scales, &wst, factor, mean + m0 * K,
+                       NVFP4_OUT_F32};
+      e = back_launch(c, L.back, ws, stream);
+    }
+    if (e != cudaSuccess) return NVFP4_ERR_CUDA;
+  }
+  return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+}
+
+nvfp4_status cross_entropy_launch(const void* x, int64_t M, int64_t K, const uint8_t* packed,
+                                  const uint8_t* scales, const float* global, int64_t N,
+                                  const int64_t* targets, float* loss, float* lse, float* mean,
+                                  void* workspace, cudaStream_t stream) {
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  return mean ? entropy_run<true>(x, M, K, packed, scales, global, N, targets, loss, lse, mean, ws,
+                                  stream)
+              : entropy_run<false>(x, M, K, packed, scales, global, N, targets, loss, lse, nullptr,
+                                   ws, stream);
+}
+
+nvfp4_status cross_entropy_back_launch(const float* mean, int64_t M, int64_t K,
+                                       const uint8_t* packed, const uint8_t* scales,
+                                       const float* global, int64_t N, const int64_t* targets,
+                                       const float* loss, const float* grad_loss,
+                                       const float* grad_lse, void* dx, int out_dtype,
+                                       cudaStream_t stream) {
+  PdlLaunch l(dim3((unsigned)M), dim3(256), 0, stream);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, entropy_back_kernel, mean, N, K, packed, scales,
+                                           global, targets, loss, grad_loss, grad_lse, dx,
+                                           (int)(out_dtype == NVFP4_OUT_BF16));
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+}
+
+}  // namespace nvfp4

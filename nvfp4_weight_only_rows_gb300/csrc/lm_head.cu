@@ -74,8 +74,8 @@ __global__ void __launch_bounds__(256) w4a16_prep_x_kernel(const uint16_t* __res
   // the GEMM may launch now: it waits for this grid's results (griddepcontrol.wait)
   // only where it reads them, and streams the weights meanwhile
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (blockIdx.x == 0) {  // a fresh call: clear the status word and the split-K flags
-    if (threadIdx.x == 0) *status = NVFP4_OK;
+  if (blockIdx.x == 0) {  // a fresh call: clear the status word (if given) and the split-K flags
+    if (threadIdx.x == 0 && status) *status = NVFP4_OK;
     for (int i = threadIdx.x; i < n_split_flags; i += blockDim.x) split_flags[i] = 0;
   }
   __shared__ int32_t s_grp[kMaxGroups + 1];
