@@ -703,7 +703,7 @@ size_t w4a16_lm_head_backward_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * where that is more).  Products are exact, sums fp32 in a fixed order (the
  * result does not depend on the schedule).  A token whose gradient holds an
  * Inf or NaN gets Inf or NaN, no other does.  A NaN block scale raises
- * NVFP4_ERR_NONFINITE in the workspace status word.  Up to 256 MiB of fp16
+ * NVFP4_ERR_NONFINITE in the workspace status word.  Up to 512 MiB of fp16
  * gradient are held at a time: more tokens are worked on in pieces.
  */
 nvfp4_status w4a16_lm_head_backward(const void *grad, int dtype, int64_t M, int64_t N,
@@ -736,10 +736,10 @@ size_t w4a16_cross_entropy_workspace_bytes(int64_t M, int64_t N, int64_t K, int 
  * Sums are fp32.  The loss keeps its relative accuracy where the target is
  * nearly certain: it is log(1 + the others' share), not a difference.  In
  * `mean` each probability is an fp16 number (off by 2^-12 of itself, or by
- * 2^-40 of the largest but the target's).  Results do not depend on the
+ * 2^-36 of the largest but the target's).  Results do not depend on the
  * schedule.  A token whose x holds an Inf or NaN gets NaN, no other does.
  * A NaN block scale raises NVFP4_ERR_NONFINITE in the workspace status word.
- * Of probabilities, 256 MiB are held at a time: more tokens are worked on in
+ * Of probabilities, 512 MiB are held at a time: more tokens are worked on in
  * pieces of at least 128.
  */
 nvfp4_status w4a16_cross_entropy(const void *x, int64_t M, int64_t K, const uint8_t *packed,

@@ -8,13 +8,13 @@
 
 namespace nvfp4 {
 
-// Workspace of one product after `off`: the counters and flags of cut units
-// (zeroed by the kernel before it), their partials, and, where the weight's
-// rows are split over several units, fp32 results per split.
+// The product's cut into tiles of 128 columns x BN tokens: n_whole of them
+// whole, n_rest in n_splits parts along the weight's rows; and its workspace
+// after `off`: the sums of those parts.
 struct BackLayout {
-  size_t cnt, ready, part, splits, total;
+  size_t part, total;
+  int64_t n_whole, n_rest;
   int grid, BN, n_splits, n_kb;
-  int n_flags() const { return (int)((part - cnt) / 4); }
 };
 BackLayout back_layout(int64_t M, int64_t N, int64_t K, int sms, size_t off);
 
@@ -33,7 +33,7 @@ cudaError_t back_launch(const BackCall& c, const BackLayout& L, uint8_t* ws, cud
 
 // Tokens of a call that are worked on at a time, so that a fp16 row of
 // `row_bytes` for each fits `kChunkBytes`: whole tiles of 128.
-constexpr int64_t kChunkBytes = (int64_t)256 << 20;
+constexpr int64_t kChunkBytes = (int64_t)512 << 20;
 static inline int64_t chunk_tokens(int64_t M, int64_t row_bytes) {
   const int64_t fit = kChunkBytes / row_bytes / kMaxBN * kMaxBN;
   return M < kMaxBN ? M : std::min(M, std::max<int64_t>(fit, kMaxBN));

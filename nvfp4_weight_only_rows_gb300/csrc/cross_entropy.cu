@@ -11,21 +11,23 @@
 // Per chunk of tokens, five kernels at most:
 //  1. w4a16_prep_x_kernel: x as fp16 (lm_head.cu).
 //  2. w4a16_tc_kernel with EntropyEpilogue: the logits of 128 rows x up to 128
-//     tokens at a time in tensor memory; per token and 32 rows an integer
-//     reference r >= max y and s = sum 2^(y - r); for the gradient also
-//     P = 2^(y - r) as fp16 in the workspace.
+//     tokens at a time in tensor memory; per token and 32 rows a reference
+//     r >= max y, a multiple of 4, and s = sum 2^(y - r); for the gradient
+//     also P = 2^(y - r) as fp16 in the workspace.
 //  3. entropy_rows_kernel: r and s joined per token, loss, lse, and P brought
 //     to the token's one reference where a group of rows used a lower one.
 //  4. w4a16_back_kernel: mean = factor P W (back.cu), fp32.
 //
 // The reference: a CTA meets a token's rows in no fixed order, so a group uses
 // the largest reference seen so far for the token, or its own maximum rounded
-// up where that is larger.  References are integers and e^z is formed as
+// up where that is larger.  References are whole and e^z is formed as
 // 2^(y - round(y)) times a power of two, so another reference changes no bit
 // of the mantissa: the sums and P do not depend on the schedule.  (P is
 // rounded to 11 bits, then truncated where fp16 is subnormal, below 2^-29 of
 // the reference; truncations to coarser and coarser grids give the last one.)
-// After the first wave of units hardly a group raises its reference.
+// In steps of 4 the reference hardly moves after the first wave of units (with
+// steps of 1 it rose late for most tokens: the largest of 128256 normal logits
+// is two above the largest of 2000).
 //
 // The target's row is left out of r, s and P: where the model is sure of the
 // target, 1 - p_t and the pull of all other rows keep their relative accuracy
@@ -43,6 +45,7 @@ constexpr float kNoRef = -3.0e38f;       // the reference of a token without row
 constexpr float kMagic = 12582912.0f;    // 1.5 * 2^23: x + it - it rounds |x| < 2^22 to an integer
 constexpr float kMagicLimit = 2097152.0f;
 constexpr int kPBits = 15;               // P is stored times 2^15
+constexpr float kRefStep = 4.0f;         // references are multiples of this
 
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -74,6 +77,7 @@ struct EntropyArgs {
 template <bool kGrad>
 struct EntropyEpilogue {
   static constexpr bool kOwn = true, kPaired = false;
+  static constexpr int kPartStages = 6;
   static constexpr int kWarpBytes = 3 * kMaxBN * 4;  // multiplier, reference, target of a token
   struct Unit {
     int64_t t0;
@@ -139,7 +143,7 @@ struct EntropyEpilogue {
       for (int t = 0; t < 16; ++t) {
         if (!__any_sync(0xFFFFFFFFu, !(y[t] <= r[t]))) continue;
         const float top = key_value(__reduce_max_sync(0xFFFFFFFFu, order_key(y[t])));
-        r[t] = ceilf(top);
+        r[t] = kRefStep * ceilf(top * (1.0f / kRefStep));
         if (lane == 0) {
           ref[c + t] = r[t];
           if (t < live) atomicMax(ref_word(p, tc + t), order_key(r[t]));
@@ -198,6 +202,13 @@ __device__ __forceinline__ float2 join(float2 a, float2 b) {
   return make_float2(a.x, a.y + b.y * pow2_down(b.x - a.x));
 }
 
+// Two fp16 times a power of two, towards zero.
+__device__ __forceinline__ uint32_t scale_down(uint32_t h, float f) {
+  const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return (uint32_t)__half_as_ushort(__float2half_rz(v.x * f)) |
+         ((uint32_t)__half_as_ushort(__float2half_rz(v.y * f)) << 16);
+}
+
 constexpr int kJoinThreads = 1024;
 
 // A CTA takes TT (a power of two) neighbouring tokens, a thread every
@@ -219,8 +230,16 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int64_t groups = (N + 31) / 32;
   float2 acc = make_float2(kNoRef, 0.0f);
   if (m < M) {
-#pragma unroll 4
-    for (int64_t g = slice; g < groups; g += slices) acc = join(acc, __ldcg(part + g * M + m));
+    const float2* v = part + m;
+    for (int64_t g = slice; g < groups; g += 8 * slices) {  // eight loads in flight
+      float2 w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        w[i] = g + i * slices < groups ? __ldcg(v + (g + i * slices) * M)
+                                       : make_float2(kNoRef, 0.0f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc = join(acc, w[i]);
+    }
   }
   s_part[threadIdx.x] = acc;
   for (int w = kJoinThreads / 2; w >= TT; w >>= 1) {
@@ -228,10 +247,9 @@ __global__ void __launch_bounds__(kJoinThreads)
     if ((int)threadIdx.x < w) s_part[threadIdx.x] = join(s_part[threadIdx.x], s_part[threadIdx.x + w]);
   }
   __syncthreads();
-  if (m >= M) return;
   const float2 all = s_part[threadIdx.x & (TT - 1)];
   const float r = all.x;
-  if (slice == 0) {
+  if (slice == 0 && m < M) {
     const float L = all.y * (1.0f / (1 << kPBits));  // the others' sum over 2^r
     const float log2L = log2f(L);
     const int64_t t = targets[m];
@@ -259,22 +277,31 @@ __global__ void __launch_bounds__(kJoinThreads)
     if (kGrad) factor[m] = *global * f * (1.0f / (1 << kPBits));
   }
   if (!kGrad) return;
-  for (int64_t g = slice; g < groups; g += slices) {
-    const float rg = __ldcg(part + g * M + m).x;
-    if (!(rg < r) || rg == kNoRef) continue;  // at the reference, NaN, or nothing there
+  // the groups below their token's reference: a warp finds those of its 32
+  // (group, token) places, then takes them eight at a time, four lanes each
+  const int lane = threadIdx.x & 31;
+  for (int64_t g = slice; g - slice < groups; g += slices) {  // (the warp's count of steps)
+    const float rg = m < M && g < groups ? __ldcg(part + g * M + m).x : r;
+    const bool low = rg < r && rg != kNoRef;  // (not NaN, and not nothing at all)
     const float scale = pow2_down(rg - r);
-    uint4* v = reinterpret_cast<uint4*>(P + m * stride + g * 32);
-    const int n16 = (int)min((int64_t)4, (stride - g * 32) / 8);
-    for (int i = 0; i < n16; ++i) {
-      uint4 w = v[i];
-      uint32_t* h = &w.x;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f2 = __half22float2(*reinterpret_cast<const __half2*>(h + j));
-        h[j] = (uint32_t)__half_as_ushort(__float2half_rz(f2.x * scale)) |
-               ((uint32_t)__half_as_ushort(__float2half_rz(f2.y * scale)) << 16);
+    uint32_t todo = __ballot_sync(0xFFFFFFFFu, low);
+    while (todo) {
+      uint32_t rest = todo;
+      for (int i = 0; i < (lane >> 2); ++i) rest &= rest - 1;  // this lane's of the first eight
+      const int src = rest ? __ffs(rest) - 1 : 0;
+      const float f = __shfl_sync(0xFFFFFFFFu, scale, src);
+      const int64_t n = __shfl_sync(0xFFFFFFFFu, g, src) * 32 + (lane & 3) * 8;
+      const int64_t row = __shfl_sync(0xFFFFFFFFu, m, src);
+      if (rest && n < stride) {
+        uint4* v = reinterpret_cast<uint4*>(P + row * stride + n);
+        uint4 w = *v;
+        w.x = scale_down(w.x, f);
+        w.y = scale_down(w.y, f);
+        w.z = scale_down(w.z, f);
+        w.w = scale_down(w.w, f);
+        *v = w;
       }
-      v[i] = w;
+      for (int i = 0; i < 8; ++i) todo &= todo - 1;
     }
   }
 }
@@ -342,14 +369,13 @@ __global__ void __launch_bounds__(256)
 
 // ------------------------------------------------------------ host side
 // Workspace: [status header][fp16 x][token multipliers][token lines][y of the
-// targets][factors][{r, s} per token and 32 rows][P][partials of the logits'
-// cut units][their counters and flags][the product back's own regions, whose
-// counters and flags come first][staged weight rows]; the prep kernel clears
-// the counters and flags of both products at once.
+// targets][factors][{r, s} per token and 32 rows][P][sums so far of the
+// logits' units][partials of their cut units][their counters and flags][the product back's sums][staged weight
+// rows].
 struct EntropyLayout {
-  size_t x16, tok, keys, y_t, factor, part, P, split_part, cnt, ready, end;
+  size_t x16, tok, keys, y_t, factor, part, P, own_part, split_part, cnt, ready, end;
   int64_t stride;
-  int BN, grid;
+  int BN, grid, n_flags;
   BackLayout back;
 };
 
@@ -367,10 +393,12 @@ static EntropyLayout entropy_layout(int64_t M, int64_t N, int64_t K, bool grad, 
   l.factor = l.y_t + align_up((size_t)M * 4, 256);
   l.part = l.factor + align_up((size_t)M * 4, 256);
   l.P = l.part + align_up((size_t)((N + 31) / 32) * M * 8, 256);
-  l.split_part = l.P + (grad ? align_up((size_t)m_pad * l.stride * 2, 256) : 0);
+  l.own_part = l.P + (grad ? align_up((size_t)m_pad * l.stride * 2, 256) : 0);
+  l.split_part = l.own_part + align_up((size_t)l.grid * 4 * l.BN * 32 * 4, 256);
   l.cnt = l.split_part + align_up((size_t)l.grid * 4 * l.BN * 32 * 4, 256);
-  l.ready = l.cnt + align_up((size_t)l.grid * 4 * 4, 256);
-  l.end = l.ready + align_up((size_t)l.grid * 4 * 4, 256);
+  l.ready = l.cnt + align_up((size_t)l.grid * 8 * 4, 256);
+  l.end = l.ready + align_up((size_t)l.grid * 8 * 4, 256);
+  l.n_flags = (int)((l.end - l.cnt) / 4);
   l.back = {};
   if (grad) {
     l.back = back_layout(M, N, K, sms, l.end);
@@ -415,10 +443,9 @@ static nvfp4_status entropy_run(const void* x, int64_t M, int64_t K, const uint8
     float* tok = reinterpret_cast<float*>(ws + L.tok);
     float* factor = reinterpret_cast<float*>(ws + L.factor);
     unsigned long long* keys = reinterpret_cast<unsigned long long*>(ws + L.keys);
-    const size_t flags_end = kGrad ? L.back.part : L.end;
     if (prep_x_launch(static_cast<const uint8_t*>(x) + (size_t)m0 * K * 2, rows, K, n_tt * L.BN,
                       global, x16, tok, m0 == 0 ? reinterpret_cast<int32_t*>(ws) : nullptr,
-                      reinterpret_cast<uint32_t*>(ws + L.cnt), (int)((flags_end - L.cnt) / 4), keys,
+                      reinterpret_cast<uint32_t*>(ws + L.cnt), L.n_flags, keys,
                       stream) != cudaSuccess)
       return NVFP4_ERR_CUDA;
     if (!encode_2d(&tm_x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x16, (uint64_t)K,
@@ -439,6 +466,7 @@ static nvfp4_status entropy_run(const void* x, int64_t M, int64_t K, const uint8
     a.split_cnt = reinterpret_cast<uint32_t*>(ws + L.cnt);
     a.split_ready = reinterpret_cast<uint32_t*>(ws + L.ready);
     a.split_part = reinterpret_cast<float*>(ws + L.split_part);
+    a.own_part = reinterpret_cast<float*>(ws + L.own_part);
     a.am_keys = keys;
     const bool deep = L.BN <= 64;
     const int stages = deep ? 3 : 2;
@@ -453,7 +481,7 @@ static nvfp4_status entropy_run(const void* x, int64_t M, int64_t K, const uint8
              : launch_gemm_with<2, 4, 2>(epi, tm_packed, tm_scales, tm_x, a, L.grid, stream);
     if (e != cudaSuccess) return NVFP4_ERR_CUDA;
     int tt_log2 = 0;
-    while (tt_log2 < 3 && (1 << (tt_log2 + 1)) <= rows) ++tt_log2;
+    while (tt_log2 < 3 && (rows >> (tt_log2 + 1)) >= sms) ++tt_log2;  // a CTA for every SM
     PdlLaunch l(dim3((unsigned)((rows + (1 << tt_log2) - 1) >> tt_log2)), dim3(kJoinThreads), 0,
                 stream);
     e = cudaLaunchKernelEx(&l.cfg, entropy_rows_kernel<kGrad>, (const float2*)ea.part, rows, N,

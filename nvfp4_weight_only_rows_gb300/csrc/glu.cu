@@ -57,6 +57,7 @@ struct GluArgs {
 template <int kAct, bool kGrad, bool kBf16>
 struct GluEpilogue {
   static constexpr bool kOwn = true, kPaired = true;
+  static constexpr int kPartStages = 0;
   static constexpr int kWarpBytes = (kGrad ? 2 : 1) * kMaxBN * 4;
   int64_t half;  // rows from a gate to its up
   GluArgs a;
@@ -183,14 +184,13 @@ __global__ void __launch_bounds__(256)
 
 // ------------------------------------------------------------ host side
 // Workspace: [status header][fp16 x][token multipliers][partials of cut
-// units][their counters and flags], and for the gradient, in place of the
-// end: [powers of two][factors][dg and du] before the partials and the
-// product back's regions, counters and flags first, after the flags; then the
-// staged weight rows.
+// units][their counters and flags][staged weight rows]; for the gradient also
+// [powers of two][factors][dg and du] before the partials, and the product
+// back's sums after the flags.
 struct GluLayout {
   size_t x16, tok, up2, factor, d16, split_part, cnt, ready, end;
   int64_t stride;
-  int BN, grid;
+  int BN, grid, n_flags;
   BackLayout back;
 };
 
@@ -207,8 +207,9 @@ static GluLayout glu_layout(int64_t M, int64_t I, int64_t K, bool grad, int sms)
   l.d16 = l.factor + (grad ? align_up((size_t)M * 4, 256) : 0);
   l.split_part = l.d16 + (grad ? align_up((size_t)m_pad * l.stride * 2, 256) : 0);
   l.cnt = l.split_part + align_up((size_t)l.grid * 4 * l.BN * 32 * 4, 256);
-  l.ready = l.cnt + align_up((size_t)l.grid * 4 * 4, 256);
-  l.end = l.ready + align_up((size_t)l.grid * 4 * 4, 256);
+  l.ready = l.cnt + align_up((size_t)l.grid * 8 * 4, 256);
+  l.end = l.ready + align_up((size_t)l.grid * 8 * 4, 256);
+  l.n_flags = (int)((l.end - l.cnt) / 4);
   l.back = {};
   if (grad) {
     l.back = back_layout(M, 2 * I, K, sms, l.end);
@@ -291,10 +292,9 @@ nvfp4_status glu_launch(const void* x, int64_t M, int64_t K, const uint8_t* pack
                                     factor);
       if (e != cudaSuccess) return NVFP4_ERR_CUDA;
     }
-    const size_t flags_end = grad ? L.back.part : L.end;
     e = prep_x_launch(xs, rows, K, n_tt * L.BN, global, x16, tok,
                       m0 == 0 ? reinterpret_cast<int32_t*>(ws) : nullptr,
-                      reinterpret_cast<uint32_t*>(ws + L.cnt), (int)((flags_end - L.cnt) / 4),
+                      reinterpret_cast<uint32_t*>(ws + L.cnt), L.n_flags,
                       nullptr, stream);
     if (e != cudaSuccess) return NVFP4_ERR_CUDA;
     if (!encode_2d(&tm_x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x16, (uint64_t)K,

@@ -24,6 +24,7 @@ cudaError_t stage_weights(const WeightStage& w, const uint8_t* packed, const uin
 // The epilogue of kOut (epilogue_role).
 struct NoEpilogue {
   static constexpr bool kOwn = false, kPaired = false;
+  static constexpr int kPartStages = 0;
 };
 
 constexpr int kKS = 256;            // k per packed/scale stage
@@ -64,18 +65,25 @@ constexpr int gemm_threads() {
   return GemmShape<kStages, kPStages, kDq>::kThreads + (kOut == kOutTopk ? 32 : 0);
 }
 
+// Epilogue warps: an epilogue of a call's own has eight for 128-token tiles,
+// where it does more than store.
+template <class E, int kStages>
+constexpr int epi_warps() { return E::kOwn && kStages < 3 ? 8 : 4; }
+
 // E: an epilogue of its own (see walk_epilogue) in place of the one of kOut.
 // E::kPaired: the unit's 128 rows are 64 rows of the weight's first half and
 // the 64 of the second half at the same place, 16 and 16 to a warp quadrant:
 // lanes l and l + 16 of an epilogue warp hold such a pair.
 template <int kOut, int kStages, int kPStages, int kDqPerQuad, bool kGrouped = false,
           class E = NoEpilogue>
-__global__ void __launch_bounds__((gemm_threads<kOut, kStages, kPStages, kDqPerQuad>()), 1)
+__global__ void __launch_bounds__((gemm_threads<kOut, kStages, kPStages, kDqPerQuad>() +
+                                   32 * (epi_warps<E, kStages>() - 4)), 1)
     w4a16_tc_kernel(const __grid_constant__ CUtensorMap tm_packed,
                     const __grid_constant__ CUtensorMap tm_scales,
                     const __grid_constant__ CUtensorMap tm_x, const GemmArgs p, const E own) {
   using Shape = GemmShape<kStages, kPStages, kDqPerQuad>;
   constexpr int kFirstEpiWarp = Shape::kFirstEpiWarp;
+  constexpr int kEpiWarps = epi_warps<E, kStages>();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -124,7 +132,7 @@ __global__ void __launch_bounds__((gemm_threads<kOut, kStages, kPStages, kDqPerQ
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&d_full[i], 1);
-      mbar_init(&d_empty[i], 4);
+      mbar_init(&d_empty[i], kEpiWarps);
     }
     mbar_init(done_bar, 1);
     *abort_flag = 0;
@@ -235,8 +243,8 @@ __global__ void __launch_bounds__((gemm_threads<kOut, kStages, kPStages, kDqPerQ
     uint32_t g = 0;
     int64_t i = 0;
     for_each_piece(sc, n_kb_u, [&](const Piece& pc) {
-      const uint32_t buf = (uint32_t)(i & ((1 << p.dbuf_log2) - 1));
-      const uint32_t dph = (uint32_t)((i >> p.dbuf_log2) & 1);
+      uint32_t buf = (uint32_t)(i & ((1 << p.dbuf_log2) - 1));
+      uint32_t dph = (uint32_t)((i >> p.dbuf_log2) & 1);
       ++i;
       // grouped 128-token tiles: a group's last, partly filled tile takes MMAs
       // only as wide as its tokens, in 16-token steps (same box, 2048 tokens:
@@ -251,8 +259,22 @@ __global__ void __launch_bounds__((gemm_threads<kOut, kStages, kPStages, kDqPerQ
       }
       if (!warp_wait(&d_empty[buf], dph ^ 1, wc)) return false;
       tc_fence_after();
-      const uint32_t d_tmem = tmem_base + buf * BN;
+      uint32_t d_tmem = tmem_base + buf * BN;
+      uint32_t part0 = pc.kb0;  // the first stage of this accumulator
       for (uint32_t kb = pc.kb0; kb < pc.kb1; ++kb, ++g) {
+        if constexpr (E::kPartStages > 0) {
+          if (kb == part0 + E::kPartStages) {  // the next part, in the next accumulator
+            if (elect_one()) tc_commit(&d_full[buf]);
+            __syncwarp();
+            part0 = kb;
+            buf = (uint32_t)(i & ((1 << p.dbuf_log2) - 1));
+            dph = (uint32_t)((i >> p.dbuf_log2) & 1);
+            ++i;
+            if (!warp_wait(&d_empty[buf], dph ^ 1, wc)) return false;
+            tc_fence_after();
+            d_tmem = tmem_base + buf * BN;
+          }
+        }
         const uint32_t st = g % kStages, ph = (g / kStages) & 1;
         if (!warp_wait(&s_full[st], ph, wc)) return false;
         tc_fence_after();
@@ -262,7 +284,7 @@ __global__ void __launch_bounds__((gemm_threads<kOut, kStages, kPStages, kDqPerQ
 #pragma unroll
           for (int kk = 0; kk < kKB / 16; ++kk)
             tc_mma_ts(d_tmem, a_t + kk * 8, bdesc + (kk >> 2) * box_desc + 2 * (kk & 3), id,
-                      (kb != pc.kb0) || (kk != 0));
+                      (kb != part0) || (kk != 0));
           tc_commit(&s_empty[st]);
         }
         __syncwarp();
@@ -342,11 +364,12 @@ __global__ void __launch_bounds__((gemm_threads<kOut, kStages, kPStages, kDqPerQ
     }
     if (__any_sync(0xFFFFFFFFu, (nan_seen & 0x80808080u) != 0u) && lane == 0)
       raise_status(p.status, NVFP4_ERR_NONFINITE);
-  } else if (warp < kFirstEpiWarp + 4) {
+  } else if (warp < kFirstEpiWarp + kEpiWarps) {
     // ---------------- epilogue: one thread per vocabulary row, BN tokens
     if constexpr (E::kOwn)
-      walk_epilogue(p, sc, own, warp, lane, tmem_base, d_full, d_empty, wc,
-                    reinterpret_cast<uint8_t*>(s_tok) + (warp - kFirstEpiWarp) * E::kWarpBytes);
+      walk_epilogue<kEpiWarps>(p, sc, own, warp, warp - kFirstEpiWarp, lane, tmem_base, d_full,
+                               d_empty, wc, reinterpret_cast<uint8_t*>(s_tok) +
+                                                (warp - kFirstEpiWarp) * E::kWarpBytes);
     else
       epilogue_role<kOut, false, kGrouped>(p, sc, warp, warp - kFirstEpiWarp, lane, tmem_base,
                                            d_full, d_empty, wc, s_tok, s_thr);
@@ -413,14 +436,15 @@ static cudaError_t launch_gemm_with(const E& own, const CUtensorMap& tm_packed,
   auto kern = w4a16_tc_kernel<NVFP4_OUT_F32, kStages, kPStages, kDq, false, E>;
   auto smem = [](int BN) {
     return 1024 + kPStages * (size_t)(kPackedStageBytes + kScaleStageBytes) +
-           kStages * (size_t)BN * kKB * 2 + 256 + 4 * (size_t)E::kWarpBytes;
+           kStages * (size_t)BN * kKB * 2 + 256 + epi_warps<E, kStages>() * (size_t)E::kWarpBytes;
   };
   static_assert(E::kWarpBytes % 16 == 0);
   static std::atomic<uint64_t> limit_set{0};
   const cudaError_t err = smem_limit_once(limit_set, reinterpret_cast<const void*>(kern),
                                           smem(kStages >= 3 ? 64 : kMaxBN));
   if (err != cudaSuccess) return err;
-  PdlLaunch l(dim3((unsigned)grid), dim3(gemm_threads<NVFP4_OUT_F32, kStages, kPStages, kDq>()),
+  PdlLaunch l(dim3((unsigned)grid), dim3(gemm_threads<NVFP4_OUT_F32, kStages, kPStages, kDq>() +
+                                         32 * (epi_warps<E, kStages>() - 4)),
               smem(a.BN), stream);
   return cudaLaunchKernelEx(&l.cfg, kern, tm_packed, tm_scales, tm_x, a, own);
 }
