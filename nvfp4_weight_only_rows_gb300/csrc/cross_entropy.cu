@@ -77,7 +77,7 @@ struct EntropyArgs {
 template <bool kGrad>
 struct EntropyEpilogue {
   static constexpr bool kOwn = true, kPaired = false;
-  static constexpr int kPartStages = 6;
+  static constexpr int kPartStages = 4;
   static constexpr int kWarpBytes = 3 * kMaxBN * 4;  // multiplier, reference, target of a token
   struct Unit {
     int64_t t0;
@@ -369,11 +369,11 @@ __global__ void __launch_bounds__(256)
 
 // ------------------------------------------------------------ host side
 // Workspace: [status header][fp16 x][token multipliers][token lines][y of the
-// targets][factors][{r, s} per token and 32 rows][P][sums so far of the
-// logits' units][partials of their cut units][their counters and flags][the product back's sums][staged weight
+// targets][factors][{r, s} per token and 32 rows][P][partials of the logits'
+// cut units][their counters and flags][the product back's sums][staged weight
 // rows].
 struct EntropyLayout {
-  size_t x16, tok, keys, y_t, factor, part, P, own_part, split_part, cnt, ready, end;
+  size_t x16, tok, keys, y_t, factor, part, P, split_part, cnt, ready, end;
   int64_t stride;
   int BN, grid, n_flags;
   BackLayout back;
@@ -393,8 +393,7 @@ static EntropyLayout entropy_layout(int64_t M, int64_t N, int64_t K, bool grad, 
   l.factor = l.y_t + align_up((size_t)M * 4, 256);
   l.part = l.factor + align_up((size_t)M * 4, 256);
   l.P = l.part + align_up((size_t)((N + 31) / 32) * M * 8, 256);
-  l.own_part = l.P + (grad ? align_up((size_t)m_pad * l.stride * 2, 256) : 0);
-  l.split_part = l.own_part + align_up((size_t)l.grid * 4 * l.BN * 32 * 4, 256);
+  l.split_part = l.P + (grad ? align_up((size_t)m_pad * l.stride * 2, 256) : 0);
   l.cnt = l.split_part + align_up((size_t)l.grid * 4 * l.BN * 32 * 4, 256);
   l.ready = l.cnt + align_up((size_t)l.grid * 8 * 4, 256);
   l.end = l.ready + align_up((size_t)l.grid * 8 * 4, 256);
@@ -466,7 +465,6 @@ static nvfp4_status entropy_run(const void* x, int64_t M, int64_t K, const uint8
     a.split_cnt = reinterpret_cast<uint32_t*>(ws + L.cnt);
     a.split_ready = reinterpret_cast<uint32_t*>(ws + L.ready);
     a.split_part = reinterpret_cast<float*>(ws + L.split_part);
-    a.own_part = reinterpret_cast<float*>(ws + L.own_part);
     a.am_keys = keys;
     const bool deep = L.BN <= 64;
     const int stages = deep ? 3 : 2;

@@ -68,7 +68,6 @@ struct GemmArgs {
                                 //   one bit per group whose word this call wrote
   int tk_hstride;               // u32 per token in tk_hist
   int tk_k;                     // k, 1 .. kTopkMax
-  float* own_part;              // [grid][4][BN][32]: sums so far of a unit in parts (walk_epilogue)
   const float* row_scale;       // [N] per-row weight scale (fp8 weights), else null
   // output mode kOutLogitsGroups only: per token, the largest order key
   // (logit_order) of every 32 rows of the fp32 logits, [M][ceil(N / 32)]
@@ -836,8 +835,8 @@ __device__ __forceinline__ void epilogue_role(const GemmArgs& p, const Sched& sc
 // of shared memory; it ends with a __syncwarp), E::chunk per 16 tokens of the
 // finished unit, a value of each for this lane's row.
 // E::kPartStages: a unit's sum in parts of that many stages, each from zero in
-// an accumulator of its own, added here in fp32 (GemmArgs::own_part keeps what
-// is there so far).  The tensor cores' sums drop the bits below fp32 at every
+// an accumulator of its own, added here in fp32: in registers, and with the
+// last part in that one's accumulator.  The tensor cores' sums drop the bits below fp32 at every
 // step, always towards zero, so the error of a long sum of one sign grows with
 // its steps; in parts it stays that of a part.
 // kWarps: 4, or 8, where two warps share a quadrant and take every other 16
@@ -853,89 +852,103 @@ __device__ __forceinline__ void walk_epilogue(const GemmArgs& p, const Sched& sc
   constexpr int kStep = 4 * kWarps;         // tokens from one of the warp's chunks to the next
   const int c0 = (epi / 4) * 16;            // its first chunk
   const uint32_t lane_off = (uint32_t)(q * 32) << 16;
-  float* acc = nullptr;
-  if constexpr (E::kPartStages > 0)
-    acc = p.own_part + (size_t)(blockIdx.x * 4 + q) * BN * 32 + lane;
   uint32_t i = 0;
   for_each_piece(sc, (uint32_t)p.n_kb, [&](const Piece& pc) {
     const typename E::Unit unit = own.begin(p, pc.u, q, lane, s_warp);
-    const uint32_t step = E::kPartStages > 0 ? (uint32_t)E::kPartStages : (uint32_t)p.n_kb;
-    for (uint32_t kb = pc.kb0; kb < pc.kb1; kb += step) {
-      const bool first = kb == pc.kb0, last = kb + step >= pc.kb1;
-      const uint32_t buf = i & ((1u << p.dbuf_log2) - 1u);
+    uint32_t buf = 0;
+    auto next = [&]() {  // the next accumulator, when it is full
+      buf = i & ((1u << p.dbuf_log2) - 1u);
       const uint32_t dph = (i >> p.dbuf_log2) & 1u;
       ++i;
-      float sum[2][16];  // the parts before, two chunks ahead
-      if constexpr (E::kPartStages > 0) {
-        if (!first) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int t = 0; t < 16; ++t)
-              sum[h][t] = c0 + kStep * h < BN ? acc[(c0 + kStep * h + t) * 32] : 0.0f;
-        }
-      }
       if (!warp_wait(&d_full[buf], dph, wc)) return false;
       tc_fence_after();
-      // a unit cut by a range boundary, as in epilogue_role
-      const bool whole = pc.kb0 == 0 && pc.kb1 == (uint32_t)p.n_kb;
-      bool finish = true;
-      float* part = nullptr;
-      uint32_t slot = 0;
-      if (last && !whole) {
-        const uint32_t key = pc.kb0 == 0 ? blockIdx.x + 1 : blockIdx.x;
-        slot = key * kWarps + epi;  // the other CTA's warp at this place has the same index
-        part = p.split_part + (size_t)(key * 4 + q) * BN * 32;
-        uint32_t earlier = 0;
-        if (lane == 0) earlier = atomicAdd(p.split_cnt + slot, 1u);
-        finish = __shfl_sync(0xFFFFFFFFu, earlier, 0) != 0u;
-        if (finish && !spin_until_set(p.split_ready + slot, wc)) return false;
-      }
-      for (int c = c0; c < BN; c += kStep) {
-        uint32_t v[16];
-        tmem_ld16(tmem_base + lane_off + buf * BN + c, v);
-        float val[16];
-        tc_wait_ld();
-#pragma unroll
-        for (int t = 0; t < 16; ++t) val[t] = __uint_as_float(v[t]);
-        if constexpr (E::kPartStages > 0) {
-          if (!first) {
-#pragma unroll
-            for (int t = 0; t < 16; ++t) {
-              val[t] = __fadd_rn(sum[0][t], val[t]);
-              sum[0][t] = sum[1][t];
-              if (c + 2 * kStep < BN) sum[1][t] = acc[(c + 2 * kStep + t) * 32];
-            }
-          }
-          if (!last) {
-#pragma unroll
-            for (int t = 0; t < 16; ++t) acc[(c + t) * 32] = val[t];
-            continue;
-          }
-        }
-        if (!finish) {
-#pragma unroll
-          for (int t = 0; t < 16; ++t) part[(c + t) * 32 + lane] = val[t];
-          continue;
-        }
-        if (!whole) {
-          float other[16];
-#pragma unroll
-          for (int t = 0; t < 16; ++t) other[t] = __ldcg(part + (c + t) * 32 + lane);
-#pragma unroll
-          for (int t = 0; t < 16; ++t) val[t] = __fadd_rn(val[t], other[t]);
-        }
-        own.chunk(p, unit, c, val, lane, s_warp);
-      }
-      if (!finish) {
-        __threadfence();  // the partial is visible before the flag
-        __syncwarp();
-        if (lane == 0) atomicExch(p.split_ready + slot, 1u);
-      }
+      return true;
+    };
+    auto drained = [&]() {
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&d_empty[buf]);
+    };
+    bool in_parts = false;
+    [[maybe_unused]] float acc[E::kPartStages > 0 ? 4 : 1][16];  // at most 64 tokens a warp
+    if constexpr (E::kPartStages > 0) {
+      for (uint32_t kb = pc.kb0; kb + E::kPartStages < pc.kb1; kb += E::kPartStages) {
+        if (!next()) return false;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int c = c0 + kStep * j;
+          if (c >= BN) continue;
+          uint32_t v[16];
+          tmem_ld16(tmem_base + lane_off + buf * BN + c, v);
+          tc_wait_ld();
+#pragma unroll
+          for (int t = 0; t < 16; ++t)
+            acc[j][t] = in_parts ? __fadd_rn(acc[j][t], __uint_as_float(v[t])) : __uint_as_float(v[t]);
+        }
+        in_parts = true;
+        drained();
+      }
     }
+    if (!next()) return false;
+    if constexpr (E::kPartStages > 0) {
+      if (in_parts) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int c = c0 + kStep * j;
+          if (c >= BN) continue;
+          const uint32_t at = tmem_base + lane_off + buf * BN + c;
+          uint32_t v[16];
+          tmem_ld16(at, v);
+          tc_wait_ld();
+#pragma unroll
+          for (int t = 0; t < 16; ++t)
+            v[t] = __float_as_uint(__fadd_rn(acc[j][t], __uint_as_float(v[t])));
+          tmem_st16(at, v);
+        }
+        tc_wait_st();
+      }
+    }
+    // a unit cut by a range boundary, as in epilogue_role
+    const bool whole = pc.kb0 == 0 && pc.kb1 == (uint32_t)p.n_kb;
+    bool finish = true;
+    float* part = nullptr;
+    uint32_t slot = 0;
+    if (!whole) {
+      const uint32_t key = pc.kb0 == 0 ? blockIdx.x + 1 : blockIdx.x;
+      slot = key * kWarps + epi;  // the other CTA's warp at this place has the same index
+      part = p.split_part + (size_t)(key * 4 + q) * BN * 32;
+      uint32_t earlier = 0;
+      if (lane == 0) earlier = atomicAdd(p.split_cnt + slot, 1u);
+      finish = __shfl_sync(0xFFFFFFFFu, earlier, 0) != 0u;
+      if (finish && !spin_until_set(p.split_ready + slot, wc)) return false;
+    }
+    for (int c = c0; c < BN; c += kStep) {
+      uint32_t v[16];
+      tmem_ld16(tmem_base + lane_off + buf * BN + c, v);
+      float val[16];
+      tc_wait_ld();
+#pragma unroll
+      for (int t = 0; t < 16; ++t) val[t] = __uint_as_float(v[t]);
+      if (!finish) {
+#pragma unroll
+        for (int t = 0; t < 16; ++t) part[(c + t) * 32 + lane] = val[t];
+        continue;
+      }
+      if (!whole) {
+        float other[16];
+#pragma unroll
+        for (int t = 0; t < 16; ++t) other[t] = __ldcg(part + (c + t) * 32 + lane);
+#pragma unroll
+        for (int t = 0; t < 16; ++t) val[t] = __fadd_rn(val[t], other[t]);
+      }
+      own.chunk(p, unit, c, val, lane, s_warp);
+    }
+    if (!finish) {
+      __threadfence();  // the partial is visible before the flag
+      __syncwarp();
+      if (lane == 0) atomicExch(p.split_ready + slot, 1u);
+    }
+    drained();
     return true;
   });
 }

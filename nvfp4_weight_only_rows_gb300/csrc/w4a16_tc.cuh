@@ -65,10 +65,29 @@ constexpr int gemm_threads() {
   return GemmShape<kStages, kPStages, kDq>::kThreads + (kOut == kOutTopk ? 32 : 0);
 }
 
-// Epilogue warps: an epilogue of a call's own has eight for 128-token tiles,
-// where it does more than store.
+// With an epilogue of a call's own the 20 warps are whole warpgroups whose
+// registers are split by what they do: 96 a thread at launch, then 40 for the
+// warps that issue copies and MMAs, 88 for the dequant warps, the rest for the
+// epilogue.  That is two warpgroups of 128 for 128-token tiles, where it does
+// more than store (5 x 96 >= 40 + 2 x 88 + 2 x 128), one of 168 for the three
+// dequant warpgroups of small ones (40 + 3 x 88 + 168).
 template <class E, int kStages>
 constexpr int epi_warps() { return E::kOwn && kStages < 3 ? 8 : 4; }
+
+template <class E, int kOut, int kStages, int kPStages, int kDq>
+constexpr int own_threads() {
+  return E::kOwn ? 32 * (4 + 4 * kDq + epi_warps<E, kStages>())
+                 : gemm_threads<kOut, kStages, kPStages, kDq>();
+}
+
+template <int kRegs>
+__device__ __forceinline__ void registers_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void registers_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
 
 // E: an epilogue of its own (see walk_epilogue) in place of the one of kOut.
 // E::kPaired: the unit's 128 rows are 64 rows of the weight's first half and
@@ -76,13 +95,13 @@ constexpr int epi_warps() { return E::kOwn && kStages < 3 ? 8 : 4; }
 // lanes l and l + 16 of an epilogue warp hold such a pair.
 template <int kOut, int kStages, int kPStages, int kDqPerQuad, bool kGrouped = false,
           class E = NoEpilogue>
-__global__ void __launch_bounds__((gemm_threads<kOut, kStages, kPStages, kDqPerQuad>() +
-                                   32 * (epi_warps<E, kStages>() - 4)), 1)
+__global__ void __launch_bounds__((own_threads<E, kOut, kStages, kPStages, kDqPerQuad>()), 1)
     w4a16_tc_kernel(const __grid_constant__ CUtensorMap tm_packed,
                     const __grid_constant__ CUtensorMap tm_scales,
                     const __grid_constant__ CUtensorMap tm_x, const GemmArgs p, const E own) {
   using Shape = GemmShape<kStages, kPStages, kDqPerQuad>;
-  constexpr int kFirstEpiWarp = Shape::kFirstEpiWarp;
+  constexpr int kFirstDq = E::kOwn ? 4 : kFirstDqWarp;  // own: a whole warpgroup before
+  constexpr int kFirstEpiWarp = kFirstDq + Shape::kDqWarps;
   constexpr int kEpiWarps = epi_warps<E, kStages>();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -165,6 +184,8 @@ __global__ void __launch_bounds__((gemm_threads<kOut, kStages, kPStages, kDqPerQ
   // the producer and MMA loops below are warp-uniform; one elected lane
   // issues each TMA / tcgen05 instruction
 
+  if (warp < kFirstDq) {
+    if constexpr (E::kOwn) registers_down<40>();
   if (warp == 0) {
     // ---------------- packed codes + scales producer
     // a weight tile read once (one token tile) is not kept in L2; one read
@@ -303,13 +324,15 @@ __global__ void __launch_bounds__((gemm_threads<kOut, kStages, kPStages, kDqPerQ
     volatile int32_t zero = 0;
     drain.abort = &zero;
     mbar_wait(done_bar, 0, drain);
+  }  // (a warp 3 completes the first warpgroup)
   } else if (warp < kFirstEpiWarp) {
+    if constexpr (E::kOwn) registers_down<88>();
     // ---------------- dequant: one thread per vocabulary row.  The kDqPerQuad
     // warps of a TMEM lane quadrant take the 256-k stages in turn: wait for
     // the packed stage, convert 64 k at a time into 32 registers and store
     // them to the stage's TMEM columns, then signal the MMA warp.
     const int q = warp & 3;
-    const int r = (warp - kFirstDqWarp) >> 2;
+    const int r = (warp - kFirstDq) >> 2;
     const int row = E::kPaired ? (lane & 16) * 4 + q * 16 + (lane & 15) : q * 32 + lane;
     const uint32_t lane_off = (uint32_t)(q * 32) << 16;
     const int sw = row & 7;
@@ -366,11 +389,12 @@ __global__ void __launch_bounds__((gemm_threads<kOut, kStages, kPStages, kDqPerQ
       raise_status(p.status, NVFP4_ERR_NONFINITE);
   } else if (warp < kFirstEpiWarp + kEpiWarps) {
     // ---------------- epilogue: one thread per vocabulary row, BN tokens
-    if constexpr (E::kOwn)
+    if constexpr (E::kOwn) {
+      registers_up<kEpiWarps == 8 ? 128 : 168>();
       walk_epilogue<kEpiWarps>(p, sc, own, warp, warp - kFirstEpiWarp, lane, tmem_base, d_full,
                                d_empty, wc, reinterpret_cast<uint8_t*>(s_tok) +
                                                 (warp - kFirstEpiWarp) * E::kWarpBytes);
-    else
+    } else
       epilogue_role<kOut, false, kGrouped>(p, sc, warp, warp - kFirstEpiWarp, lane, tmem_base,
                                            d_full, d_empty, wc, s_tok, s_thr);
     if (kOut == kOutTopk && lane == 0) atomicAdd(s_last + 1, 1);  // this warp is done
@@ -436,15 +460,15 @@ static cudaError_t launch_gemm_with(const E& own, const CUtensorMap& tm_packed,
   auto kern = w4a16_tc_kernel<NVFP4_OUT_F32, kStages, kPStages, kDq, false, E>;
   auto smem = [](int BN) {
     return 1024 + kPStages * (size_t)(kPackedStageBytes + kScaleStageBytes) +
-           kStages * (size_t)BN * kKB * 2 + 256 + epi_warps<E, kStages>() * (size_t)E::kWarpBytes;
+           kStages * (size_t)BN * kKB * 2 + 256 +
+           epi_warps<E, kStages>() * (size_t)E::kWarpBytes;
   };
   static_assert(E::kWarpBytes % 16 == 0);
   static std::atomic<uint64_t> limit_set{0};
   const cudaError_t err = smem_limit_once(limit_set, reinterpret_cast<const void*>(kern),
                                           smem(kStages >= 3 ? 64 : kMaxBN));
   if (err != cudaSuccess) return err;
-  PdlLaunch l(dim3((unsigned)grid), dim3(gemm_threads<NVFP4_OUT_F32, kStages, kPStages, kDq>() +
-                                         32 * (epi_warps<E, kStages>() - 4)),
+  PdlLaunch l(dim3((unsigned)grid), dim3(own_threads<E, NVFP4_OUT_F32, kStages, kPStages, kDq>()),
               smem(a.BN), stream);
   return cudaLaunchKernelEx(&l.cfg, kern, tm_packed, tm_scales, tm_x, a, own);
 }
