@@ -28,7 +28,20 @@ namespace nvfp4 {
 
 constexpr uint32_t kBackPacked = 256 * 64;  // bytes: 256 rows x 128 columns of codes
 constexpr uint32_t kBackScales = 256 * 16;  // 256 rows x the 16 scales of 256 columns
-constexpr uint32_t kBackScratch = 2 * 256 * 2;  // a warp's scales: 2 column groups x 256 rows, fp16
+
+// Warps of the kernel: kDq a quadrant take the stages in turn, or kDq pairs of
+// warps, each half of a stage's rows.
+template <int kStages, int kPStages, int kDq, int kHalves>
+struct BackShape {
+  static_assert(kStages % kDq == 0 && kPStages % kDq == 0,
+                "dequant warps per quadrant must divide every ring depth they wait on");
+  static constexpr int kDqWarps = 4 * kDq * kHalves;
+  static constexpr int kFirstEpiWarp = kFirstDqWarp + kDqWarps;
+  static constexpr int kThreads = 32 * (kFirstEpiWarp + 4);
+  static constexpr int kRowsOfWarp = kKB / kHalves;
+  // a warp's scales: 2 column groups x its rows, fp16
+  static constexpr uint32_t kScratch = 2 * kRowsOfWarp * 2;
+};
 
 struct BackArgs {
   uint32_t n_ft;         // 128-column tiles
@@ -150,13 +163,13 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 
 // Warp roles as in w4a16_tc_kernel: 0 codes and scales, 1 dy, 2 MMA, then
 // kDq dequant warps a quadrant, then four epilogue warps.
-template <int kStages, int kPStages, int kDq>
-__global__ void __launch_bounds__((GemmShape<kStages, kPStages, kDq>::kThreads), 1)
+template <int kStages, int kPStages, int kDq, int kHalves>
+__global__ void __launch_bounds__((BackShape<kStages, kPStages, kDq, kHalves>::kThreads), 1)
     w4a16_back_kernel(const __grid_constant__ CUtensorMap tm_packed,
                       const __grid_constant__ CUtensorMap tm_scales,
                       const __grid_constant__ CUtensorMap tm_d, const GemmArgs p,
                       const BackArgs b) {
-  using Shape = GemmShape<kStages, kPStages, kDq>;
+  using Shape = BackShape<kStages, kPStages, kDq, kHalves>;
   constexpr int kFirstEpiWarp = Shape::kFirstEpiWarp;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -168,7 +181,7 @@ __global__ void __launch_bounds__((GemmShape<kStages, kPStages, kDq>::kThreads),
   uint8_t* s_d = s_packed + kPStages * kBackPacked;
   uint8_t* s_scales = s_d + kStages * d_stage_bytes;
   uint8_t* s_scratch = s_scales + kPStages * kBackScales;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(s_scratch + Shape::kDqWarps * kBackScratch);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_scratch + Shape::kDqWarps * Shape::kScratch);
   uint64_t* p_full = bars;
   uint64_t* p_empty = p_full + kPStages;
   uint64_t* s_full = p_empty + kPStages;
@@ -185,10 +198,10 @@ __global__ void __launch_bounds__((GemmShape<kStages, kPStages, kDq>::kThreads),
   if (threadIdx.x == 0) {
     for (int i = 0; i < kPStages; ++i) {
       mbar_init(&p_full[i], 1);
-      mbar_init(&p_empty[i], 4);
+      mbar_init(&p_empty[i], 4 * kHalves);
     }
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&s_full[i], 4 + 1);
+      mbar_init(&s_full[i], 4 * kHalves + 1);
       mbar_init(&s_empty[i], 1);
     }
     for (int i = 0; i < 4; ++i) {
@@ -253,7 +266,7 @@ __global__ void __launch_bounds__((GemmShape<kStages, kPStages, kDq>::kThreads),
       }
       return true;
     });
-    drain_loads(s_full, kStages, issued, 5, p.status);
+    drain_loads(s_full, kStages, issued, 4 * kHalves + 1, p.status);
   } else if (warp == 2) {
     const uint32_t idesc = idesc_f16_f32((uint32_t)BN);
     const uint64_t desc0 = smem_desc_sw128(smem_u32(s_d));
@@ -294,15 +307,16 @@ __global__ void __launch_bounds__((GemmShape<kStages, kPStages, kDq>::kThreads),
   } else if (warp < kFirstEpiWarp) {
     // Dequant and turn: quadrant q's 32 columns of a stage, 256 rows.
     const int q = warp & 3;
-    const int r = (warp - kFirstDqWarp) >> 2;
+    const int r = ((warp - kFirstDqWarp) >> 2) % kDq;
+    const int row0 = (warp - kFirstDqWarp) / (4 * kDq) * Shape::kRowsOfWarp;  // of the stage
     const int t = lane & 3;
     const uint32_t lane_off = (uint32_t)(q * 32) << 16;
-    uint8_t* scratch = s_scratch + (warp - kFirstDqWarp) * kBackScratch;
+    uint8_t* scratch = s_scratch + (warp - kFirstDqWarp) * Shape::kScratch;
     // where this lane's row of a 32-row block keeps its scale: the order in
     // which a lane (., t) reads the rows 8 j + 2 t, 8 j + 2 t + 1, j = 0 .. 3
     uint8_t* put = scratch + (((lane & 7) >> 1) * 8 + (lane >> 3) * 2 + (lane & 1)) * 2;
-    const uint8_t* get = scratch + (lane >> 4) * 512 + t * 16;  // column group (lane >> 2) >> 2
-    const uint32_t swz = (uint32_t)((q ^ ((lane >> 1) & 3)) << 4) + lane * 64;
+    const uint8_t* get = scratch + (lane >> 4) * (Shape::kScratch / 2) + t * 16;  // column group (lane >> 2) >> 2
+    const uint32_t swz = (uint32_t)((q ^ ((lane >> 1) & 3)) << 4) + (row0 + lane) * 64;
     uint32_t nan_seen = 0;
     uint32_t g = 0;  // stage of the CTA's sequence
     for_each_back_piece(p, b, [&](const BackPiece& pc) {
@@ -311,21 +325,21 @@ __global__ void __launch_bounds__((GemmShape<kStages, kPStages, kDq>::kThreads),
         const uint32_t ps = g % kPStages, pph = (g / kPStages) & 1;
         const uint32_t st = g % kStages, ph = (g / kStages) & 1;
         if (!warp_wait(&p_full[ps], pph, wc)) return false;
-        const uint8_t* srow = s_scales + ps * kBackScales + lane * 16 + (pc.ft & 1) * 8 + q * 2;
+        const uint8_t* srow = s_scales + ps * kBackScales + (row0 + lane) * 16 + (pc.ft & 1) * 8 + q * 2;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < Shape::kRowsOfWarp / 32; ++i) {
           const uint32_t two = *reinterpret_cast<const uint16_t*>(srow + i * 512);
           nan_seen |= (two & 0x7F7Fu) + 0x0101u;
           uint32_t f, unused;
           scales4_to_f16(two, f, unused);
           *reinterpret_cast<uint16_t*>(put + i * 64) = (uint16_t)f;
-          *reinterpret_cast<uint16_t*>(put + i * 64 + 512) = (uint16_t)(f >> 16);
+          *reinterpret_cast<uint16_t*>(put + i * 64 + Shape::kScratch / 2) = (uint16_t)(f >> 16);
         }
         __syncwarp();
         const uint32_t codes = smem_u32(s_packed + ps * kBackPacked) + swz;
-        const uint32_t ta = tmem_a + lane_off + st * (kKB / 2);
+        const uint32_t ta = tmem_a + lane_off + st * (kKB / 2) + row0 / 2;
 #pragma unroll
-        for (int c4 = 0; c4 < kKB / 64; ++c4) {
+        for (int c4 = 0; c4 < Shape::kRowsOfWarp / 64; ++c4) {
           uint32_t lo[16], hi[16];  // TMEM lanes 0-15 and 16-31 of the quadrant
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
@@ -466,10 +480,11 @@ __global__ void __launch_bounds__(512) back_prep_kernel(const T* __restrict__ dy
 }
 
 // ------------------------------------------------------------ host side
-template <int kStages, int kPStages, int kDq>
+template <int kStages, int kPStages, int kDq, int kHalves>
 static size_t back_smem_bytes(int BN) {
   return 1024 + kPStages * (size_t)(kBackPacked + kBackScales) + kStages * (size_t)BN * kKB * 2 +
-         GemmShape<kStages, kPStages, kDq>::kDqWarps * (size_t)kBackScratch + 256 +
+         BackShape<kStages, kPStages, kDq, kHalves>::kDqWarps *
+             (size_t)BackShape<kStages, kPStages, kDq, kHalves>::kScratch + 256 +
          4 * (size_t)kMaxBN * 4;
 }
 
@@ -516,17 +531,17 @@ BackLayout back_layout(int64_t M, int64_t N, int64_t K, int sms, size_t off) {
   return l;
 }
 
-template <int kStages, int kPStages, int kDq>
+template <int kStages, int kPStages, int kDq, int kHalves>
 static cudaError_t back_gemm(const CUtensorMap& tm_packed, const CUtensorMap& tm_scales,
                              const CUtensorMap& tm_d, const GemmArgs& a, const BackArgs& b,
                              int grid, int max_bn, cudaStream_t stream) {
-  auto kern = w4a16_back_kernel<kStages, kPStages, kDq>;
+  auto kern = w4a16_back_kernel<kStages, kPStages, kDq, kHalves>;
   static std::atomic<uint64_t> limit_set{0};
   const cudaError_t e = smem_limit_once(limit_set, reinterpret_cast<const void*>(kern),
-                                        back_smem_bytes<kStages, kPStages, kDq>(max_bn));
+                                        back_smem_bytes<kStages, kPStages, kDq, kHalves>(max_bn));
   if (e != cudaSuccess) return e;
-  PdlLaunch l(dim3((unsigned)grid), dim3(GemmShape<kStages, kPStages, kDq>::kThreads),
-              back_smem_bytes<kStages, kPStages, kDq>(a.BN), stream);
+  PdlLaunch l(dim3((unsigned)grid), dim3(BackShape<kStages, kPStages, kDq, kHalves>::kThreads),
+              back_smem_bytes<kStages, kPStages, kDq, kHalves>(a.BN), stream);
   return cudaLaunchKernelEx(&l.cfg, kern, tm_packed, tm_scales, tm_d, a, b);
 }
 
@@ -566,8 +581,8 @@ cudaError_t back_launch(const BackCall& c, const BackLayout& L, uint8_t* ws, cud
   b.part = reinterpret_cast<float*>(ws + L.part);
   b.bf16 = c.out_dtype == NVFP4_OUT_BF16;
   const cudaError_t e =
-      deep ? back_gemm<3, 6, 3>(tm_packed, tm_scales, tm_d, a, b, L.grid, kBackDeepBN, stream)
-           : back_gemm<2, 4, 2>(tm_packed, tm_scales, tm_d, a, b, L.grid, kMaxBN, stream);
+      deep ? back_gemm<3, 6, 3, 1>(tm_packed, tm_scales, tm_d, a, b, L.grid, kBackDeepBN, stream)
+           : back_gemm<2, 4, 2, 2>(tm_packed, tm_scales, tm_d, a, b, L.grid, kMaxBN, stream);
   if (e != cudaSuccess || L.n_rest == 0) return e;
   PdlLaunch l(dim3((unsigned)(L.n_rest * (L.BN / 8))), dim3(256), 0, stream);
   return cudaLaunchKernelEx(&l.cfg, back_join_kernel, b, c.M, c.K, L.BN, (int)n_tt);
