@@ -30,28 +30,39 @@ constexpr uint32_t kBackPacked = 256 * 64;  // bytes: 256 rows x 128 columns of 
 constexpr uint32_t kBackScales = 256 * 16;  // 256 rows x the 16 scales of 256 columns
 
 // Warps of the kernel: kDq a quadrant take the stages in turn, or kDq pairs of
-// warps, each half of a stage's rows.
-template <int kStages, int kPStages, int kDq, int kHalves>
+// warps, each half of a stage's rows.  kPair: two CTAs work on one tile of 256
+// columns x 256 tokens, each on 128 of its columns with half of the tokens'
+// dy in shared memory: a stage then brings 84 KB into an SM for twice the
+// MMAs.
+template <int kStages_, int kPStages_, int kDq_, int kHalves_, bool kPair_>
 struct BackShape {
+  static constexpr int kStages = kStages_, kPStages = kPStages_, kDq = kDq_, kHalves = kHalves_;
+  static constexpr bool kPair = kPair_;
   static_assert(kStages % kDq == 0 && kPStages % kDq == 0,
                 "dequant warps per quadrant must divide every ring depth they wait on");
+  static constexpr int kCtas = kPair ? 2 : 1;
   static constexpr int kDqWarps = 4 * kDq * kHalves;
+  static constexpr int kEpiWarps = kPair ? 8 : 4;  // a pair's one accumulator is drained quickly
   static constexpr int kFirstEpiWarp = kFirstDqWarp + kDqWarps;
-  static constexpr int kThreads = 32 * (kFirstEpiWarp + 4);
+  static constexpr int kThreads = 32 * (kFirstEpiWarp + kEpiWarps);
   static constexpr int kRowsOfWarp = kKB / kHalves;
   // a warp's scales: 2 column groups x its rows, fp16
   static constexpr uint32_t kScratch = 2 * kRowsOfWarp * 2;
+  static constexpr int kMaxTokens = kCtas * kMaxBN;  // of a tile
+  static size_t smem_bytes(int BN) {
+    return 1024 + kPStages * (size_t)(kBackPacked + kBackScales) + kStages * (size_t)BN * kKB * 2 +
+           kDqWarps * (size_t)kScratch + 256 + kEpiWarps * (size_t)kMaxTokens * 4;
+  }
 };
 
 struct BackArgs {
-  uint32_t n_ft;         // 128-column tiles
   uint32_t n_whole;      // tiles worked on whole, n_whole / grid in a CTA's row
   uint32_t n_rest;       // tiles after those, each split along the weight's rows
   uint32_t n_splits;     // ... into so many
   uint32_t split_len;    // ... of so many stages (the last may have fewer)
   const float* factor;   // [M]
   void* out;             // [M, K]
-  float* part;           // [n_splits][n_rest][BN][128] sums of the split tiles
+  float* part;           // [n_splits][n_rest][CTAs of a tile][tokens][128] sums
   int bf16;
 };
 
@@ -63,52 +74,60 @@ struct BackArgs {
 // somewhere else, read 10.7 GB for 1024 tokens of a 128256 x 4096 head and took
 // 1291 us.
 struct BackPiece {
-  uint32_t ft;
-  int64_t t0;
+  uint32_t ft;           // this CTA's 128 columns
+  int64_t t0;            // the tile's first token
   uint32_t kb0, kb1;
-  int64_t part;  // its tile in BackArgs::part, or -1: a whole one
+  int64_t part;          // its tile in BackArgs::part, or -1: a whole one
 };
 
-template <typename F>
+template <class Shape, typename F>
 __device__ __forceinline__ void for_each_back_piece(const GemmArgs& p, const BackArgs& b,
                                                     F&& body) {
-  const uint32_t n_tt = (uint32_t)p.n_ttiles;
-  for (uint32_t u = blockIdx.x; u < b.n_whole; u += gridDim.x)
-    if (!body(BackPiece{u / n_tt, (int64_t)(u % n_tt) * p.BN, 0u, (uint32_t)p.n_kb, -1})) return;
-  for (uint32_t v = blockIdx.x; v < b.n_rest * b.n_splits; v += gridDim.x) {
+  constexpr uint32_t kCtas = Shape::kCtas;
+  const uint32_t n_tt = (uint32_t)p.n_ttiles, tokens = (uint32_t)p.BN * kCtas;
+  const uint32_t rank = blockIdx.x % kCtas, step = gridDim.x / kCtas;
+  for (uint32_t u = blockIdx.x / kCtas; u < b.n_whole; u += step)
+    if (!body(BackPiece{u / n_tt * kCtas + rank, (int64_t)(u % n_tt) * tokens, 0u,
+                        (uint32_t)p.n_kb, -1}))
+      return;
+  for (uint32_t v = blockIdx.x / kCtas; v < b.n_rest * b.n_splits; v += step) {
     const uint32_t split = v / b.n_rest, u = b.n_whole + v % b.n_rest;
     const uint32_t kb0 = split * b.split_len;
-    if (!body(BackPiece{u / n_tt, (int64_t)(u % n_tt) * p.BN, kb0,
-                        min(kb0 + b.split_len, (uint32_t)p.n_kb), (int64_t)v}))
+    if (!body(BackPiece{u / n_tt * kCtas + rank, (int64_t)(u % n_tt) * tokens, kb0,
+                        min(kb0 + b.split_len, (uint32_t)p.n_kb), (int64_t)v * kCtas + rank}))
       return;
   }
 }
 
-// Four warps, one TMEM lane quadrant each: 16 tokens at a time, a column a lane.
+// Four warps, one TMEM lane quadrant each, or eight, where two share one and
+// take every other 16 tokens: a column a lane.
+template <class Shape>
 __device__ __forceinline__ void back_epilogue(const GemmArgs& p, const BackArgs& b, int warp,
-                                              int lane, uint32_t tmem_base, uint64_t* d_full,
-                                              uint64_t* d_empty, const WaitCtl& wc, float* fac) {
+                                              int epi, int lane, uint32_t tmem_base,
+                                              uint64_t* d_full, uint64_t* d_empty,
+                                              const WaitCtl& wc, float* fac) {
   grid_dependency_wait();  // the factors come from the kernel before
+  const int tokens = p.BN * Shape::kCtas;
   const int q = warp & 3;
   const uint32_t lane_off = (uint32_t)(q * 32) << 16;
   const int col = q * 32 + 4 * (lane & 7) + (lane >> 3);
   uint32_t i = 0;
-  for_each_back_piece(p, b, [&](const BackPiece& pc) {
+  for_each_back_piece<Shape>(p, b, [&](const BackPiece& pc) {
     const uint32_t buf = i & ((1u << p.dbuf_log2) - 1u);
     const uint32_t dph = (i >> p.dbuf_log2) & 1u;
     ++i;
-    for (int t = lane; t < p.BN; t += 32)
+    for (int t = lane; t < tokens; t += 32)
       fac[t] = pc.t0 + t < p.M ? __ldcg(b.factor + pc.t0 + t) : 0.0f;
     __syncwarp();
     if (!warp_wait(&d_full[buf], dph, wc)) return false;
     tc_fence_after();
     const int64_t k = (int64_t)pc.ft * kRows + col;
-    for (int c = 0; c < p.BN; c += 16) {
+    for (int c = epi / 4 * 16; c < tokens; c += 4 * Shape::kEpiWarps) {
       uint32_t v[16];
-      tmem_ld16(tmem_base + lane_off + buf * p.BN + c, v);
+      tmem_ld16(tmem_base + lane_off + buf * tokens + c, v);
       tc_wait_ld();
       if (pc.part >= 0) {
-        float* o = b.part + (pc.part * p.BN + c) * kRows + col;
+        float* o = b.part + (pc.part * tokens + c) * kRows + col;
 #pragma unroll
         for (int t = 0; t < 16; ++t) o[t * kRows] = __uint_as_float(v[t]);
         continue;
@@ -131,7 +150,10 @@ __device__ __forceinline__ void back_epilogue(const GemmArgs& p, const BackArgs&
     }
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&d_empty[buf]);
+    if (lane == 0) {
+      if constexpr (Shape::kPair) mbar_arrive_at(&d_empty[buf], 0);
+      else mbar_arrive(&d_empty[buf]);
+    }
     return true;
   });
 }
@@ -162,19 +184,23 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 }
 
 // Warp roles as in w4a16_tc_kernel: 0 codes and scales, 1 dy, 2 MMA, then
-// kDq dequant warps a quadrant, then four epilogue warps.
-template <int kStages, int kPStages, int kDq, int kHalves>
-__global__ void __launch_bounds__((BackShape<kStages, kPStages, kDq, kHalves>::kThreads), 1)
+// dequant, then epilogue.  Of a pair, the first CTA's warp 2 issues the MMAs
+// of both; the second's tells it when a stage of its own is complete.
+template <class Shape>
+__global__ void __launch_bounds__(Shape::kThreads, 1)
     w4a16_back_kernel(const __grid_constant__ CUtensorMap tm_packed,
                       const __grid_constant__ CUtensorMap tm_scales,
                       const __grid_constant__ CUtensorMap tm_d, const GemmArgs p,
                       const BackArgs b) {
-  using Shape = BackShape<kStages, kPStages, kDq, kHalves>;
+  constexpr int kStages = Shape::kStages, kPStages = Shape::kPStages;
+  constexpr int kDq = Shape::kDq, kHalves = Shape::kHalves;
+  constexpr bool kPair = Shape::kPair;
   constexpr int kFirstEpiWarp = Shape::kFirstEpiWarp;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  const int BN = p.BN;
+  const int BN = p.BN;  // tokens of this CTA's dy
+  const uint32_t rank = blockIdx.x % Shape::kCtas;
   const uint32_t box_bytes = (uint32_t)BN * 128;
   const uint32_t d_stage_bytes = (kKB / 64) * box_bytes;
   uint8_t* s_packed = smem;
@@ -188,10 +214,11 @@ __global__ void __launch_bounds__((BackShape<kStages, kPStages, kDq, kHalves>::k
   uint64_t* s_empty = s_full + kStages;
   uint64_t* d_full = s_empty + kStages;
   uint64_t* d_empty = d_full + 4;
-  uint64_t* done_bar = d_empty + 4;
+  uint64_t* peer_full = d_empty + 4;  // pair: the second CTA's half of a stage is complete
+  uint64_t* done_bar = peer_full + kStages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(tmem_slot + 1);
-  float* s_fac = reinterpret_cast<float*>(bars + 32);  // 4 epilogue warps x kMaxBN
+  float* s_fac = reinterpret_cast<float*>(bars + 32);  // of a tile's tokens, per epilogue warp
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -203,10 +230,11 @@ __global__ void __launch_bounds__((BackShape<kStages, kPStages, kDq, kHalves>::k
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&s_full[i], 4 * kHalves + 1);
       mbar_init(&s_empty[i], 1);
+      mbar_init(&peer_full[i], 1);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&d_full[i], 1);
-      mbar_init(&d_empty[i], 4);
+      mbar_init(&d_empty[i], Shape::kCtas * Shape::kEpiWarps);
     }
     mbar_init(done_bar, 1);
     *abort_flag = 0;
@@ -219,18 +247,20 @@ __global__ void __launch_bounds__((BackShape<kStages, kPStages, kDq, kHalves>::k
     tma_prefetch_desc(&tm_d);
   }
   if (warp == 2) {
-    tmem_alloc(tmem_slot, p.tmem_cols);
+    if constexpr (kPair) tmem_alloc_pair(tmem_slot, p.tmem_cols);
+    else tmem_alloc(tmem_slot, p.tmem_cols);
     tc_fence_before();
   }
   __syncthreads();
+  if constexpr (kPair) cluster_sync();  // the barriers of both exist
   tc_fence_after();
   const uint32_t tmem_base = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
-  const uint32_t tmem_a = tmem_base + ((uint32_t)BN << p.dbuf_log2);
+  const uint32_t tmem_a = tmem_base + ((uint32_t)(BN * Shape::kCtas) << p.dbuf_log2);
   const WaitCtl wc{p.status, abort_flag, kWaitLimitNs};
 
   if (warp == 0) {
     uint32_t issued = 0;
-    for_each_back_piece(p, b, [&](const BackPiece& pc) {
+    for_each_back_piece<Shape>(p, b, [&](const BackPiece& pc) {
       for (uint32_t kb = pc.kb0; kb < pc.kb1; ++kb, ++issued) {
         const uint32_t st = issued % kPStages, ph = (issued / kPStages) & 1;
         if (!warp_wait(&p_empty[st], ph ^ 1, wc)) return false;
@@ -250,7 +280,7 @@ __global__ void __launch_bounds__((BackShape<kStages, kPStages, kDq, kHalves>::k
   } else if (warp == 1) {
     grid_dependency_wait();  // dy comes from the kernel before
     uint32_t issued = 0;
-    for_each_back_piece(p, b, [&](const BackPiece& pc) {
+    for_each_back_piece<Shape>(p, b, [&](const BackPiece& pc) {
       for (uint32_t kb = pc.kb0; kb < pc.kb1; ++kb, ++issued) {
         const uint32_t st = issued % kStages, ph = (issued / kStages) & 1;
         if (!warp_wait(&s_empty[st], ph ^ 1, wc)) return false;
@@ -260,7 +290,7 @@ __global__ void __launch_bounds__((BackShape<kStages, kPStages, kDq, kHalves>::k
           uint8_t* dst = s_d + st * d_stage_bytes;
 #pragma unroll
           for (int x = 0; x < kKB / 64; ++x)
-            tma_load_2d(dst + x * box_bytes, &tm_d, n0 + 64 * x, (int32_t)pc.t0, &s_full[st]);
+            tma_load_2d(dst + x * box_bytes, &tm_d, n0 + 64 * x, (int32_t)pc.t0 + (int32_t)rank * BN, &s_full[st]);
         }
         __syncwarp();
       }
@@ -268,42 +298,67 @@ __global__ void __launch_bounds__((BackShape<kStages, kPStages, kDq, kHalves>::k
     });
     drain_loads(s_full, kStages, issued, 4 * kHalves + 1, p.status);
   } else if (warp == 2) {
-    const uint32_t idesc = idesc_f16_f32((uint32_t)BN);
-    const uint64_t desc0 = smem_desc_sw128(smem_u32(s_d));
-    const uint32_t box_desc = box_bytes >> 4;
-    uint32_t g = 0, i = 0;
-    for_each_back_piece(p, b, [&](const BackPiece& pc) {
-      const uint32_t buf = i & ((1u << p.dbuf_log2) - 1u);
-      const uint32_t dph = (i >> p.dbuf_log2) & 1u;
-      ++i;
-      if (!warp_wait(&d_empty[buf], dph ^ 1, wc)) return false;
-      tc_fence_after();
-      const uint32_t d_tmem = tmem_base + buf * BN;
-      for (uint32_t kb = pc.kb0; kb < pc.kb1; ++kb, ++g) {
-        const uint32_t st = g % kStages, ph = (g / kStages) & 1;
-        if (!warp_wait(&s_full[st], ph, wc)) return false;
-        tc_fence_after();
-        const uint64_t bdesc = desc0 + ((st * d_stage_bytes) >> 4);
-        const uint32_t a_t = tmem_a + st * (kKB / 2);
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < kKB / 16; ++kk)
-            tc_mma_ts(d_tmem, a_t + kk * 8, bdesc + (kk >> 2) * box_desc + 2 * (kk & 3), idesc,
-                      (kb != pc.kb0) || (kk != 0));
-          tc_commit(&s_empty[st]);
+    uint32_t g = 0;
+    if (kPair && rank != 0) {
+      for_each_back_piece<Shape>(p, b, [&](const BackPiece& pc) {
+        for (uint32_t kb = pc.kb0; kb < pc.kb1; ++kb, ++g) {
+          const uint32_t st = g % kStages, ph = (g / kStages) & 1;
+          if (!warp_wait(&s_full[st], ph, wc)) return false;
+          tc_fence_after();
+          tc_fence_before();
+          if (lane == 0) mbar_arrive_at(&peer_full[st], 0);
+          __syncwarp();
         }
+        return true;
+      });
+      asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    } else {
+      const uint32_t idesc = idesc_f16_f32((uint32_t)BN * Shape::kCtas, 128 * Shape::kCtas);
+      const uint64_t desc0 = smem_desc_sw128(smem_u32(s_d));
+      const uint32_t box_desc = box_bytes >> 4;
+      auto commit = [](uint64_t* bar) {
+        if constexpr (kPair) tc_commit_pair(bar);
+        else tc_commit(bar);
+      };
+      uint32_t i = 0;
+      for_each_back_piece<Shape>(p, b, [&](const BackPiece& pc) {
+        const uint32_t buf = i & ((1u << p.dbuf_log2) - 1u);
+        const uint32_t dph = (i >> p.dbuf_log2) & 1u;
+        ++i;
+        if (!warp_wait<kPair>(&d_empty[buf], dph ^ 1, wc)) return false;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + buf * BN * Shape::kCtas;
+        for (uint32_t kb = pc.kb0; kb < pc.kb1; ++kb, ++g) {
+          const uint32_t st = g % kStages, ph = (g / kStages) & 1;
+          if (!warp_wait(&s_full[st], ph, wc)) return false;
+          if constexpr (kPair)
+            if (!warp_wait<true>(&peer_full[st], ph, wc)) return false;
+          tc_fence_after();
+          const uint64_t bdesc = desc0 + ((st * d_stage_bytes) >> 4);
+          const uint32_t a_t = tmem_a + st * (kKB / 2);
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < kKB / 16; ++kk) {
+              const uint64_t bd = bdesc + (kk >> 2) * box_desc + 2 * (kk & 3);
+              const uint32_t add = (kb != pc.kb0) || (kk != 0);
+              if constexpr (kPair) tc_mma_ts_pair(d_tmem, a_t + kk * 8, bd, idesc, add);
+              else tc_mma_ts(d_tmem, a_t + kk * 8, bd, idesc, add);
+            }
+            commit(&s_empty[st]);
+          }
+          __syncwarp();
+        }
+        if (elect_one()) commit(&d_full[buf]);
         __syncwarp();
-      }
-      if (elect_one()) tc_commit(&d_full[buf]);
+        return true;
+      });
+      asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+      if (elect_one()) commit(done_bar);
       __syncwarp();
-      return true;
-    });
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (elect_one()) tc_commit(done_bar);
-    __syncwarp();
-    volatile int32_t zero = 0;
-    const WaitCtl drain{p.status, &zero, 100000000ull};
-    mbar_wait(done_bar, 0, drain);
+      volatile int32_t zero = 0;
+      const WaitCtl drain{p.status, &zero, 100000000ull};
+      mbar_wait(done_bar, 0, drain);
+    }
   } else if (warp < kFirstEpiWarp) {
     // Dequant and turn: quadrant q's 32 columns of a stage, 256 rows.
     const int q = warp & 3;
@@ -319,7 +374,7 @@ __global__ void __launch_bounds__((BackShape<kStages, kPStages, kDq, kHalves>::k
     const uint32_t swz = (uint32_t)((q ^ ((lane >> 1) & 3)) << 4) + (row0 + lane) * 64;
     uint32_t nan_seen = 0;
     uint32_t g = 0;  // stage of the CTA's sequence
-    for_each_back_piece(p, b, [&](const BackPiece& pc) {
+    for_each_back_piece<Shape>(p, b, [&](const BackPiece& pc) {
       for (uint32_t kb = pc.kb0; kb < pc.kb1; ++kb, ++g) {
         if (g % kDq != (uint32_t)r) continue;
         const uint32_t ps = g % kPStages, pph = (g / kPStages) & 1;
@@ -384,13 +439,16 @@ __global__ void __launch_bounds__((BackShape<kStages, kPStages, kDq, kHalves>::k
     if (__any_sync(0xFFFFFFFFu, (nan_seen & 0x8080u) != 0u) && lane == 0)
       raise_status(p.status, NVFP4_ERR_NONFINITE);
   } else {
-    back_epilogue(p, b, warp, lane, tmem_base, d_full, d_empty, wc,
-                  s_fac + (warp - kFirstEpiWarp) * kMaxBN);
+    back_epilogue<Shape>(p, b, warp, warp - kFirstEpiWarp, lane, tmem_base, d_full, d_empty, wc,
+                         s_fac + (warp - kFirstEpiWarp) * Shape::kMaxTokens);
   }
   __syncthreads();
+  // neither CTA of a pair leaves while the other's MMAs or arrivals may reach it
+  if constexpr (kPair) cluster_sync();
   if (warp == 2) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, p.tmem_cols);
+    if constexpr (kPair) tmem_dealloc_pair(tmem_base, p.tmem_cols);
+    else tmem_dealloc(tmem_base, p.tmem_cols);
   }
 }
 
@@ -398,18 +456,20 @@ __global__ void __launch_bounds__((BackShape<kStages, kPStages, kDq, kHalves>::k
 // The split tiles' sums, in the splits' order: one CTA for 8 tokens of a tile,
 // a thread for four columns.
 __global__ void __launch_bounds__(256) back_join_kernel(const BackArgs b, int64_t M, int64_t K,
-                                                        int BN, int n_ttiles) {
+                                                        int tokens, int n_ttiles, int ctas) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const uint32_t per = (uint32_t)BN / 8;
-  const uint32_t r = blockIdx.x / per, u = b.n_whole + r;
+  const uint32_t per = (uint32_t)tokens / 8;
+  const uint32_t r = blockIdx.x / per;  // tile and CTA of it
+  const uint32_t u = b.n_whole + r / (uint32_t)ctas;
   const int t = (int)(blockIdx.x % per) * 8 + (threadIdx.x >> 5);
-  const int64_t m = (int64_t)(u % (uint32_t)n_ttiles) * BN + t;
-  const int64_t k = (int64_t)(u / (uint32_t)n_ttiles) * kRows + (threadIdx.x & 31) * 4;
+  const int64_t m = (int64_t)(u % (uint32_t)n_ttiles) * tokens + t;
+  const int64_t k = (int64_t)(u / (uint32_t)n_ttiles * ctas + r % (uint32_t)ctas) * kRows +
+                    (threadIdx.x & 31) * 4;
   if (m >= M || k >= K) return;
   const float4* v = reinterpret_cast<const float4*>(b.part) +
-                    ((int64_t)r * BN + t) * (kRows / 4) + (threadIdx.x & 31);
-  const int64_t step = (int64_t)b.n_rest * BN * (kRows / 4);
+                    ((int64_t)r * tokens + t) * (kRows / 4) + (threadIdx.x & 31);
+  const int64_t step = (int64_t)b.n_rest * ctas * tokens * (kRows / 4);
   float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
   for (uint32_t s = 0; s < b.n_splits; ++s) {
@@ -480,31 +540,25 @@ __global__ void __launch_bounds__(512) back_prep_kernel(const T* __restrict__ dy
 }
 
 // ------------------------------------------------------------ host side
-template <int kStages, int kPStages, int kDq, int kHalves>
-static size_t back_smem_bytes(int BN) {
-  return 1024 + kPStages * (size_t)(kBackPacked + kBackScales) + kStages * (size_t)BN * kKB * 2 +
-         BackShape<kStages, kPStages, kDq, kHalves>::kDqWarps *
-             (size_t)BackShape<kStages, kPStages, kDq, kHalves>::kScratch + 256 +
-         4 * (size_t)kMaxBN * 4;
-}
-
-// Token tiles up to this take the deep ring (three stages of A and dy, six of
-// codes, three dequant warps a quadrant): its shared memory ends there.
+// Token tiles up to this take deep rings; longer ones would not fit them.
 constexpr int kBackDeepBN = 48;
+using BackDeep = BackShape<3, 6, 3, 1, false>;
+using BackFull = BackShape<2, 4, 2, 2, false>;
+using BackPairs = BackShape<2, 4, 2, 1, true>;
 
 // How the tiles past the last full round of the SMs are split: the number of
 // parts with the least time by this model, in us: a stage 0.55 (128 tokens) to
 // 0.3, 1 for a part's start and end, its sums written and read again at 4
-// TB/s, 3 for the kernel that joins them.
-static int best_splits(int64_t rest, int64_t stages, int BN, int sms) {
-  const double stage = std::max(0.3, 0.55 * BN / kMaxBN);
+// TB/s, 3 for the kernel that joins them.  `tokens` and `ctas` of a tile.
+static int best_splits(int64_t rest, int64_t stages, int tokens, int ctas, int workers) {
+  const double stage = std::max(0.3, 0.55 * tokens / kMaxBN);
   int best = 1;
   double least = 0.0;
   for (int64_t s = 1; s <= std::min<int64_t>(stages, 64); ++s) {
     const int64_t len = (stages + s - 1) / s;
     if ((stages + len - 1) / len != s) continue;
-    double us = (double)((rest * s + sms - 1) / sms) * (len * stage + 1.0);
-    if (s > 1) us += 3.0 + (double)(s * rest) * BN * kRows * 8 / 4e6;
+    double us = (double)((rest * s + workers - 1) / workers) * (len * stage + 1.0);
+    if (s > 1) us += 3.0 + (double)(s * rest) * ctas * tokens * kRows * 8 / 4e6;
     if (s == 1 || us < least) {
       least = us;
       best = (int)s;
@@ -516,38 +570,52 @@ static int best_splits(int64_t rest, int64_t stages, int BN, int sms) {
 BackLayout back_layout(int64_t M, int64_t N, int64_t K, int sms, size_t off) {
   BackLayout l;
   l.BN = lm_head_token_tile(M);
-  const int64_t tiles = ((K + kRows - 1) / kRows) * ((M + l.BN - 1) / l.BN);
+  l.pair = M >= 256;
+  const int ctas = l.pair ? 2 : 1, tokens = l.BN * ctas;
+  const int workers = std::max(1, sms / ctas);
+  l.n_ttiles = (int)((M + tokens - 1) / tokens);
+  const int64_t tiles = (K + kRows * ctas - 1) / (kRows * ctas) * l.n_ttiles;
   l.n_kb = (int)((N + kKB - 1) / kKB);
-  l.n_whole = tiles / sms * sms;
+  l.n_whole = tiles / workers * workers;
   l.n_rest = tiles - l.n_whole;
-  l.n_splits = l.n_rest ? best_splits(l.n_rest, l.n_kb, l.BN, sms) : 1;
+  l.n_splits = l.n_rest ? best_splits(l.n_rest, l.n_kb, tokens, ctas, workers) : 1;
   if (l.n_splits == 1) {
     l.n_whole = tiles;
     l.n_rest = 0;
   }
-  l.grid = (int)std::min<int64_t>(sms, std::max(l.n_whole, l.n_rest * l.n_splits));
+  l.grid = ctas * (int)std::min<int64_t>(workers, std::max(l.n_whole, l.n_rest * l.n_splits));
   l.part = align_up(off, 256);
-  l.total = l.part + align_up((size_t)l.n_rest * l.n_splits * l.BN * kRows * 4, 256);
+  l.total = l.part + align_up((size_t)l.n_rest * l.n_splits * ctas * tokens * kRows * 4, 256);
   return l;
 }
 
-template <int kStages, int kPStages, int kDq, int kHalves>
+template <class Shape>
 static cudaError_t back_gemm(const CUtensorMap& tm_packed, const CUtensorMap& tm_scales,
                              const CUtensorMap& tm_d, const GemmArgs& a, const BackArgs& b,
                              int grid, int max_bn, cudaStream_t stream) {
-  auto kern = w4a16_back_kernel<kStages, kPStages, kDq, kHalves>;
+  auto kern = w4a16_back_kernel<Shape>;
   static std::atomic<uint64_t> limit_set{0};
   const cudaError_t e = smem_limit_once(limit_set, reinterpret_cast<const void*>(kern),
-                                        back_smem_bytes<kStages, kPStages, kDq, kHalves>(max_bn));
+                                        Shape::smem_bytes(max_bn));
   if (e != cudaSuccess) return e;
-  PdlLaunch l(dim3((unsigned)grid), dim3(BackShape<kStages, kPStages, kDq, kHalves>::kThreads),
-              back_smem_bytes<kStages, kPStages, kDq, kHalves>(a.BN), stream);
-  return cudaLaunchKernelEx(&l.cfg, kern, tm_packed, tm_scales, tm_d, a, b);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = Shape::kCtas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(Shape::kThreads);
+  cfg.dynamicSmemBytes = Shape::smem_bytes(a.BN);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = Shape::kPair ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, tm_packed, tm_scales, tm_d, a, b);
 }
 
 cudaError_t back_launch(const BackCall& c, const BackLayout& L, uint8_t* ws, cudaStream_t stream) {
   const WeightStage& w = *c.stage;
-  const int64_t n_tt = (c.M + L.BN - 1) / L.BN;
   CUtensorMap tm_packed, tm_scales, tm_d;
   if (!encode_2d(&tm_packed, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.packed ? ws + w.packed_off : c.packed,
                  (uint64_t)c.K / 2, (uint64_t)c.N, w.packed ? w.packed_stride : (uint64_t)c.K / 2,
@@ -555,7 +623,7 @@ cudaError_t back_launch(const BackCall& c, const BackLayout& L, uint8_t* ws, cud
       !encode_2d(&tm_scales, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.scales ? ws + w.scales_off : c.scales,
                  (uint64_t)c.K / 16, (uint64_t)c.N, w.scales ? w.scales_stride : (uint64_t)c.K / 16,
                  16, kKB, CU_TENSOR_MAP_SWIZZLE_NONE) ||
-      !encode_2d(&tm_d, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, c.d, (uint64_t)c.N, (uint64_t)n_tt * L.BN,
+      !encode_2d(&tm_d, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, c.d, (uint64_t)c.N, (uint64_t)((c.M + L.BN - 1) / L.BN * L.BN),
                  (uint64_t)c.d_stride * 2, 64, (uint32_t)L.BN, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   GemmArgs a = {};
@@ -563,15 +631,15 @@ cudaError_t back_launch(const BackCall& c, const BackLayout& L, uint8_t* ws, cud
   a.N = c.N;
   a.K = c.K;
   a.BN = L.BN;
-  a.n_ttiles = (int)n_tt;
+  a.n_ttiles = L.n_ttiles;
   a.n_kb = L.n_kb;
   a.status = reinterpret_cast<int32_t*>(ws);
   const bool deep = L.BN <= kBackDeepBN;
-  const int stages = deep ? 3 : 2;
-  a.dbuf_log2 = (4 * L.BN + stages * (kKB / 2) <= 512) ? 2u : 1u;
-  a.tmem_cols = ((L.BN << a.dbuf_log2) + stages * (kKB / 2) <= 256) ? 256u : 512u;
+  const int a_cols = (deep ? BackDeep::kStages : BackFull::kStages) * (kKB / 2);
+  const int ctas = L.pair ? 2 : 1, tokens = L.BN * ctas;
+  a.dbuf_log2 = L.pair ? 0u : (4 * tokens + a_cols <= 512) ? 2u : 1u;
+  a.tmem_cols = ((tokens << a.dbuf_log2) + a_cols <= 256) ? 256u : 512u;
   BackArgs b = {};
-  b.n_ft = (uint32_t)((c.K + kRows - 1) / kRows);
   b.n_whole = (uint32_t)L.n_whole;
   b.n_rest = (uint32_t)L.n_rest;
   b.n_splits = (uint32_t)L.n_splits;
@@ -581,11 +649,12 @@ cudaError_t back_launch(const BackCall& c, const BackLayout& L, uint8_t* ws, cud
   b.part = reinterpret_cast<float*>(ws + L.part);
   b.bf16 = c.out_dtype == NVFP4_OUT_BF16;
   const cudaError_t e =
-      deep ? back_gemm<3, 6, 3, 1>(tm_packed, tm_scales, tm_d, a, b, L.grid, kBackDeepBN, stream)
-           : back_gemm<2, 4, 2, 2>(tm_packed, tm_scales, tm_d, a, b, L.grid, kMaxBN, stream);
+      L.pair ? back_gemm<BackPairs>(tm_packed, tm_scales, tm_d, a, b, L.grid, kMaxBN, stream)
+      : deep ? back_gemm<BackDeep>(tm_packed, tm_scales, tm_d, a, b, L.grid, kBackDeepBN, stream)
+             : back_gemm<BackFull>(tm_packed, tm_scales, tm_d, a, b, L.grid, kMaxBN, stream);
   if (e != cudaSuccess || L.n_rest == 0) return e;
-  PdlLaunch l(dim3((unsigned)(L.n_rest * (L.BN / 8))), dim3(256), 0, stream);
-  return cudaLaunchKernelEx(&l.cfg, back_join_kernel, b, c.M, c.K, L.BN, (int)n_tt);
+  PdlLaunch l(dim3((unsigned)(L.n_rest * ctas * (tokens / 8))), dim3(256), 0, stream);
+  return cudaLaunchKernelEx(&l.cfg, back_join_kernel, b, c.M, c.K, tokens, L.n_ttiles, ctas);
 }
 
 // ------------------------------------------------------------ the call

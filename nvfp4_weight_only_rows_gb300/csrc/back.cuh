@@ -8,13 +8,15 @@
 
 namespace nvfp4 {
 
-// The product's cut into tiles of 128 columns x BN tokens: n_whole of them
-// whole, n_rest in n_splits parts along the weight's rows; and its workspace
-// after `off`: the sums of those parts.
+// The product's cut into tiles of 128 columns x BN tokens, or, for a pair of
+// CTAs, 256 columns x 2 BN tokens: n_whole of them whole, n_rest in n_splits
+// parts along the weight's rows; and its workspace after `off`: the sums of
+// those parts.
 struct BackLayout {
   size_t part, total;
   int64_t n_whole, n_rest;
-  int grid, BN, n_splits, n_kb;
+  int grid, BN, n_ttiles, n_splits, n_kb;
+  bool pair;
 };
 BackLayout back_layout(int64_t M, int64_t N, int64_t K, int sms, size_t off);
 

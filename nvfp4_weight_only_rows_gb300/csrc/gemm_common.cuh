@@ -303,8 +303,9 @@ __device__ __forceinline__ bool spin_until_set(const uint32_t* flag, const WaitC
 }
 
 // warp-uniform bounded wait: every lane polls, the warp agrees on the outcome
+template <bool kCluster = false>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& wc) {
-  const bool ok = mbar_wait(bar, parity, wc);
+  const bool ok = mbar_wait<kCluster>(bar, parity, wc);
   return __all_sync(0xFFFFFFFFu, ok);
 }
 
