@@ -498,8 +498,8 @@ __device__ __forceinline__ float grad_value(const uint16_t* p) {
 
 // One CTA a token: its largest magnitude, then the row as fp16 after the
 // power of two that takes that to [2^14, 2^15).  bf16 gradients keep every
-// value down to 2^-28 of the largest; fp32 ones are rounded to 11 bits, 2^-12
-// of themselves, where a bf16 result is off by 2^-9 of itself.  The second
+// value down to 2^-28 of the largest; fp32 ones are rounded to 11 bits, 2^-11
+// of themselves, where a bf16 result is off by 2^-8 of itself.  The second
 // read finds the row in L2.
 template <typename T>
 __global__ void __launch_bounds__(512) back_prep_kernel(const T* __restrict__ dy, int64_t N,

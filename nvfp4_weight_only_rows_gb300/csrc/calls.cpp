@@ -438,6 +438,11 @@ void check_workspace(PyObject* o, const at::Tensor& first) {
   if (!ws.is_contiguous()) throw ValueError("workspace must be contiguous");
 }
 
+int out_dtype_code(at::ScalarType dt) {
+  if (dt != at::kFloat && dt != at::kBFloat16) throw ValueError("out must be float32 or bfloat16");
+  return dt == at::kFloat ? NVFP4_OUT_F32 : NVFP4_OUT_BF16;
+}
+
 size_t bytes_of(const at::Tensor& ws) { return (size_t)ws.numel() * ws.element_size(); }
 
 // grad_logits, packed, scales, global_scale, out, bf16 out (if out is None), workspace, stream
@@ -451,11 +456,11 @@ PyObject* lm_head_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     check(dy, dy.scalar_type(), "grad_logits", {M, w.N}, dy);
     at::ScalarType dt = integer(a[5]) ? at::kBFloat16 : at::kFloat;
     if (a[4] != Py_None) dt = tensor(a[4], "out").scalar_type();
+    const int out_code = out_dtype_code(dt);
     at::Tensor out = optional(a[4], dt, "out", {M, w.K}, dy);
     check_workspace(a[6], dy);
     const OnStream on(a[7], dy);
     if (!out.defined()) out = at::empty({M, w.K}, dy.options().dtype(dt));
-    const int out_code = dtype_code(out, "out must be float32 or bfloat16");
     const at::Tensor ws =
         workspace_arg(a[6], w4a16_lm_head_backward_workspace_bytes(M, w.N, w.K), dy);
     done(w4a16_lm_head_backward(dy.data_ptr(), code, M, w.N, w.packed, w.scales, w.global, w.K,
@@ -514,6 +519,7 @@ PyObject* cross_entropy_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const void* gz = optional_f32(a[7], "grad_lse", M, mean);
     at::ScalarType dt = integer(a[9]) ? at::kBFloat16 : at::kFloat;
     if (a[8] != Py_None) dt = tensor(a[8], "out").scalar_type();
+    const int out_code = out_dtype_code(dt);
     at::Tensor out = optional(a[8], dt, "out", {M, w.K}, mean);
     const OnStream on(a[10], mean);
     if (!out.defined()) out = at::empty({M, w.K}, mean.options().dtype(dt));
@@ -522,7 +528,7 @@ PyObject* cross_entropy_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
              f32(mean.data_ptr()), M, w.K, w.packed, w.scales, w.global, w.N,
              static_cast<const int64_t*>(targets.data_ptr()), f32(loss.data_ptr()),
              f32(g.data_ptr()), f32(gz), out.data_ptr(),
-             dtype_code(out, "out must be float32 or bfloat16"), on.handle()),
+             out_code, on.handle()),
          "w4a16_cross_entropy_backward");
     if (a[8] == Py_None) on.result(out);
     return THPVariable_Wrap(out);
@@ -552,14 +558,14 @@ PyObject* glu(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Glu g = glu_args(x, a[1], a[2], a[3], x);
     at::ScalarType dt = integer(a[6]) ? at::kBFloat16 : at::kFloat;
     if (a[5] != Py_None) dt = tensor(a[5], "out").scalar_type();
+    const int out_code = out_dtype_code(dt);
     at::Tensor out = optional(a[5], dt, "out", {g.M, g.I}, x);
     check_workspace(a[7], x);
     const OnStream on(a[8], x);
     if (!out.defined()) out = at::empty({g.M, g.I}, x.options().dtype(dt));
-    const int code = dtype_code(out, "out must be float32 or bfloat16");
     const at::Tensor ws = workspace_arg(a[7], w4a16_glu_workspace_bytes(g.M, g.I, g.w.K), x);
     done(w4a16_glu(x.data_ptr(), g.M, g.w.K, g.w.packed, g.w.scales, g.w.global, g.I,
-                   (int)integer(a[4]), out.data_ptr(), code, ws.data_ptr(), bytes_of(ws),
+                   (int)integer(a[4]), out.data_ptr(), out_code, ws.data_ptr(), bytes_of(ws),
                    on.handle()),
          "w4a16_glu");
     if (a[5] == Py_None) on.result(out);
@@ -577,11 +583,11 @@ PyObject* glu_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     check(dh, dh.scalar_type(), "grad", {g.M, g.I}, dh);
     at::ScalarType dt = integer(a[7]) ? at::kBFloat16 : at::kFloat;
     if (a[6] != Py_None) dt = tensor(a[6], "out").scalar_type();
+    const int out_code = out_dtype_code(dt);
     at::Tensor out = optional(a[6], dt, "out", {g.M, g.w.K}, dh);
     check_workspace(a[8], dh);
     const OnStream on(a[9], dh);
     if (!out.defined()) out = at::empty({g.M, g.w.K}, dh.options().dtype(dt));
-    const int out_code = dtype_code(out, "out must be float32 or bfloat16");
     const at::Tensor ws =
         workspace_arg(a[8], w4a16_glu_backward_workspace_bytes(g.M, g.I, g.w.K), dh);
     done(w4a16_glu_backward(dh.data_ptr(), code, x.data_ptr(), g.M, g.w.K, g.w.packed, g.w.scales,

@@ -31,9 +31,9 @@
 //
 // The target's row is left out of r, s and P: where the model is sure of the
 // target, 1 - p_t and the pull of all other rows keep their relative accuracy
-// (a P of the target, rounded to 2^-12, would be larger than that pull).
-// P in fp16 is off by 2^-12 of each term, at random; the result is rounded to
-// bf16, 2^-9 of itself.
+// (a P of the target, rounded to 2^-11, would be larger than that pull).
+// P in fp16 is off by 2^-11 of each term, at random; the result is rounded to
+// bf16, 2^-8 of itself.
 #include "back.cuh"
 #include "w4a16_tc.cuh"
 
@@ -190,7 +190,7 @@ struct EntropyEpilogue {
 };
 
 // ------------------------------------------------------------ rows joined
-// 2^d for an integer d <= 0 (0 below 2^-126).
+// 2^d for an integer d <= 0 (0 below 2^-116).
 __device__ __forceinline__ float pow2_down(float d) {
   return d > -127.0f ? __int_as_float((127 + (int)d) << 23) : 0.0f;
 }
@@ -406,12 +406,12 @@ static EntropyLayout entropy_layout(int64_t M, int64_t N, int64_t K, bool grad, 
   return l;
 }
 
-static int64_t entropy_chunk(int64_t M, int64_t N, bool grad) {
-  return chunk_tokens(M, grad ? (N + 7) / 8 * 16 : (N + 31) / 32 * 8);
+static int64_t entropy_chunk(int64_t M, int64_t N, int64_t K, bool grad) {
+  return chunk_tokens(M, std::max(2 * K, grad ? (N + 7) / 8 * 16 : (N + 31) / 32 * 8));
 }
 
 static WeightStage entropy_stage(int64_t M, int64_t N, int64_t K, bool grad, int sms) {
-  const int64_t chunk = entropy_chunk(M, N, grad);
+  const int64_t chunk = entropy_chunk(M, N, K, grad);
   size_t end = entropy_layout(chunk, N, K, grad, sms).end;
   if (M % chunk) end = std::max(end, entropy_layout(M % chunk, N, K, grad, sms).end);
   return weight_stage(N, K, end, true);
@@ -433,7 +433,7 @@ static nvfp4_status entropy_run(const void* x, int64_t M, int64_t K, const uint8
   CUtensorMap tm_packed, tm_scales, tm_x;
   if (!encode_weight_maps(&tm_packed, &tm_scales, wst, packed, scales, N, K, ws))
     return NVFP4_ERR_CUDA;
-  const int64_t chunk = entropy_chunk(M, N, kGrad);
+  const int64_t chunk = entropy_chunk(M, N, K, kGrad);
   for (int64_t m0 = 0; m0 < M; m0 += chunk) {
     const int64_t rows = std::min(chunk, M - m0);
     const EntropyLayout L = entropy_layout(rows, N, K, kGrad, sms);

@@ -15,9 +15,9 @@
 // that no value overflows: |g|, |u| <= |x|_1 max|W13| and max|W13| <= 2688
 // global, |act(v)| <= |v|, |act'| < 1.13, so |dg|, |du| < 1.13 max|dh| |x|_1
 // 2688 |global|.  The bound is loose by about 2^10 for normal activations and
-// weights; fp16's 40 binades from 2^15 down to its last subnormal leave 2^-29
-// of the bound at full precision, 11 bits, and 2^-40 of it as the smallest
-// step.
+// weights, and taking it by exponents costs up to 2^4 more; fp16's 40 binades
+// from 2^15 down to its last subnormal leave 2^-25 of it at full precision, 11
+// bits, and an error of 2^-36 of it below.
 #include "back.cuh"
 #include "w4a16_tc.cuh"
 
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(256)
   int e = 0;
   // logarithms, each rounded up (and one for 1.13): the product itself may be out of range
   if (!bad && mx > 0.0f && l1 > 0.0f && l1 <= 3.4028235e38f && top > 0.0f && top <= 3.4028235e38f)
-    // (at most 2^101 max|dh|, so that activations near 2^-126 meet no infinity)
+    // (at most 2^101 max|dh|, so that activations near 2^-116 meet no infinity)
     e = min(max(min(15 - (ilogbf(mx) + ilogbf(l1) + ilogbf(top) + 4), 100 - ilogbf(mx)), -126), 126);
   up2[m] = __int_as_float((127 + e) << 23);
   factor[m] = __fmul_rn(*global, __int_as_float((127 - e) << 23));
