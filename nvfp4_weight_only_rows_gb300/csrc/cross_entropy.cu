@@ -109,15 +109,21 @@ struct EntropyEpilogue {
     float* ref = reinterpret_cast<float*>(s) + kMaxBN;
     const int32_t* tgt = reinterpret_cast<const int32_t*>(ref + kMaxBN);
     const int64_t tc = u.t0 + c, live = p.M - tc;
-    const bool valid = u.n_base + (uint32_t)lane < p.N;
     const float none = __int_as_float(0xFF800000);
-    float mul[16], y[16], r[16];
-    lds_f32x16(reinterpret_cast<const float*>(s) + c, mul);
+    float y[16], r[16];
+    {
+      float mul[16];
+      lds_f32x16(reinterpret_cast<const float*>(s) + c, mul);
 #pragma unroll
-    for (int t = 0; t < 16; t += 2) {
-      const float2 w = __fmul2_rn(make_float2(v[t], v[t + 1]), make_float2(mul[t], mul[t + 1]));
-      y[t] = valid ? w.x : none;
-      y[t + 1] = valid ? w.y : none;
+      for (int t = 0; t < 16; t += 2) {
+        const float2 w = __fmul2_rn(make_float2(v[t], v[t + 1]), make_float2(mul[t], mul[t + 1]));
+        y[t] = w.x;
+        y[t + 1] = w.y;
+      }
+    }
+    if (u.n_base + 32 > p.N) {  // warp-uniform: the last rows
+#pragma unroll
+      for (int t = 0; t < 16; ++t) y[t] = u.n_base + (uint32_t)lane < p.N ? y[t] : none;
     }
     // targets among these 32 rows: their y is kept, and they count no further
     const int32_t d = lane < 16 ? tgt[c + lane] - (int32_t)u.n_base : -1;
@@ -152,40 +158,57 @@ struct EntropyEpilogue {
       __syncwarp();
     }
     // 2^(y - r + 15): y is at most r; below r - 140 nothing is left of it
-    float e[16];
+    float2 e[8];
     const bool far = __any_sync(0xFFFFFFFFu, !(fabsf(ref[c + (lane & 15)]) < kMagicLimit));
     if (!far) {
 #pragma unroll
-      for (int t = 0; t < 16; ++t) {
-        const float x = fmaxf(y[t], r[t] - 140.0f);
-        const float whole = x + kMagic;
-        const int32_t shift = __float_as_int(whole) - __float_as_int(r[t] + kMagic);
-        e[t] = ex2(x - (whole - kMagic)) * __int_as_float((shift + 127 + kPBits) << 23);
+      for (int t = 0; t < 8; ++t) {
+        // (scalar sums: built from packed ones, nvcc 13.0.88 gave the first of a pair shift 0)
+        const float x0 = fmaxf(y[2 * t], r[2 * t] - 140.0f);
+        const float x1 = fmaxf(y[2 * t + 1], r[2 * t + 1] - 140.0f);
+        const float w0 = x0 + kMagic, w1 = x1 + kMagic;
+        const int32_t s0 = __float_as_int(w0) - __float_as_int(r[2 * t] + kMagic);
+        const int32_t s1 = __float_as_int(w1) - __float_as_int(r[2 * t + 1] + kMagic);
+        e[t] = __fmul2_rn(make_float2(ex2(x0 - (w0 - kMagic)), ex2(x1 - (w1 - kMagic))),
+                          make_float2(__int_as_float((s0 << 23) + ((127 + kPBits) << 23)),
+                                      __int_as_float((s1 << 23) + ((127 + kPBits) << 23))));
       }
     } else {  // no reference yet, one that is no number, or logits in the millions
 #pragma unroll
-      for (int t = 0; t < 16; ++t) e[t] = ex2(y[t] - r[t]) * (float)(1 << kPBits);
+      for (int t = 0; t < 8; ++t)
+        e[t] = make_float2(ex2(y[2 * t] - r[2 * t]) * (float)(1 << kPBits),
+                           ex2(y[2 * t + 1] - r[2 * t + 1]) * (float)(1 << kPBits));
     }
-    if (kGrad && valid) {
+    if (kGrad && u.n_base + (uint32_t)lane < p.N) {
       uint16_t* o = reinterpret_cast<uint16_t*>(a.P) + tc * a.stride + u.n_base + lane;
 #pragma unroll
-      for (int t = 0; t < 16; ++t, o += a.stride) *o = f16_canonical(e[t]);
-    }
-    // sums over the warp's rows: as group_maxima, lanes 2 t and 2 t + 1 end with token t's
-#pragma unroll
-    for (int w = 8; w >= 1; w >>= 1) {
-      const bool upper = (lane & (2 * w)) != 0;
-#pragma unroll
-      for (int j = 0; j < w; ++j) {
-        const float mine = upper ? e[j + w] : e[j];
-        const float send = upper ? e[j] : e[j + w];
-        e[j] = mine + __shfl_xor_sync(0xFFFFFFFFu, send, 2 * w);
+      for (int t = 0; t < 8; ++t) {
+        *o = f16_canonical(e[t].x);
+        o += a.stride;
+        *o = f16_canonical(e[t].y);
+        o += a.stride;
       }
     }
-    e[0] += __shfl_xor_sync(0xFFFFFFFFu, e[0], 1);
+    // sums over the warp's rows, as group_maxima does it: of 2 w pairs of
+    // tokens a lane keeps w, lane bits 4, 3, 2 choose which, and of the last
+    // pair bit 1 one token; lanes 2 t and 2 t + 1 end with token t's sum
+#pragma unroll
+    for (int w = 4; w >= 1; w >>= 1) {
+      const bool upper = (lane & (4 * w)) != 0;
+#pragma unroll
+      for (int j = 0; j < w; ++j) {
+        const float2 mine = upper ? e[j + w] : e[j], send = upper ? e[j] : e[j + w];
+        e[j] = __fadd2_rn(mine, make_float2(__shfl_xor_sync(0xFFFFFFFFu, send.x, 4 * w),
+                                            __shfl_xor_sync(0xFFFFFFFFu, send.y, 4 * w)));
+      }
+    }
+    const bool second = (lane & 2) != 0;
+    float sum = (second ? e[0].y : e[0].x) +
+                __shfl_xor_sync(0xFFFFFFFFu, second ? e[0].x : e[0].y, 2);
+    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
     const int t = (lane >> 1) & 15;
     if ((lane & 1) == 0 && t < live)
-      a.part[(int64_t)(u.n_base >> 5) * p.M + tc + t] = make_float2(ref[c + t], e[0]);
+      a.part[(int64_t)(u.n_base >> 5) * p.M + tc + t] = make_float2(ref[c + t], sum);
   }
 };
 
