@@ -77,7 +77,7 @@ struct EntropyArgs {
 template <bool kGrad>
 struct EntropyEpilogue {
   static constexpr bool kOwn = true, kPaired = false;
-  static constexpr int kPartStages = 6;
+  static constexpr int kFirstPart = 7, kNextPart = 5;  // stages of 256
   static constexpr int kWarpBytes = 3 * kMaxBN * 4;  // multiplier, reference, target of a token
   struct Unit {
     int64_t t0;

@@ -835,9 +835,12 @@ __device__ __forceinline__ void epilogue_role(const GemmArgs& p, const Sched& sc
 // accumulator is ready (what the unit's tokens need, into the warp's E::kWarpBytes
 // of shared memory; it ends with a __syncwarp), E::chunk per 16 tokens of the
 // finished unit, a value of each for this lane's row.
-// E::kPartStages: a unit's sum in parts of that many stages, each from zero in
-// an accumulator of its own, added here in fp32: in registers, and with the
-// last part in that one's accumulator.  The tensor cores' sums drop the bits below fp32 at every
+// E::kFirstPart, E::kNextPart: a unit's sum in parts, the first of up to
+// kFirstPart stages, the others of up to kNextPart (0: one part), each from
+// zero in an accumulator of its own, added here in fp32: in registers, and with
+// the last part in that one's accumulator.  (What a finished unit takes here
+// has to end within the next unit's first part, so that is the longest.)  The
+// tensor cores' sums drop the bits below fp32 at every
 // step, always towards zero, so the error of a long sum of one sign grows with
 // its steps; in parts it stays that of a part.
 // kWarps: 4, or 8, where two warps share a quadrant and take every other 16
@@ -871,9 +874,9 @@ __device__ __forceinline__ void walk_epilogue(const GemmArgs& p, const Sched& sc
       if (lane == 0) mbar_arrive(&d_empty[buf]);
     };
     bool in_parts = false;
-    [[maybe_unused]] float acc[E::kPartStages > 0 ? 4 : 1][16];  // at most 64 tokens a warp
-    if constexpr (E::kPartStages > 0) {
-      for (uint32_t kb = pc.kb0; kb + E::kPartStages < pc.kb1; kb += E::kPartStages) {
+    [[maybe_unused]] float acc[E::kFirstPart > 0 ? 4 : 1][16];  // at most 64 tokens a warp
+    if constexpr (E::kFirstPart > 0) {
+      for (uint32_t kb = pc.kb0 + E::kFirstPart; kb < pc.kb1; kb += E::kNextPart) {
         if (!next()) return false;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -891,7 +894,7 @@ __device__ __forceinline__ void walk_epilogue(const GemmArgs& p, const Sched& sc
       }
     }
     if (!next()) return false;
-    if constexpr (E::kPartStages > 0) {
+    if constexpr (E::kFirstPart > 0) {
       if (in_parts) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {

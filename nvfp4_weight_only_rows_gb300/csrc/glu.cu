@@ -57,7 +57,7 @@ struct GluArgs {
 template <int kAct, bool kGrad, bool kBf16>
 struct GluEpilogue {
   static constexpr bool kOwn = true, kPaired = true;
-  static constexpr int kPartStages = 0;
+  static constexpr int kFirstPart = 0, kNextPart = 0;
   static constexpr int kWarpBytes = (kGrad ? 2 : 1) * kMaxBN * 4;
   int64_t half;  // rows from a gate to its up
   GluArgs a;

@@ -24,7 +24,7 @@ cudaError_t stage_weights(const WeightStage& w, const uint8_t* packed, const uin
 // The epilogue of kOut (epilogue_role).
 struct NoEpilogue {
   static constexpr bool kOwn = false, kPaired = false;
-  static constexpr int kPartStages = 0;
+  static constexpr int kFirstPart = 0, kNextPart = 0;
 };
 
 constexpr int kKS = 256;            // k per packed/scale stage
@@ -281,13 +281,14 @@ __global__ void __launch_bounds__((own_threads<E, kOut, kStages, kPStages, kDqPe
       if (!warp_wait(&d_empty[buf], dph ^ 1, wc)) return false;
       tc_fence_after();
       uint32_t d_tmem = tmem_base + buf * BN;
-      uint32_t part0 = pc.kb0;  // the first stage of this accumulator
+      uint32_t part0 = pc.kb0, part1 = pc.kb0 + E::kFirstPart;  // this accumulator's stages
       for (uint32_t kb = pc.kb0; kb < pc.kb1; ++kb, ++g) {
-        if constexpr (E::kPartStages > 0) {
-          if (kb == part0 + E::kPartStages) {  // the next part, in the next accumulator
+        if constexpr (E::kFirstPart > 0) {
+          if (kb == part1) {  // the next part, in the next accumulator
             if (elect_one()) tc_commit(&d_full[buf]);
             __syncwarp();
             part0 = kb;
+            part1 = kb + E::kNextPart;
             buf = (uint32_t)(i & ((1 << p.dbuf_log2) - 1));
             dph = (uint32_t)((i >> p.dbuf_log2) & 1);
             ++i;
