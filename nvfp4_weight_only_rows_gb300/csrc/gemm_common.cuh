@@ -895,22 +895,19 @@ __device__ __forceinline__ void walk_epilogue(const GemmArgs& p, const Sched& sc
     }
     if (!next()) return false;
     if constexpr (E::kFirstPart > 0) {
-      if (in_parts) {
+      // the last part, and the accumulator is free: what follows reads registers
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int c = c0 + kStep * j;
-          if (c >= BN) continue;
-          const uint32_t at = tmem_base + lane_off + buf * BN + c;
-          uint32_t v[16];
-          tmem_ld16(at, v);
-          tc_wait_ld();
+      for (int j = 0; j < 4; ++j) {
+        const int c = c0 + kStep * j;
+        if (c >= BN) continue;
+        uint32_t v[16];
+        tmem_ld16(tmem_base + lane_off + buf * BN + c, v);
+        tc_wait_ld();
 #pragma unroll
-          for (int t = 0; t < 16; ++t)
-            v[t] = __float_as_uint(__fadd_rn(acc[j][t], __uint_as_float(v[t])));
-          tmem_st16(at, v);
-        }
-        tc_wait_st();
+        for (int t = 0; t < 16; ++t)
+          acc[j][t] = in_parts ? __fadd_rn(acc[j][t], __uint_as_float(v[t])) : __uint_as_float(v[t]);
       }
+      drained();
     }
     // a unit cut by a range boundary, as in epilogue_role
     const bool whole = pc.kb0 == 0 && pc.kb1 == (uint32_t)p.n_kb;
@@ -927,12 +924,22 @@ __device__ __forceinline__ void walk_epilogue(const GemmArgs& p, const Sched& sc
       if (finish && !spin_until_set(p.split_ready + slot, wc)) return false;
     }
     for (int c = c0; c < BN; c += kStep) {
-      uint32_t v[16];
-      tmem_ld16(tmem_base + lane_off + buf * BN + c, v);
       float val[16];
-      tc_wait_ld();
+      if constexpr (E::kFirstPart > 0) {
 #pragma unroll
-      for (int t = 0; t < 16; ++t) val[t] = __uint_as_float(v[t]);
+        for (int t = 0; t < 16; ++t) {
+          val[t] = acc[0][t];
+          acc[0][t] = acc[1][t];
+          acc[1][t] = acc[2][t];
+          acc[2][t] = acc[3][t];
+        }
+      } else {
+        uint32_t v[16];
+        tmem_ld16(tmem_base + lane_off + buf * BN + c, v);
+        tc_wait_ld();
+#pragma unroll
+        for (int t = 0; t < 16; ++t) val[t] = __uint_as_float(v[t]);
+      }
       if (!finish) {
 #pragma unroll
         for (int t = 0; t < 16; ++t) part[(c + t) * 32 + lane] = val[t];
@@ -952,7 +959,7 @@ __device__ __forceinline__ void walk_epilogue(const GemmArgs& p, const Sched& sc
       __syncwarp();
       if (lane == 0) atomicExch(p.split_ready + slot, 1u);
     }
-    drained();
+    if constexpr (E::kFirstPart == 0) drained();
     return true;
   });
 }
