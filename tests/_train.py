@@ -142,7 +142,7 @@ def entropy_reference(x, W, targets):
     pW = others @ W.abs()
     r["mean"] = others @ W
     r["mean_tol"] = (2.0 ** -11 + 2 * top[:, None] + 2.0 ** -18 + sum_error(N)) * pW \
-        + 2.0 ** -35 * others.amax(1, keepdim=True) * W.abs().sum(0) \
+        + 2.0 ** -31 * others.amax(1, keepdim=True) * W.abs().sum(0) \
         + 2.0 ** -125 * W.abs().sum(0)  # probabilities below fp32's smallest normal number, 2^-126
     r["has"], r["t"] = has, t[:, 0]
     return r
