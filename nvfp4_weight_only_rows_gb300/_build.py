@@ -21,7 +21,7 @@ LIB = os.path.join(HERE, "libnvfp4_lm_head.so")
 CALLS = os.path.join(HERE, "_calls.so")
 SOURCES = ("quantize.cu", "lm_head.cu", "fp8.cu", "w4a4.cu", "topk.cu", "api.cu", "noalloc.cu",
            "selftest.cu", "moe_route.cu", "moe.cu", "moe_tc.cu",
-           "logprobs.cu", "back.cu", "cross_entropy.cu", "glu.cu")
+           "logprobs.cu", "prologue.cu", "back.cu", "cross_entropy.cu", "glu.cu")
 CALLS_SOURCES = ("calls.cpp",)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

@@ -22,6 +22,7 @@
 // dy enters as fp16 after an exact power of two per token (as x does in the
 // forward product), products are exact, sums fp32 in a fixed order.
 #include "back.cuh"
+#include "prologue.cuh"
 #include "w4a16_tc.cuh"
 
 namespace nvfp4 {
@@ -64,6 +65,7 @@ struct BackArgs {
   void* out;             // [M, K]
   float* part;           // [n_splits][n_rest][CTAs of a tile][tokens][128] sums
   int bf16;
+  int fresh;             // the kernel before writes the copy the weight is read from
 };
 
 // A CTA's work: every grid-th whole tile, then every grid-th split, all first
@@ -259,6 +261,7 @@ __global__ void __launch_bounds__(Shape::kThreads, 1)
   const WaitCtl wc{p.status, abort_flag, kWaitLimitNs};
 
   if (warp == 0) {
+    if (b.fresh) grid_dependency_wait();
     uint32_t issued = 0;
     for_each_back_piece<Shape>(p, b, [&](const BackPiece& pc) {
       for (uint32_t kb = pc.kb0; kb < pc.kb1; ++kb, ++issued) {
@@ -490,55 +493,6 @@ __global__ void __launch_bounds__(256) back_join_kernel(const BackArgs b, int64_
   }
 }
 
-// ------------------------------------------------------------ dy to fp16
-__device__ __forceinline__ float grad_value(const float* p) { return __ldg(p); }
-__device__ __forceinline__ float grad_value(const uint16_t* p) {
-  return __uint_as_float((uint32_t)__ldg(p) << 16);
-}
-
-// One CTA a token: its largest magnitude, then the row as fp16 after the
-// power of two that takes that to [2^14, 2^15).  bf16 gradients keep every
-// value down to 2^-28 of the largest; fp32 ones are rounded to 11 bits, 2^-11
-// of themselves, where a bf16 result is off by 2^-8 of itself.  The second
-// read finds the row in L2.
-template <typename T>
-__global__ void __launch_bounds__(512) back_prep_kernel(const T* __restrict__ dy, int64_t N,
-                                                        const float* __restrict__ global,
-                                                        __half* __restrict__ d16, int64_t stride,
-                                                        float* __restrict__ factor,
-                                                        int32_t* status) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (blockIdx.x == 0 && threadIdx.x == 0 && status) *status = NVFP4_OK;  // a call's first chunk
-  const int64_t m = blockIdx.x;
-  const T* row = dy + m * N;
-  float mx = 0.0f;
-  bool bad = false;  // Inf or NaN: the row stays as it is
-#pragma unroll 8
-  for (int64_t n = threadIdx.x; n < N; n += blockDim.x) {
-    const float a = fabsf(grad_value(row + n));
-    mx = fmaxf(mx, a);
-    bad |= !(a <= 3.4028235e38f);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-  __shared__ float red[16];
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = mx;
-  bad = __syncthreads_or(bad);
-  mx = red[0];
-  for (int w = 1; w < (int)(blockDim.x >> 5); ++w) mx = fmaxf(mx, red[w]);
-  const int e = (mx > 0.0f && !bad) ? min(max(14 - ilogbf(mx), -126), 126) : 0;
-  if (threadIdx.x == 0) factor[m] = __fmul_rn(*global, __int_as_float((127 - e) << 23));
-  const float p2 = __int_as_float((127 + e) << 23);
-  __half* o = d16 + m * stride;
-#pragma unroll 4
-  for (int64_t n = 2 * (int64_t)threadIdx.x; n < N; n += 2 * blockDim.x) {
-    const float a = grad_value(row + n);
-    const float b = n + 1 < N ? grad_value(row + n + 1) : 0.0f;
-    *reinterpret_cast<__half2*>(o + n) = __floats2half2_rn(a * p2, b * p2);
-  }
-}
-
 // ------------------------------------------------------------ host side
 // Token tiles up to this take deep rings; longer ones would not fit them.
 constexpr int kBackDeepBN = 48;
@@ -648,6 +602,7 @@ cudaError_t back_launch(const BackCall& c, const BackLayout& L, uint8_t* ws, cud
   b.out = c.out;
   b.part = reinterpret_cast<float*>(ws + L.part);
   b.bf16 = c.out_dtype == NVFP4_OUT_BF16;
+  b.fresh = c.fresh && (w.packed || w.scales);
   const cudaError_t e =
       L.pair ? back_gemm<BackPairs>(tm_packed, tm_scales, tm_d, a, b, L.grid, kMaxBN, stream)
       : deep ? back_gemm<BackDeep>(tm_packed, tm_scales, tm_d, a, b, L.grid, kBackDeepBN, stream)
@@ -699,26 +654,28 @@ nvfp4_status lm_head_back_launch(const void* dy, int dtype, int64_t M, int64_t N
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   __half* d16 = reinterpret_cast<__half*>(ws + L.d16);
   float* factor = reinterpret_cast<float*>(ws + L.factor);
-  if (stage_weights(L.stage, packed, scales, N, K, ws, stream) != cudaSuccess)
-    return NVFP4_ERR_CUDA;
   const size_t out_size = out_dtype == NVFP4_OUT_BF16 ? 2 : 4;
   const size_t in_size = dtype == NVFP4_OUT_BF16 ? 2 : 4;
   for (int64_t m = 0; m < M; m += L.chunk) {
     const int64_t rows = std::min(L.chunk, M - m);
     const void* src = static_cast<const uint8_t*>(dy) + (size_t)m * N * in_size;
     const BackLayout back = back_layout(rows, N, K, sms, L.back.part);
-    PdlLaunch l(dim3((unsigned)rows), dim3(512), 0, stream);
-    int32_t* status = m == 0 ? reinterpret_cast<int32_t*>(ws) : nullptr;
-    const cudaError_t e =
-        dtype == NVFP4_OUT_BF16
-            ? cudaLaunchKernelEx(&l.cfg, back_prep_kernel<uint16_t>,
-                                 static_cast<const uint16_t*>(src), N, global, d16, L.stride,
-                                 factor, status)
-            : cudaLaunchKernelEx(&l.cfg, back_prep_kernel<float>, static_cast<const float*>(src), N,
-                                 global, d16, L.stride, factor, status);
-    if (e != cudaSuccess) return NVFP4_ERR_CUDA;
+    Prologue pro = {};
+    pro.dy = src;
+    pro.n_dy = rows;
+    pro.N = N;
+    pro.dy_stride = L.stride;
+    pro.d16 = d16;
+    pro.factor = factor;
+    pro.grad_bf16 = dtype == NVFP4_OUT_BF16;
+    pro.global = global;
+    if (m == 0) {
+      pro.status = reinterpret_cast<int32_t*>(ws);
+      prologue_weights(pro, L.stage, packed, scales, N, K, ws);
+    }
+    if (prologue_launch(pro, stream) != cudaSuccess) return NVFP4_ERR_CUDA;
     const BackCall c{rows, N, K, d16, L.stride, packed, scales, &L.stage, factor,
-                     static_cast<uint8_t*>(dx) + (size_t)m * K * out_size, out_dtype};
+                     static_cast<uint8_t*>(dx) + (size_t)m * K * out_size, out_dtype, true};
     if (back_launch(c, back, ws, stream) != cudaSuccess) return NVFP4_ERR_CUDA;
   }
   return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;

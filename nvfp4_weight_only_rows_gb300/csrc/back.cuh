@@ -29,6 +29,7 @@ struct BackCall {
   const float* factor;  // [M]
   void* out;            // [M, K]
   int out_dtype;
+  bool fresh;           // the kernel before may have staged the weight
 };
 // Two kernels at most, programmatic dependents of the kernel before.
 cudaError_t back_launch(const BackCall& c, const BackLayout& L, uint8_t* ws, cudaStream_t stream);

@@ -9,7 +9,7 @@
 // of training costs the logits once (2 M N K) and the product back once.
 //
 // Per chunk of tokens, five kernels at most:
-//  1. w4a16_prep_x_kernel: x as fp16 (lm_head.cu).
+//  1. train_prologue_kernel: x as fp16 (prologue.cu).
 //  2. w4a16_tc_kernel with EntropyEpilogue: the logits of 128 rows x up to 128
 //     tokens at a time in tensor memory; per token and 32 rows a reference
 //     r >= max y, one of .., -4, 4, 12, .., and s = sum 2^(y - r); for the
@@ -37,6 +37,7 @@
 // P in fp16 is off by 2^-11 of each term, at random; the result is rounded to
 // bf16, 2^-8 of itself.
 #include "back.cuh"
+#include "prologue.cuh"
 #include "w4a16_tc.cuh"
 
 namespace nvfp4 {
@@ -87,6 +88,7 @@ struct EntropyEpilogue {
     uint32_t n_base;  // the warp's first row
   };
   EntropyArgs a;
+  int staged;  // the weight is read from a copy in the workspace
 
   __device__ Unit begin(const GemmArgs& p, uint32_t u, int q, int lane, uint8_t* s) const {
     float* mul = reinterpret_cast<float*>(s);
@@ -235,10 +237,10 @@ __device__ __forceinline__ uint32_t scale_down(uint32_t h, float f) {
          ((uint32_t)__half_as_ushort(__float2half_rz(v.y * f)) << 16);
 }
 
-constexpr int kJoinThreads = 1024;
+constexpr int kJoinThreads = 512;
 
 // A CTA takes TT (a power of two) neighbouring tokens, a thread every
-// (1024 / TT)-th group of one of them.
+// (512 / TT)-th group of one of them.
 template <bool kGrad>
 __global__ void __launch_bounds__(kJoinThreads)
     entropy_rows_kernel(const float2* __restrict__ part, int64_t M, int64_t N, int tt_log2,
@@ -306,38 +308,48 @@ __global__ void __launch_bounds__(kJoinThreads)
   // the groups below their token's reference: a warp finds those of its 32
   // (group, token) places, then takes them in eights, four lanes each
   const int lane = threadIdx.x & 31;
-  for (int64_t g = slice; g - slice < groups; g += slices) {  // (the warp's count of steps)
-    const float rg = m < M && g < groups ? __ldcg(part + g * M + m).x : r;
-    const bool low = rg < r && rg != kNoRef;  // (not NaN, and not nothing at all)
-    const float scale = pow2_down(rg - r);
-    uint32_t todo = __ballot_sync(0xFFFFFFFFu, low);
-    uint4 w[4];
-    uint4* at[4];
-    float f[4];
+  for (int64_t g0 = slice; g0 - slice < groups; g0 += 8 * slices) {  // (the warp's count of steps)
+    float rg[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {  // all of them in flight together
-      at[k] = nullptr;
-      if (todo == 0u) continue;  // warp-uniform
-      uint32_t rest = todo;
-      for (int i = 0; i < (lane >> 2); ++i) rest &= rest - 1;  // this lane's of the next eight
-      const int src = rest ? __ffs(rest) - 1 : 0;
-      f[k] = __shfl_sync(0xFFFFFFFFu, scale, src);
-      const int64_t n = __shfl_sync(0xFFFFFFFFu, g, src) * 32 + (lane & 3) * 8;
-      const int64_t row = __shfl_sync(0xFFFFFFFFu, m, src);
-      if (rest && n < stride) {
-        at[k] = reinterpret_cast<uint4*>(P + row * stride + n);
-        w[k] = __ldcs(at[k]);
+    for (int i = 0; i < 8; ++i)
+      rg[i] = m < M && g0 + i * slices < groups ? __ldcg(&part[(g0 + i * slices) * M + m].x) : r;
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+      const int64_t g = g0 + i * slices;
+      const bool low = rg[0] < r && rg[0] != kNoRef;  // (not NaN, and not nothing at all)
+      const float scale = pow2_down(rg[0] - r);
+#pragma unroll
+      for (int k = 0; k < 7; ++k) rg[k] = rg[k + 1];
+      uint32_t todo = __ballot_sync(0xFFFFFFFFu, low);
+      if (todo == 0u) continue;
+      uint4 w[4];
+      uint4* at[4];
+      float f[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {  // all of them in flight together
+        at[k] = nullptr;
+        if (todo == 0u) continue;  // warp-uniform
+        uint32_t rest = todo;
+        for (int h = 0; h < (lane >> 2); ++h) rest &= rest - 1;  // this lane's of the next eight
+        const int src = rest ? __ffs(rest) - 1 : 0;
+        f[k] = __shfl_sync(0xFFFFFFFFu, scale, src);
+        const int64_t n = __shfl_sync(0xFFFFFFFFu, g, src) * 32 + (lane & 3) * 8;
+        const int64_t row = __shfl_sync(0xFFFFFFFFu, m, src);
+        if (rest && n < stride) {
+          at[k] = reinterpret_cast<uint4*>(P + row * stride + n);
+          w[k] = __ldcs(at[k]);
+        }
+        for (int h = 0; h < 8; ++h) todo &= todo - 1;
       }
-      for (int i = 0; i < 8; ++i) todo &= todo - 1;
-    }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (!at[k]) continue;
-      w[k].x = scale_down(w[k].x, f[k]);
-      w[k].y = scale_down(w[k].y, f[k]);
-      w[k].z = scale_down(w[k].z, f[k]);
-      w[k].w = scale_down(w[k].w, f[k]);
-      *at[k] = w[k];
+      for (int k = 0; k < 4; ++k) {
+        if (!at[k]) continue;
+        w[k].x = scale_down(w[k].x, f[k]);
+        w[k].y = scale_down(w[k].y, f[k]);
+        w[k].z = scale_down(w[k].z, f[k]);
+        w[k].w = scale_down(w[k].w, f[k]);
+        *at[k] = w[k];
+      }
     }
   }
 }
@@ -465,7 +477,6 @@ static nvfp4_status entropy_run(const void* x, int64_t M, int64_t K, const uint8
   const int sms = sm_count();
   if (sms <= 0) return NVFP4_ERR_CUDA;
   const WeightStage wst = entropy_stage(M, N, K, kGrad, sms);
-  if (stage_weights(wst, packed, scales, N, K, ws, stream) != cudaSuccess) return NVFP4_ERR_CUDA;
   CUtensorMap tm_packed, tm_scales, tm_x;
   if (!encode_weight_maps(&tm_packed, &tm_scales, wst, packed, scales, N, K, ws))
     return NVFP4_ERR_CUDA;
@@ -478,11 +489,22 @@ static nvfp4_status entropy_run(const void* x, int64_t M, int64_t K, const uint8
     float* tok = reinterpret_cast<float*>(ws + L.tok);
     float* factor = reinterpret_cast<float*>(ws + L.factor);
     unsigned long long* keys = reinterpret_cast<unsigned long long*>(ws + L.keys);
-    if (prep_x_launch(static_cast<const uint8_t*>(x) + (size_t)m0 * K * 2, rows, K, n_tt * L.BN,
-                      global, x16, tok, m0 == 0 ? reinterpret_cast<int32_t*>(ws) : nullptr,
-                      reinterpret_cast<uint32_t*>(ws + L.cnt), L.n_flags, keys,
-                      stream) != cudaSuccess)
-      return NVFP4_ERR_CUDA;
+    Prologue pro = {};
+    pro.x = static_cast<const uint16_t*>(x) + m0 * K;
+    pro.M = rows;
+    pro.K = K;
+    pro.m_rows = n_tt * L.BN;
+    pro.x16 = x16;
+    pro.tok_scale = tok;
+    pro.keys = keys;
+    pro.global = global;
+    pro.flags = reinterpret_cast<uint32_t*>(ws + L.cnt);
+    pro.n_flags = L.n_flags;
+    if (m0 == 0) {
+      pro.status = reinterpret_cast<int32_t*>(ws);
+      prologue_weights(pro, wst, packed, scales, N, K, ws);
+    }
+    if (prologue_launch(pro, stream) != cudaSuccess) return NVFP4_ERR_CUDA;
     if (!encode_2d(&tm_x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x16, (uint64_t)K,
                    (uint64_t)(n_tt * L.BN), (uint64_t)K * 2, 64, (uint32_t)L.BN,
                    CU_TENSOR_MAP_SWIZZLE_128B))
@@ -509,7 +531,7 @@ static nvfp4_status entropy_run(const void* x, int64_t M, int64_t K, const uint8
     const EntropyArgs ea{targets + m0, reinterpret_cast<float*>(ws + L.y_t),
                          reinterpret_cast<float2*>(ws + L.part),
                          kGrad ? reinterpret_cast<__half*>(ws + L.P) : nullptr, L.stride};
-    const EntropyEpilogue<kGrad> epi{ea};
+    const EntropyEpilogue<kGrad> epi{ea, wst.packed || wst.scales};
     cudaError_t e =
         deep ? launch_gemm_with<3, 6, 3>(epi, tm_packed, tm_scales, tm_x, a, L.grid, stream)
              : launch_gemm_with<2, 4, 2>(epi, tm_packed, tm_scales, tm_x, a, L.grid, stream);
@@ -523,7 +545,7 @@ static nvfp4_status entropy_run(const void* x, int64_t M, int64_t K, const uint8
                            factor, ea.P, L.stride);
     if (e == cudaSuccess && kGrad) {
       const BackCall c{rows, N, K, ea.P, L.stride, packed, scales, &wst, factor, mean + m0 * K,
-                       NVFP4_OUT_F32};
+                       NVFP4_OUT_F32, false};
       e = back_launch(c, L.back, ws, stream);
     }
     if (e != cudaSuccess) return NVFP4_ERR_CUDA;

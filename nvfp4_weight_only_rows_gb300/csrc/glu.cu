@@ -19,6 +19,7 @@
 // from 2^15 down to its last subnormal leave 2^-25 of it at full precision, 11
 // bits, and an error of 2^-36 of it below.
 #include "back.cuh"
+#include "prologue.cuh"
 #include "w4a16_tc.cuh"
 
 namespace nvfp4 {
@@ -60,6 +61,7 @@ struct GluEpilogue {
   static constexpr int kFirstPart = 0, kNextPart = 0;
   static constexpr int kWarpBytes = (kGrad ? 2 : 1) * kMaxBN * 4;
   int64_t half;  // rows from a gate to its up
+  int staged;    // the weight is read from a copy in the workspace
   GluArgs a;
   struct Unit {
     int64_t i;     // column of h
@@ -129,59 +131,6 @@ struct GluEpilogue {
   }
 };
 
-// One CTA a token: the power of two for dg and du, and its inverse times the
-// weight's global scale.
-template <typename T>
-__global__ void __launch_bounds__(256)
-    glu_scale_kernel(const T* __restrict__ dh, const uint16_t* __restrict__ x, int64_t I, int64_t K,
-                     const float* __restrict__ global, float* __restrict__ up2,
-                     float* __restrict__ factor) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int64_t m = blockIdx.x;
-  float mx = 0.0f, l1 = 0.0f;
-  bool bad = false;
-#pragma unroll 8
-  for (int64_t i = threadIdx.x; i < I; i += blockDim.x) {
-    float v;
-    if constexpr (sizeof(T) == 2) v = __uint_as_float((uint32_t)__ldg(dh + m * I + i) << 16);
-    else v = __ldg(dh + m * I + i);
-    mx = fmaxf(mx, fabsf(v));
-    bad |= !(fabsf(v) <= 3.4028235e38f);
-  }
-  for (int64_t k = (int64_t)threadIdx.x * 8; k < K; k += (int64_t)blockDim.x * 8) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(x + m * K + k));
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      l1 += fabsf(__uint_as_float(u[j] << 16)) + fabsf(__uint_as_float(u[j] & 0xFFFF0000u));
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-    l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, o);
-  }
-  __shared__ float red[2][8];
-  if ((threadIdx.x & 31) == 0) {
-    red[0][threadIdx.x >> 5] = mx;
-    red[1][threadIdx.x >> 5] = l1;
-  }
-  bad = __syncthreads_or(bad);
-  if (threadIdx.x != 0) return;
-  for (int w = 1; w < 8; ++w) {
-    mx = fmaxf(mx, red[0][w]);
-    l1 += red[1][w];
-  }
-  const float top = fabsf(*global) * 2688.0f;  // at least max|W13|
-  int e = 0;
-  // logarithms, each rounded up (and one for 1.13): the product itself may be out of range
-  if (!bad && mx > 0.0f && l1 > 0.0f && l1 <= 3.4028235e38f && top > 0.0f && top <= 3.4028235e38f)
-    // (at most 2^101 max|dh|, so that activations near 2^-116 meet no infinity)
-    e = min(max(min(15 - (ilogbf(mx) + ilogbf(l1) + ilogbf(top) + 4), 100 - ilogbf(mx)), -126), 126);
-  up2[m] = __int_as_float((127 + e) << 23);
-  factor[m] = __fmul_rn(*global, __int_as_float((127 - e) << 23));
-}
-
 // ------------------------------------------------------------ host side
 // Workspace: [status header][fp16 x][token multipliers][partials of cut
 // units][their counters and flags][staged weight rows]; for the gradient also
@@ -234,22 +183,23 @@ size_t glu_workspace_bytes(int64_t M, int64_t I, int64_t K, bool grad) {
 }
 
 template <int kAct, bool kGrad, bool kBf16>
-static cudaError_t glu_gemm(const GluArgs& ga, const CUtensorMap& tm_packed,
+static cudaError_t glu_gemm(const GluArgs& ga, bool staged, const CUtensorMap& tm_packed,
                             const CUtensorMap& tm_scales, const CUtensorMap& tm_x,
                             const GemmArgs& a, int grid, cudaStream_t stream) {
   GluEpilogue<kAct, kGrad, kBf16> epi;
   epi.half = ga.I;
+  epi.staged = staged;
   epi.a = ga;
   return a.BN <= 64 ? launch_gemm_with<3, 6, 3>(epi, tm_packed, tm_scales, tm_x, a, grid, stream)
                     : launch_gemm_with<2, 4, 2>(epi, tm_packed, tm_scales, tm_x, a, grid, stream);
 }
 
 template <int kAct, bool kGrad>
-static cudaError_t glu_gemm_typed(bool bf16, const GluArgs& ga, const CUtensorMap& tm_packed,
+static cudaError_t glu_gemm_typed(bool bf16, const GluArgs& ga, bool staged, const CUtensorMap& tm_packed,
                                   const CUtensorMap& tm_scales, const CUtensorMap& tm_x,
                                   const GemmArgs& a, int grid, cudaStream_t stream) {
-  return bf16 ? glu_gemm<kAct, kGrad, true>(ga, tm_packed, tm_scales, tm_x, a, grid, stream)
-              : glu_gemm<kAct, kGrad, false>(ga, tm_packed, tm_scales, tm_x, a, grid, stream);
+  return bf16 ? glu_gemm<kAct, kGrad, true>(ga, staged, tm_packed, tm_scales, tm_x, a, grid, stream)
+              : glu_gemm<kAct, kGrad, false>(ga, staged, tm_packed, tm_scales, tm_x, a, grid, stream);
 }
 
 // dh null: h to out.  dtype: h's or dh's; out_dtype: dx's.
@@ -262,8 +212,7 @@ nvfp4_status glu_launch(const void* x, int64_t M, int64_t K, const uint8_t* pack
   const bool grad = dh != nullptr;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const WeightStage wst = glu_stage(M, I, K, grad, sms);
-  if (stage_weights(wst, packed, scales, 2 * I, K, ws, stream) != cudaSuccess)
-    return NVFP4_ERR_CUDA;
+  const bool staged = wst.packed || wst.scales;
   CUtensorMap tm_packed, tm_scales, tm_x;
   if (!encode_weight_maps(&tm_packed, &tm_scales, wst, packed, scales, 2 * I, K, ws, kRows / 2))
     return NVFP4_ERR_CUDA;
@@ -280,22 +229,27 @@ nvfp4_status glu_launch(const void* x, int64_t M, int64_t K, const uint8_t* pack
     float* tok = reinterpret_cast<float*>(ws + L.tok);
     float* up2 = reinterpret_cast<float*>(ws + L.up2);
     float* factor = reinterpret_cast<float*>(ws + L.factor);
-    cudaError_t e = cudaSuccess;
-    if (grad) {
-      PdlLaunch l(dim3((unsigned)rows), dim3(256), 0, stream);
-      const uint16_t* x_bits = reinterpret_cast<const uint16_t*>(xs);
-      e = bf16 ? cudaLaunchKernelEx(&l.cfg, glu_scale_kernel<uint16_t>,
-                                    reinterpret_cast<const uint16_t*>(dhs), x_bits, I, K, global,
-                                    up2, factor)
-               : cudaLaunchKernelEx(&l.cfg, glu_scale_kernel<float>,
-                                    reinterpret_cast<const float*>(dhs), x_bits, I, K, global, up2,
-                                    factor);
-      if (e != cudaSuccess) return NVFP4_ERR_CUDA;
+    Prologue pro = {};
+    pro.x = reinterpret_cast<const uint16_t*>(xs);
+    pro.M = rows;
+    pro.K = K;
+    pro.m_rows = n_tt * L.BN;
+    pro.x16 = x16;
+    pro.tok_scale = tok;
+    pro.dh = dhs;
+    pro.n_dh = grad ? rows : 0;
+    pro.I = I;
+    pro.up2 = up2;
+    pro.factor = factor;
+    pro.grad_bf16 = bf16;
+    pro.global = global;
+    pro.flags = reinterpret_cast<uint32_t*>(ws + L.cnt);
+    pro.n_flags = L.n_flags;
+    if (m0 == 0) {
+      pro.status = reinterpret_cast<int32_t*>(ws);
+      prologue_weights(pro, wst, packed, scales, 2 * I, K, ws);
     }
-    e = prep_x_launch(xs, rows, K, n_tt * L.BN, global, x16, tok,
-                      m0 == 0 ? reinterpret_cast<int32_t*>(ws) : nullptr,
-                      reinterpret_cast<uint32_t*>(ws + L.cnt), L.n_flags,
-                      nullptr, stream);
+    cudaError_t e = prologue_launch(pro, stream);
     if (e != cudaSuccess) return NVFP4_ERR_CUDA;
     if (!encode_2d(&tm_x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x16, (uint64_t)K,
                    (uint64_t)(n_tt * L.BN), (uint64_t)K * 2, 64, (uint32_t)L.BN,
@@ -326,18 +280,18 @@ nvfp4_status glu_launch(const void* x, int64_t M, int64_t K, const uint8_t* pack
     ga.d16 = reinterpret_cast<__half*>(ws + L.d16);
     ga.stride = L.stride;
     if (act == NVFP4_ACT_SILU)
-      e = grad ? glu_gemm_typed<NVFP4_ACT_SILU, true>(bf16, ga, tm_packed, tm_scales, tm_x, a,
+      e = grad ? glu_gemm_typed<NVFP4_ACT_SILU, true>(bf16, ga, staged, tm_packed, tm_scales, tm_x, a,
                                                       L.grid, stream)
-               : glu_gemm_typed<NVFP4_ACT_SILU, false>(bf16, ga, tm_packed, tm_scales, tm_x, a,
+               : glu_gemm_typed<NVFP4_ACT_SILU, false>(bf16, ga, staged, tm_packed, tm_scales, tm_x, a,
                                                        L.grid, stream);
     else
-      e = grad ? glu_gemm_typed<NVFP4_ACT_GELU_TANH, true>(bf16, ga, tm_packed, tm_scales, tm_x, a,
+      e = grad ? glu_gemm_typed<NVFP4_ACT_GELU_TANH, true>(bf16, ga, staged, tm_packed, tm_scales, tm_x, a,
                                                            L.grid, stream)
-               : glu_gemm_typed<NVFP4_ACT_GELU_TANH, false>(bf16, ga, tm_packed, tm_scales, tm_x,
+               : glu_gemm_typed<NVFP4_ACT_GELU_TANH, false>(bf16, ga, staged, tm_packed, tm_scales, tm_x,
                                                             a, L.grid, stream);
     if (e == cudaSuccess && grad) {
       const BackCall c{rows, 2 * I, K, ga.d16, L.stride, packed, scales, &wst, factor,
-                       static_cast<uint8_t*>(out) + (size_t)m0 * K * out_size, out_dtype};
+                       static_cast<uint8_t*>(out) + (size_t)m0 * K * out_size, out_dtype, false};
       e = back_launch(c, L.back, ws, stream);
     }
     if (e != cudaSuccess) return NVFP4_ERR_CUDA;

@@ -74,8 +74,8 @@ __global__ void __launch_bounds__(256) w4a16_prep_x_kernel(const uint16_t* __res
   // the GEMM may launch now: it waits for this grid's results (griddepcontrol.wait)
   // only where it reads them, and streams the weights meanwhile
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (blockIdx.x == 0) {  // a fresh call: clear the status word (if given) and the split-K flags
-    if (threadIdx.x == 0 && status) *status = NVFP4_OK;
+  if (blockIdx.x == 0) {  // a fresh call: clear the status word and the split-K flags
+    if (threadIdx.x == 0) *status = NVFP4_OK;
     for (int i = threadIdx.x; i < n_split_flags; i += blockDim.x) split_flags[i] = 0;
   }
   __shared__ int32_t s_grp[kMaxGroups + 1];
@@ -185,8 +185,9 @@ cudaError_t stage_rows_launch(const uint8_t* src, int64_t rows, int64_t row_byte
 
 // Stage the weight rows that TMA cannot read in place (both copies are
 // no-ops for K % 256 == 0, the usual lm_head width).
-cudaError_t stage_weights(const WeightStage& w, const uint8_t* packed, const uint8_t* scales,
-                          int64_t rows, int64_t K, uint8_t* ws, cudaStream_t stream) {
+static cudaError_t stage_weights(const WeightStage& w, const uint8_t* packed,
+                                 const uint8_t* scales, int64_t rows, int64_t K, uint8_t* ws,
+                                 cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   if (w.packed)
     e = stage_rows_launch(packed, rows, K / 2, ws + w.packed_off, (int64_t)w.packed_stride, stream);
@@ -198,18 +199,6 @@ cudaError_t stage_weights(const WeightStage& w, const uint8_t* packed, const uin
 
 // Up to this many token rows the prep kernel gives each row a whole CTA.
 constexpr int64_t kPrepWideRows = 256;
-
-cudaError_t prep_x_launch(const void* x, int64_t M, int64_t K, int64_t m_rows, const float* global,
-                          __half* x16, float* tok_scale, int32_t* status, uint32_t* flags,
-                          int n_flags, unsigned long long* keys, cudaStream_t stream) {
-  const bool wide = M <= kPrepWideRows;
-  PdlLaunch l(dim3((unsigned)(wide ? m_rows : (m_rows + 7) / 8)), dim3(wide ? 128 : 256), 0,
-              stream);
-  return cudaLaunchKernelEx(&l.cfg, wide ? w4a16_prep_x_kernel<4> : w4a16_prep_x_kernel<1>,
-                            static_cast<const uint16_t*>(x), M, K, m_rows, global, x16, tok_scale,
-                            status, flags, n_flags, keys, (uint32_t*)nullptr, 0,
-                            (const int32_t*)nullptr, (const float*)nullptr, 0);
-}
 
 // ------------------------------------------------------------ host side
 size_t lm_head_workspace_bytes(int64_t M, int64_t N, int64_t K, bool argmax) {

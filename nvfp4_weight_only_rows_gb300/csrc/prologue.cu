@@ -1,0 +1,234 @@
+// prologue.cu -- the kernel before the first product of a training call.  Its
+// parts are independent and short (5 to 10 us each for a few hundred tokens),
+// so they run side by side as blocks of one grid: as kernels of their own,
+// each of which waits for the one before, they took 14 us of the 40 of a gated
+// block's gradient (203 tokens, I = K = 2880) and 11 of the 16 of a product
+// back (77 x 4099 x 1008).
+#include "prologue.cuh"
+
+namespace nvfp4 {
+
+constexpr int kProThreads = 256;
+constexpr int64_t kRowBlocks = 1024;  // up to so many tokens take a block each, more a warp each
+
+struct ProBlocks {
+  uint32_t x, dy, dh, codes, scales;  // first block of each part after x; `scales`: its end is the grid
+};
+
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) << 23); }
+
+// The exponent that takes a largest magnitude to [2^14, 2^15).
+__device__ __forceinline__ int row_exponent(float mx) {
+  return mx > 0.0f && mx <= 3.4028235e38f ? min(max(14 - ilogbf(mx), -126), 126) : 0;
+}
+
+template <bool kBlock>
+__device__ __forceinline__ float row_max(float v, float* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  if constexpr (kBlock) {
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int w = 1; w < kProThreads / 32; ++w) v = fmaxf(v, red[w]);
+  }
+  return v;
+}
+
+// A row of x by a block or a warp.
+template <bool kBlock>
+__device__ __forceinline__ void x_row(const Prologue& p, int64_t m, float* red) {
+  constexpr int kT = kBlock ? kProThreads : 32;
+  const int tid = threadIdx.x % kT;
+  if (p.keys && tid == 0) {
+    p.keys[m * kKeyStride] = 0ull;
+    p.keys[m * kKeyStride + 2] = 0ull;
+  }
+  uint4* to = reinterpret_cast<uint4*>(p.x16 + m * p.K);
+  const int64_t nv = p.K / 8;
+  if (m >= p.M) {
+    for (int64_t i = tid; i < nv; i += kT) to[i] = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  const uint4* from = reinterpret_cast<const uint4*>(p.x + m * p.K);
+  uint32_t mx = 0;  // bf16 magnitudes order as integers, Inf and NaN above
+#pragma unroll 2
+  for (int64_t i = tid; i < nv; i += kT) {
+    const uint4 v = from[i];
+    const uint32_t k = 0x7FFF7FFFu;
+    mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(v.x & k, v.y & k), __vmaxu2(v.z & k, v.w & k)));
+  }
+  // (as floats: a NaN's maximum with anything is the other, an Inf stays)
+  const uint32_t top = max(mx & 0xFFFFu, mx >> 16);
+  const float most = row_max<kBlock>(__uint_as_float(min(top, 0x7F80u) << 16), red);
+  const int e = row_exponent(most);
+  if (tid == 0) p.tok_scale[m] = __fmul_rn(*p.global, pow2(-e));
+  const float p2 = pow2(e);
+#pragma unroll 2
+  for (int64_t i = tid; i < nv; i += kT) {
+    const uint4 v = from[i];
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __half2 h = __floats2half2_rn(__fmul_rn(__uint_as_float(w[j] << 16), p2),
+                                          __fmul_rn(__uint_as_float(w[j] & 0xFFFF0000u), p2));
+      o[j] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    to[i] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+__device__ __forceinline__ float grad_value(const float* p) { return __ldg(p); }
+__device__ __forceinline__ float grad_value(const uint16_t* p) {
+  return __uint_as_float((uint32_t)__ldg(p) << 16);
+}
+
+// The largest magnitude of a row of gradients; Inf where it holds an Inf or NaN.
+template <typename T>
+__device__ __forceinline__ float grad_max(const T* row, int64_t n_values) {
+  float mx = 0.0f;
+#pragma unroll 8
+  for (int64_t n = threadIdx.x; n < n_values; n += kProThreads) {
+    const float a = fabsf(grad_value(row + n));
+    mx = a <= 3.4028235e38f ? fmaxf(mx, a) : __int_as_float(0x7F800000);
+  }
+  return mx;
+}
+
+// A token of dy: bf16 gradients keep every value down to 2^-28 of the largest;
+// fp32 ones are rounded to 11 bits, 2^-11 of themselves, where a bf16 result is
+// off by 2^-8 of itself.  A row with an Inf or NaN stays as it is.  The second
+// read finds the row in L2.
+template <typename T>
+__device__ __forceinline__ void dy_row(const Prologue& p, int64_t m, float* red) {
+  const T* row = static_cast<const T*>(p.dy) + m * p.N;
+  const int e = row_exponent(row_max<true>(grad_max(row, p.N), red));
+  if (threadIdx.x == 0) p.factor[m] = __fmul_rn(*p.global, pow2(-e));
+  const float p2 = pow2(e);
+  __half* to = p.d16 + m * p.dy_stride;
+#pragma unroll 4
+  for (int64_t n = 2 * (int64_t)threadIdx.x; n < p.N; n += 2 * kProThreads) {
+    const float a = grad_value(row + n);
+    const float b = n + 1 < p.N ? grad_value(row + n + 1) : 0.0f;
+    *reinterpret_cast<__half2*>(to + n) = __floats2half2_rn(a * p2, b * p2);
+  }
+}
+
+// A token of dh: the power of two for dg and du from the bound in glu.cu, and
+// its inverse times the weight's global scale.
+template <typename T>
+__device__ __forceinline__ void dh_row(const Prologue& p, int64_t m, float* red) {
+  const float mx = row_max<true>(grad_max(static_cast<const T*>(p.dh) + m * p.I, p.I), red);
+  float l1 = 0.0f;
+  const uint4* x = reinterpret_cast<const uint4*>(p.x + m * p.K);
+  for (int64_t k = threadIdx.x; k < p.K / 8; k += kProThreads) {
+    const uint4 w = __ldg(x + k);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      l1 += fabsf(__uint_as_float(u[j] << 16)) + fabsf(__uint_as_float(u[j] & 0xFFFF0000u));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, o);
+  __syncthreads();  // red is read
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = l1;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int w = 1; w < kProThreads / 32; ++w) l1 += red[w];
+  const float top = fabsf(*p.global) * 2688.0f;  // at least max|W13|
+  const float huge = 3.4028235e38f;
+  int e = 0;
+  // logarithms, each rounded up (and one for 1.13): the product itself may be out of range
+  // (at most 2^101 max|dh|, so that activations near 2^-126 meet no infinity)
+  if (mx > 0.0f && mx <= huge && l1 > 0.0f && l1 <= huge && top > 0.0f && top <= huge)
+    e = min(max(min(15 - (ilogbf(mx) + ilogbf(l1) + ilogbf(top) + 4), 100 - ilogbf(mx)), -126), 126);
+  p.up2[m] = pow2(e);
+  p.factor[m] = __fmul_rn(*p.global, pow2(-e));
+}
+
+// Rows of codes, 8-byte multiples, a warp a row.
+__device__ __forceinline__ void stage_codes(const Prologue& p, uint32_t block, uint32_t blocks) {
+  const int lane = threadIdx.x & 31;
+  const int64_t n = p.packed_bytes / 8;
+  for (int64_t r = (int64_t)block * (kProThreads / 32) + (threadIdx.x >> 5); r < p.w_rows;
+       r += (int64_t)blocks * (kProThreads / 32)) {
+    const uint2* from = reinterpret_cast<const uint2*>(p.packed + r * p.packed_bytes);
+    uint2* to = reinterpret_cast<uint2*>(p.packed_to + r * p.packed_stride);
+#pragma unroll 4
+    for (int64_t j = lane; j < n; j += 32) to[j] = __ldg(from + j);
+  }
+}
+
+// Rows of block scales, of any length, by 4 bytes of the copy: two aligned
+// words of the source, shifted (the copy's words behind a row's end are not
+// read by the TMA).
+__device__ __forceinline__ void stage_scales(const Prologue& p, uint32_t block, uint32_t blocks) {
+  const int64_t per = (p.scales_bytes + 3) / 4, total = p.w_rows * p.scales_bytes;
+  const uint32_t* from = reinterpret_cast<const uint32_t*>(p.scales);
+  for (int64_t i = (int64_t)block * kProThreads + threadIdx.x; i < p.w_rows * per;
+       i += (int64_t)blocks * kProThreads) {
+    const int64_t r = i / per, w = i - r * per;
+    const int64_t at = r * p.scales_bytes + 4 * w;
+    uint32_t v = 0;
+    if ((at & ~(int64_t)3) + 8 <= total) {
+      v = __funnelshift_r(__ldg(from + (at >> 2)), __ldg(from + (at >> 2) + 1), (at & 3) * 8);
+    } else {  // the end of the array: nothing is read past it
+      for (int b = 0; b < 4; ++b)
+        if (at + b < total) v |= (uint32_t)__ldg(p.scales + at + b) << (8 * b);
+    }
+    *reinterpret_cast<uint32_t*>(p.scales_to + r * p.scales_stride + 4 * w) = v;
+  }
+}
+
+__global__ void __launch_bounds__(kProThreads) train_prologue_kernel(const Prologue p,
+                                                                     const ProBlocks b) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ float red[kProThreads / 32];
+  const uint32_t at = blockIdx.x;
+  if (at == 0) {
+    if (threadIdx.x == 0 && p.status) *p.status = NVFP4_OK;
+    for (int i = threadIdx.x; i < p.n_flags; i += kProThreads) p.flags[i] = 0;
+  }
+  if (at < b.x) {
+    if (p.m_rows <= kRowBlocks) {
+      x_row<true>(p, at, red);
+    } else {
+      const int64_t m = (int64_t)at * (kProThreads / 32) + (threadIdx.x >> 5);
+      if (m < p.m_rows) x_row<false>(p, m, red);
+    }
+  } else if (at < b.dy) {
+    if (p.grad_bf16) dy_row<uint16_t>(p, at - b.x, red);
+    else dy_row<float>(p, at - b.x, red);
+  } else if (at < b.dh) {
+    if (p.grad_bf16) dh_row<uint16_t>(p, at - b.dy, red);
+    else dh_row<float>(p, at - b.dy, red);
+  } else if (at < b.codes) {
+    stage_codes(p, at - b.dh, b.codes - b.dh);
+  } else {
+    stage_scales(p, at - b.codes, b.scales - b.codes);
+  }
+}
+
+cudaError_t prologue_launch(const Prologue& p, cudaStream_t stream) {
+  const int sms = std::max(sm_count(), 1);
+  ProBlocks b;
+  const int64_t per = kProThreads / 32;
+  b.x = (uint32_t)(p.m_rows <= kRowBlocks ? p.m_rows : (p.m_rows + per - 1) / per);
+  b.dy = b.x + (uint32_t)p.n_dy;
+  b.dh = b.dy + (uint32_t)p.n_dh;
+  b.codes = b.dh + (p.packed_to ? (uint32_t)std::min<int64_t>((p.w_rows + per - 1) / per,
+                                                              (int64_t)sms * 6)
+                                : 0u);
+  const int64_t words = p.w_rows * ((p.scales_bytes + 3) / 4);
+  b.scales = b.codes + (p.scales_to ? (uint32_t)std::min<int64_t>(
+                                          (words + 4 * kProThreads - 1) / (4 * kProThreads),
+                                          (int64_t)sms * 4)
+                                    : 0u);
+  PdlLaunch l(dim3(std::max(b.scales, 1u)), dim3(kProThreads), 0, stream);
+  return cudaLaunchKernelEx(&l.cfg, train_prologue_kernel, p, b);
+}
+
+}  // namespace nvfp4

@@ -10,17 +10,6 @@
 
 namespace nvfp4 {
 
-// The rescaled activations of a product (lm_head.cu): x bf16 [M, K] to fp16
-// [m_rows, K] with an exact power of two per token, its inverse times
-// *global to tok_scale, the call's status word and counters cleared, and,
-// where keys are given, their lines.
-cudaError_t prep_x_launch(const void* x, int64_t M, int64_t K, int64_t m_rows, const float* global,
-                          __half* x16, float* tok_scale, int32_t* status, uint32_t* flags,
-                          int n_flags, unsigned long long* keys, cudaStream_t stream);
-// The copies of weight rows that TMA cannot read in place (lm_head.cu).
-cudaError_t stage_weights(const WeightStage& w, const uint8_t* packed, const uint8_t* scales,
-                          int64_t rows, int64_t K, uint8_t* ws, cudaStream_t stream);
-
 // The epilogue of kOut (epilogue_role).
 struct NoEpilogue {
   static constexpr bool kOwn = false, kPaired = false;
@@ -191,6 +180,8 @@ __global__ void __launch_bounds__((own_threads<E, kOut, kStages, kPStages, kDqPe
     // a weight tile read once (one token tile) is not kept in L2; one read
     // by several token tiles in a row is
     const uint64_t pol_once = policy_evict_first(), pol_reused = policy_evict_last();
+    if constexpr (E::kOwn)
+      if (own.staged) grid_dependency_wait();  // the weight rows come from the kernel before
     uint32_t issued = 0, piece = 0;
     for_each_piece(sc, n_kb_u, [&](const Piece& pc) {
       const UnitGeom geo = unit_geom<kGrouped>(p, sc, pc.u, piece++);
