@@ -96,13 +96,23 @@ struct EntropyEpilogue {
     int32_t* tgt = reinterpret_cast<int32_t*>(ref + kMaxBN);
     const uint32_t tile = u / (uint32_t)p.n_ttiles;
     const int64_t t0 = (int64_t)(u - tile * (uint32_t)p.n_ttiles) * p.BN;
-    for (int t = lane; t < p.BN; t += 32) {
-      const bool live = t0 + t < p.M;
-      mul[t] = live ? __ldcg(p.tok_scale + t0 + t) * kLog2e : 0.0f;
-      const uint32_t key = live ? __ldcg(ref_word(p, t0 + t)) : 0u;
-      ref[t] = key ? key_value(key) : (live ? kNoRef : 0.0f);
-      const int64_t want = live ? __ldg(a.targets + t0 + t) : -1;
-      tgt[t] = want >= 0 && want < p.N ? (int32_t)want : -1;
+    float scale[kMaxBN / 32];
+    uint32_t key[kMaxBN / 32];
+    int64_t want[kMaxBN / 32];
+#pragma unroll
+    for (int i = 0; i < kMaxBN / 32; ++i) {  // all loads in flight together
+      const int t = lane + 32 * i;
+      const bool live = t < p.BN && t0 + t < p.M;
+      scale[i] = live ? __ldcg(p.tok_scale + t0 + t) : 0.0f;
+      key[i] = live ? __ldcg(ref_word(p, t0 + t)) : order_key(0.0f);
+      want[i] = live ? __ldg(a.targets + t0 + t) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kMaxBN / 32; ++i) {
+      const int t = lane + 32 * i;
+      mul[t] = scale[i] * kLog2e;
+      ref[t] = key[i] ? key_value(key[i]) : kNoRef;
+      tgt[t] = want[i] >= 0 && want[i] < p.N ? (int32_t)want[i] : -1;
     }
     __syncwarp();
     return {t0, tile * kRows + (uint32_t)q * 32u};

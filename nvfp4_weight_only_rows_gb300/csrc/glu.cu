@@ -73,10 +73,18 @@ struct GluEpilogue {
     float* mul = reinterpret_cast<float*>(s);
     const uint32_t tile = u / (uint32_t)p.n_ttiles;
     const int64_t t0 = (int64_t)(u - tile * (uint32_t)p.n_ttiles) * p.BN;
-    for (int t = lane; t < p.BN; t += 32) {
-      const bool live = t0 + t < p.M;
-      mul[t] = live ? __ldcg(p.tok_scale + t0 + t) : 0.0f;
-      if (kGrad) mul[kMaxBN + t] = live ? __ldcg(a.up2 + t0 + t) : 0.0f;
+    float scale[kMaxBN / 32], up2[kMaxBN / 32];
+#pragma unroll
+    for (int i = 0; i < kMaxBN / 32; ++i) {  // all loads in flight together
+      const int t = lane + 32 * i;
+      const bool live = t < p.BN && t0 + t < p.M;
+      scale[i] = live ? __ldcg(p.tok_scale + t0 + t) : 0.0f;
+      up2[i] = kGrad && live ? __ldcg(a.up2 + t0 + t) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < kMaxBN / 32; ++i) {
+      mul[lane + 32 * i] = scale[i];
+      if (kGrad) mul[kMaxBN + lane + 32 * i] = up2[i];
     }
     __syncwarp();
     const int64_t i = (int64_t)tile * 64 + q * 16 + (lane & 15);

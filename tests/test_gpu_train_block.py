@@ -1,6 +1,8 @@
 """The training calls together, as a model's last layer and loss use them: a
 gated block, its down projection, the residual and the cross entropy over the
 lm_head, with the gradient through all of it."""
+import threading
+
 import pytest
 import torch
 
@@ -16,6 +18,26 @@ def _built():
 
     __graft_entry__.build()
     assert torch.cuda.is_available()
+
+
+@pytest.mark.parametrize("call", ["lm_head", "back", "glu", "glu_backward", "cross_entropy"])
+def test_first_call_of_a_thread(call):
+    """A thread that has made no CUDA call, as an autograd thread is at first."""
+    w, _ = weight(512, 256, seed=1)
+    x, dy = hidden(20, 256, seed=2), hidden(20, 512, seed=3)
+    t = torch.arange(20, device="cuda")
+    calls = {"lm_head": lambda: nv.w4a16_lm_head(x, *w), "back": lambda: nv.w4a16_lm_head_backward(dy, *w),
+             "glu": lambda: nv.w4a16_glu(x, *w),
+             "glu_backward": lambda: nv.w4a16_glu_backward(dy[:, :256].contiguous(), x, *w),
+             "cross_entropy": lambda: nv.w4a16_cross_entropy(x, *w, t, with_mean=True)[2]}
+    want = calls[call]()
+    torch.cuda.synchronize()
+    got = []
+    thread = threading.Thread(target=lambda: got.append(calls[call]()))
+    thread.start()
+    thread.join()
+    torch.cuda.synchronize()
+    assert got and torch.equal(got[0], want)
 
 
 @pytest.mark.parametrize("M", [1, 50, 300])
@@ -53,7 +75,7 @@ def test_block_and_loss(M, act):
     X = x.detach().double().requires_grad_(True)
     want = plain(X)
     (dX,) = torch.autograd.grad(want, X)
-    assert abs(float(value) - float(want)) <= 4 * 2.0 ** -8 * 3 ** 0.5 * abs(float(want))
+    assert abs(float(value.detach()) - float(want.detach())) <= 4 * 2.0 ** -8 * 3 ** 0.5 * abs(float(want.detach()))
     err = (dx.double() - dX).norm(dim=1) / dX.norm(dim=1)
     assert float(err.max()) <= 4 * 2.0 ** -8 * 7 ** 0.5
 
