@@ -736,7 +736,7 @@ size_t w4a16_cross_entropy_workspace_bytes(int64_t M, int64_t N, int64_t K, int 
  * Sums are fp32.  The loss keeps its relative accuracy where the target is
  * nearly certain: it is log(1 + the others' share), not a difference.  In
  * `mean` each probability is an fp16 number (off by 2^-11 of itself, or by
- * 2^-31 of the largest but the target's).  Results do not depend on the
+ * 2^-31 of the largest but the target's, or of that of a logit 2.7 where this is more).  Results do not depend on the
  * schedule.  A token whose x holds an Inf or NaN gets NaN, no other does.
  * A NaN block scale raises NVFP4_ERR_NONFINITE in the workspace status word.
  * Of probabilities, 512 MiB are held at a time: more tokens are worked on in

@@ -12,7 +12,7 @@
 //  1. train_prologue_kernel: x as fp16 (prologue.cu).
 //  2. w4a16_tc_kernel with EntropyEpilogue: the logits of 128 rows x up to 128
 //     tokens at a time in tensor memory; per token and 32 rows a reference
-//     r >= max y, one of .., -4, 4, 12, .., and s = sum 2^(y - r); for the
+//     r >= max y (mostly 12, or 20, 28, ..) and s = sum 2^(y - r); for the
 //     gradient also P = 2^(y - r) as fp16 in the workspace.
 //  3. entropy_rows_kernel: r and s joined per token, loss, lse, and P brought
 //     to the token's one reference where a group of rows used a lower one.
@@ -25,11 +25,11 @@
 // of the mantissa: the sums and P do not depend on the schedule.  (P is
 // rounded to 11 bits, then truncated where fp16 is subnormal, below 2^-29 of
 // the reference; truncations to coarser and coarser grids give the last one.)
-// In steps of 8 the reference seldom moves after the first wave of units: the
-// largest of 128256 normal logits is two above the largest of 2000.  In steps
-// of 1 it rose late for most tokens, in steps of 4 for those whose maximum
-// passed 8, as it does for logits of standard deviation 1.3: 84 of 106 us of
-// kernel 3 went into P (2048 tokens of 128256 rows).
+// One reference, 12 (8.3 nats), serves all maxima from -52 to 12, and above it
+// steps of 8 seldom move after the first waves of units, unless one row stands
+// out.  In steps of 1 the reference rose late for most tokens, in steps
+// of 4 for those whose maximum passed 8: 84 of 106 us of kernel 3 went into P
+// (2048 tokens of 128256 rows).
 //
 // The target's row is left out of r, s and P: where the model is sure of the
 // target, 1 - p_t and the pull of all other rows keep their relative accuracy
@@ -49,7 +49,7 @@ constexpr float kMagic = 12582912.0f;    // 1.5 * 2^23: x + it - it rounds |x| <
 constexpr float kMagicLimit = 2097152.0f;
 constexpr int kPBits = 15;               // P is stored times 2^15
 constexpr float kRefStep = 8.0f;         // references are these apart
-constexpr float kRefAt = 4.0f;           // and one of them
+constexpr float kHomeRef = 12.0f;        // and one of them
 
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -62,6 +62,13 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint16_t f16_canonical(float v) {
   const float r = __uint_as_float((__float_as_uint(v) + 0x1000u) & 0xFFFFE000u);
   return __half_as_ushort(__float2half_rz(r));
+}
+
+// The reference of a largest y: rounded up to one of .., -60, 12, 20, 28, ..,
+// where 12 serves all from -52 on (the others below are 8 apart again).
+__device__ __forceinline__ float reference(float y) {
+  const float r = kRefStep * ceilf((y - kHomeRef) * (1.0f / kRefStep)) + kHomeRef;
+  return y >= kHomeRef - 64.0f && r < kHomeRef ? kHomeRef : r;
 }
 
 // A token's reference word: the low half of its line (see WsLayout keys),
@@ -82,7 +89,7 @@ template <bool kGrad>
 struct EntropyEpilogue {
   static constexpr bool kOwn = true, kPaired = false;
   static constexpr int kFirstPart = 7, kNextPart = 5;  // stages of 256
-  static constexpr int kWarpBytes = 3 * kMaxBN * 4;  // multiplier, reference, target of a token
+  static constexpr int kInfoBytes = 3 * kMaxBN * 4;  // multiplier, reference, target of a token
   struct Unit {
     int64_t t0;
     uint32_t n_base;  // the warp's first row
@@ -90,12 +97,16 @@ struct EntropyEpilogue {
   EntropyArgs a;
   int staged;  // the weight is read from a copy in the workspace
 
-  __device__ Unit begin(const GemmArgs& p, uint32_t u, int q, int lane, uint8_t* s) const {
+  __device__ Unit unit(const GemmArgs& p, uint32_t u, int q, int) const {
+    const uint32_t tile = u / (uint32_t)p.n_ttiles;
+    return {(int64_t)(u - tile * (uint32_t)p.n_ttiles) * p.BN, tile * kRows + (uint32_t)q * 32u};
+  }
+
+  __device__ void info(const GemmArgs& p, uint32_t u, int lane, uint8_t* s) const {
     float* mul = reinterpret_cast<float*>(s);
     float* ref = mul + kMaxBN;
     int32_t* tgt = reinterpret_cast<int32_t*>(ref + kMaxBN);
-    const uint32_t tile = u / (uint32_t)p.n_ttiles;
-    const int64_t t0 = (int64_t)(u - tile * (uint32_t)p.n_ttiles) * p.BN;
+    const int64_t t0 = (int64_t)(u % (uint32_t)p.n_ttiles) * p.BN;
     float scale[kMaxBN / 32];
     uint32_t key[kMaxBN / 32];
     int64_t want[kMaxBN / 32];
@@ -104,24 +115,22 @@ struct EntropyEpilogue {
       const int t = lane + 32 * i;
       const bool live = t < p.BN && t0 + t < p.M;
       scale[i] = live ? __ldcg(p.tok_scale + t0 + t) : 0.0f;
-      key[i] = live ? __ldcg(ref_word(p, t0 + t)) : order_key(0.0f);
+      key[i] = live ? __ldcg(ref_word(p, t0 + t)) : 0u;
       want[i] = live ? __ldg(a.targets + t0 + t) : -1;
     }
 #pragma unroll
     for (int i = 0; i < kMaxBN / 32; ++i) {
       const int t = lane + 32 * i;
       mul[t] = scale[i] * kLog2e;
-      ref[t] = key[i] ? key_value(key[i]) : kNoRef;
+      ref[t] = key[i] ? key_value(key[i]) : (t0 + t < p.M ? kNoRef : 0.0f);
       tgt[t] = want[i] >= 0 && want[i] < p.N ? (int32_t)want[i] : -1;
     }
-    __syncwarp();
-    return {t0, tile * kRows + (uint32_t)q * 32u};
   }
 
   __device__ void chunk(const GemmArgs& p, const Unit& u, int c, const float (&v)[16], int lane,
-                        uint8_t* s) const {
+                        const uint8_t* s) const {
     if (u.n_base >= p.N) return;  // warp-uniform
-    float* ref = reinterpret_cast<float*>(s) + kMaxBN;
+    const float* ref = reinterpret_cast<const float*>(s) + kMaxBN;
     const int32_t* tgt = reinterpret_cast<const int32_t*>(ref + kMaxBN);
     const int64_t tc = u.t0 + c, live = p.M - tc;
     const float none = __int_as_float(0xFF800000);
@@ -155,26 +164,24 @@ struct EntropyEpilogue {
       }
     }
     lds_f32x16(ref + c, r);
+    const int mine = (lane >> 1) & 15;  // the token whose sum this lane ends with
+    float r_mine = ref[c + mine];
     bool above = false;
 #pragma unroll
     for (int t = 0; t < 16; ++t) above |= !(y[t] <= r[t]);
     if (__any_sync(0xFFFFFFFFu, above)) {  // a reference rises (or a NaN becomes one)
-      __syncwarp();
 #pragma unroll
       for (int t = 0; t < 16; ++t) {
         if (!__any_sync(0xFFFFFFFFu, !(y[t] <= r[t]))) continue;
         const float top = key_value(__reduce_max_sync(0xFFFFFFFFu, order_key(y[t])));
-        r[t] = kRefStep * ceilf((top - kRefAt) * (1.0f / kRefStep)) + kRefAt;
-        if (lane == 0) {
-          ref[c + t] = r[t];
-          if (t < live) atomicMax(ref_word(p, tc + t), order_key(r[t]));
-        }
+        r[t] = reference(top);
+        if (mine == t) r_mine = r[t];
+        if (lane == 0 && t < live) atomicMax(ref_word(p, tc + t), order_key(r[t]));
       }
-      __syncwarp();
     }
     // 2^(y - r + 15): y is at most r; below r - 140 nothing is left of it
     float2 e[8];
-    const bool far = __any_sync(0xFFFFFFFFu, !(fabsf(ref[c + (lane & 15)]) < kMagicLimit));
+    const bool far = __any_sync(0xFFFFFFFFu, !(fabsf(r_mine) < kMagicLimit));
     if (!far) {
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
@@ -221,9 +228,8 @@ struct EntropyEpilogue {
     float sum = (second ? e[0].y : e[0].x) +
                 __shfl_xor_sync(0xFFFFFFFFu, second ? e[0].x : e[0].y, 2);
     sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-    const int t = (lane >> 1) & 15;
-    if ((lane & 1) == 0 && t < live)
-      a.part[(int64_t)(u.n_base >> 5) * p.M + tc + t] = make_float2(ref[c + t], sum);
+    if ((lane & 1) == 0 && mine < live)
+      a.part[(int64_t)(u.n_base >> 5) * p.M + tc + mine] = make_float2(r_mine, sum);
   }
 };
 

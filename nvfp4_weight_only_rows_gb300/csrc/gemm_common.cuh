@@ -831,10 +831,12 @@ __device__ __forceinline__ void epilogue_role(const GemmArgs& p, const Sched& sc
   });
 }
 
-// The same walk for an epilogue of a call's own: E::begin per unit, before its
-// accumulator is ready (what the unit's tokens need, into the warp's E::kWarpBytes
-// of shared memory; it ends with a __syncwarp), E::chunk per 16 tokens of the
-// finished unit, a value of each for this lane's row.
+// The same walk for an epilogue of a call's own: E::unit for where a unit lies,
+// E::chunk per 16 tokens of the finished unit, a value of each for this lane's
+// row.  What a unit's tokens need lies in shared memory: another warp
+// (token_info_role) brings it a unit ahead into one of two buffers of
+// E::kInfoBytes, since three global loads and their latency, 3000 cycles at
+// the head of every unit, were a fifth of an epilogue-bound product's time.
 // E::kFirstPart, E::kNextPart: a unit's sum in parts, the first of up to
 // kFirstPart stages, the others of up to kNextPart (0: one part), each from
 // zero in an accumulator of its own, added here in fp32: in registers, and with
@@ -849,16 +851,20 @@ template <int kWarps, class E>
 __device__ __forceinline__ void walk_epilogue(const GemmArgs& p, const Sched& sc, const E& own,
                                               int warp, int epi, int lane, uint32_t tmem_base,
                                               uint64_t* d_full, uint64_t* d_empty,
-                                              const WaitCtl& wc, uint8_t* s_warp) {
+                                              uint64_t* i_full, uint64_t* i_empty,
+                                              const WaitCtl& wc, uint8_t* s_info) {
   grid_dependency_wait();  // what the units read, and the split flags, come from the kernel before
   const int BN = p.BN;
   const int q = warp & 3;
   constexpr int kStep = 4 * kWarps;         // tokens from one of the warp's chunks to the next
   const int c0 = (epi / 4) * 16;            // its first chunk
   const uint32_t lane_off = (uint32_t)(q * 32) << 16;
-  uint32_t i = 0;
+  uint32_t i = 0, n_unit = 0;
   for_each_piece(sc, (uint32_t)p.n_kb, [&](const Piece& pc) {
-    const typename E::Unit unit = own.begin(p, pc.u, q, lane, s_warp);
+    const typename E::Unit unit = own.unit(p, pc.u, q, lane);
+    const uint32_t slot_i = n_unit & 1u, iph = (n_unit >> 1) & 1u;
+    const uint8_t* info = s_info + slot_i * E::kInfoBytes;
+    ++n_unit;
     uint32_t buf = 0;
     auto next = [&]() {  // the next accumulator, when it is full
       buf = i & ((1u << p.dbuf_log2) - 1u);
@@ -909,6 +915,7 @@ __device__ __forceinline__ void walk_epilogue(const GemmArgs& p, const Sched& sc
       }
       drained();
     }
+    if (!warp_wait(&i_full[slot_i], iph, wc)) return false;
     // a unit cut by a range boundary, as in epilogue_role
     const bool whole = pc.kb0 == 0 && pc.kb1 == (uint32_t)p.n_kb;
     bool finish = true;
@@ -952,7 +959,7 @@ __device__ __forceinline__ void walk_epilogue(const GemmArgs& p, const Sched& sc
 #pragma unroll
         for (int t = 0; t < 16; ++t) val[t] = __fadd_rn(val[t], other[t]);
       }
-      own.chunk(p, unit, c, val, lane, s_warp);
+      own.chunk(p, unit, c, val, lane, info);
     }
     if (!finish) {
       __threadfence();  // the partial is visible before the flag
@@ -960,6 +967,26 @@ __device__ __forceinline__ void walk_epilogue(const GemmArgs& p, const Sched& sc
       if (lane == 0) atomicExch(p.split_ready + slot, 1u);
     }
     if constexpr (E::kFirstPart == 0) drained();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&i_empty[slot_i]);
+    return true;
+  });
+}
+
+// The warp that brings each unit's token information (E::info), a unit ahead.
+template <class E>
+__device__ __forceinline__ void token_info_role(const GemmArgs& p, const Sched& sc, const E& own,
+                                                int lane, uint64_t* i_full, uint64_t* i_empty,
+                                                const WaitCtl& wc, uint8_t* s_info) {
+  grid_dependency_wait();
+  uint32_t n_unit = 0;
+  for_each_piece(sc, (uint32_t)p.n_kb, [&](const Piece& pc) {
+    const uint32_t slot = n_unit & 1u, ph = (n_unit >> 1) & 1u;
+    ++n_unit;
+    if (!warp_wait(&i_empty[slot], ph ^ 1u, wc)) return false;
+    own.info(p, pc.u, lane, s_info + slot * E::kInfoBytes);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&i_full[slot]);
     return true;
   });
 }

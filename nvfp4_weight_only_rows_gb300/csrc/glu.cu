@@ -59,7 +59,7 @@ template <int kAct, bool kGrad, bool kBf16>
 struct GluEpilogue {
   static constexpr bool kOwn = true, kPaired = true;
   static constexpr int kFirstPart = 0, kNextPart = 0;
-  static constexpr int kWarpBytes = (kGrad ? 2 : 1) * kMaxBN * 4;
+  static constexpr int kInfoBytes = (kGrad ? 2 : 1) * kMaxBN * 4;
   int64_t half;  // rows from a gate to its up
   int staged;    // the weight is read from a copy in the workspace
   GluArgs a;
@@ -69,10 +69,16 @@ struct GluEpilogue {
     bool valid;
   };
 
-  __device__ Unit begin(const GemmArgs& p, uint32_t u, int q, int lane, uint8_t* s) const {
-    float* mul = reinterpret_cast<float*>(s);
+  __device__ Unit unit(const GemmArgs& p, uint32_t u, int q, int lane) const {
     const uint32_t tile = u / (uint32_t)p.n_ttiles;
     const int64_t t0 = (int64_t)(u - tile * (uint32_t)p.n_ttiles) * p.BN;
+    const int64_t i = (int64_t)tile * 64 + q * 16 + (lane & 15);
+    return {i, t0 + (lane & 16) / 2, i < a.I};
+  }
+
+  __device__ void info(const GemmArgs& p, uint32_t u, int lane, uint8_t* s) const {
+    float* mul = reinterpret_cast<float*>(s);
+    const int64_t t0 = (int64_t)(u % (uint32_t)p.n_ttiles) * p.BN;
     float scale[kMaxBN / 32], up2[kMaxBN / 32];
 #pragma unroll
     for (int i = 0; i < kMaxBN / 32; ++i) {  // all loads in flight together
@@ -86,9 +92,6 @@ struct GluEpilogue {
       mul[lane + 32 * i] = scale[i];
       if (kGrad) mul[kMaxBN + lane + 32 * i] = up2[i];
     }
-    __syncwarp();
-    const int64_t i = (int64_t)tile * 64 + q * 16 + (lane & 15);
-    return {i, t0 + (lane & 16) / 2, i < a.I};
   }
 
   __device__ void chunk(const GemmArgs& p, const Unit& u, int c, const float (&v)[16], int lane,

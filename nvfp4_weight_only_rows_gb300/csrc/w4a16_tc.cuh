@@ -111,6 +111,9 @@ __global__ void __launch_bounds__((own_threads<E, kOut, kStages, kPStages, kDqPe
   uint64_t* done_bar = d_empty + 4;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(tmem_slot + 1);
+  uint64_t* i_full = done_bar + 2;  // own epilogue: token information of a unit
+  uint64_t* i_empty = i_full + 2;
+  static_assert(2 * (kStages + kPStages) + 8 + 2 + 4 <= 32);
   float* s_tok = reinterpret_cast<float*>(bars + 32);  // 4 epilogue warps x kMaxBN multipliers
   // argmax: the "last CTA" flag, then per epilogue warp the thresholds of
   // its current unit's tokens (lower bounds of each token's largest logit)
@@ -143,6 +146,12 @@ __global__ void __launch_bounds__((own_threads<E, kOut, kStages, kPStages, kDqPe
       mbar_init(&d_empty[i], kEpiWarps);
     }
     mbar_init(done_bar, 1);
+    if constexpr (E::kOwn) {
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&i_full[i], 1);
+        mbar_init(&i_empty[i], kEpiWarps);
+      }
+    }
     *abort_flag = 0;
     if (kOut == kOutTopk) s_last[1] = 0;  // epilogue warps done (the region exists in this mode)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -316,7 +325,9 @@ __global__ void __launch_bounds__((own_threads<E, kOut, kStages, kPStages, kDqPe
     volatile int32_t zero = 0;
     drain.abort = &zero;
     mbar_wait(done_bar, 0, drain);
-  }  // (a warp 3 completes the first warpgroup)
+  } else if constexpr (E::kOwn) {  // warp 3
+    token_info_role(p, sc, own, lane, i_full, i_empty, wc, reinterpret_cast<uint8_t*>(s_tok));
+  }
   } else if (warp < kFirstEpiWarp) {
     if constexpr (E::kOwn) registers_down<88>();
     // ---------------- dequant: one thread per vocabulary row.  The kDqPerQuad
@@ -384,8 +395,7 @@ __global__ void __launch_bounds__((own_threads<E, kOut, kStages, kPStages, kDqPe
     if constexpr (E::kOwn) {
       registers_up<kEpiWarps == 8 ? 128 : 168>();
       walk_epilogue<kEpiWarps>(p, sc, own, warp, warp - kFirstEpiWarp, lane, tmem_base, d_full,
-                               d_empty, wc, reinterpret_cast<uint8_t*>(s_tok) +
-                                                (warp - kFirstEpiWarp) * E::kWarpBytes);
+                               d_empty, i_full, i_empty, wc, reinterpret_cast<uint8_t*>(s_tok));
     } else
       epilogue_role<kOut, false, kGrouped>(p, sc, warp, warp - kFirstEpiWarp, lane, tmem_base,
                                            d_full, d_empty, wc, s_tok, s_thr);
@@ -452,10 +462,9 @@ static cudaError_t launch_gemm_with(const E& own, const CUtensorMap& tm_packed,
   auto kern = w4a16_tc_kernel<NVFP4_OUT_F32, kStages, kPStages, kDq, false, E>;
   auto smem = [](int BN) {
     return 1024 + kPStages * (size_t)(kPackedStageBytes + kScaleStageBytes) +
-           kStages * (size_t)BN * kKB * 2 + 256 +
-           epi_warps<E, kStages>() * (size_t)E::kWarpBytes;
+           kStages * (size_t)BN * kKB * 2 + 256 + 2 * (size_t)E::kInfoBytes;
   };
-  static_assert(E::kWarpBytes % 16 == 0);
+  static_assert(E::kInfoBytes % 16 == 0);
   static std::atomic<uint64_t> limit_set{0};
   const cudaError_t err = smem_limit_once(limit_set, reinterpret_cast<const void*>(kern),
                                           smem(kStages >= 3 ? 64 : kMaxBN));
