@@ -97,7 +97,7 @@ struct EntropyEpilogue {
   EntropyArgs a;
   int staged;  // the weight is read from a copy in the workspace
 
-  __device__ Unit unit(const GemmArgs& p, uint32_t u, int q, int) const {
+  __device__ Unit unit(const GemmArgs& p, uint32_t u, int q, int, int) const {
     const uint32_t tile = u / (uint32_t)p.n_ttiles;
     return {(int64_t)(u - tile * (uint32_t)p.n_ttiles) * p.BN, tile * kRows + (uint32_t)q * 32u};
   }
@@ -127,8 +127,8 @@ struct EntropyEpilogue {
     }
   }
 
-  __device__ void chunk(const GemmArgs& p, const Unit& u, int c, const float (&v)[16], int lane,
-                        const uint8_t* s) const {
+  __device__ void chunk(const GemmArgs& p, const Unit& u, int c, int, const float (&v)[16],
+                        int lane, const uint8_t* s) const {
     if (u.n_base >= p.N) return;  // warp-uniform
     const float* ref = reinterpret_cast<const float*>(s) + kMaxBN;
     const int32_t* tgt = reinterpret_cast<const int32_t*>(ref + kMaxBN);

@@ -831,9 +831,10 @@ __device__ __forceinline__ void epilogue_role(const GemmArgs& p, const Sched& sc
   });
 }
 
-// The same walk for an epilogue of a call's own: E::unit for where a unit lies,
-// E::chunk per 16 tokens of the finished unit, a value of each for this lane's
-// row.  What a unit's tokens need lies in shared memory: another warp
+// The same walk for an epilogue of a call's own: E::unit for where a unit lies
+// (and loads for the warp's first chunk, which end while the products run),
+// E::chunk per 16 tokens c of the finished unit, a value of each for this
+// lane's row (and loads for the warp's next chunk, if that is below BN).  What a unit's tokens need lies in shared memory: another warp
 // (token_info_role) brings it a unit ahead into one of two buffers of
 // E::kInfoBytes, since three global loads and their latency, 3000 cycles at
 // the head of every unit, were a fifth of an epilogue-bound product's time.
@@ -861,7 +862,7 @@ __device__ __forceinline__ void walk_epilogue(const GemmArgs& p, const Sched& sc
   const uint32_t lane_off = (uint32_t)(q * 32) << 16;
   uint32_t i = 0, n_unit = 0;
   for_each_piece(sc, (uint32_t)p.n_kb, [&](const Piece& pc) {
-    const typename E::Unit unit = own.unit(p, pc.u, q, lane);
+    typename E::Unit unit = own.unit(p, pc.u, q, lane, c0);
     const uint32_t slot_i = n_unit & 1u, iph = (n_unit >> 1) & 1u;
     const uint8_t* info = s_info + slot_i * E::kInfoBytes;
     ++n_unit;
@@ -959,7 +960,7 @@ __device__ __forceinline__ void walk_epilogue(const GemmArgs& p, const Sched& sc
 #pragma unroll
         for (int t = 0; t < 16; ++t) val[t] = __fadd_rn(val[t], other[t]);
       }
-      own.chunk(p, unit, c, val, lane, info);
+      own.chunk(p, unit, c, c + kStep, val, lane, info);
     }
     if (!finish) {
       __threadfence();  // the partial is visible before the flag

@@ -67,13 +67,31 @@ struct GluEpilogue {
     int64_t i;     // column of h
     int64_t t;     // this lane's first token of a chunk
     bool valid;
+    float dh[kGrad ? 8 : 1];  // of the next chunk
   };
 
-  __device__ Unit unit(const GemmArgs& p, uint32_t u, int q, int lane) const {
+  // dh of this lane's eight tokens of a chunk
+  __device__ void load(const GemmArgs& p, Unit& u, int c) const {
+    const int64_t t0 = u.t + c, live = u.valid && c < p.BN ? p.M - t0 : 0;
+    const int64_t at = t0 * a.I + u.i;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      u.dh[j] = 0.0f;
+      if (j >= live) continue;
+      if constexpr (kBf16)
+        u.dh[j] = __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(a.dh) + at + j * a.I));
+      else
+        u.dh[j] = __ldg(static_cast<const float*>(a.dh) + at + j * a.I);
+    }
+  }
+
+  __device__ Unit unit(const GemmArgs& p, uint32_t u, int q, int lane, int c0) const {
     const uint32_t tile = u / (uint32_t)p.n_ttiles;
     const int64_t t0 = (int64_t)(u - tile * (uint32_t)p.n_ttiles) * p.BN;
     const int64_t i = (int64_t)tile * 64 + q * 16 + (lane & 15);
-    return {i, t0 + (lane & 16) / 2, i < a.I};
+    Unit r = {i, t0 + (lane & 16) / 2, i < a.I};
+    if constexpr (kGrad) load(p, r, c0);
+    return r;
   }
 
   __device__ void info(const GemmArgs& p, uint32_t u, int lane, uint8_t* s) const {
@@ -94,23 +112,16 @@ struct GluEpilogue {
     }
   }
 
-  __device__ void chunk(const GemmArgs& p, const Unit& u, int c, const float (&v)[16], int lane,
-                        const uint8_t* s) const {
+  __device__ void chunk(const GemmArgs& p, Unit& u, int c, int c_next, const float (&v)[16],
+                        int lane, const uint8_t* s) const {
     const bool up = (lane & 16) != 0;
     const int64_t t0 = u.t + c;
     const int64_t live = u.valid ? p.M - t0 : 0;
-    float dh[8];
+    float dh[kGrad ? 8 : 1];
     if constexpr (kGrad) {
-      const int64_t at = t0 * a.I + u.i;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        dh[j] = 0.0f;
-        if (j >= live) continue;
-        if constexpr (kBf16)
-          dh[j] = __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(a.dh) + at + j * a.I));
-        else
-          dh[j] = __ldg(static_cast<const float*>(a.dh) + at + j * a.I);
-      }
+      for (int j = 0; j < 8; ++j) dh[j] = u.dh[j];
+      load(p, u, c_next);
     }
     float mul[16];
     lds_f32x16(reinterpret_cast<const float*>(s) + c, mul);

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import nvfp4_weight_only_rows_gb300 as nv
+from tests._operators import dequant
 from tests._train import entropy_grad_reference, entropy_reference, hidden, stored, weight, within
 
 pytestmark = pytest.mark.gpu
@@ -109,6 +110,22 @@ def test_large_logits():
     z = (x.float() * 1e30).to(torch.bfloat16).double() @ W.T
     within(lse, z.amax(1), 1e-5 * z.abs().amax(1))
     assert bool(torch.isfinite(loss).all()) and bool(torch.isfinite(mean).all())
+
+
+@pytest.mark.parametrize("M", [5, 140])
+@pytest.mark.parametrize("low", [30, 36, 200, 3000])
+def test_logits_far_below_zero(M, low):
+    """Every logit around -low: below and above where one reference ends."""
+    N, K = 700, 256
+    rng = torch.Generator().manual_seed(low)
+    packed = torch.randint(0, 8, (N, K // 2), generator=rng) * 17  # two equal positive codes
+    scales = (40 + 400 * torch.rand(N, K // 16, generator=rng)).to(torch.float8_e4m3fn)
+    W = dequant(packed.to(torch.uint8), scales, torch.tensor(1e-4)).cuda()
+    w = packed.to(torch.uint8).cuda(), scales.cuda(), torch.tensor([1e-4]).cuda()
+    x = (-low / W.sum(1).mean() * (1 + 0.05 * torch.randn(M, K, generator=rng).cuda())).to(torch.bfloat16)
+    t = torch.randint(0, N, (M,), generator=rng).cuda()
+    t[1] = -1
+    check(x, t, w, W)
 
 
 @pytest.mark.parametrize("M", [12, 260])
