@@ -170,14 +170,21 @@ struct EntropyEpilogue {
 #pragma unroll
     for (int t = 0; t < 16; ++t) above |= !(y[t] <= r[t]);
     if (__any_sync(0xFFFFFFFFu, above)) {  // a reference rises (or a NaN becomes one)
+      uint32_t raised = 0;
 #pragma unroll
       for (int t = 0; t < 16; ++t) {
         if (!__any_sync(0xFFFFFFFFu, !(y[t] <= r[t]))) continue;
-        const float top = key_value(__reduce_max_sync(0xFFFFFFFFu, order_key(y[t])));
-        r[t] = reference(top);
+        // mostly from none to the home reference
+        if (!__any_sync(0xFFFFFFFFu, !(y[t] <= kHomeRef)) &&
+            __any_sync(0xFFFFFFFFu, y[t] >= kHomeRef - 64.0f))
+          r[t] = kHomeRef;
+        else
+          r[t] = reference(key_value(__reduce_max_sync(0xFFFFFFFFu, order_key(y[t]))));
+        raised |= 1u << t;
         if (mine == t) r_mine = r[t];
-        if (lane == 0 && t < live) atomicMax(ref_word(p, tc + t), order_key(r[t]));
       }
+      if ((lane & 1) == 0 && mine < live && ((raised >> mine) & 1u))
+        atomicMax(ref_word(p, tc + mine), order_key(r_mine));
     }
     // 2^(y - r + 15): y is at most r; below r - 140 nothing is left of it
     float2 e[8];
