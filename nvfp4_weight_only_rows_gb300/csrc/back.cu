@@ -521,10 +521,23 @@ static int best_splits(int64_t rest, int64_t stages, int tokens, int ctas, int w
   return best;
 }
 
+// Pairs of CTAs where their 256 x 256 tiles fill the SMs at least once and
+// cover no more than 6% beyond what 128 x 128 tiles cover.  Alone and at burst
+// clocks the two are level (28672 x 4096, 1536 tokens: 273 and 271 us; 2048
+// tokens, one and a half rounds of pairs: 378 and 344), below that single CTAs
+// win by up to half (4096 x 2880, 700 tokens: 30 and 18).  In a run of calls,
+// where power limits the clocks, pairs gain 3 to 6% (2048 tokens: 4096 x 14336
+// 178 -> 167 us, training on 128256 x 4096 3190 -> 3070 us).
+static bool use_pairs(int64_t M, int64_t K, int sms) {
+  const int64_t one = ((M + kMaxBN - 1) / kMaxBN) * ((K + kRows - 1) / kRows);
+  const int64_t two = ((M + 2 * kMaxBN - 1) / (2 * kMaxBN)) * ((K + 2 * kRows - 1) / (2 * kRows));
+  return M >= 2 * kMaxBN && two >= sms / 2 && 4 * two * 100 <= 106 * one;
+}
+
 BackLayout back_layout(int64_t M, int64_t N, int64_t K, int sms, size_t off) {
   BackLayout l;
   l.BN = lm_head_token_tile(M);
-  l.pair = M >= 256;
+  l.pair = use_pairs(M, K, sms);
   const int ctas = l.pair ? 2 : 1, tokens = l.BN * ctas;
   const int workers = std::max(1, sms / ctas);
   l.n_ttiles = (int)((M + tokens - 1) / tokens);

@@ -115,7 +115,7 @@ def glu_grad_reference(dh, x, W, glob, name):
 
 
 # ----------------------------------------------------------- cross entropy
-PART = 1536  # terms of a logit's sum that are added without a break
+PART = 1792  # terms of a logit's sum that are added without a break, at the most
 
 
 def entropy_reference(x, W, targets):

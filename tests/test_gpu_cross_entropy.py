@@ -57,11 +57,12 @@ def check(x, t, w, W, a=None, b=None, stream=None):
 
 
 # token tiles and pairs as in the product back; vocabularies around a unit of
-# 128, a group of 32 and a stage of 256 rows; sums of the logits in one part, in
-# two and in three (K above 1536)
+# 128, a group of 32 and a stage of 256 rows; sums of the logits in one part and
+# in several (K above 1792)
 SHAPES = [(1, 1, 16), (1, 2, 32), (1, 33, 256), (2, 128, 272), (5, 129, 48), (16, 300, 512),
           (17, 1000, 144), (49, 257, 1552), (64, 700, 272), (100, 95, 1024), (128, 513, 256),
-          (130, 2000, 1616), (256, 384, 144), (300, 1111, 528), (520, 4099, 272), (40, 800, 3328)]
+          (130, 2000, 1616), (256, 384, 144), (300, 1111, 528), (520, 4099, 272), (40, 800, 3328),
+          (512, 700, 9984)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
