@@ -85,8 +85,9 @@ struct EntropyArgs {
   int64_t stride;
 };
 
-template <bool kGrad>
+template <bool kGrad, int kWarps>
 struct EntropyEpilogue {
+  static constexpr int kWideWarps = kWarps;
   static constexpr bool kOwn = true, kPaired = false;
   static constexpr int kFirstPart = 7, kNextPart = 5;  // stages of 256
   static constexpr int kInfoBytes = 3 * kMaxBN * 4;  // multiplier, reference, target of a token
@@ -466,8 +467,8 @@ static EntropyLayout entropy_layout(int64_t M, int64_t N, int64_t K, bool grad, 
   l.P = l.part + align_up((size_t)((N + 31) / 32) * M * 8, 256);
   l.split_part = l.P + (grad ? align_up((size_t)m_pad * l.stride * 2, 256) : 0);
   l.cnt = l.split_part + align_up((size_t)l.grid * 4 * l.BN * 32 * 4, 256);
-  l.ready = l.cnt + align_up((size_t)l.grid * 8 * 4, 256);
-  l.end = l.ready + align_up((size_t)l.grid * 8 * 4, 256);
+  l.ready = l.cnt + align_up((size_t)l.grid * 16 * 4, 256);
+  l.end = l.ready + align_up((size_t)l.grid * 16 * 4, 256);
   l.n_flags = (int)((l.end - l.cnt) / 4);
   l.back = {};
   if (grad) {
@@ -554,10 +555,14 @@ static nvfp4_status entropy_run(const void* x, int64_t M, int64_t K, const uint8
     const EntropyArgs ea{targets + m0, reinterpret_cast<float*>(ws + L.y_t),
                          reinterpret_cast<float2*>(ws + L.part),
                          kGrad ? reinterpret_cast<__half*>(ws + L.P) : nullptr, L.stride};
-    const EntropyEpilogue<kGrad> epi{ea, wst.packed || wst.scales};
+    const int staged = wst.packed || wst.scales;
+    const EntropyEpilogue<kGrad, 8> few{ea, staged};
+    const EntropyEpilogue<kGrad, 16> many{ea, staged};
     cudaError_t e =
-        deep ? launch_gemm_with<3, 6, 3>(epi, tm_packed, tm_scales, tm_x, a, L.grid, stream)
-             : launch_gemm_with<2, 4, 2>(epi, tm_packed, tm_scales, tm_x, a, L.grid, stream);
+        deep ? launch_gemm_with<3, 6, 3>(few, tm_packed, tm_scales, tm_x, a, L.grid, stream)
+        : a.n_kb > kManyWarpStages
+            ? launch_gemm_with<2, 4, 2>(few, tm_packed, tm_scales, tm_x, a, L.grid, stream)
+            : launch_gemm_with<2, 4, 2>(many, tm_packed, tm_scales, tm_x, a, L.grid, stream);
     if (e != cudaSuccess) return NVFP4_ERR_CUDA;
     int tt_log2 = 0;
     while (tt_log2 < 3 && (rows >> (tt_log2 + 1)) >= sms) ++tt_log2;  // a CTA for every SM

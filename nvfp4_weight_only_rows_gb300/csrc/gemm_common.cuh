@@ -846,8 +846,8 @@ __device__ __forceinline__ void epilogue_role(const GemmArgs& p, const Sched& sc
 // tensor cores' sums drop the bits below fp32 at every
 // step, always towards zero, so the error of a long sum of one sign grows with
 // its steps; in parts it stays that of a part.
-// kWarps: 4, or 8, where two warps share a quadrant and take every other 16
-// tokens; `epi` is the warp's index among them.
+// kWarps: 4, or 8 or 16, where two or four warps share a quadrant and take 16
+// tokens in turn; `epi` is the warp's index among them.
 template <int kWarps, class E>
 __device__ __forceinline__ void walk_epilogue(const GemmArgs& p, const Sched& sc, const E& own,
                                               int warp, int epi, int lane, uint32_t tmem_base,
@@ -881,12 +881,13 @@ __device__ __forceinline__ void walk_epilogue(const GemmArgs& p, const Sched& sc
       if (lane == 0) mbar_arrive(&d_empty[buf]);
     };
     bool in_parts = false;
-    [[maybe_unused]] float acc[E::kFirstPart > 0 ? 4 : 1][16];  // at most 64 tokens a warp
+    constexpr int kChunks = kWarps == 16 ? 2 : 4;  // of a warp: 64 tokens' tiles have 4 warps
+    [[maybe_unused]] float acc[E::kFirstPart > 0 ? kChunks : 1][16];
     if constexpr (E::kFirstPart > 0) {
       for (uint32_t kb = pc.kb0 + E::kFirstPart; kb < pc.kb1; kb += E::kNextPart) {
         if (!next()) return false;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kChunks; ++j) {
           const int c = c0 + kStep * j;
           if (c >= BN) continue;
           uint32_t v[16];
@@ -904,7 +905,7 @@ __device__ __forceinline__ void walk_epilogue(const GemmArgs& p, const Sched& sc
     if constexpr (E::kFirstPart > 0) {
       // the last part, and the accumulator is free: what follows reads registers
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < kChunks; ++j) {
         const int c = c0 + kStep * j;
         if (c >= BN) continue;
         uint32_t v[16];
@@ -937,9 +938,8 @@ __device__ __forceinline__ void walk_epilogue(const GemmArgs& p, const Sched& sc
 #pragma unroll
         for (int t = 0; t < 16; ++t) {
           val[t] = acc[0][t];
-          acc[0][t] = acc[1][t];
-          acc[1][t] = acc[2][t];
-          acc[2][t] = acc[3][t];
+#pragma unroll
+          for (int j = 0; j + 1 < kChunks; ++j) acc[j][t] = acc[j + 1][t];
         }
       } else {
         uint32_t v[16];

@@ -55,8 +55,9 @@ struct GluArgs {
 };
 
 // kGrad: dg and du to d16 from dh; else h to out.  kBf16: dh's or h's type.
-template <int kAct, bool kGrad, bool kBf16>
+template <int kAct, bool kGrad, bool kBf16, int kWarps>
 struct GluEpilogue {
+  static constexpr int kWideWarps = kWarps;
   static constexpr bool kOwn = true, kPaired = true;
   static constexpr int kFirstPart = 0, kNextPart = 0;
   static constexpr int kInfoBytes = (kGrad ? 2 : 1) * kMaxBN * 4;
@@ -178,8 +179,8 @@ static GluLayout glu_layout(int64_t M, int64_t I, int64_t K, bool grad, int sms)
   l.d16 = l.factor + (grad ? align_up((size_t)M * 4, 256) : 0);
   l.split_part = l.d16 + (grad ? align_up((size_t)m_pad * l.stride * 2, 256) : 0);
   l.cnt = l.split_part + align_up((size_t)l.grid * 4 * l.BN * 32 * 4, 256);
-  l.ready = l.cnt + align_up((size_t)l.grid * 8 * 4, 256);
-  l.end = l.ready + align_up((size_t)l.grid * 8 * 4, 256);
+  l.ready = l.cnt + align_up((size_t)l.grid * 16 * 4, 256);
+  l.end = l.ready + align_up((size_t)l.grid * 16 * 4, 256);
   l.n_flags = (int)((l.end - l.cnt) / 4);
   l.back = {};
   if (grad) {
@@ -208,12 +209,19 @@ template <int kAct, bool kGrad, bool kBf16>
 static cudaError_t glu_gemm(const GluArgs& ga, bool staged, const CUtensorMap& tm_packed,
                             const CUtensorMap& tm_scales, const CUtensorMap& tm_x,
                             const GemmArgs& a, int grid, cudaStream_t stream) {
-  GluEpilogue<kAct, kGrad, kBf16> epi;
-  epi.half = ga.I;
-  epi.staged = staged;
-  epi.a = ga;
-  return a.BN <= 64 ? launch_gemm_with<3, 6, 3>(epi, tm_packed, tm_scales, tm_x, a, grid, stream)
-                    : launch_gemm_with<2, 4, 2>(epi, tm_packed, tm_scales, tm_x, a, grid, stream);
+  GluEpilogue<kAct, kGrad, kBf16, 8> few;
+  few.half = ga.I;
+  few.staged = staged;
+  few.a = ga;
+  if (a.BN <= 64)
+    return launch_gemm_with<3, 6, 3>(few, tm_packed, tm_scales, tm_x, a, grid, stream);
+  if constexpr (kGrad) {  // (forward, 8 warps are level with 16 for short sums, too)
+    if (a.n_kb <= kManyWarpStages) {
+      const GluEpilogue<kAct, kGrad, kBf16, 16> many{ga.I, staged, ga};
+      return launch_gemm_with<2, 4, 2>(many, tm_packed, tm_scales, tm_x, a, grid, stream);
+    }
+  }
+  return launch_gemm_with<2, 4, 2>(few, tm_packed, tm_scales, tm_x, a, grid, stream);
 }
 
 template <int kAct, bool kGrad>

@@ -13,6 +13,7 @@ namespace nvfp4 {
 // The epilogue of kOut (epilogue_role).
 struct NoEpilogue {
   static constexpr bool kOwn = false, kPaired = false;
+  static constexpr int kWideWarps = 4;
   static constexpr int kFirstPart = 0, kNextPart = 0;
 };
 
@@ -54,14 +55,26 @@ constexpr int gemm_threads() {
   return GemmShape<kStages, kPStages, kDq>::kThreads + (kOut == kOutTopk ? 32 : 0);
 }
 
-// With an epilogue of a call's own the 20 warps are whole warpgroups whose
-// registers are split by what they do: 96 a thread at launch, then 40 for the
-// warps that issue copies and MMAs, 88 for the dequant warps, the rest for the
-// epilogue.  That is two warpgroups of 128 for 128-token tiles, where it does
-// more than store (5 x 96 >= 40 + 2 x 88 + 2 x 128), one of 168 for the three
-// dequant warpgroups of small ones (40 + 3 x 88 + 168).
+// With an epilogue of a call's own the warps are whole warpgroups whose
+// registers are split by what they do: for 128-token tiles, where that epilogue
+// does more than store,
+//   8 epilogue warps:  96 a thread at launch, then 40 for the warps that issue
+//     copies and MMAs, 88 for dequant, 128 for the epilogue
+//     (5 x 96 >= 40 + 2 x 88 + 2 x 128);
+//   16 epilogue warps: 72 at launch, then 40, 72 and 80
+//     (7 x 72 >= 40 + 2 x 72 + 4 x 80);
+// and for small tiles, with three dequant warpgroups, 4 epilogue warps of 168
+// (5 x 96 >= 40 + 3 x 88 + 168).  An epilogue instruction takes its warp 4 to 5
+// cycles, so more warps are more of them, until they take the dequant warps'
+// turns: see kManyWarpStages.
 template <class E, int kStages>
-constexpr int epi_warps() { return E::kOwn && kStages < 3 ? 8 : 4; }
+constexpr int epi_warps() { return E::kOwn && kStages < 3 ? E::kWideWarps : 4; }
+
+// Sums of up to so many stages end before an epilogue of 8 warps is done, and
+// take 16.  1981 tokens of 66815 x 1040 (5 stages), logits' product of the
+// cross entropy with P: 395 us with 8, 303 with 16; 2048 tokens of 43776 x 4096
+// (16 stages) 465 and 470, the gated block of that size 283 and 290.
+constexpr int kManyWarpStages = 12;
 
 template <class E, int kOut, int kStages, int kPStages, int kDq>
 constexpr int own_threads() {
@@ -329,7 +342,7 @@ __global__ void __launch_bounds__((own_threads<E, kOut, kStages, kPStages, kDqPe
     token_info_role(p, sc, own, lane, i_full, i_empty, wc, reinterpret_cast<uint8_t*>(s_tok));
   }
   } else if (warp < kFirstEpiWarp) {
-    if constexpr (E::kOwn) registers_down<88>();
+    if constexpr (E::kOwn && kEpiWarps != 16) registers_down<88>();
     // ---------------- dequant: one thread per vocabulary row.  The kDqPerQuad
     // warps of a TMEM lane quadrant take the 256-k stages in turn: wait for
     // the packed stage, convert 64 k at a time into 32 registers and store
@@ -393,7 +406,7 @@ __global__ void __launch_bounds__((own_threads<E, kOut, kStages, kPStages, kDqPe
   } else if (warp < kFirstEpiWarp + kEpiWarps) {
     // ---------------- epilogue: one thread per vocabulary row, BN tokens
     if constexpr (E::kOwn) {
-      registers_up<kEpiWarps == 8 ? 128 : 168>();
+      registers_up<kEpiWarps == 16 ? 80 : kEpiWarps == 8 ? 128 : 168>();
       walk_epilogue<kEpiWarps>(p, sc, own, warp, warp - kFirstEpiWarp, lane, tmem_base, d_full,
                                d_empty, i_full, i_empty, wc, reinterpret_cast<uint8_t*>(s_tok));
     } else
