@@ -735,8 +735,9 @@ size_t w4a16_cross_entropy_workspace_bytes(int64_t M, int64_t N, int64_t K, int 
  *                256-byte aligned.
  * Sums are fp32.  The loss keeps its relative accuracy where the target is
  * nearly certain: it is log(1 + the others' share), not a difference.  In
- * `mean` each probability is an fp16 number (off by 2^-11 of itself, or by
- * 2^-31 of the largest but the target's, or of that of a logit 2.7 where this is more).  Results do not depend on the
+ * `mean` each probability is an fp16 number: off by 2^-11 of itself, or by
+ * 2^-31 of the largest but the target's (2^-23 of it where that one's logit
+ * lies between -2.8 and 2.8) if this is more.  Results do not depend on the
  * schedule.  A token whose x holds an Inf or NaN gets NaN, no other does.
  * A NaN block scale raises NVFP4_ERR_NONFINITE in the workspace status word.
  * Of probabilities, 512 MiB are held at a time: more tokens are worked on in
@@ -752,7 +753,8 @@ nvfp4_status w4a16_cross_entropy(const void *x, int64_t M, int64_t K, const uint
  * b of lse, with p = exp(-loss[m]):
  *   dx[m, :] = (a + b) mean[m, :] + (b p - a (1 - p)) W[t, :].
  * Where the target lies outside [0, N), a counts as 0 and the second term
- * falls away; a token with a + b = 0 reads no `mean`.
+ * falls away; a token with a + b = 0 reads no `mean`, and one with a = b = 0
+ * gets zeros whatever it holds.
  *   mean, targets, loss, packed, scales, global_scale, N, K  of the forward call.
  *   grad_loss    fp32 [M];  grad_lse fp32 [M], or NULL (zero).
  *   dx           [M, K], bf16 (NVFP4_OUT_BF16) or fp32, device, 16-byte aligned.

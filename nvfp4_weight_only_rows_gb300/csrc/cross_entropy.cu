@@ -25,9 +25,10 @@
 // of the mantissa: the sums and P do not depend on the schedule.  (P is
 // rounded to 11 bits, then truncated where fp16 is subnormal, below 2^-29 of
 // the reference; truncations to coarser and coarser grids give the last one.)
-// One reference, 12 (8.3 nats), serves all maxima from -52 to 12, and above it
-// steps of 8 seldom move after the first waves of units, unless one row stands
-// out.  In steps of 1 the reference rose late for most tokens, in steps
+// One reference, 12 (8.3 nats), serves all maxima from -4 to 12, where P keeps
+// 2^-23 of the largest, and outside steps of 8, which keep 2^-31 of it, seldom
+// move after the first waves of units, unless one row stands out.  (Served
+// down to -52, logits that are all near -30 left nothing of P.)  In steps of 1 the reference rose late for most tokens, in steps
 // of 4 for those whose maximum passed 8: 84 of 106 us of kernel 3 went into P
 // (2048 tokens of 128256 rows).
 //
@@ -49,7 +50,8 @@ constexpr float kMagic = 12582912.0f;    // 1.5 * 2^23: x + it - it rounds |x| <
 constexpr float kMagicLimit = 2097152.0f;
 constexpr int kPBits = 15;               // P is stored times 2^15
 constexpr float kRefStep = 8.0f;         // references are these apart
-constexpr float kHomeRef = 12.0f;        // and one of them
+constexpr float kHomeRef = 12.0f;        // and one of them,
+constexpr float kHomeSpan = 16.0f;       // which serves maxima so far below it
 
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -64,11 +66,10 @@ __device__ __forceinline__ uint16_t f16_canonical(float v) {
   return __half_as_ushort(__float2half_rz(r));
 }
 
-// The reference of a largest y: rounded up to one of .., -60, 12, 20, 28, ..,
-// where 12 serves all from -52 on (the others below are 8 apart again).
+// The reference of a largest y: rounded up to one of .., -12, -4, 12, 20, ..
 __device__ __forceinline__ float reference(float y) {
   const float r = kRefStep * ceilf((y - kHomeRef) * (1.0f / kRefStep)) + kHomeRef;
-  return y >= kHomeRef - 64.0f && r < kHomeRef ? kHomeRef : r;
+  return y > kHomeRef - kHomeSpan && r < kHomeRef ? kHomeRef : r;
 }
 
 // A token's reference word: the low half of its line (see WsLayout keys),
@@ -177,7 +178,7 @@ struct EntropyEpilogue {
         if (!__any_sync(0xFFFFFFFFu, !(y[t] <= r[t]))) continue;
         // mostly from none to the home reference
         if (!__any_sync(0xFFFFFFFFu, !(y[t] <= kHomeRef)) &&
-            __any_sync(0xFFFFFFFFu, y[t] >= kHomeRef - 64.0f))
+            __any_sync(0xFFFFFFFFu, y[t] > kHomeRef - kHomeSpan))
           r[t] = kHomeRef;
         else
           r[t] = reference(key_value(__reduce_max_sync(0xFFFFFFFFu, order_key(y[t]))));
@@ -390,9 +391,10 @@ __global__ void __launch_bounds__(256)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t m = blockIdx.x;
   const int64_t t = targets[m];
-  const bool has = t >= 0 && t < N;
-  const float a = has ? grad_loss[m] : 0.0f;
+  const float a = t >= 0 && t < N ? grad_loss[m] : 0.0f;
   const float b = grad_lse ? grad_lse[m] : 0.0f;
+  // a token that counts nowhere gets zeros whatever its hidden state holds
+  const bool has = t >= 0 && t < N && (a != 0.0f || b != 0.0f);
   const float others = has ? -expm1f(-loss[m]) : 0.0f;  // 1 - p_t
   const float fm = a + b;
   const float ft = has ? (b * (1.0f - others) - a * others) * *global : 0.0f;
@@ -402,7 +404,6 @@ __global__ void __launch_bounds__(256)
     float v[8];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      // a token that counts nowhere gets zeros whatever its hidden state holds
       const float4 f = fm == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
                                   : __ldg(reinterpret_cast<const float4*>(mean + m * K + k) + i);
       v[4 * i] = fm * f.x;

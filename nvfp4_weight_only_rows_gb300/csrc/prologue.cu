@@ -41,10 +41,7 @@ template <bool kBlock>
 __device__ __forceinline__ void x_row(const Prologue& p, int64_t m, float* red) {
   constexpr int kT = kBlock ? kProThreads : 32;
   const int tid = threadIdx.x % kT;
-  if (p.keys && tid == 0) {
-    p.keys[m * kKeyStride] = 0ull;
-    p.keys[m * kKeyStride + 2] = 0ull;
-  }
+  if (p.keys && tid == 0) p.keys[m * kKeyStride] = 0ull;
   uint4* to = reinterpret_cast<uint4*>(p.x16 + m * p.K);
   const int64_t nv = p.K / 8;
   if (m >= p.M) {

@@ -142,9 +142,9 @@ def entropy_reference(x, W, targets):
     pW = others @ W.abs()
     r["mean"] = others @ W
     # a probability is stored in steps of 2^-39 of 2^r, r at most 8 above the
-    # largest y but the target's, or 12 where that is more and y at least -52
+    # largest y but the target's, or 12 where that is more and y above -4
     y = torch.where(has[:, None], z.scatter(1, t, float("-inf")), z).amax(1) / math.log(2)
-    r_at_most = torch.where(y >= -52.0, (y + 8).clamp(min=12.0), y + 8)
+    r_at_most = torch.where(y >= -4.001, (y + 8).clamp(min=12.0), y + 8)
     step = 2.0 ** -39 * torch.exp2(r_at_most - lse / math.log(2))
     r["mean_tol"] = (2.0 ** -11 + 2 * top[:, None] + 2.0 ** -18 + sum_error(N)) * pW \
         + step[:, None] * W.abs().sum(0) \
