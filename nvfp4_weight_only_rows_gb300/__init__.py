@@ -4,8 +4,9 @@ Every step of the path runs in the CUDA kernels of ``libnvfp4_lm_head.so``
 (see ``include/nvfp4_lm_head.h``); this module only checks tensor metadata,
 allocates outputs and workspaces with PyTorch when the caller gives none,
 and passes device pointers plus the current CUDA stream through the C ABI:
-with ctypes, or, for the router, the expert layer and the log probabilities,
-whose kernels are shorter than that, in the compiled module ``_calls``.
+with ctypes, or, for the router, the expert layer, the log probabilities and
+the training calls, whose kernels can be shorter than that, in the compiled
+module ``_calls``.
 There is no CPU or PyTorch fallback: if the library is missing, every call
 raises.
 
@@ -43,6 +44,19 @@ Entry points (same names as the C ABI):
 * ``token_logprobs(logits, token_ids, k)`` -> ``(logprobs, entropy, lse, ranks,
   top_ids, top_logprobs)`` -- log probabilities of given tokens with the top
   alternatives; ``token_logprobs_backward`` -- their gradient.
+* ``w4a16_cross_entropy(x, packed, scales, global_scale, targets)`` -> ``(loss f32[M],
+  lse f32[M])`` -- softmax cross entropy over the lm_head's rows without the
+  logits; ``w4a16_cross_entropy_backward`` -- its gradient in x.
+* ``w4a16_glu(x, w13_packed, w13_scales, w13_global, activation)`` -> ``out[M, I]`` --
+  act(gate) * up in one product kernel; ``w4a16_glu_backward`` -- its gradient in x.
+* ``w4a16_lm_head_backward(grad_logits, packed, scales, global_scale)`` -> ``dx[M, K]``
+  -- the gradient of ``w4a16_lm_head`` in x.
+
+``w4a16_lm_head``, ``w4a16_cross_entropy``, ``w4a16_glu`` and ``token_logprobs`` give
+their results an autograd graph where the input requires a gradient; weights
+have none.  PyTorch ends the process when a backward pass is captured into a
+CUDA graph while an eager graph of the same leaves is alive: drop that one
+first, or capture the ``*_backward`` calls themselves.
 """
 from __future__ import annotations
 
