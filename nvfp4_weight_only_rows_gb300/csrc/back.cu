@@ -6,7 +6,7 @@
 // The contraction runs over the weight's rows, along which the packed codes
 // are not contiguous.  The MMA keeps the forward product's orientation, D[k,
 // token] = A . B^T with A = W^T in tensor memory, one lane per weight column,
-// and B = dy in shared memory, so each 256-row stage of 128 columns has to be
+// and B = dy in shared memory, so each stage of 256 rows and 128 columns has to be
 // turned as it is dequantized.  That costs no extra pass and no second copy of
 // the weight: `ldmatrix.trans` on 16-bit units of four codes hands each lane
 // the codes of rows n and n + 1 for four neighbouring columns; two byte
@@ -27,32 +27,37 @@
 
 namespace nvfp4 {
 
-constexpr uint32_t kBackPacked = 256 * 64;  // bytes: 256 rows x 128 columns of codes
-constexpr uint32_t kBackScales = 256 * 16;  // 256 rows x the 16 scales of 256 columns
+constexpr int kBackBars = 64;  // 8-byte words of shared memory for barriers and flags
 
-// Warps of the kernel: kDq a quadrant take the stages in turn, or kDq pairs of
-// warps, each half of a stage's rows.  kPair: two CTAs work on one tile of 256
+// Stages of kRowsOfStage rows.  Warps of the kernel: kDq a quadrant take the
+// stages in turn, or kDq pairs of warps, each half of a stage's rows; a pair's
+// one accumulator is drained by eight.  kPair: two CTAs work on one tile of 256
 // columns x 256 tokens, each on 128 of its columns with half of the tokens'
 // dy in shared memory: a stage then brings 84 KB into an SM for twice the
 // MMAs.
-template <int kStages_, int kPStages_, int kDq_, int kHalves_, bool kPair_>
+template <int kRowsOfStage_, int kStages_, int kPStages_, int kDq_, int kHalves_, int kEpiWarps_,
+          bool kPair_>
 struct BackShape {
+  static constexpr int kRowsOfStage = kRowsOfStage_;
+  static constexpr uint32_t kPacked = kRowsOfStage * 64;  // bytes: codes of 128 columns
+  static constexpr uint32_t kScales = kRowsOfStage * 16;  // the 16 scales of 256 columns
   static constexpr int kStages = kStages_, kPStages = kPStages_, kDq = kDq_, kHalves = kHalves_;
   static constexpr bool kPair = kPair_;
   static_assert(kStages % kDq == 0 && kPStages % kDq == 0,
                 "dequant warps per quadrant must divide every ring depth they wait on");
   static constexpr int kCtas = kPair ? 2 : 1;
   static constexpr int kDqWarps = 4 * kDq * kHalves;
-  static constexpr int kEpiWarps = kPair ? 8 : 4;  // a pair's one accumulator is drained quickly
+  static constexpr int kEpiWarps = kEpiWarps_;
+  static_assert(2 * kPStages + 3 * kStages + 8 + 2 <= kBackBars);
   static constexpr int kFirstEpiWarp = kFirstDqWarp + kDqWarps;
   static constexpr int kThreads = 32 * (kFirstEpiWarp + kEpiWarps);
-  static constexpr int kRowsOfWarp = kKB / kHalves;
+  static constexpr int kRowsOfWarp = kRowsOfStage / kHalves;
   // a warp's scales: 2 column groups x its rows, fp16
   static constexpr uint32_t kScratch = 2 * kRowsOfWarp * 2;
   static constexpr int kMaxTokens = kCtas * kMaxBN;  // of a tile
   static size_t smem_bytes(int BN) {
-    return 1024 + kPStages * (size_t)(kBackPacked + kBackScales) + kStages * (size_t)BN * kKB * 2 +
-           kDqWarps * (size_t)kScratch + 256 + kEpiWarps * (size_t)kMaxTokens * 4;
+    return 1024 + kPStages * (size_t)(kPacked + kScales) + kStages * (size_t)BN * kRowsOfStage * 2 +
+           kDqWarps * (size_t)kScratch + kBackBars * 8 + kEpiWarps * (size_t)kMaxTokens * 4;
   }
 };
 
@@ -196,6 +201,7 @@ __global__ void __launch_bounds__(Shape::kThreads, 1)
                       const BackArgs b) {
   constexpr int kStages = Shape::kStages, kPStages = Shape::kPStages;
   constexpr int kDq = Shape::kDq, kHalves = Shape::kHalves;
+  constexpr int kRowsOfStage = Shape::kRowsOfStage;
   constexpr bool kPair = Shape::kPair;
   constexpr int kFirstEpiWarp = Shape::kFirstEpiWarp;
   extern __shared__ uint8_t smem_raw[];
@@ -204,11 +210,11 @@ __global__ void __launch_bounds__(Shape::kThreads, 1)
   const int BN = p.BN;  // tokens of this CTA's dy
   const uint32_t rank = blockIdx.x % Shape::kCtas;
   const uint32_t box_bytes = (uint32_t)BN * 128;
-  const uint32_t d_stage_bytes = (kKB / 64) * box_bytes;
+  const uint32_t d_stage_bytes = (kRowsOfStage / 64) * box_bytes;
   uint8_t* s_packed = smem;
-  uint8_t* s_d = s_packed + kPStages * kBackPacked;
+  uint8_t* s_d = s_packed + kPStages * Shape::kPacked;
   uint8_t* s_scales = s_d + kStages * d_stage_bytes;
-  uint8_t* s_scratch = s_scales + kPStages * kBackScales;
+  uint8_t* s_scratch = s_scales + kPStages * Shape::kScales;
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_scratch + Shape::kDqWarps * Shape::kScratch);
   uint64_t* p_full = bars;
   uint64_t* p_empty = p_full + kPStages;
@@ -220,7 +226,7 @@ __global__ void __launch_bounds__(Shape::kThreads, 1)
   uint64_t* done_bar = peer_full + kStages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(tmem_slot + 1);
-  float* s_fac = reinterpret_cast<float*>(bars + 32);  // of a tile's tokens, per epilogue warp
+  float* s_fac = reinterpret_cast<float*>(bars + kBackBars);  // of a tile's tokens, per epilogue warp
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -268,11 +274,11 @@ __global__ void __launch_bounds__(Shape::kThreads, 1)
         const uint32_t st = issued % kPStages, ph = (issued / kPStages) & 1;
         if (!warp_wait(&p_empty[st], ph ^ 1, wc)) return false;
         if (elect_one()) {
-          const int32_t n0 = (int32_t)(kb * kKB);
-          mbar_arrive_expect_tx(&p_full[st], kBackPacked + kBackScales);
-          tma_load_2d(s_packed + st * kBackPacked, &tm_packed, (int32_t)pc.ft * (kRows / 2), n0,
+          const int32_t n0 = (int32_t)(kb * kRowsOfStage);
+          mbar_arrive_expect_tx(&p_full[st], Shape::kPacked + Shape::kScales);
+          tma_load_2d(s_packed + st * Shape::kPacked, &tm_packed, (int32_t)pc.ft * (kRows / 2), n0,
                       &p_full[st]);
-          tma_load_2d(s_scales + st * kBackScales, &tm_scales, (int32_t)(pc.ft / 2) * 16, n0,
+          tma_load_2d(s_scales + st * Shape::kScales, &tm_scales, (int32_t)(pc.ft / 2) * 16, n0,
                       &p_full[st]);
         }
         __syncwarp();
@@ -288,11 +294,11 @@ __global__ void __launch_bounds__(Shape::kThreads, 1)
         const uint32_t st = issued % kStages, ph = (issued / kStages) & 1;
         if (!warp_wait(&s_empty[st], ph ^ 1, wc)) return false;
         if (elect_one()) {
-          const int32_t n0 = (int32_t)(kb * kKB);
+          const int32_t n0 = (int32_t)(kb * kRowsOfStage);
           mbar_arrive_expect_tx(&s_full[st], d_stage_bytes);
           uint8_t* dst = s_d + st * d_stage_bytes;
 #pragma unroll
-          for (int x = 0; x < kKB / 64; ++x)
+          for (int x = 0; x < kRowsOfStage / 64; ++x)
             tma_load_2d(dst + x * box_bytes, &tm_d, n0 + 64 * x, (int32_t)pc.t0 + (int32_t)rank * BN, &s_full[st]);
         }
         __syncwarp();
@@ -338,10 +344,10 @@ __global__ void __launch_bounds__(Shape::kThreads, 1)
             if (!warp_wait<true>(&peer_full[st], ph, wc)) return false;
           tc_fence_after();
           const uint64_t bdesc = desc0 + ((st * d_stage_bytes) >> 4);
-          const uint32_t a_t = tmem_a + st * (kKB / 2);
+          const uint32_t a_t = tmem_a + st * (kRowsOfStage / 2);
           if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < kKB / 16; ++kk) {
+            for (int kk = 0; kk < kRowsOfStage / 16; ++kk) {
               const uint64_t bd = bdesc + (kk >> 2) * box_desc + 2 * (kk & 3);
               const uint32_t add = (kb != pc.kb0) || (kk != 0);
               if constexpr (kPair) tc_mma_ts_pair(d_tmem, a_t + kk * 8, bd, idesc, add);
@@ -383,7 +389,7 @@ __global__ void __launch_bounds__(Shape::kThreads, 1)
         const uint32_t ps = g % kPStages, pph = (g / kPStages) & 1;
         const uint32_t st = g % kStages, ph = (g / kStages) & 1;
         if (!warp_wait(&p_full[ps], pph, wc)) return false;
-        const uint8_t* srow = s_scales + ps * kBackScales + (row0 + lane) * 16 + (pc.ft & 1) * 8 + q * 2;
+        const uint8_t* srow = s_scales + ps * Shape::kScales + (row0 + lane) * 16 + (pc.ft & 1) * 8 + q * 2;
 #pragma unroll
         for (int i = 0; i < Shape::kRowsOfWarp / 32; ++i) {
           const uint32_t two = *reinterpret_cast<const uint16_t*>(srow + i * 512);
@@ -394,8 +400,8 @@ __global__ void __launch_bounds__(Shape::kThreads, 1)
           *reinterpret_cast<uint16_t*>(put + i * 64 + Shape::kScratch / 2) = (uint16_t)(f >> 16);
         }
         __syncwarp();
-        const uint32_t codes = smem_u32(s_packed + ps * kBackPacked) + swz;
-        const uint32_t ta = tmem_a + lane_off + st * (kKB / 2) + row0 / 2;
+        const uint32_t codes = smem_u32(s_packed + ps * Shape::kPacked) + swz;
+        const uint32_t ta = tmem_a + lane_off + st * (kRowsOfStage / 2) + row0 / 2;
 #pragma unroll
         for (int c4 = 0; c4 < Shape::kRowsOfWarp / 64; ++c4) {
           uint32_t lo[16], hi[16];  // TMEM lanes 0-15 and 16-31 of the quadrant
@@ -496,16 +502,34 @@ __global__ void __launch_bounds__(256) back_join_kernel(const BackArgs b, int64_
 // ------------------------------------------------------------ host side
 // Token tiles up to this take deep rings; longer ones would not fit them.
 constexpr int kBackDeepBN = 48;
-using BackDeep = BackShape<3, 6, 3, 1, false>;
-using BackFull = BackShape<2, 4, 2, 2, false>;
-using BackPairs = BackShape<2, 4, 2, 1, true>;
+using BackDeep = BackShape<256, 3, 6, 3, 1, 4, false>;
+using BackFull = BackShape<256, 2, 4, 2, 2, 4, false>;
+using BackFine = BackShape<128, 4, 6, 2, 2, 4, false>;
+using BackPairs = BackShape<256, 2, 4, 2, 1, 8, true>;
+
+static_assert(BackDeep::kRowsOfStage == BackFull::kRowsOfStage);
+static int rows_of_stage(const BackLayout& l) {
+  return l.pair ? BackPairs::kRowsOfStage
+         : l.fine ? BackFine::kRowsOfStage
+                  : BackFull::kRowsOfStage;
+}
+
+// Stages of half as many rows, so that each part of shared memory is free for
+// the next load earlier: where dy and the weight together take more than about
+// 40% of L2, and loads come from farther away (kernel, 4096 columns: 20000 rows,
+// 600 tokens 85 -> 76 us, 28672 rows, 1024 tokens 196 -> 176; below, the handoffs
+// cost more than that gains: 14336 columns x 4096 rows, 600 tokens 52 -> 54).
+static bool use_fine(int64_t M, int64_t N, int64_t K, int BN) {
+  return BN >= 96 && 2 * M * N + N * K / 16 * 9 >= ((int64_t)52 << 20);
+}
 
 // How the tiles past the last full round of the SMs are split: the number of
-// parts with the least time by this model, in us: a stage 0.55 (128 tokens) to
+// parts with the least time by this model, in us: 256 rows 0.55 (128 tokens) to
 // 0.3, 1 for a part's start and end, its sums written and read again at 4
 // TB/s, 3 for the kernel that joins them.  `tokens` and `ctas` of a tile.
-static int best_splits(int64_t rest, int64_t stages, int tokens, int ctas, int workers) {
-  const double stage = std::max(0.3, 0.55 * tokens / kMaxBN);
+static int best_splits(int64_t rest, int64_t stages, int tokens, int ctas, int workers,
+                       int stage_rows) {
+  const double stage = std::max(0.3, 0.55 * tokens / kMaxBN) * stage_rows / 256.0;
   int best = 1;
   double least = 0.0;
   for (int64_t s = 1; s <= std::min<int64_t>(stages, 64); ++s) {
@@ -542,10 +566,12 @@ BackLayout back_layout(int64_t M, int64_t N, int64_t K, int sms, size_t off) {
   const int workers = std::max(1, sms / ctas);
   l.n_ttiles = (int)((M + tokens - 1) / tokens);
   const int64_t tiles = (K + kRows * ctas - 1) / (kRows * ctas) * l.n_ttiles;
-  l.n_kb = (int)((N + kKB - 1) / kKB);
+  l.fine = !l.pair && use_fine(M, N, K, l.BN);
+  const int stage_rows = rows_of_stage(l);
+  l.n_kb = (int)((N + stage_rows - 1) / stage_rows);
   l.n_whole = tiles / workers * workers;
   l.n_rest = tiles - l.n_whole;
-  l.n_splits = l.n_rest ? best_splits(l.n_rest, l.n_kb, tokens, ctas, workers) : 1;
+  l.n_splits = l.n_rest ? best_splits(l.n_rest, l.n_kb, tokens, ctas, workers, stage_rows) : 1;
   if (l.n_splits == 1) {
     l.n_whole = tiles;
     l.n_rest = 0;
@@ -583,13 +609,14 @@ static cudaError_t back_gemm(const CUtensorMap& tm_packed, const CUtensorMap& tm
 
 cudaError_t back_launch(const BackCall& c, const BackLayout& L, uint8_t* ws, cudaStream_t stream) {
   const WeightStage& w = *c.stage;
+  const uint32_t stage_rows = (uint32_t)rows_of_stage(L);
   CUtensorMap tm_packed, tm_scales, tm_d;
   if (!encode_2d(&tm_packed, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.packed ? ws + w.packed_off : c.packed,
                  (uint64_t)c.K / 2, (uint64_t)c.N, w.packed ? w.packed_stride : (uint64_t)c.K / 2,
-                 kRows / 2, kKB, CU_TENSOR_MAP_SWIZZLE_64B) ||
+                 kRows / 2, stage_rows, CU_TENSOR_MAP_SWIZZLE_64B) ||
       !encode_2d(&tm_scales, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.scales ? ws + w.scales_off : c.scales,
                  (uint64_t)c.K / 16, (uint64_t)c.N, w.scales ? w.scales_stride : (uint64_t)c.K / 16,
-                 16, kKB, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+                 16, stage_rows, CU_TENSOR_MAP_SWIZZLE_NONE) ||
       !encode_2d(&tm_d, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, c.d, (uint64_t)c.N, (uint64_t)((c.M + L.BN - 1) / L.BN * L.BN),
                  (uint64_t)c.d_stride * 2, 64, (uint32_t)L.BN, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
@@ -602,7 +629,11 @@ cudaError_t back_launch(const BackCall& c, const BackLayout& L, uint8_t* ws, cud
   a.n_kb = L.n_kb;
   a.status = reinterpret_cast<int32_t*>(ws);
   const bool deep = L.BN <= kBackDeepBN;
-  const int a_cols = (deep ? BackDeep::kStages : BackFull::kStages) * (kKB / 2);
+  const int stages = L.pair ? BackPairs::kStages
+                     : deep ? BackDeep::kStages
+                     : L.fine ? BackFine::kStages
+                              : BackFull::kStages;
+  const int a_cols = stages * (int)(stage_rows / 2);
   const int ctas = L.pair ? 2 : 1, tokens = L.BN * ctas;
   a.dbuf_log2 = L.pair ? 0u : (4 * tokens + a_cols <= 512) ? 2u : 1u;
   a.tmem_cols = ((tokens << a.dbuf_log2) + a_cols <= 256) ? 256u : 512u;
@@ -619,7 +650,8 @@ cudaError_t back_launch(const BackCall& c, const BackLayout& L, uint8_t* ws, cud
   const cudaError_t e =
       L.pair ? back_gemm<BackPairs>(tm_packed, tm_scales, tm_d, a, b, L.grid, kMaxBN, stream)
       : deep ? back_gemm<BackDeep>(tm_packed, tm_scales, tm_d, a, b, L.grid, kBackDeepBN, stream)
-             : back_gemm<BackFull>(tm_packed, tm_scales, tm_d, a, b, L.grid, kMaxBN, stream);
+      : L.fine ? back_gemm<BackFine>(tm_packed, tm_scales, tm_d, a, b, L.grid, kMaxBN, stream)
+               : back_gemm<BackFull>(tm_packed, tm_scales, tm_d, a, b, L.grid, kMaxBN, stream);
   if (e != cudaSuccess || L.n_rest == 0) return e;
   PdlLaunch l(dim3((unsigned)(L.n_rest * ctas * (tokens / 8))), dim3(256), 0, stream);
   return cudaLaunchKernelEx(&l.cfg, back_join_kernel, b, c.M, c.K, tokens, L.n_ttiles, ctas);

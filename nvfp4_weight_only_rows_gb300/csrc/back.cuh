@@ -16,7 +16,7 @@ struct BackLayout {
   size_t part, total;
   int64_t n_whole, n_rest;
   int grid, BN, n_ttiles, n_splits, n_kb;
-  bool pair;
+  bool pair, fine;  // pairs of CTAs; stages of 128 rows
 };
 BackLayout back_layout(int64_t M, int64_t N, int64_t K, int sms, size_t off);
 

@@ -265,11 +265,14 @@ __device__ __forceinline__ uint32_t scale_down(uint32_t h, float f) {
 constexpr int kJoinThreads = 512;
 
 // A CTA takes TT (a power of two) neighbouring tokens, a thread every
-// (512 / TT)-th group of one of them.
+// (512 / TT)-th group of one of them.  For the gradient `splits` CTAs do so for
+// the same tokens and each brings its part of P to their references (37 tokens
+// of 50257 rows: 20.8 us with one, 15.8 with four; 600 tokens, with a CTA for
+// every SM anyway: 20.6 and 23.9).
 template <bool kGrad>
 __global__ void __launch_bounds__(kJoinThreads)
     entropy_rows_kernel(const float2* __restrict__ part, int64_t M, int64_t N, int tt_log2,
-                        const int64_t* __restrict__ targets, const float* __restrict__ y_t,
+                        int splits, const int64_t* __restrict__ targets, const float* __restrict__ y_t,
                         const float* __restrict__ global, float* __restrict__ loss,
                         float* __restrict__ lse, float* __restrict__ factor, __half* P,
                         int64_t stride) {
@@ -278,7 +281,8 @@ __global__ void __launch_bounds__(kJoinThreads)
   __shared__ float2 s_part[kJoinThreads];
   const int TT = 1 << tt_log2;
   const int slices = kJoinThreads >> tt_log2;
-  const int64_t m = (int64_t)blockIdx.x * TT + (threadIdx.x & (TT - 1));
+  const uint32_t tile = blockIdx.x / (uint32_t)splits, split = blockIdx.x % (uint32_t)splits;
+  const int64_t m = (int64_t)tile * TT + (threadIdx.x & (TT - 1));
   const int slice = threadIdx.x >> tt_log2;
   const int64_t groups = (N + 31) / 32;
   float2 acc = make_float2(kNoRef, 0.0f);
@@ -302,7 +306,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   __syncthreads();
   const float2 all = s_part[threadIdx.x & (TT - 1)];
   const float r = all.x;
-  if (slice == 0 && m < M) {
+  if (slice == 0 && split == 0 && m < M) {
     const float L = all.y * (1.0f / (1 << kPBits));  // the others' sum over 2^r
     const float log2L = log2f(L);
     const int64_t t = targets[m];
@@ -333,11 +337,13 @@ __global__ void __launch_bounds__(kJoinThreads)
   // the groups below their token's reference: a warp finds those of its 32
   // (group, token) places, then takes them in eights, four lanes each
   const int lane = threadIdx.x & 31;
-  for (int64_t g0 = slice; g0 - slice < groups; g0 += 8 * slices) {  // (the warp's count of steps)
+  const int64_t per = (groups + splits - 1) / splits, first = split * per;
+  const int64_t end = min(groups, first + per);
+  for (int64_t g0 = first + slice; g0 - slice < end; g0 += 8 * slices) {  // (the warp's count of steps)
     float rg[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      rg[i] = m < M && g0 + i * slices < groups ? __ldcg(&part[(g0 + i * slices) * M + m].x) : r;
+      rg[i] = m < M && g0 + i * slices < end ? __ldcg(&part[(g0 + i * slices) * M + m].x) : r;
 #pragma unroll 1
     for (int i = 0; i < 8; ++i) {
       const int64_t g = g0 + i * slices;
@@ -567,10 +573,11 @@ static nvfp4_status entropy_run(const void* x, int64_t M, int64_t K, const uint8
     if (e != cudaSuccess) return NVFP4_ERR_CUDA;
     int tt_log2 = 0;
     while (tt_log2 < 3 && (rows >> (tt_log2 + 1)) >= sms) ++tt_log2;  // a CTA for every SM
-    PdlLaunch l(dim3((unsigned)((rows + (1 << tt_log2) - 1) >> tt_log2)), dim3(kJoinThreads), 0,
-                stream);
+    const int64_t tiles = (rows + (1 << tt_log2) - 1) >> tt_log2;
+    const int splits = kGrad ? (int)std::max<int64_t>(1, std::min<int64_t>(8, sms / tiles)) : 1;
+    PdlLaunch l(dim3((unsigned)(tiles * splits)), dim3(kJoinThreads), 0, stream);
     e = cudaLaunchKernelEx(&l.cfg, entropy_rows_kernel<kGrad>, (const float2*)ea.part, rows, N,
-                           tt_log2, ea.targets, (const float*)ea.y_t, global, loss + m0, lse + m0,
+                           tt_log2, splits, ea.targets, (const float*)ea.y_t, global, loss + m0, lse + m0,
                            factor, ea.P, L.stride);
     if (e == cudaSuccess && kGrad) {
       const BackCall c{rows, N, K, ea.P, L.stride, packed, scales, &wst, factor, mean + m0 * K,

@@ -32,14 +32,16 @@ def check(dy, w, W, **kw):
 
 
 # token tiles 16 .. 48 (deep rings), 64 .. 128, pairs of CTAs where 256 x 256
-# tiles fill 76 of them (the last three, with and without tiles that are split);
+# tiles fill 76 of them (three, with and without tiles that are split);
 # weight rows around a stage of 256; columns around tiles of 128 and pairs of
-# 256, staged rows where K % 256 != 0
+# 256, staged rows where K % 256 != 0; the last two: stages of 128 rows, where
+# gradient and weight are large
 SHAPES = [(1, 1, 16), (1, 700, 48), (3, 255, 144), (16, 256, 128), (17, 257, 256), (33, 1000, 272),
           (48, 64, 1024), (49, 513, 400), (64, 2000, 512), (100, 31, 96), (127, 300, 640),
           (128, 256, 256), (129, 4099, 1008), (255, 77, 128), (256, 511, 384), (257, 1500, 512),
           (300, 640, 2064), (700, 2049, 272),
-          (512, 300, 9728), (500, 1111, 10000), (1000, 300, 5120)]
+          (512, 300, 9728), (500, 1111, 10000), (1000, 300, 5120),
+          (700, 40001, 272), (99, 100_100, 640)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
