@@ -43,6 +43,8 @@ struct BackShape {
   static constexpr uint32_t kScales = kRowsOfStage * 16;  // the 16 scales of 256 columns
   static constexpr int kStages = kStages_, kPStages = kPStages_, kDq = kDq_, kHalves = kHalves_;
   static constexpr bool kPair = kPair_;
+  // else a set of warps could be a whole turn of a ring ahead of the others, and
+  // a barrier's parity would stand for another phase than the one it waits for
   static_assert(kStages % kDq == 0 && kPStages % kDq == 0,
                 "dequant warps per quadrant must divide every ring depth they wait on");
   static constexpr int kCtas = kPair ? 2 : 1;
