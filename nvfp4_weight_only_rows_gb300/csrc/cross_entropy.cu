@@ -172,18 +172,29 @@ struct EntropyEpilogue {
 #pragma unroll
     for (int t = 0; t < 16; ++t) above |= !(y[t] <= r[t]);
     if (__any_sync(0xFFFFFFFFu, above)) {  // a reference rises (or a NaN becomes one)
-      uint32_t raised = 0;
+      // tokens (bits) that rise; low half: that pass the home reference, high
+      // half: that it would serve
+      uint32_t raised = 0, home = 0;
 #pragma unroll
       for (int t = 0; t < 16; ++t) {
-        if (!__any_sync(0xFFFFFFFFu, !(y[t] <= r[t]))) continue;
-        // mostly from none to the home reference
-        if (!__any_sync(0xFFFFFFFFu, !(y[t] <= kHomeRef)) &&
-            __any_sync(0xFFFFFFFFu, y[t] > kHomeRef - kHomeSpan))
-          r[t] = kHomeRef;
-        else
+        raised |= (!(y[t] <= r[t]) ? 1u : 0u) << t;
+        home |= (!(y[t] <= kHomeRef) ? 1u : 0u) << t;
+        home |= (y[t] > kHomeRef - kHomeSpan ? 1u : 0u) << (16 + t);
+      }
+      raised = __reduce_or_sync(0xFFFFFFFFu, raised);
+      home = __reduce_or_sync(0xFFFFFFFFu, home);
+      const uint32_t first = raised & ~home & (home >> 16);  // mostly from none to home
+      const uint32_t rest = raised & ~first;
+#pragma unroll
+      for (int t = 0; t < 16; ++t) r[t] = (first >> t) & 1u ? kHomeRef : r[t];
+      if ((first >> mine) & 1u) r_mine = kHomeRef;
+      if (rest) {
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+          if (!((rest >> t) & 1u)) continue;
           r[t] = reference(key_value(__reduce_max_sync(0xFFFFFFFFu, order_key(y[t]))));
-        raised |= 1u << t;
-        if (mine == t) r_mine = r[t];
+          if (mine == t) r_mine = r[t];
+        }
       }
       if ((lane & 1) == 0 && mine < live && ((raised >> mine) & 1u))
         atomicMax(ref_word(p, tc + mine), order_key(r_mine));
@@ -555,7 +566,8 @@ static nvfp4_status entropy_run(const void* x, int64_t M, int64_t K, const uint8
     a.split_ready = reinterpret_cast<uint32_t*>(ws + L.ready);
     a.split_part = reinterpret_cast<float*>(ws + L.split_part);
     a.am_keys = keys;
-    const bool deep = L.BN <= 64;
+    const bool brief = a.n_kb <= kManyWarpStages;
+    const bool deep = L.BN <= kDeepTokens;
     const int stages = deep ? 3 : 2;
     a.dbuf_log2 = (4 * L.BN + stages * (kKB / 2) <= 512) ? 2u : 1u;
     a.tmem_cols = ((L.BN << a.dbuf_log2) + stages * (kKB / 2) <= 256) ? 256u : 512u;
@@ -567,9 +579,8 @@ static nvfp4_status entropy_run(const void* x, int64_t M, int64_t K, const uint8
     const EntropyEpilogue<kGrad, 16> many{ea, staged};
     cudaError_t e =
         deep ? launch_gemm_with<3, 6, 3>(few, tm_packed, tm_scales, tm_x, a, L.grid, stream)
-        : a.n_kb > kManyWarpStages
-            ? launch_gemm_with<2, 4, 2>(few, tm_packed, tm_scales, tm_x, a, L.grid, stream)
-            : launch_gemm_with<2, 4, 2>(many, tm_packed, tm_scales, tm_x, a, L.grid, stream);
+        : brief ? launch_gemm_with<2, 4, 2>(many, tm_packed, tm_scales, tm_x, a, L.grid, stream)
+                : launch_gemm_with<2, 4, 2>(few, tm_packed, tm_scales, tm_x, a, L.grid, stream);
     if (e != cudaSuccess) return NVFP4_ERR_CUDA;
     int tt_log2 = 0;
     while (tt_log2 < 3 && (rows >> (tt_log2 + 1)) >= sms) ++tt_log2;  // a CTA for every SM

@@ -213,7 +213,7 @@ static cudaError_t glu_gemm(const GluArgs& ga, bool staged, const CUtensorMap& t
   few.half = ga.I;
   few.staged = staged;
   few.a = ga;
-  if (a.BN <= 64)
+  if (a.BN <= kDeepTokens)
     return launch_gemm_with<3, 6, 3>(few, tm_packed, tm_scales, tm_x, a, grid, stream);
   if constexpr (kGrad) {  // (forward, 8 warps are level with 16 for short sums, too)
     if (a.n_kb <= kManyWarpStages) {
@@ -299,7 +299,7 @@ nvfp4_status glu_launch(const void* x, int64_t M, int64_t K, const uint8_t* pack
     a.split_cnt = reinterpret_cast<uint32_t*>(ws + L.cnt);
     a.split_ready = reinterpret_cast<uint32_t*>(ws + L.ready);
     a.split_part = reinterpret_cast<float*>(ws + L.split_part);
-    const int stages = L.BN <= 64 ? 3 : 2;
+    const int stages = L.BN <= kDeepTokens ? 3 : 2;
     a.dbuf_log2 = (4 * L.BN + stages * (kKB / 2) <= 512) ? 2u : 1u;
     a.tmem_cols = ((L.BN << a.dbuf_log2) + stages * (kKB / 2) <= 256) ? 256u : 512u;
     GluArgs ga = {};

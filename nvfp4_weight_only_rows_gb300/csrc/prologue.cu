@@ -9,7 +9,9 @@
 namespace nvfp4 {
 
 constexpr int kProThreads = 256;
-constexpr int64_t kRowBlocks = 1024;  // up to so many tokens take a block each, more a warp each
+// Up to so many tokens take a block each, more a warp each (2048 x 4096: 7.7 us by
+// blocks, 11.2 by warps).
+constexpr int64_t kRowBlocks = 16384;
 
 struct ProBlocks {
   uint32_t x, dy, dh, codes, scales;  // first block of each part after x; `scales`: its end is the grid
@@ -82,16 +84,66 @@ __device__ __forceinline__ float grad_value(const uint16_t* p) {
   return __uint_as_float((uint32_t)__ldg(p) << 16);
 }
 
+// Magnitudes order as integers, Inf and NaN above all others.
+__device__ __forceinline__ uint32_t top_word(uint32_t top, uint32_t v, float) {
+  return max(top, v & 0x7FFFFFFFu);
+}
+__device__ __forceinline__ uint32_t top_word(uint32_t top, uint32_t v, uint16_t) {
+  return __vmaxu2(top, v & 0x7FFF7FFFu);
+}
+__device__ __forceinline__ float top_value(uint32_t top, float) {
+  return __uint_as_float(min(top, 0x7F800000u));
+}
+__device__ __forceinline__ float top_value(uint32_t top, uint16_t) {
+  return __uint_as_float(min(max(top & 0xFFFFu, top >> 16), 0x7F80u) << 16);
+}
+
+// Whether rows of n values are read in 16 bytes.
+template <typename T>
+__device__ __forceinline__ bool wide_rows(int64_t n) {
+  return n % (int64_t)(16 / sizeof(T)) == 0;
+}
+
 // The largest magnitude of a row of gradients; Inf where it holds an Inf or NaN.
 template <typename T>
 __device__ __forceinline__ float grad_max(const T* row, int64_t n_values) {
-  float mx = 0.0f;
+  uint32_t top = 0;
+  if (wide_rows<T>(n_values)) {
+    const uint4* v = reinterpret_cast<const uint4*>(row);
+#pragma unroll 4
+    for (int64_t i = threadIdx.x; i < n_values / (int64_t)(16 / sizeof(T)); i += kProThreads) {
+      const uint4 w = __ldg(v + i);
+      top = top_word(top_word(top, w.x, T()), w.y, T());
+      top = top_word(top_word(top, w.z, T()), w.w, T());
+    }
+  } else {
 #pragma unroll 8
-  for (int64_t n = threadIdx.x; n < n_values; n += kProThreads) {
-    const float a = fabsf(grad_value(row + n));
-    mx = a <= 3.4028235e38f ? fmaxf(mx, a) : __int_as_float(0x7F800000);
+    for (int64_t n = threadIdx.x; n < n_values; n += kProThreads)
+      top = top_word(top, __float_as_uint(grad_value(row + n)), 0.0f);
+    return top_value(top, 0.0f);
   }
-  return mx;
+  return top_value(top, T());
+}
+
+// Eight gradients from 16-byte loads.
+__device__ __forceinline__ void grad_eight(const uint16_t* p, float (&v)[8]) {
+  const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = __uint_as_float(u[j] << 16);
+    v[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void grad_eight(const float* p, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const float4 w = __ldg(reinterpret_cast<const float4*>(p) + j);
+    v[4 * j] = w.x;
+    v[4 * j + 1] = w.y;
+    v[4 * j + 2] = w.z;
+    v[4 * j + 3] = w.w;
+  }
 }
 
 // A token of dy: bf16 gradients keep every value down to 2^-28 of the largest;
@@ -105,6 +157,21 @@ __device__ __forceinline__ void dy_row(const Prologue& p, int64_t m, float* red)
   if (threadIdx.x == 0) p.factor[m] = __fmul_rn(*p.global, pow2(-e));
   const float p2 = pow2(e);
   __half* to = p.d16 + m * p.dy_stride;
+  if (p.N % 8 == 0) {
+#pragma unroll 2
+    for (int64_t n = 8 * (int64_t)threadIdx.x; n < p.N; n += 8 * kProThreads) {
+      float v[8];
+      grad_eight(row + n, v);
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const __half2 h = __floats2half2_rn(v[2 * j] * p2, v[2 * j + 1] * p2);
+        o[j] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      *reinterpret_cast<uint4*>(to + n) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    return;
+  }
 #pragma unroll 4
   for (int64_t n = 2 * (int64_t)threadIdx.x; n < p.N; n += 2 * kProThreads) {
     const float a = grad_value(row + n);
@@ -179,7 +246,8 @@ __device__ __forceinline__ void stage_scales(const Prologue& p, uint32_t block, 
   }
 }
 
-__global__ void __launch_bounds__(kProThreads) train_prologue_kernel(const Prologue p,
+// (Eight blocks an SM: 2048 gradient rows of 14336 19.8 us, 21.4 with six.)
+__global__ void __launch_bounds__(kProThreads, 8) train_prologue_kernel(const Prologue p,
                                                                      const ProBlocks b) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -76,6 +76,13 @@ constexpr int epi_warps() { return E::kOwn && kStages < 3 ? E::kWideWarps : 4; }
 // (16 stages) 465 and 470, the gated block of that size 283 and 290.
 constexpr int kManyWarpStages = 12;
 
+// Token tiles up to this take the deep rings and 4 epilogue warps.  One chunk of
+// 16 tokens a unit needs no more; from two on more warps gain more than rings do:
+// training calls of 37 tokens, 50257 x 1040 63 -> 52 us, 50257 x 4096 87 -> 80,
+// the gated block's gradient of 64 tokens, 14336 x 4096 55 -> 50 (at most 0.5 us is
+// lost, where a gated block of 2880 x 5120 takes 15).
+constexpr int kDeepTokens = 16;
+
 template <class E, int kOut, int kStages, int kPStages, int kDq>
 constexpr int own_threads() {
   return E::kOwn ? 32 * (4 + 4 * kDq + epi_warps<E, kStages>())
@@ -480,7 +487,7 @@ static cudaError_t launch_gemm_with(const E& own, const CUtensorMap& tm_packed,
   static_assert(E::kInfoBytes % 16 == 0);
   static std::atomic<uint64_t> limit_set{0};
   const cudaError_t err = smem_limit_once(limit_set, reinterpret_cast<const void*>(kern),
-                                          smem(kStages >= 3 ? 64 : kMaxBN));
+                                          smem(kStages >= 3 ? kDeepTokens : kMaxBN));
   if (err != cudaSuccess) return err;
   PdlLaunch l(dim3((unsigned)grid), dim3(own_threads<E, NVFP4_OUT_F32, kStages, kPStages, kDq>()),
               smem(a.BN), stream);
