@@ -526,12 +526,13 @@ static bool use_fine(int64_t M, int64_t N, int64_t K, int BN) {
 }
 
 // How the tiles past the last full round of the SMs are split: the number of
-// parts with the least time by this model, in us: 256 rows 0.55 (128 tokens) to
-// 0.3, 1 for a part's start and end, its sums written and read again at 4
+// parts with the least time by this model, in us: 256 rows 0.85, for a pair 1.7, with
+// deep rings 0.45, 1 for a part's start and end, its sums written and read again at 4
 // TB/s, 3 for the kernel that joins them.  `tokens` and `ctas` of a tile.
 static int best_splits(int64_t rest, int64_t stages, int tokens, int ctas, int workers,
                        int stage_rows) {
-  const double stage = std::max(0.3, 0.55 * tokens / kMaxBN) * stage_rows / 256.0;
+  const double stage =
+      (tokens <= kBackDeepBN ? 0.45 : std::max(0.85, 0.85 * tokens / kMaxBN)) * stage_rows / 256.0;
   int best = 1;
   double least = 0.0;
   for (int64_t s = 1; s <= std::min<int64_t>(stages, 64); ++s) {
@@ -547,23 +548,23 @@ static int best_splits(int64_t rest, int64_t stages, int tokens, int ctas, int w
   return best;
 }
 
-// Pairs of CTAs where their 256 x 256 tiles fill the SMs at least once and
-// cover no more than 6% beyond what 128 x 128 tiles cover.  Alone and at burst
-// clocks the two are level (28672 x 4096, 1536 tokens: 273 and 271 us; 2048
-// tokens, one and a half rounds of pairs: 378 and 344), below that single CTAs
-// win by up to half (4096 x 2880, 700 tokens: 30 and 18).  In a run of calls,
-// where power limits the clocks, pairs gain 3 to 6% (2048 tokens: 4096 x 14336
-// 178 -> 167 us, training on 128256 x 4096 3190 -> 3070 us).
-static bool use_pairs(int64_t M, int64_t K, int sms) {
+// Pairs of CTAs where their 256 x 256 tiles cover no more than 6% beyond what
+// 128 x 128 tiles cover and either fill the SMs three times or have long sums.
+// In a run of calls, where power limits the clock, pairs gain 3 to 6% then (2048
+// tokens: 4096 x 14336 178 -> 166 us, training on 128256 x 4096 3140 -> 3060 us).
+// Alone they are level at best, and fewer, larger tiles fit the SMs worse (28672
+// x 4096, 2048 tokens, one and a half rounds: 377 us, single CTAs 314, and level
+// in a run; 4096 x 2880: 53 and 42).
+static bool use_pairs(int64_t M, int64_t N, int64_t K, int sms) {
   const int64_t one = ((M + kMaxBN - 1) / kMaxBN) * ((K + kRows - 1) / kRows);
   const int64_t two = ((M + 2 * kMaxBN - 1) / (2 * kMaxBN)) * ((K + 2 * kRows - 1) / (2 * kRows));
-  return M >= 2 * kMaxBN && two >= sms / 2 && 4 * two * 100 <= 106 * one;
+  return M >= 2 * kMaxBN && 2 * two >= sms * (N > 65536 ? 1 : 3) && 4 * two * 100 <= 106 * one;
 }
 
 BackLayout back_layout(int64_t M, int64_t N, int64_t K, int sms, size_t off) {
   BackLayout l;
-  l.BN = lm_head_token_tile(M);
-  l.pair = use_pairs(M, K, sms);
+  l.pair = use_pairs(M, N, K, sms);
+  l.BN = l.pair ? kMaxBN : train_token_tile(M);
   const int ctas = l.pair ? 2 : 1, tokens = l.BN * ctas;
   const int workers = std::max(1, sms / ctas);
   l.n_ttiles = (int)((M + tokens - 1) / tokens);
@@ -619,7 +620,7 @@ cudaError_t back_launch(const BackCall& c, const BackLayout& L, uint8_t* ws, cud
       !encode_2d(&tm_scales, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.scales ? ws + w.scales_off : c.scales,
                  (uint64_t)c.K / 16, (uint64_t)c.N, w.scales ? w.scales_stride : (uint64_t)c.K / 16,
                  16, stage_rows, CU_TENSOR_MAP_SWIZZLE_NONE) ||
-      !encode_2d(&tm_d, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, c.d, (uint64_t)c.N, (uint64_t)((c.M + L.BN - 1) / L.BN * L.BN),
+      !encode_2d(&tm_d, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, c.d, (uint64_t)c.N, (uint64_t)c.M,
                  (uint64_t)c.d_stride * 2, 64, (uint32_t)L.BN, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   GemmArgs a = {};
@@ -673,11 +674,9 @@ static LmHeadBackLayout lm_head_back_layout(int64_t M, int64_t N, int64_t K, int
   LmHeadBackLayout l;
   l.stride = (N + 7) / 8 * 8;
   l.chunk = chunk_tokens(M, l.stride * 2);
-  const int BN = lm_head_token_tile(l.chunk);
-  const int64_t rows = (l.chunk + BN - 1) / BN * BN;
   l.d16 = kWsHeader;
-  l.factor = l.d16 + align_up((size_t)rows * l.stride * 2, 1024);
-  const size_t own = l.factor + align_up((size_t)rows * 4, 256);
+  l.factor = l.d16 + align_up((size_t)l.chunk * l.stride * 2, 1024);
+  const size_t own = l.factor + align_up((size_t)l.chunk * 4, 256);
   l.back = back_layout(l.chunk, N, K, sms, own);
   // a last chunk of fewer tokens may be split further
   size_t end = l.back.total;

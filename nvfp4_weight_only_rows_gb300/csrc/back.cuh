@@ -20,9 +20,16 @@ struct BackLayout {
 };
 BackLayout back_layout(int64_t M, int64_t N, int64_t K, int sms, size_t off);
 
+// The token tile of a call: as many tiles as 128-token ones would be, of equal
+// size (203 tokens: two of 112, not 128).
+static inline int train_token_tile(int64_t M) {
+  const int64_t tiles = std::max<int64_t>(1, (M + kMaxBN - 1) / kMaxBN);
+  return lm_head_token_tile((M + tiles - 1) / tiles);
+}
+
 struct BackCall {
   int64_t M, N, K;
-  const __half* d;      // [tokens rounded up to BN, stride]: rows past M hold anything
+  const __half* d;      // [M, stride]
   int64_t d_stride;     // elements, a multiple of 8, >= N
   const uint8_t *packed, *scales;  // as in the call; `stage` says where TMA reads them
   const WeightStage* stage;

@@ -471,7 +471,7 @@ struct EntropyLayout {
 
 static EntropyLayout entropy_layout(int64_t M, int64_t N, int64_t K, bool grad, int sms) {
   EntropyLayout l;
-  l.BN = lm_head_token_tile(M);
+  l.BN = train_token_tile(M);
   const int64_t m_pad = (M + l.BN - 1) / l.BN * l.BN;
   const int64_t units = ((N + kRows - 1) / kRows) * (m_pad / l.BN);
   l.grid = (int)std::min<int64_t>(sms, units);

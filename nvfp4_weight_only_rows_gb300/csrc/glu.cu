@@ -168,7 +168,7 @@ struct GluLayout {
 
 static GluLayout glu_layout(int64_t M, int64_t I, int64_t K, bool grad, int sms) {
   GluLayout l;
-  l.BN = lm_head_token_tile(M);
+  l.BN = train_token_tile(M);
   const int64_t m_pad = (M + l.BN - 1) / l.BN * l.BN;
   l.grid = (int)std::min<int64_t>(sms, ((I + 63) / 64) * (m_pad / l.BN));
   l.stride = (2 * I + 7) / 8 * 8;

@@ -31,17 +31,18 @@ def check(dy, w, W, **kw):
     return got
 
 
-# token tiles 16 .. 48 (deep rings), 64 .. 128, pairs of CTAs where 256 x 256
-# tiles fill 76 of them (three, with and without tiles that are split);
-# weight rows around a stage of 256; columns around tiles of 128 and pairs of
-# 256, staged rows where K % 256 != 0; the last two: stages of 128 rows, where
-# gradient and weight are large
+# token tiles 16 .. 48 (deep rings), 64 .. 128; weight rows around a stage of
+# 256; columns around tiles of 128 and pairs of 256, staged rows where K % 256 !=
+# 0; many tiles; stages of 128 rows, where gradient and weight are large; pairs of
+# CTAs, where 256 x 256 tiles fill 76 of them three times, with and without tiles
+# that are split, or once with more than 65536 rows
 SHAPES = [(1, 1, 16), (1, 700, 48), (3, 255, 144), (16, 256, 128), (17, 257, 256), (33, 1000, 272),
           (48, 64, 1024), (49, 513, 400), (64, 2000, 512), (100, 31, 96), (127, 300, 640),
           (128, 256, 256), (129, 4099, 1008), (255, 77, 128), (256, 511, 384), (257, 1500, 512),
           (300, 640, 2064), (700, 2049, 272),
           (512, 300, 9728), (500, 1111, 10000), (1000, 300, 5120),
-          (700, 40001, 272), (99, 100_100, 640)]
+          (700, 40001, 272), (99, 100_100, 640),
+          (512, 300, 29184), (500, 1111, 29456), (1000, 300, 15104), (1280, 65664, 3904)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
