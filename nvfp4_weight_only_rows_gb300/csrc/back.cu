@@ -228,7 +228,8 @@ __global__ void __launch_bounds__(Shape::kThreads, 1)
   uint64_t* done_bar = peer_full + kStages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(tmem_slot + 1);
-  float* s_fac = reinterpret_cast<float*>(bars + kBackBars);  // of a tile's tokens, per epilogue warp
+  // factors of a tile's tokens, per epilogue warp
+  float* s_fac = reinterpret_cast<float*>(bars + kBackBars);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -301,7 +302,8 @@ __global__ void __launch_bounds__(Shape::kThreads, 1)
           uint8_t* dst = s_d + st * d_stage_bytes;
 #pragma unroll
           for (int x = 0; x < kRowsOfStage / 64; ++x)
-            tma_load_2d(dst + x * box_bytes, &tm_d, n0 + 64 * x, (int32_t)pc.t0 + (int32_t)rank * BN, &s_full[st]);
+            tma_load_2d(dst + x * box_bytes, &tm_d, n0 + 64 * x,
+                        (int32_t)pc.t0 + (int32_t)rank * BN, &s_full[st]);
         }
         __syncwarp();
       }
@@ -381,7 +383,8 @@ __global__ void __launch_bounds__(Shape::kThreads, 1)
     // where this lane's row of a 32-row block keeps its scale: the order in
     // which a lane (., t) reads the rows 8 j + 2 t, 8 j + 2 t + 1, j = 0 .. 3
     uint8_t* put = scratch + (((lane & 7) >> 1) * 8 + (lane >> 3) * 2 + (lane & 1)) * 2;
-    const uint8_t* get = scratch + (lane >> 4) * (Shape::kScratch / 2) + t * 16;  // column group (lane >> 2) >> 2
+    // (column group (lane >> 2) >> 2)
+    const uint8_t* get = scratch + (lane >> 4) * (Shape::kScratch / 2) + t * 16;
     const uint32_t swz = (uint32_t)((q ^ ((lane >> 1) & 3)) << 4) + (row0 + lane) * 64;
     uint32_t nan_seen = 0;
     uint32_t g = 0;  // stage of the CTA's sequence
@@ -391,7 +394,8 @@ __global__ void __launch_bounds__(Shape::kThreads, 1)
         const uint32_t ps = g % kPStages, pph = (g / kPStages) & 1;
         const uint32_t st = g % kStages, ph = (g / kStages) & 1;
         if (!warp_wait(&p_full[ps], pph, wc)) return false;
-        const uint8_t* srow = s_scales + ps * Shape::kScales + (row0 + lane) * 16 + (pc.ft & 1) * 8 + q * 2;
+        const uint8_t* srow =
+            s_scales + ps * Shape::kScales + (row0 + lane) * 16 + (pc.ft & 1) * 8 + q * 2;
 #pragma unroll
         for (int i = 0; i < Shape::kRowsOfWarp / 32; ++i) {
           const uint32_t two = *reinterpret_cast<const uint16_t*>(srow + i * 512);

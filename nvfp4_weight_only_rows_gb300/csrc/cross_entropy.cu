@@ -28,9 +28,9 @@
 // One reference, 12 (8.3 nats), serves all maxima from -4 to 12, where P keeps
 // 2^-23 of the largest, and outside steps of 8, which keep 2^-31 of it, seldom
 // move after the first waves of units, unless one row stands out.  (Served
-// down to -52, logits that are all near -30 left nothing of P.)  In steps of 1 the reference rose late for most tokens, in steps
-// of 4 for those whose maximum passed 8: 84 of 106 us of kernel 3 went into P
-// (2048 tokens of 128256 rows).
+// down to -52, logits that are all near -30 left nothing of P.)  Of kernel 3's
+// 106 us in steps of 4 and 87 now, 84 and 66 went into P
+// (2048 tokens of 128256 rows): tokens whose largest y just passes a reference.
 //
 // The target's row is left out of r, s and P: where the model is sure of the
 // target, 1 - p_t and the pull of all other rows keep their relative accuracy
@@ -283,7 +283,8 @@ constexpr int kJoinThreads = 512;
 template <bool kGrad>
 __global__ void __launch_bounds__(kJoinThreads)
     entropy_rows_kernel(const float2* __restrict__ part, int64_t M, int64_t N, int tt_log2,
-                        int splits, const int64_t* __restrict__ targets, const float* __restrict__ y_t,
+                        int splits, const int64_t* __restrict__ targets,
+                        const float* __restrict__ y_t,
                         const float* __restrict__ global, float* __restrict__ loss,
                         float* __restrict__ lse, float* __restrict__ factor, __half* P,
                         int64_t stride) {
@@ -312,7 +313,8 @@ __global__ void __launch_bounds__(kJoinThreads)
   s_part[threadIdx.x] = acc;
   for (int w = kJoinThreads / 2; w >= TT; w >>= 1) {
     __syncthreads();
-    if ((int)threadIdx.x < w) s_part[threadIdx.x] = join(s_part[threadIdx.x], s_part[threadIdx.x + w]);
+    if ((int)threadIdx.x < w)
+      s_part[threadIdx.x] = join(s_part[threadIdx.x], s_part[threadIdx.x + w]);
   }
   __syncthreads();
   const float2 all = s_part[threadIdx.x & (TT - 1)];
@@ -350,7 +352,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int lane = threadIdx.x & 31;
   const int64_t per = (groups + splits - 1) / splits, first = split * per;
   const int64_t end = min(groups, first + per);
-  for (int64_t g0 = first + slice; g0 - slice < end; g0 += 8 * slices) {  // (the warp's count of steps)
+  for (int64_t g0 = first + slice; g0 - slice < end; g0 += 8 * slices) {  // (warp-uniform)
     float rg[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -588,8 +590,8 @@ static nvfp4_status entropy_run(const void* x, int64_t M, int64_t K, const uint8
     const int splits = kGrad ? (int)std::max<int64_t>(1, std::min<int64_t>(8, sms / tiles)) : 1;
     PdlLaunch l(dim3((unsigned)(tiles * splits)), dim3(kJoinThreads), 0, stream);
     e = cudaLaunchKernelEx(&l.cfg, entropy_rows_kernel<kGrad>, (const float2*)ea.part, rows, N,
-                           tt_log2, splits, ea.targets, (const float*)ea.y_t, global, loss + m0, lse + m0,
-                           factor, ea.P, L.stride);
+                           tt_log2, splits, ea.targets, (const float*)ea.y_t, global, loss + m0,
+                           lse + m0, factor, ea.P, L.stride);
     if (e == cudaSuccess && kGrad) {
       const BackCall c{rows, N, K, ea.P, L.stride, packed, scales, &wst, factor, mean + m0 * K,
                        NVFP4_OUT_F32, false};

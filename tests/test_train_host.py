@@ -27,7 +27,7 @@ def test_lm_head_backward(lib):
     assert size(4, 8, 24) == 0 and size(-1, 8, 32) == 0 and size(4, -1, 32) == 0 and size(4, 8, 0) == 0
     assert size(4, 8, 1 << 31) == 0
     assert size(0, 8, 32) >= 256 and size(4, 0, 32) >= 256
-    assert size(4, 1001, 32) >= 16 * 1001 * 2
+    assert size(4, 1001, 32) >= 4 * 1008 * 2  # fp16 rows of a multiple of 8
     # pieces: the workspace stops growing with the tokens
     assert size(1_000_000, 128256, 4096) < 1 << 30
 
